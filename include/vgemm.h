@@ -474,6 +474,151 @@ vg_status vg_verify_plan_grid(const vg_verify_plan *plan, int *ctas);
 
 vg_status vg_verify_plan_destroy(vg_verify_plan *plan);
 
+/* ------------------------------------- the rest of a verify round
+ * What runs between the products of a verify round and behind its head:
+ * rotary positions with the append to a paged key/value cache, attention of
+ * a tree of drafted tokens over that cache, the probabilities of logits and
+ * the verification of the drafted tokens.
+ *
+ * A sequence's tree has n nodes: node 0 is the last committed token, nodes
+ * 1..n-1 are drafted, every parent comes before its children, and a plain
+ * chain is the tree whose node i follows node i - 1.  lens[b] is the number
+ * of tokens that sequence b has committed to the cache; node i lies in the
+ * cache at slot lens[b] + i, and its position is lens[b] + its depth.
+ * counts[b], where given, is the number of nodes in use (clamped to 0..n).
+ * lens, counts and the page table are device memory and are read by the
+ * kernels, so one captured graph serves every length.
+ *
+ * Device pointers of this section need the alignment of their type unless
+ * a function says otherwise. */
+
+enum { VG_TYPE_BF16 = 0, VG_TYPE_FP16 = 1, VG_TYPE_FP32 = 2, VG_TYPE_E4M3 = 3 };
+enum { VG_ROPE_HALF = 0, VG_ROPE_INTERLEAVED = 1 };
+
+/* A paged cache: element (page, token, head, i) of k lies at
+ * k + page * k_stride[0] + token * k_stride[1] + head * k_stride[2] + i
+ * (strides in elements), the same for v.  Slot s of sequence b is token
+ * s % page_size of page page_table[b * table_stride + s / page_size].
+ * Fill every field but `opaque`, then call vg_kv_cache_init, which checks
+ * them and prepares the copies' descriptors; the struct is host memory, is
+ * only read by later calls and holds no resource.
+ * Limits: head_dim a multiple of 16, at most 256; page_size a multiple of
+ * 16; k, v 16-byte aligned, strides multiples of 16 bytes.
+ * type: VG_TYPE_BF16, VG_TYPE_FP16 (that of q) or VG_TYPE_E4M3, whose codes
+ * are worth k_scale (v_scale) times their value; the scales are 1 otherwise.
+ * An entry of the table outside 0..pages-1 is no page, and neither is a slot
+ * past max_pages: what would be written there is dropped, and a key there
+ * is left out of the attention. */
+typedef struct vg_kv_cache {
+    void *k, *v;
+    const int32_t *page_table;
+    int32_t type, heads, head_dim, page_size;
+    int64_t pages;
+    int64_t k_stride[3], v_stride[3];
+    int64_t table_stride;
+    int32_t batch, max_pages;
+    float k_scale, v_scale;
+    uint64_t opaque[34];
+} vg_kv_cache;
+
+vg_status vg_kv_cache_init(vg_kv_cache *cache);
+
+/* Rotary positions and the append to the cache, in one launch.
+ * For element pairs j < rot / 2 of a head (elements j and j + rot / 2 for
+ * VG_ROPE_HALF, 2j and 2j + 1 for VG_ROPE_INTERLEAVED), with the angle
+ * a = position * inv_freq[j]:
+ *     x1' = factor * (x1 cos a - x2 sin a),  x2' = factor * (x1 sin a + x2 cos a);
+ * elements rot..head_dim-1 pass unchanged.  q turns into q_out, k goes to
+ * the cache turned and v as it is (E4M3: the code nearest to the value times
+ * 1 / scale in FP32, ties to even, saturating at 448; NaN stays NaN).  The angle is
+ * held as a 64-bit fraction of a turn, so it is as exact at position 10^6
+ * as at 1.  Nodes past counts[b] append nothing and their q_out is 0.
+ *   q [batch][n][q_heads][head_dim], k, v [batch][n][heads][head_dim] with
+ *   strides (batch, node, head) in elements, 16-bit types (`type`).
+ *   q_out contiguous; it may be q itself where q is contiguous.
+ *   inv_freq device FP64 [rot / 2], finite and >= 0; rot even, 0..head_dim.
+ *   depth device int32 [batch][n], or NULL: node i has depth i.
+ *   counts device int32 [batch], or NULL: n each.
+ * Here n may be any length >= 1 (a prompt is a chain). */
+typedef struct vg_rope_desc {
+    const void *q, *k, *v;
+    void *q_out;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    const double *inv_freq;
+    const int32_t *lens, *depth, *counts;
+    int32_t type, layout, n, q_heads, rot;
+    float factor;
+} vg_rope_desc;
+
+vg_status vg_rope_append(const vg_rope_desc *desc, const vg_kv_cache *cache, vg_stream_t stream);
+
+/* Attention of the n <= 64 nodes of each sequence's tree over its cache:
+ *     out[b][i][h] = sum_s p_s v_s,  p = softmax_s(scale * q[b][i][h] . k_s),
+ * over the slots s < lens[b] and the slots lens[b] + j with j < counts[b]
+ * and bit j of tree[b * n + i] set (tree NULL: j <= i).  Query head h reads
+ * cache head h / (q_heads / heads).  Scores and sums are FP32.  What a node
+ * does not attend to has no influence on it, NaN and infinities included.
+ * A node without any key, and a node past counts[b], gives out = 0 and
+ * lse = -infinity.
+ *   q strides (batch, node, head) in elements, multiples of 8, q 16-byte
+ *   aligned; out contiguous [batch][n][q_heads][head_dim] in q's type.
+ *   lse FP32 [batch][n][q_heads] or NULL: log of the sum of exponentials.
+ *   workspace: vg_tree_attention_workspace_size bytes, 16-byte aligned,
+ *   zero-filled once; calls that share one must not overlap on the GPU.  Its
+ *   error word (vg_gemv_workspace_check reads and clears it) is set by
+ *   bounded waits that run out. */
+typedef struct vg_attention_desc {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *lens, *counts;
+    const uint64_t *tree;
+    int64_t q_stride[3];
+    int32_t type, n, q_heads;
+    float scale;
+} vg_attention_desc;
+
+vg_status vg_tree_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
+                                           size_t *bytes);
+vg_status vg_tree_attention(const vg_attention_desc *desc, const vg_kv_cache *cache,
+                            void *workspace, size_t workspace_bytes, vg_stream_t stream);
+
+/* out[r][i] = exp((x[r][i] - max) / T[r]) / sum of the same over the row,
+ * FP32, for contiguous rows of logits (BF16, FP16 or FP32).  temperature:
+ * device FP32 [rows], or NULL for 1; a row with T <= 0 gives 1 at its first
+ * largest logit and 0 elsewhere.  A logit of -infinity has probability 0; a
+ * row of nothing else is all 0.  x and out 16-byte aligned. */
+vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
+                           const float *temperature, float *out, vg_stream_t stream);
+
+/* Verification of a tree of drafted tokens against the target's
+ * probabilities, from given random numbers.
+ *   p [batch][n][vocab] FP32: the target's distribution after each node.
+ *   q [batch][q_rows][vocab] FP32: the distribution that a node's children
+ *     were drafted from.
+ *   tokens, parents [batch][n] int32: a drafted node's token, and its parent
+ *     (entries of node 0 are not read; a node whose parent is not before it
+ *     or is not below q_rows, or whose token is outside the vocabulary, is
+ *     passed over).
+ *   u [batch][n] FP32 in [0, 1): u[i] decides node i, u[0] draws the token.
+ * From node 0 on, the children of the current node are tried in order: a
+ * child is accepted if u q(t) S < r(t), where r = p and S = 1 at first and,
+ * after each refusal, r = max(r - S q, 0) and S = sum r.  An accepted child
+ * becomes the current node.  When no child is left a last token is drawn
+ * from r: the first index whose running sum exceeds u[0] times the whole
+ * (from p where r is zero everywhere; -1 where p is, too).
+ *   accepted [batch]; path [batch][n]: accepted nodes, then -1; out
+ *   [batch][n + 1]: their tokens, the last token, then -1.
+ * Sums are taken in 64-bit fixed point (units of 2^-60), so the order of
+ * addition does not change them; negative and NaN entries count as 0,
+ * entries above 1 as 1, and a row must sum to less than 16.
+ * 1 <= n <= 1024, 1 <= q_rows <= n (q may be NULL and q_rows 0 when n is 1),
+ * 1 <= vocab < 2^28; p and q 16-byte aligned. */
+vg_status vg_verify_tree(const float *p, const float *q, const int32_t *tokens,
+                         const int32_t *parents, const int32_t *counts, const float *u,
+                         int batch, int n, int q_rows, int64_t vocab, int32_t *accepted,
+                         int32_t *path, int32_t *out, vg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,7 +5,9 @@ for several requests' drafts in one pass), the weight-streaming product of
 decode and speculative verification (the "GEMVs" row of the
 mtp7-device-confidence engine card's Design table); MXFP8 and groupwise
 INT4 weights as well, and a fused verify pass over a layer stack with RMS
-norms and the gated activation.
+norms and the gated activation.  ``verify_round`` has what a verify round
+runs around these products: rotary positions with the append to a paged
+cache, tree attention over it, probabilities and the drafts' verification.
 
 Every step runs in the CUDA kernels of ``libvgemm.so`` (C ABI declared in
 ``include/vgemm.h``); this module only marshals torch tensors (device
@@ -23,6 +25,8 @@ import torch
 from . import _lib
 from ._lib import (VG_FMT_FP8_ROWSCALE, VG_FMT_INT4G, VG_FMT_MXFP8, VG_FMT_NVFP4,  # noqa: F401
                    VG_OP_GEMV, VG_OP_RMSNORM, VG_OP_SWIGLU, VGError)
+from .verify_round import (KVCache, probabilities, rope_append, rope_frequencies,  # noqa: F401
+                           tree_attention, tree_attention_workspace, verify_tree)
 
 __all__ = [
     "NVFP4Weight", "FP8Weight", "nvfp4_pack", "fp8_pack", "nvfp4_unpack", "fp8_unpack",
@@ -31,6 +35,8 @@ __all__ = [
     "nvfp4_pack_gated", "fp8_pack_gated", "RMSNorm", "BlockScaledWeight", "mxfp8_pack",
     "int4g_pack", "mxfp8_unpack", "int4g_unpack", "mxfp8_from_canonical",
     "int4g_from_canonical", "VG_FMT_MXFP8", "VG_FMT_INT4G",
+    "KVCache", "rope_frequencies", "rope_append", "tree_attention_workspace", "tree_attention",
+    "probabilities", "verify_tree",
 ]
 
 

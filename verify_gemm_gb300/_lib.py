@@ -28,6 +28,12 @@ VG_FMT_INT4G = 3
 VG_OP_GEMV = 0
 VG_OP_SWIGLU = 1
 VG_OP_RMSNORM = 2
+VG_TYPE_BF16 = 0
+VG_TYPE_FP16 = 1
+VG_TYPE_FP32 = 2
+VG_TYPE_E4M3 = 3
+VG_ROPE_HALF = 0
+VG_ROPE_INTERLEAVED = 1
 
 P = ctypes.c_void_p
 i64 = ctypes.c_int64
@@ -48,6 +54,29 @@ class vg_plan_options(ctypes.Structure):
     _fields_ = [("ordered", ctypes.c_int32), ("max_ctas", ctypes.c_int32),
                 ("wait_timeout_ns", i64), ("hold_group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class vg_kv_cache(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("page_table", P), ("type", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", i64), ("k_stride", i64 * 3),
+                ("v_stride", i64 * 3), ("table_stride", i64), ("batch", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("k_scale", f32), ("v_scale", f32),
+                ("opaque", ctypes.c_uint64 * 34)]
+
+
+class vg_rope_desc(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("q_out", P), ("q_stride", i64 * 3),
+                ("k_stride", i64 * 3), ("v_stride", i64 * 3), ("inv_freq", P), ("lens", P),
+                ("depth", P), ("counts", P), ("type", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("factor", f32)]
+
+
+class vg_attention_desc(ctypes.Structure):
+    _fields_ = [("q", P), ("out", P), ("lse", P), ("lens", P), ("counts", P), ("tree", P),
+                ("q_stride", i64 * 3), ("type", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("scale", f32)]
 
 
 SIGNATURES = {
@@ -93,6 +122,12 @@ SIGNATURES = {
     "vg_verify_plan_bytes": (st, [P, ctypes.POINTER(i64)]),
     "vg_verify_plan_grid": (st, [P, ctypes.POINTER(i32)]),
     "vg_verify_plan_destroy": (st, [P]),
+    "vg_kv_cache_init": (st, [ctypes.POINTER(vg_kv_cache)]),
+    "vg_rope_append": (st, [P, P, P]),
+    "vg_tree_attention_workspace_size": (st, [i32, i32, P, ctypes.POINTER(sz)]),
+    "vg_tree_attention": (st, [P, P, P, sz, P]),
+    "vg_probabilities": (st, [P, i32, i64, i64, P, P, P]),
+    "vg_verify_tree": (st, [P, P, P, P, P, P, i32, i32, i32, i64, P, P, P, P]),
 }
 
 _lock = threading.Lock()

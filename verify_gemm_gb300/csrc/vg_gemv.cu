@@ -2027,23 +2027,6 @@ vg_status device_info(int *dev_out, DeviceInfo **info) {
   return VG_OK;
 }
 
-// The tensor-map encoder of the driver, looked up once through the runtime.
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
 // x viewed as [K/64 units][N rows][64 columns] (strides 128 bytes and 2K
 // bytes), copied in boxes of `units` units x 8 rows with the 128-byte
 // swizzle; rows >= N and units past K read as zeros.  False when K is not a

@@ -2,6 +2,8 @@
 // units: argument validation and CUDA error capture.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -13,6 +15,13 @@ namespace vg {
 
 // Last CUDA error message (per host thread), surfaced by vg_last_cuda_error.
 void set_cuda_error(cudaError_t e);
+
+// The tensor-map encoder of the driver, looked up once through the runtime
+// (NULL if the driver has none).
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();
+
+// SM count of the current device; VG_ERR_UNSUPPORTED unless it is sm_103.
+vg_status device_sms(int *sms);
 
 inline cudaStream_t as_cuda(vg_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 

@@ -1,0 +1,234 @@
+// vg_rope.cu -- vg_kv_cache_init, and vg_rope_append: rotary positions of q
+// and k with the append of k and v to the paged cache, in one launch.
+//
+// The angle of pair j at position s is s * inv_freq[j].  As a fraction of a
+// turn it is s * f mod 1 with f = inv_freq[j] / 2 pi, so f is taken as a
+// 64-bit integer in units of 2^-64 turns and the product with the integer
+// position wraps by itself: no range reduction and no loss at far positions
+// (an FP32 product is 0.06 radians off at position 10^6).  What remains, a
+// signed fraction of a turn, goes through sincospif in FP32.
+//
+// Bytes bound it for prompts and latency for single tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "vg_cache.h"
+
+namespace vg {
+namespace {
+
+struct RopeParams {
+  const void *q, *k, *v;
+  void *q_out, *ck, *cv;
+  int64_t qs[3], ks[3], vs[3];     // batch, node, head
+  int64_t cks[3], cvs[3];          // page, token, head
+  const double *inv_freq;
+  const int32_t *lens, *depth, *counts;
+  CacheView cache;
+  int64_t tokens;                  // batch * n
+  int n, hq, hkv, d, rot;
+  float factor, k_inv, v_inv;       // E4M3: 1 / scale
+};
+
+constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_f(__nv_bfloat16 &o, float x) { o = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(__half &o, float x) { o = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(__nv_fp8_e4m3 &o, float x) {
+  o.__x = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Cosine and sine, times the factor, of pair j at `position`.
+__device__ __forceinline__ float2 turn(const RopeParams &p, int64_t position, int j) {
+  const double f = p.inv_freq[j] * 0.15915494309189535;      // 1 / 2 pi
+  const uint64_t step = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+  const int64_t at = int64_t(uint64_t(position) * step);
+  float s, c;
+  sincospif(__ll2float_rn(at) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63: half turns
+  return make_float2(c * p.factor, s * p.factor);
+}
+
+// One pair of elements at a time: right for every size and alignment.
+template <typename T, typename C, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  extern __shared__ float2 angles[];                          // [rot / 2]
+  const int64_t tok = blockIdx.x;
+  const int b = int(tok / p.n), i = int(tok % p.n);
+  const int64_t len = p.lens[b];
+  const int count = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
+  const bool used = i < count;
+  const int half = p.rot / 2;
+  const int64_t position = len + (p.depth ? p.depth[tok] : i);
+  for (int j = threadIdx.x; j < half; j += kRopeThreads) angles[j] = turn(p, position, j);
+  __syncthreads();
+  const int64_t slot = len + i;
+  const int64_t page = used && slot >= 0 ? cache_page(p.cache, b, slot) : -1;
+  const int64_t off = slot % p.cache.page_size;
+  const int pairs = half + (p.d - p.rot);                     // turned pairs, then single elements
+  const int heads = p.hq + 2 * p.hkv;
+  for (int w = threadIdx.x; w < heads * pairs; w += kRopeThreads) {
+    const int h = w / pairs, e = w % pairs;
+    const bool single = e >= half;
+    const int e1 = single ? p.rot + e - half : kInterleaved ? 2 * e : e;
+    const int e2 = single ? e1 : kInterleaved ? 2 * e + 1 : e + half;
+    const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
+    const T *src = is_q ? static_cast<const T *>(p.q) + b * p.qs[0] + i * p.qs[1] + h * p.qs[2]
+                 : is_v ? static_cast<const T *>(p.v) + b * p.vs[0] + i * p.vs[1] +
+                              (h - p.hq - p.hkv) * p.vs[2]
+                        : static_cast<const T *>(p.k) + b * p.ks[0] + i * p.ks[1] +
+                              (h - p.hq) * p.ks[2];
+    float x1 = to_f(src[e1]), x2 = to_f(src[e2]);
+    if (!single && !is_v) {
+      const float2 cs = angles[e];
+      const float y1 = x1 * cs.x - x2 * cs.y;
+      x2 = x1 * cs.y + x2 * cs.x;
+      x1 = y1;
+    }
+    if (is_q) {
+      T *dst = static_cast<T *>(p.q_out) + (tok * p.hq + h) * p.d;
+      from_f(dst[e1], used ? x1 : 0.f);
+      if (!single) from_f(dst[e2], used ? x2 : 0.f);
+    } else if (page >= 0) {
+      const int hc = is_v ? h - p.hq - p.hkv : h - p.hq;
+      const int64_t *cs = is_v ? p.cvs : p.cks;
+      C *dst = static_cast<C *>(is_v ? p.cv : p.ck) + page * cs[0] + off * cs[1] + hc * cs[2];
+      if (sizeof(C) == 1) {
+        const float inv = is_v ? p.v_inv : p.k_inv;
+        x1 *= inv;
+        x2 *= inv;
+      }
+      from_f(dst[e1], x1);
+      if (!single) from_f(dst[e2], x2);
+    }
+  }
+}
+
+template <typename T, typename C>
+void launch_rope(const RopeParams &p, bool interleaved, cudaStream_t st) {
+  const size_t smem = size_t(p.rot / 2) * sizeof(float2);
+  if (interleaved)
+    rope_kernel<T, C, true><<<unsigned(p.tokens), kRopeThreads, smem, st>>>(p);
+  else
+    rope_kernel<T, C, false><<<unsigned(p.tokens), kRopeThreads, smem, st>>>(p);
+}
+
+bool map_cache(CUtensorMap *map, const vg_kv_cache &c, void *base, const int64_t *stride) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (!fn) return false;
+  const bool f8 = c.type == VG_TYPE_E4M3;
+  const cuuint64_t size = f8 ? 1 : 2;
+  const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.page_size), cuuint64_t(c.heads),
+                              cuuint64_t(c.pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(stride[1]) * size, cuuint64_t(stride[2]) * size,
+                                 cuuint64_t(stride[0]) * size};
+  const cuuint32_t box[4] = {cuuint32_t(kCacheBoxElems), cuuint32_t(cache_box_tokens(c.page_size)),
+                             1u, 1u};
+  const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+  return fn(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace vg
+
+using namespace vg;
+
+extern "C" vg_status vg_kv_cache_init(vg_kv_cache *c) {
+  if (!c) return VG_ERR_INVALID_ARG;
+  c->opaque[kCacheMark] = 0;
+  if (!c->k || !c->v || !c->page_table || c->heads < 1 || c->batch < 1 || c->max_pages < 1 ||
+      c->pages < 1 || c->head_dim < 16 || c->head_dim % 16 || c->page_size < 16 ||
+      c->page_size % 16 || c->table_stride < c->max_pages)
+    return VG_ERR_INVALID_ARG;
+  if (c->type != VG_TYPE_BF16 && c->type != VG_TYPE_FP16 && c->type != VG_TYPE_E4M3)
+    return VG_ERR_INVALID_ARG;
+  if (c->head_dim > 256 || c->pages >= (int64_t(1) << 31) || c->heads > 65535 ||
+      c->batch > 65535 || int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 31))
+    return VG_ERR_UNSUPPORTED;
+  const int64_t size = c->type == VG_TYPE_E4M3 ? 1 : 2;
+  if (c->type == VG_TYPE_E4M3) {
+    if (!(c->k_scale > 0 && c->v_scale > 0) || !std::isfinite(c->k_scale) ||
+        !std::isfinite(c->v_scale))
+      return VG_ERR_INVALID_ARG;
+  } else if (c->k_scale != 1.f || c->v_scale != 1.f) {
+    return VG_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < 3; ++i)
+    for (const int64_t st : {c->k_stride[i], c->v_stride[i]}) {
+      if (st < c->head_dim || st * size % 16) return VG_ERR_INVALID_ARG;
+      if (st * size >= (int64_t(1) << 40)) return VG_ERR_UNSUPPORTED;
+    }
+  if (!aligned16(c->k) || !aligned16(c->v)) return VG_ERR_ALIGNMENT;
+  alignas(64) CUtensorMap map;
+  if (!map_cache(&map, *c, c->k, c->k_stride)) return VG_ERR_UNSUPPORTED;
+  std::memcpy(c->opaque, &map, sizeof map);
+  if (!map_cache(&map, *c, c->v, c->v_stride)) return VG_ERR_UNSUPPORTED;
+  std::memcpy(c->opaque + kCacheMapWords, &map, sizeof map);
+  c->opaque[kCacheMark] = cache_mark(*c);
+  return VG_OK;
+}
+
+extern "C" vg_status vg_rope_append(const vg_rope_desc *d, const vg_kv_cache *cache,
+                                    vg_stream_t stream) {
+  if (!d) return VG_ERR_INVALID_ARG;
+  if (vg_status s = cache_ready(cache)) return s;
+  if (!d->q || !d->k || !d->v || !d->q_out || !d->lens || d->n < 1 || d->q_heads < 1 ||
+      d->rot < 0 || d->rot % 2 || d->rot > cache->head_dim || (d->rot && !d->inv_freq))
+    return VG_ERR_INVALID_ARG;
+  if (d->type != VG_TYPE_BF16 && d->type != VG_TYPE_FP16) return VG_ERR_INVALID_ARG;
+  if (cache->type != VG_TYPE_E4M3 && cache->type != d->type) return VG_ERR_INVALID_ARG;
+  if (d->layout != VG_ROPE_HALF && d->layout != VG_ROPE_INTERLEAVED) return VG_ERR_INVALID_ARG;
+  for (const void *p : {d->q, d->k, d->v, static_cast<const void *>(d->q_out)})
+    if (reinterpret_cast<uintptr_t>(p) & 1) return VG_ERR_ALIGNMENT;
+  const int64_t tokens = int64_t(cache->batch) * d->n;
+  if (tokens >= (int64_t(1) << 31) || d->q_heads > 65535) return VG_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (vg_status s = device_sms(&sms)) return s;
+  RopeParams p;
+  p.q = d->q;
+  p.k = d->k;
+  p.v = d->v;
+  p.q_out = d->q_out;
+  p.ck = cache->k;
+  p.cv = cache->v;
+  for (int i = 0; i < 3; ++i) {
+    p.qs[i] = d->q_stride[i];
+    p.ks[i] = d->k_stride[i];
+    p.vs[i] = d->v_stride[i];
+    p.cks[i] = cache->k_stride[i];
+    p.cvs[i] = cache->v_stride[i];
+  }
+  p.inv_freq = d->inv_freq;
+  p.lens = d->lens;
+  p.depth = d->depth;
+  p.counts = d->counts;
+  p.cache = cache_view(*cache);
+  p.tokens = tokens;
+  p.n = d->n;
+  p.hq = d->q_heads;
+  p.hkv = cache->heads;
+  p.d = cache->head_dim;
+  p.rot = d->rot;
+  p.factor = d->factor;
+  p.k_inv = 1.f / cache->k_scale;
+  p.v_inv = 1.f / cache->v_scale;
+  const bool il = d->layout == VG_ROPE_INTERLEAVED, f8 = cache->type == VG_TYPE_E4M3;
+  cudaStream_t st = as_cuda(stream);
+  if (d->type == VG_TYPE_BF16) {
+    if (f8) launch_rope<__nv_bfloat16, __nv_fp8_e4m3>(p, il, st);
+    else launch_rope<__nv_bfloat16, __nv_bfloat16>(p, il, st);
+  } else {
+    if (f8) launch_rope<__half, __nv_fp8_e4m3>(p, il, st);
+    else launch_rope<__half, __half>(p, il, st);
+  }
+  VG_LAUNCH_CHECK();
+  return VG_OK;
+}

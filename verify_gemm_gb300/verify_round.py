@@ -1,0 +1,270 @@
+"""The operators of a verify round between and behind its products: rotary
+positions with the append to a paged cache, attention of a tree of drafted
+tokens over that cache, the probabilities of logits and the verification of
+the drafted tokens.
+
+Every step runs in the CUDA kernels of ``libvgemm.so``; this module only
+checks and marshals torch tensors.  Lengths, node counts and page tables are
+read on the device, so a captured graph serves every length.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _lib
+from ._lib import (VG_ROPE_HALF, VG_ROPE_INTERLEAVED, VG_TYPE_BF16, VG_TYPE_E4M3, VG_TYPE_FP16,
+                   VG_TYPE_FP32, vg_attention_desc, vg_kv_cache, vg_rope_desc)
+
+_TYPES = {torch.bfloat16: VG_TYPE_BF16, torch.float16: VG_TYPE_FP16, torch.float32: VG_TYPE_FP32,
+          torch.float8_e4m3fn: VG_TYPE_E4M3}
+_LAYOUTS = {"half": VG_ROPE_HALF, "interleaved": VG_ROPE_INTERLEAVED}
+
+
+def _stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _int32(t, shape, name):
+    """Address of a contiguous CUDA int32 tensor of that shape (None: 0)."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()) or t.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, name):
+    """A CUDA tensor [batch, n, heads, head_dim] with contiguous heads."""
+    if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name}: expected a CUDA tensor [batch, n, heads, head_dim] whose last "
+                         "dimension is contiguous")
+    return t
+
+
+class KVCache:
+    """A paged key/value cache: k and v [pages, page_size, heads, head_dim]
+    (views of other orders are fine, the last dimension contiguous) in
+    bfloat16, float16 or float8_e4m3fn, and page_table int32 [batch,
+    max_pages]; slot s of sequence b is token s % page_size of page
+    page_table[b, s // page_size].  An 8-bit code is worth k_scale (v_scale)
+    times its value.  The tensors are kept alive and read at every call; the
+    table's contents may change between calls."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                 k_scale: float = 1.0, v_scale: float = 1.0):
+        for t, name in ((k, "k"), (v, "v")):
+            if not t.is_cuda or t.dim() != 4 or t.dtype not in _TYPES or t.stride(3) != 1:
+                raise ValueError(f"{name}: expected a CUDA tensor [pages, page_size, heads, "
+                                 "head_dim] whose last dimension is contiguous")
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have the same shape, type and device")
+        if not (page_table.device == k.device and page_table.dtype == torch.int32
+                and page_table.dim() == 2 and page_table.stride(1) == 1):
+            raise ValueError("page_table: expected a CUDA int32 tensor [batch, max_pages]")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.batch, self.heads, self.head_dim, self.dtype = (page_table.shape[0], k.shape[2],
+                                                             k.shape[3], k.dtype)
+        c = vg_kv_cache()
+        c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
+        c.type, c.heads, c.head_dim, c.page_size = _TYPES[k.dtype], k.shape[2], k.shape[3], k.shape[1]
+        c.pages = k.shape[0]
+        for i, dim in enumerate((0, 1, 2)):
+            # the stride of a dimension of one is arbitrary: any legal one will do
+            c.k_stride[i] = k.stride(dim) if k.shape[dim] > 1 else 256
+            c.v_stride[i] = v.stride(dim) if v.shape[dim] > 1 else 256
+        c.batch, c.max_pages = page_table.shape
+        c.table_stride = page_table.stride(0) if c.batch > 1 else c.max_pages
+        c.k_scale, c.v_scale = k_scale, v_scale
+        _lib.check(_lib.vg_kv_cache_init(ctypes.byref(c)), "vg_kv_cache_init")
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, context: int = 0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq float64 [rot / 2], attention factor) for rope_append.
+
+    inv_freq[j] = base ** (-2 j / rot).  scaling "linear" divides all of them
+    by `factor`; "ntk" raises the base so that the slowest pair is divided by
+    it; "yarn" leaves the pairs that turn more than beta_fast times in the
+    original `context`, divides those that turn less than beta_slow times, and
+    goes over evenly in the logarithm of the turns between the two, with the
+    attention factor 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2 or base <= 1 or factor < 1:
+        raise ValueError("rot must be even and positive, base > 1 and factor >= 1")
+    j = torch.arange(rot // 2, dtype=torch.float64)
+    m = 1.0
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    inv = base ** (-2.0 * j / rot)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        if context < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn scaling needs the original context and beta_fast > beta_slow > 0")
+        turns = context * inv / (2 * math.pi)
+        keep = ((torch.log(turns) - math.log(beta_slow))
+                / (math.log(beta_fast) - math.log(beta_slow))).clamp(0, 1)
+        inv = inv * keep + inv / factor * (1 - keep)
+        m = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling: None, 'linear', 'ntk' or 'yarn'")
+    return inv.to(device), m
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
+                cache: KVCache, lens: torch.Tensor, depth: torch.Tensor | None = None,
+                counts: torch.Tensor | None = None, layout: str = "half", factor: float = 1.0,
+                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotates q [batch, n, q_heads, head_dim] and k, and appends k and v
+    [batch, n, heads, head_dim] to the cache; returns the rotated q.
+
+    Node i of sequence b goes to slot lens[b] + i and has position lens[b] +
+    depth[b, i] (depth None: i).  The first 2 * inv_freq.numel() elements of a
+    head turn: pairs (j, j + rot/2) for layout "half", (2j, 2j + 1) for
+    "interleaved".  Nodes past counts[b] append nothing and give 0."""
+    _heads(q, "q")
+    _heads(k, "k")
+    _heads(v, "v")
+    B, n, hq, d = q.shape
+    if B != cache.batch or d != cache.head_dim or k.shape != (B, n, cache.heads, d) \
+            or v.shape != k.shape:
+        raise ValueError("q, k, v and the cache do not fit together")
+    if not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q, k and v must have the same type")
+    if not (inv_freq.is_cuda and inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()):
+        raise ValueError("inv_freq: expected a contiguous CUDA float64 tensor")
+    if layout not in _LAYOUTS:
+        raise ValueError("layout: 'half' or 'interleaved'")
+    if q_out is None:
+        q_out = torch.empty((B, n, hq, d), dtype=q.dtype, device=q.device)
+    elif not (q_out.is_cuda and q_out.shape == q.shape and q_out.dtype == q.dtype
+              and q_out.is_contiguous()):
+        raise ValueError("q_out: expected a contiguous CUDA tensor like q")
+    desc = vg_rope_desc(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                        q.stride()[:3], k.stride()[:3], v.stride()[:3], inv_freq.data_ptr(),
+                        _int32(lens, (B,), "lens"), _int32(depth, (B, n), "depth"),
+                        _int32(counts, (B,), "counts"), _TYPES.get(q.dtype, -1), _LAYOUTS[layout],
+                        n, hq, 2 * inv_freq.numel(), factor)
+    s = _lib.vg_rope_append(ctypes.byref(desc), cache._ref, _stream(stream))
+    if s:
+        _lib.check(s, "vg_rope_append")
+    return q_out
+
+
+def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
+    """A zero-filled workspace for tree_attention with q of this shape."""
+    n = ctypes.c_size_t()
+    _lib.check(_lib.vg_tree_attention_workspace_size(q.shape[1], q.shape[2], cache._ref,
+                                                     ctypes.byref(n)),
+               "vg_tree_attention_workspace_size")
+    return torch.zeros(n.value, dtype=torch.uint8, device=q.device)
+
+
+def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
+                   tree: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                   scale: float | None = None, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of q [batch, n, q_heads, head_dim], n <= 64, over the cache.
+
+    Node i of sequence b attends to the lens[b] committed slots and to the
+    nodes whose bits are set in tree[b, i] (int64 words; None: a chain), those
+    below counts[b] alone.  A node without any key and a node past counts[b]
+    give 0.  scale: 1 / sqrt(head_dim) by default.  lse: float32 [batch, n,
+    q_heads], written if given.  workspace: from tree_attention_workspace,
+    made anew by each call that is given none; calls that share one must not
+    overlap."""
+    _heads(q, "q")
+    B, n, hq, d = q.shape
+    if B != cache.batch or d != cache.head_dim:
+        raise ValueError("q and the cache do not fit together")
+    if tree is not None and not (tree.is_cuda and tree.dtype == torch.int64
+                                 and tree.is_contiguous() and tree.shape == (B, n)):
+        raise ValueError("tree: expected a contiguous CUDA int64 tensor [batch, n]")
+    if out is None:
+        out = torch.empty((B, n, hq, d), dtype=q.dtype, device=q.device)
+    elif not (out.is_cuda and out.shape == q.shape and out.dtype == q.dtype
+              and out.is_contiguous()):
+        raise ValueError("out: expected a contiguous CUDA tensor like q")
+    if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32
+                                and lse.is_contiguous() and lse.shape == (B, n, hq)):
+        raise ValueError("lse: expected a contiguous CUDA float32 tensor [batch, n, q_heads]")
+    if workspace is None:
+        workspace = tree_attention_workspace(q, cache)
+    desc = vg_attention_desc(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                             _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts"),
+                             tree.data_ptr() if tree is not None else None, q.stride()[:3],
+                             _TYPES.get(q.dtype, -1), n, hq, d ** -0.5 if scale is None else scale)
+    s = _lib.vg_tree_attention(ctypes.byref(desc), cache._ref, workspace.data_ptr(),
+                               workspace.numel(), _stream(stream))
+    if s:
+        _lib.check(s, "vg_tree_attention")
+    return out
+
+
+def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """float32 softmax over the last dimension of contiguous logits (bfloat16,
+    float16 or float32), each row over its own temperature (float32, one for
+    every row; None: 1).  A temperature <= 0 gives 1 at the row's first
+    largest logit."""
+    if not (logits.is_cuda and logits.is_contiguous() and logits.dim() >= 1 and logits.numel()):
+        raise ValueError("logits: expected a contiguous CUDA tensor that is not empty")
+    vocab = logits.shape[-1]
+    rows = logits.numel() // vocab
+    if temperature is not None and not (temperature.is_cuda and temperature.dtype == torch.float32
+                                        and temperature.is_contiguous()
+                                        and temperature.numel() == rows):
+        raise ValueError("temperature: expected a contiguous CUDA float32 tensor, one for each row")
+    if out is None:
+        out = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+    elif not (out.is_cuda and out.shape == logits.shape and out.dtype == torch.float32
+              and out.is_contiguous()):
+        raise ValueError("out: expected a contiguous CUDA float32 tensor like logits")
+    s = _lib.vg_probabilities(logits.data_ptr(), _TYPES.get(logits.dtype, -1), rows, vocab,
+                              temperature.data_ptr() if temperature is not None else None,
+                              out.data_ptr(), _stream(stream))
+    if s:
+        _lib.check(s, "vg_probabilities")
+    return out
+
+
+def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
+                parents: torch.Tensor, u: torch.Tensor, counts: torch.Tensor | None = None,
+                stream=None):
+    """Verifies each sequence's drafted tokens: p float32 [batch, n, vocab],
+    the target's distribution after each node; q float32 [batch, rows, vocab],
+    the distribution each node's children were drafted from; tokens and
+    parents int32 [batch, n]; u float32 [batch, n], random numbers in [0, 1).
+
+    Returns int32 (accepted [batch], path [batch, n], out [batch, n + 1]): how
+    many drafts hold, their nodes, and their tokens with the one drawn after
+    them; -1 behind.  include/vgemm.h (vg_verify_tree) has the rule."""
+    if not (p.is_cuda and p.dtype == torch.float32 and p.dim() == 3 and p.is_contiguous()):
+        raise ValueError("p: expected a contiguous CUDA float32 tensor [batch, n, vocab]")
+    B, n, V = p.shape
+    if q is not None and not (q.is_cuda and q.dtype == torch.float32 and q.dim() == 3
+                              and q.is_contiguous() and q.shape[0] == B and q.shape[2] == V):
+        raise ValueError("q: expected a contiguous CUDA float32 tensor [batch, rows, vocab]")
+    if not (u.is_cuda and u.dtype == torch.float32 and u.is_contiguous() and u.shape == (B, n)):
+        raise ValueError("u: expected a contiguous CUDA float32 tensor [batch, n]")
+    # one allocation for the three results
+    flat = torch.empty(B * (2 * n + 2), dtype=torch.int32, device=p.device)
+    accepted, path, out = flat.split_with_sizes((B, B * n, B * (n + 1)))
+    path, out = path.view(B, n), out.view(B, n + 1)
+    at = flat.data_ptr()
+    s = _lib.vg_verify_tree(p.data_ptr(), q.data_ptr() if q is not None else None,
+                            _int32(tokens, (B, n), "tokens"), _int32(parents, (B, n), "parents"),
+                            _int32(counts, (B,), "counts"), u.data_ptr(), B, n,
+                            q.shape[1] if q is not None else 0, V, at, at + 4 * B,
+                            at + 4 * B * (n + 1), _stream(stream))
+    if s:
+        _lib.check(s, "vg_verify_tree")
+    return accepted, path, out
