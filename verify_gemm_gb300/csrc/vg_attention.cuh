@@ -1,0 +1,837 @@
+// vg_attention.cuh -- the kernel of vg_tree_attention: the nodes of each sequence's tree
+// over its paged cache.
+//
+// The rows that share a cache head (n nodes x the query heads of the group,
+// node-major) are one operand; a unit is (sequence, cache head, block of up
+// to 16 RW rows), and its keys are cut into tiles of 64.  With scores in
+// base 2, x = c q.k (c = scale log2 e), each row keeps a running maximum m,
+// sum l and output o:
+//     m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + v 2^(x - m').
+//
+// Keys and values are read once from HBM, which bounds the kernel for up to
+// about 64 rows a head.  One block per SM: a producer warp copies tiles by
+// TMA (a box of a page at a time, 128-byte swizzle) into a ring of slots,
+// K and V in turn; eight consumer warps share out rows (RW groups of 16) and
+// keys (16 at a time), each with a softmax state of its own, and are joined
+// in shared memory at the end of a unit.  mma.sync carries the products:
+// at 16 rows they take a fifth of the time that the bytes take.
+//
+// The tiles of all units form one line that is cut into equal runs, one a
+// block, from the lengths in device memory: ragged lengths and long single
+// sequences fill the device alike, and the host need not know a length.  A
+// unit that is cut leaves partial results in the workspace; the block that
+// arrives last joins them in block order, so the bits do not depend on which
+// that is.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "vg_cache.h"
+#include "vg_device.cuh"
+
+namespace vg {
+namespace attn {
+
+constexpr int kTile = 64;                     // keys of a tile
+constexpr int kConsumers = 8;                 // warps
+constexpr int kAttnThreads = (kConsumers + 4) * 32;   // three warpgroups, one warp of the last copies
+// Registers a thread: 168 at the launch (384 x 168 = 64512); the producer's
+// warpgroup gives up what the consumers' two take, 128 x 56 + 256 x 224 = 64512.
+constexpr int kProducerRegs = 56, kConsumerRegs = 224;
+constexpr int kHeader = 256;                  // workspace: error word, then ...
+constexpr int kMaxGrid = 512;                 // ... a counter for each block
+constexpr uint64_t kWaitNs = 2000000000ull;   // bound of every wait
+constexpr int kErrAttnWait = 16;              // the error word of a wait that ran out
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum { kBf16 = 0, kF16 = 1, kE4M3 = 2 };
+
+struct AttnParams {
+  const void *q;
+  void *out;
+  float *lse;
+  const int32_t *lens, *counts;
+  const uint64_t *tree;
+  int64_t qs[3];
+  CacheView cache;
+  int *error;
+  uint32_t *arrived;                // [grid]
+  float *partial;                   // [grid][2] of (rows x (head_dim padded) + 2 rows)
+  int batch, n, hq, hkv, d, q_f16;
+  int rows, blocks;                 // rows that share a cache head, row blocks of a unit
+  int box, slots;                   // tokens of a TMA box, ring slots
+  float c, v_scale;                 // scale * k_scale * log2 e
+};
+
+// ----------------------------------------------------------------- layout
+template <int kType, int DC, int RW>
+struct Cfg {
+  static constexpr int kSize = kType == kE4M3 ? 1 : 2;
+  static constexpr int kRow = 64 * kSize;                // bytes of a key's 64-element chunk
+  static constexpr int kChunk = kTile * kRow;
+  static constexpr int kSlot = DC * kChunk;              // one tile of K or of V
+  static constexpr int D = DC * 64;
+  static constexpr int kRows = 16 * RW;
+  static constexpr int KT = RW == 1 ? 4 : RW == 2 ? 4 : RW == 4 ? 2 : 1;   // key warps of a tile
+  static constexpr int NG = RW == 1 ? 2 : 1;             // groups that take tiles in turn
+  static constexpr int kSub = 4 / KT;                    // 16-key steps of a warp in a tile
+  static constexpr int KW = KT * NG;                     // key warps of a row group
+  static constexpr int NT = D / 8;                       // output tiles of 8 columns
+  static constexpr bool kQReg = DC <= 2;                 // q fragments stay in registers
+  static constexpr int kQRow = D * 2 + 16;               // q row in shared memory, padded
+  static constexpr int kQBytes = kRows * kQRow;
+  static constexpr int kWarpState = NT * 32 * 16;        // one warp's o
+  static constexpr int kScratch = (KW / 2) * RW * kWarpState;
+  static constexpr int kState = kConsumers * 16 * 8;     // m, l of each warp's rows
+  // header: barriers, flags and the tiles' page bits
+  static constexpr int kMaxSlots = 16;
+  static constexpr int kFixed = 1024 + kState + kRows * 4 + kQBytes + kScratch;
+  static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / kSlot;
+  static constexpr int kSlots = (kFit > kMaxSlots ? kMaxSlots : kFit) & ~1;
+  static constexpr int kSmem = 1024 + kFixed + kSlots * kSlot;
+  static_assert(kSlots >= 2, "room for a tile of K and one of V");
+  // floats of a partial result: o in fragment order, then m and l
+  static constexpr int kPartial = RW * NT * 32 * 4 + 2 * kRows;
+};
+
+// ------------------------------------------------------------- small pieces
+template <int kType>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (kType == kBf16)
+    mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 codes (the low 16 bits) as FP16, exact.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
+  uint32_t y;
+  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(y) : "r"(w));
+  return y;
+}
+template <int kType>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t y;
+  if constexpr (kType == kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(b), "f"(a));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_out(float a, float b, bool f16) {
+  return f16 ? pack2<kF16>(a, b) : pack2<kBf16>(a, b);
+}
+// Whether a half of a 16-bit pair is infinite or NaN.
+template <int kType>
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  constexpr uint32_t e = kType == kBf16 ? 0x7F80u : 0x7C00u;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+template <int kType>
+__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
+  constexpr uint32_t e = kType == kBf16 ? 0x7F80u : 0x7C00u;
+  return ((w & e) == e ? 0u : 0xFFFFu) | (((w >> 16) & e) == e ? 0u : 0xFFFF0000u);
+}
+
+// Byte offset of 16-byte chunk `ch` of key `key` inside a 64-element chunk:
+// TMA's 128-byte (16-bit types) or 64-byte (E4M3) swizzle.
+template <int kSize>
+__device__ __forceinline__ uint32_t swz(uint32_t key, uint32_t ch) {
+  return kSize == 2 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int x, int token,
+                                       int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// Bounded wait for a phase; gives up at once after another wait has failed.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *failed,
+                                           int *error) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t end = globaltimer() + kWaitNs;
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return false;
+    if (globaltimer() > end) {
+      *failed = 1;
+      atomicCAS(error, 0, kErrAttnWait);
+      return false;
+    }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ the line
+// Where a block is on the line of tiles: unit u (= head * blocks + row block)
+// of sequence b, its tiles, and those of them that are the block's.
+struct Line {
+  int64_t total, at, end, unit0;    // tiles in all, the block's run, the unit's first
+  int64_t runs;                     // blocks that have a run: no more than tiles
+  int b, u, units, tiles, t0, t1;   // units per sequence; this unit's tiles [t0, t1)
+  int len, count;
+
+  __device__ __forceinline__ static int used(const AttnParams &p, int b, int &len) {
+    // no slot past the table exists: such lengths end with it
+    const int64_t room = int64_t(p.cache.max_pages) * p.cache.page_size;
+    len = int(min(int64_t(max(p.lens[b], 0)), room));
+    return p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
+  }
+  __device__ __forceinline__ static int tiles_of(const AttnParams &p, int b) {
+    int len;
+    const int count = used(p, b, len);
+    return max(1, (len + count + kTile - 1) / kTile);
+  }
+  // The whole warp computes it.
+  __device__ void init(const AttnParams &p, int units_) {
+    const int lane = threadIdx.x % 32;
+    units = units_;
+    int64_t sum = 0;
+    for (int i = lane; i < p.batch; i += 32) sum += tiles_of(p, i);
+#pragma unroll
+    for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
+    total = sum * units;
+    runs = min(int64_t(gridDim.x), total);
+    const int64_t mine = min(int64_t(blockIdx.x), runs);
+    at = total * mine / runs;
+    end = mine < runs ? total * (mine + 1) / runs : at;
+    // the sequence that holds tile `at`
+    int64_t before = 0;
+    b = 0;
+    tiles = 1;
+    for (int i0 = 0; i0 < p.batch; i0 += 32) {
+      const int each = i0 + lane < p.batch ? tiles_of(p, i0 + lane) : 0;
+      int64_t run = each;
+#pragma unroll
+      for (int w = 1; w < 32; w *= 2) {
+        const int64_t y = __shfl_up_sync(~0u, run, w);
+        if (lane >= w) run += y;
+      }
+      const uint32_t over = __ballot_sync(~0u, (before + run) * units > at);
+      if (over) {
+        const int f = __ffs(over) - 1;
+        tiles = __shfl_sync(~0u, each, f);
+        b = i0 + f;
+        before += __shfl_sync(~0u, run, f) - tiles;
+        break;
+      }
+      before += __shfl_sync(~0u, run, 31);
+    }
+    const int64_t in = at - before * units;
+    u = int(in / tiles);
+    t0 = int(in % tiles);
+    unit0 = at - t0;
+    fill(p);
+  }
+  __device__ __forceinline__ void fill(const AttnParams &p) {
+    t1 = int(min(int64_t(tiles), t0 + (end - at)));
+    if (at < end) count = used(p, b, len);
+  }
+  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ void next(const AttnParams &p) {
+    at += t1 - t0;
+    unit0 = at;
+    t0 = 0;
+    if (at < end) {
+      if (++u == units) {
+        u = 0;
+        ++b;
+        tiles = tiles_of(p, b);
+      }
+    }
+    fill(p);
+  }
+  // The block that holds tile x of the line.
+  __device__ __forceinline__ int block_of(int64_t x) const {
+    return int(((x + 1) * runs + total - 1) / total) - 1;
+  }
+};
+
+// Column of element e of output tile nt in thread t of a quad.  E4M3: the
+// transposed load hands out pairs of columns, tile 2k has the even ones.
+template <int kType>
+__device__ __forceinline__ int out_col(int nt, int t, int e) {
+  return kType == kE4M3 ? 16 * (nt / 2) + 4 * t + 2 * e + (nt & 1) : 8 * nt + 2 * t + e;
+}
+
+template <int kType, int DC, int RW>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using L = Cfg<kType, DC, RW>;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *ring = smem;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kSlots * L::kSlot);
+  uint32_t *page_ok = reinterpret_cast<uint32_t *>(bars + 2 * L::kMaxSlots);   // [kMaxSlots]
+  volatile int *failed = reinterpret_cast<volatile int *>(page_ok + L::kMaxSlots);
+  int *last = const_cast<int *>(failed) + 1;
+  float2 *state = reinterpret_cast<float2 *>(smem + L::kSlots * L::kSlot + 1024);   // [warp][16]
+  float *q_unit = reinterpret_cast<float *>(state) + L::kState / 4;                  // [kRows]
+  uint8_t *q_smem = reinterpret_cast<uint8_t *>(q_unit + L::kRows);
+  uint8_t *scratch = q_smem + L::kQBytes;
+  constexpr int NS = L::kSlots;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + L::kMaxSlots);
+  if (tid == 0) {
+    *failed = 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, L::KT * RW);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  Line at;
+  at.init(p, p.hkv * p.blocks);
+
+  if (warp >= kConsumers) {
+    // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (warp > kConsumers) return;
+    const int boxes = kTile / p.box, copies = boxes * DC;
+    const uint32_t ring0 = smem_addr(ring);
+    int s = 0;
+    uint32_t par = 1;                                    // slots start empty
+    for (; at.valid(); at.next(p)) {
+      const int head = at.u / p.blocks;
+      const int total = at.len + at.count;
+      for (int t = at.t0; t < at.t1; ++t) {
+        // lane = box * DC + chunk; a box without a page, or past the end,
+        // is copied from outside the tensor: zeros, and no traffic
+        const int box = lane / DC, chunk = lane % DC;
+        int page = int(p.cache.pages), token = 0;
+        bool ok = false;
+        if (lane < copies) {
+          const int slot = t * kTile + box * p.box;
+          if (slot < total) {
+            const int64_t pg = cache_page(p.cache, at.b, slot);
+            if (pg >= 0) {
+              ok = true;
+              page = int(pg);
+              token = slot % p.cache.page_size;
+            }
+          }
+        }
+        // one bit for every 16 keys
+        uint32_t bits = ok ? ((1u << (p.box / 16)) - 1) << (box * (p.box / 16)) : 0;
+        bits = __reduce_or_sync(~0u, bits);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t bar = full0 + 8 * s;
+          wait_phase(empty0 + 8 * s, par, failed, p.error);
+          if (lane == 0) {
+            page_ok[s] = bits;
+            mbar_arrive_expect_tx(bar, L::kSlot);
+          }
+          __syncwarp();
+          if (lane < copies)
+            tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow,
+                   kv ? &vmap : &kmap, chunk * 64, token, head, page, bar);
+          if (++s == NS) {
+            s = 0;
+            par ^= 1;
+          }
+        }
+      }
+    }
+    // every copy has been read, so has landed, before the block may end; after
+    // a failure they get 10 ms to land
+    for (int k = 0; k < NS; ++k) {
+      wait_phase(empty0 + 8 * s, par, failed, p.error);
+      if (++s == NS) {
+        s = 0;
+        par ^= 1;
+      }
+    }
+    if (*failed) {
+      const uint64_t end = globaltimer() + 10000000;
+      while (globaltimer() < end) __nanosleep(1000);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------- consumers
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+  const int g = lane >> 2, t = lane & 3;
+  const int rw = warp / L::KW, kg = warp % L::KW;        // row group, key warp
+  const int grp = kg / L::KT, kt = kg % L::KT;
+  const uint32_t ring0 = smem_addr(ring), q0 = smem_addr(q_smem);
+  const int group = p.hq / p.hkv;
+  uint32_t tile_no = 0;                                  // tiles of the block so far
+  for (; at.valid(); at.next(p)) {
+    const int head = at.u / p.blocks, rb = at.u % p.blocks;
+    const int row0 = rb * L::kRows;
+    // ---------------------------------------------------------- q to shared
+    // a warp a row; E4M3: in FP16, each row brought near the middle of its
+    // range by a power of two, which keeps every bit of a BF16 row that
+    // counts (2^-29 of the row's largest element and more)
+    for (int r = warp; r < L::kRows; r += kConsumers) {
+      const int row = row0 + r, node = row / group, h = head * group + row % group;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const bool live = row < p.rows && lane * 8 < p.d;
+      if (live)
+        v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at.b * p.qs[0] +
+                                             node * p.qs[1] + h * p.qs[2] + lane * 8);
+      if constexpr (kType == kE4M3) {
+        float f[8];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint16_t x = uint16_t(w[k / 2] >> (16 * (k & 1)));
+          f[k] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
+          top = fmaxf(top, fabsf(f[k]));
+        }
+#pragma unroll
+        for (int m = 16; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+        int e = 0;
+        if (top > 0.f && top < INFINITY) {
+          frexpf(top, &e);
+          e = min(max(e - 14, -100), 120);
+        }
+        const float down = ldexpf(1.f, -e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= down;
+        v = make_uint4(pack2<kF16>(f[0], f[1]), pack2<kF16>(f[2], f[3]), pack2<kF16>(f[4], f[5]),
+                       pack2<kF16>(f[6], f[7]));
+        if (lane == 0) q_unit[r] = ldexpf(1.f, e);
+      }
+      if (lane * 8 < L::D) *reinterpret_cast<uint4 *>(q_smem + r * L::kQRow + lane * 16) = v;
+    }
+    named_bar(1, kConsumers * 32);
+
+    uint32_t qf[L::kQReg ? DC * 4 : 1][4];
+    auto load_q = [&](uint32_t (&a)[4], int ks) {
+      if constexpr (kType == kE4M3) {
+        // k order of a step: thread t has elements 4t .. 4t + 3
+        const uint32_t base = q0 + (rw * 16 + g) * L::kQRow + ks * 32 + t * 8;
+        const uint2 lo = lds64(base), hi = lds64(base + 8 * L::kQRow);
+        a[0] = lo.x;
+        a[1] = hi.x;
+        a[2] = lo.y;
+        a[3] = hi.y;
+      } else {
+        ldsm4(a, q0 + (rw * 16 + (lane & 15)) * L::kQRow + ks * 32 + (lane >> 4) * 16);
+      }
+    };
+    if constexpr (L::kQReg) {
+#pragma unroll
+      for (int ks = 0; ks < DC * 4; ++ks) load_q(qf[ks], ks);
+    }
+    float cr[2] = {p.c, p.c};
+    if constexpr (kType == kE4M3) {
+      cr[0] *= q_unit[rw * 16 + g];
+      cr[1] *= q_unit[rw * 16 + g + 8];
+    }
+    // the drafted nodes that this thread's two rows attend to
+    uint64_t word[2];
+    const uint64_t used = at.count >= 64 ? ~0ull : (1ull << at.count) - 1;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int node = (row0 + rw * 16 + g + 8 * r) / group;
+      word[r] = 0;
+      if (node < p.n)
+        word[r] = used & (p.tree ? p.tree[int64_t(at.b) * p.n + node] : ~0ull >> (63 - node));
+    }
+    float o[L::NT][4];
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    // ---------------------------------------------------------------- tiles
+    for (int tile = at.t0; tile < at.t1; ++tile, ++tile_no) {
+      if (L::NG == 2 && (tile_no & 1) != uint32_t(grp)) continue;
+      const uint32_t ik = 2 * tile_no, iv = ik + 1;
+      const uint32_t sk = ik % NS, sv = iv % NS;
+      wait_phase(full0 + 8 * sk, (ik / NS) & 1, failed, p.error);
+      const uint32_t ok_bits = page_ok[sk];
+#pragma unroll
+      for (int j = 0; j < L::kSub; ++j) {
+        const int key0 = (j * L::KT + kt) * 16;          // within the tile
+        const uint32_t kb = ring0 + sk * L::kSlot;
+        float sc[2][4] = {}, sd[2][4] = {};
+        uint32_t pf[4];
+#pragma unroll
+        for (int ks = 0; ks < DC * 4; ++ks) {
+          uint32_t a[4];
+          if constexpr (L::kQReg) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = qf[ks][e];
+          } else {
+            load_q(a, ks);
+          }
+          auto &acc = ks & 1 ? sd : sc;
+          uint32_t b[4];
+          if constexpr (kType == kE4M3) {
+            // 16 codes of a key are one 16-byte chunk: matrices (keys 0-7),
+            // (keys 8-15) of steps ks and ks + 1 come together
+            if ((ks & 1) == 0) {
+              const uint32_t key = key0 + (lane & 15);
+              ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<1>(key, (ks & 3) + (lane >> 4)));
+              mma<kType>(sc[0], a, e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
+              mma<kType>(sc[1], a, e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
+              uint32_t a2[4];
+              if constexpr (L::kQReg) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a2[e] = qf[ks + 1][e];
+              } else {
+                load_q(a2, ks + 1);
+              }
+              mma<kType>(sd[0], a2, e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
+              mma<kType>(sd[1], a2, e4m3_f16(b[3]), e4m3_f16(b[3] >> 16));
+            }
+          } else {
+            const uint32_t key = key0 + (lane & 7) + ((lane >> 4) << 3);
+            ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<2>(key, (ks & 3) * 2 + ((lane >> 3) & 1)));
+            mma<kType>(acc[0], a, b[0], b[1]);
+            mma<kType>(acc[1], a, b[2], b[3]);
+          }
+        }
+        // scores in base 2; masks where a key is not everybody's
+        const int s0 = tile * kTile + key0;
+        const bool there = ok_bits >> (key0 / 16) & 1;
+        const bool open = there && s0 + 16 <= at.len;
+        float x[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[nt][e] = (sc[nt][e] + sd[nt][e]) * cr[e >> 1];
+        if (!open) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rel = s0 + nt * 8 + 2 * t + (e & 1) - at.len;
+              const bool see = there && (rel < 0 || (rel < 64 && (word[e >> 1] >> (rel & 63) & 1)));
+              if (!see) x[nt][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float top = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          const float m2 = fmaxf(m[r], top);
+          // rescale where a row's maximum has moved, which is rare after the first tiles
+          if (__any_sync(~0u, m2 > m[r])) {
+            const float keep = m[r] == -INFINITY ? 0.f : ex2(m[r] - m2);
+            l[r] *= keep;
+#pragma unroll
+            for (int i = 0; i < L::NT; ++i) {
+              o[i][2 * r] *= keep;
+              o[i][2 * r + 1] *= keep;
+            }
+          }
+          m[r] = m2;
+          const float base = m2 == -INFINITY ? 0.f : m2;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const float a0 = ex2(x[nt][2 * r] - base), a1 = ex2(x[nt][2 * r + 1] - base);
+            l[r] += a0 + a1;
+            pf[r + 2 * nt] = pack2<kType>(a0, a1);
+          }
+        }
+        if (j == L::kSub - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty0 + 8 * sk);
+        }
+
+        // ----------------------------------------------------------- p . v
+        if (j == 0) wait_phase(full0 + 8 * sv, (iv / NS) & 1, failed, p.error);
+        const uint32_t vb = ring0 + sv * L::kSlot;
+        if (open) {
+#pragma unroll
+          for (int i = 0; i < L::NT / 2; ++i) {
+            uint32_t b[4];
+            if constexpr (kType == kE4M3) {
+              // 16 columns: matrices (keys 0-7), (keys 8-15) of two blocks of 16
+              if ((i & 1) == 0) {
+                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key0 + (lane & 15), (i & 3) + (lane >> 4)));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t w0 = prmt(b[2 * k], 0, 0x3120), w1 = prmt(b[2 * k + 1], 0, 0x3120);
+                  mma<kType>(o[2 * (i + k)], pf, e4m3_f16(w0), e4m3_f16(w1));
+                  mma<kType>(o[2 * (i + k) + 1], pf, e4m3_f16(w0 >> 16), e4m3_f16(w1 >> 16));
+                }
+              }
+            } else {
+              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key0 + (lane & 15), (i & 3) * 2 + (lane >> 4)));
+              mma<kType>(o[2 * i], pf, b[0], b[1]);
+              mma<kType>(o[2 * i + 1], pf, b[2], b[3]);
+            }
+          }
+        } else {
+          // Keys that some row does not attend to.  A weight of 0 does not
+          // keep an infinity or NaN of v out of the product, so those are
+          // left out of it and added to the rows that do attend.
+          uint32_t odd = 0;
+#pragma unroll
+          for (int i = 0; i < L::NT / 2; ++i) {
+            uint32_t b[4];
+            if constexpr (kType == kE4M3) {
+              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key0 + (lane & 15), i & 3));
+              const uint32_t w0 = prmt(b[0], 0, 0x3120), w1 = prmt(b[1], 0, 0x3120);
+              b[0] = e4m3_f16(w0);
+              b[1] = e4m3_f16(w1);
+              b[2] = e4m3_f16(w0 >> 16);
+              b[3] = e4m3_f16(w1 >> 16);
+            } else {
+              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key0 + (lane & 15), (i & 3) * 2 + (lane >> 4)));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t keep = finite_mask<kType>(b[e]);
+              odd |= ~keep;
+              b[e] &= keep;
+            }
+            mma<kType>(o[2 * i], pf, b[0], b[1]);
+            mma<kType>(o[2 * i + 1], pf, b[2], b[3]);
+          }
+          if (__any_sync(~0u, odd != 0)) {
+            for (int k = 0; k < 16; ++k) {
+              const int rel = s0 + k - at.len;
+              const uint32_t key = key0 + k;
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                if (!there || !(rel < 0 || (rel < 64 && (word[r] >> (rel & 63) & 1)))) continue;
+#pragma unroll
+                for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int col = out_col<kType>(i, t, e);
+                    const uint8_t *chunk = ring + sv * L::kSlot + (col / 64) * L::kChunk;
+                    float v;
+                    if constexpr (kType == kE4M3) {
+                      const uint32_t c = chunk[swz<1>(key, (col % 64) / 16) + col % 16];
+                      v = __half2float(__ushort_as_half(uint16_t(e4m3_f16(c))));
+                    } else {
+                      const uint16_t c = *reinterpret_cast<const uint16_t *>(
+                          chunk + swz<2>(key, (col % 64) / 8) + (col % 8) * 2);
+                      v = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(c))
+                                         : __half2float(__ushort_as_half(c));
+                    }
+                    if (!(fabsf(v) < INFINITY)) o[i][2 * r + e] += v;
+                  }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * sv);
+    }
+
+    // -------------------------------------------------- join the key warps
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+    }
+    float4 *box = reinterpret_cast<float4 *>(scratch);
+#pragma unroll
+    for (int half = L::KW / 2; half >= 1; half /= 2) {
+      if (kg >= half && kg < 2 * half) {
+        float4 *to = box + ((kg - half) * RW + rw) * (L::NT * 32);
+#pragma unroll
+        for (int i = 0; i < L::NT; ++i)
+          to[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        if (t == 0) {
+          state[warp * 16 + g] = make_float2(m[0], l[0]);
+          state[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+        }
+      }
+      named_bar(1, kConsumers * 32);
+      if (kg < half) {
+        const float4 *from = box + (kg * RW + rw) * (L::NT * 32);
+        float wa[2], wb[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 other = state[(warp + half) * 16 + g + 8 * r];
+          const float m2 = fmaxf(m[r], other.x);
+          wa[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - m2);
+          wb[r] = other.x == -INFINITY ? 0.f : ex2(other.x - m2);
+          l[r] = l[r] * wa[r] + other.y * wb[r];
+          m[r] = m2;
+        }
+#pragma unroll
+        for (int i = 0; i < L::NT; ++i) {
+          const float4 v = from[i * 32 + lane];
+          o[i][0] = o[i][0] * wa[0] + v.x * wb[0];
+          o[i][1] = o[i][1] * wa[0] + v.y * wb[0];
+          o[i][2] = o[i][2] * wa[1] + v.z * wb[1];
+          o[i][3] = o[i][3] * wa[1] + v.w * wb[1];
+        }
+      }
+      if (half > 1) named_bar(1, kConsumers * 32);
+    }
+
+    // -------------------------------------------------------------- results
+    auto finish = [&](int rw_, const float (&mm)[2], const float (&ll)[2], int i, const float4 &a,
+                      const float4 &b2) {
+      // output tiles i and i + 1 of row group rw_, this lane's share
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + rw_ * 16 + g + 8 * r, node = row / group;
+        if (row >= p.rows) continue;
+        const int h = head * group + row % group;
+        const bool empty = node >= at.count || mm[r] == -INFINITY;
+        const float inv = empty ? 0.f : p.v_scale / ll[r];
+        const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
+        float v0 = r ? a.z : a.x, v1 = r ? a.w : a.y, v2 = r ? b2.z : b2.x, v3 = r ? b2.w : b2.y;
+        if (empty) {
+          v0 = v1 = v2 = v3 = 0.f;
+        } else {
+          v0 *= inv;
+          v1 *= inv;
+          v2 *= inv;
+          v3 *= inv;
+        }
+        const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
+        if constexpr (kType == kE4M3) {
+          const int col = 8 * i + 4 * t;                 // i is even
+          if (col < p.d)
+            *reinterpret_cast<uint2 *>(out + col) =
+                make_uint2(pack_out(v0, v2, f16), pack_out(v1, v3, f16));
+        } else {
+          const int c0 = 8 * i + 2 * t, c1 = c0 + 8;
+          if (c0 < p.d) *reinterpret_cast<uint32_t *>(out + c0) = pack_out(v0, v1, f16);
+          if (c1 < p.d) *reinterpret_cast<uint32_t *>(out + c1) = pack_out(v2, v3, f16);
+        }
+        if (p.lse && i == 0 && t == 0)
+          p.lse[at_row] = empty ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
+      }
+    };
+    const bool whole = at.t0 == 0 && at.t1 == at.tiles;
+    if (whole) {
+      if (kg == 0) {
+#pragma unroll
+        for (int i = 0; i < L::NT; i += 2)
+          finish(rw, m, l, i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]),
+                 make_float4(o[i + 1][0], o[i + 1][1], o[i + 1][2], o[i + 1][3]));
+      }
+    } else {
+      const int first = at.block_of(at.unit0), final = at.block_of(at.unit0 + at.tiles - 1);
+      auto slot_of = [&](int block) {
+        return p.partial + (int64_t(block) * 2 + (block == first ? 1 : 0)) * L::kPartial;
+      };
+      if (kg == 0) {
+        float *mine = slot_of(blockIdx.x);
+        float4 *to = reinterpret_cast<float4 *>(mine) + rw * (L::NT * 32);
+#pragma unroll
+        for (int i = 0; i < L::NT; ++i)
+          to[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        if (t == 0) {
+          float2 *st = reinterpret_cast<float2 *>(mine + RW * L::NT * 32 * 4) + rw * 16;
+          st[g] = make_float2(m[0], l[0]);
+          st[g + 8] = make_float2(m[1], l[1]);
+        }
+        __threadfence();
+      }
+      named_bar(1, kConsumers * 32);
+      if (tid == 0) {
+        const uint32_t before = atomicAdd(p.arrived + first, 1u);
+        *last = before == uint32_t(final - first);
+        if (*last) p.arrived[first] = 0;
+        __threadfence();
+      }
+      named_bar(1, kConsumers * 32);
+      if (*last) {
+        __threadfence();
+        // pairs of output tiles are shared out over the warps
+        for (int w = warp; w < RW * L::NT / 2; w += kConsumers) {
+          const int rw_ = w / (L::NT / 2), i = w % (L::NT / 2) * 2;
+          float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};
+          float4 a = make_float4(0, 0, 0, 0), b2 = a;
+          for (int blk = first; blk <= final; ++blk) {
+            const float *part = slot_of(blk);
+            const float2 *st = reinterpret_cast<const float2 *>(part + RW * L::NT * 32 * 4) + rw_ * 16;
+            const float4 *from = reinterpret_cast<const float4 *>(part) + (rw_ * L::NT + i) * 32 + lane;
+            const float2 s[2] = {__ldcg(st + g), __ldcg(st + g + 8)};
+            const float4 va = __ldcg(from), vb = __ldcg(from + 32);
+            float wa[2], wb[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float m2 = fmaxf(mm[r], s[r].x);
+              wa[r] = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - m2);
+              wb[r] = s[r].x == -INFINITY ? 0.f : ex2(s[r].x - m2);
+              ll[r] = ll[r] * wa[r] + s[r].y * wb[r];
+              mm[r] = m2;
+            }
+            a.x = a.x * wa[0] + va.x * wb[0];
+            a.y = a.y * wa[0] + va.y * wb[0];
+            a.z = a.z * wa[1] + va.z * wb[1];
+            a.w = a.w * wa[1] + va.w * wb[1];
+            b2.x = b2.x * wa[0] + vb.x * wb[0];
+            b2.y = b2.y * wa[0] + vb.y * wb[0];
+            b2.z = b2.z * wa[1] + vb.z * wb[1];
+            b2.w = b2.w * wa[1] + vb.w * wb[1];
+          }
+          finish(rw_, mm, ll, i, a, b2);
+        }
+      }
+    }
+    named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
+  }
+}
+
+// -------------------------------------------------------------------- host
+using Kernel = void (*)(AttnParams, CUtensorMap, CUtensorMap);
+
+struct Variant {
+  Kernel fn;
+  int smem, rows, partial;
+};
+
+template <int kType, int DC, int RW>
+Variant variant() {
+  using L = Cfg<kType, DC, RW>;
+  return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW>), L::kSmem, L::kRows, L::kPartial};
+}
+
+// The variants of one cache type, by head_dim up to 64, 128, 256 and by row
+// groups 1, 2, 4, 8: a translation unit each.
+using Variants = Variant[3][4];
+extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
+
+#define VG_ATTENTION_ROWS(T, DC) \
+  {variant<T, DC, 1>(), variant<T, DC, 2>(), variant<T, DC, 4>(), variant<T, DC, 8>()}
+#define VG_ATTENTION_VARIANTS(T) \
+  {VG_ATTENTION_ROWS(T, 1), VG_ATTENTION_ROWS(T, 2), VG_ATTENTION_ROWS(T, 4)}
+
+}  // namespace attn
+}  // namespace vg
