@@ -93,9 +93,12 @@ struct Cfg {
   static constexpr int kMaxSlots = 16;
   static constexpr int kFixed = 1024 + kState + kRows * 4 + kQBytes + kScratch;
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / kSlot;
-  static constexpr int kSlots = (kFit > kMaxSlots ? kMaxSlots : kFit) & ~1;
+  // A slot always serves the same group: a warp that waits for a slot's next
+  // filling has then seen the one before (a phase's parity tells only
+  // neighbours apart, and copies land in any order).
+  static constexpr int kSlots = (kFit > kMaxSlots ? kMaxSlots : kFit) / (2 * NG) * (2 * NG);
   static constexpr int kSmem = 1024 + kFixed + kSlots * kSlot;
-  static_assert(kSlots >= 2, "room for a tile of K and one of V");
+  static_assert(kSlots >= 2 * NG, "room for a tile of K and one of V of each group");
   // floats of a partial result: o in fragment order, then m and l
   static constexpr int kPartial = RW * NT * 32 * 4 + 2 * kRows;
 };
