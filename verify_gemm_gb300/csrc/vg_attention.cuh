@@ -52,6 +52,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 enum { kBf16 = 0, kF16 = 1, kE4M3 = 2 };
 
+// Weights are 2^(x - m + lift).  FP16 holds them with 11 bits down to 2^-14
+// only, so there they are lifted to the top of its range: a weight then loses
+// bits from 2^-29 of the largest on.  o and l carry the same factor.
+template <int kType>
+constexpr float kLift = kType == kBf16 ? 0.f : 15.f;
+
 struct AttnParams {
   const void *q;
   void *out;
@@ -78,10 +84,13 @@ struct Cfg {
   static constexpr int kSlot = DC * kChunk;              // one tile of K or of V
   static constexpr int D = DC * 64;
   static constexpr int kRows = 16 * RW;
-  static constexpr int KT = RW == 1 ? 4 : RW == 2 ? 4 : RW == 4 ? 2 : 1;   // key warps of a tile
-  static constexpr int NG = RW == 1 ? 2 : 1;             // groups that take tiles in turn
-  static constexpr int kSub = 4 / KT;                    // 16-key steps of a warp in a tile
-  static constexpr int KW = KT * NG;                     // key warps of a row group
+  // keys of a step: 32 halve the maxima, shuffles and waits of a key against
+  // 16 and give the products twice the chains; o of 256 columns leaves room for 16
+  static constexpr int SK = DC == 4 ? 16 : 32;
+  static constexpr int KW = kConsumers / RW;             // key warps of a row group
+  static constexpr int KT = KW < kTile / SK ? KW : kTile / SK;   // ... that share a tile
+  static constexpr int NG = KW / KT;                     // groups that take tiles in turn
+  static constexpr int kSub = kTile / SK / KT;           // steps of a warp in a tile
   static constexpr int NT = D / 8;                       // output tiles of 8 columns
   static constexpr bool kQReg = DC <= 2;                 // q fragments stay in registers
   static constexpr int kQRow = D * 2 + 16;               // q row in shared memory, padded
@@ -322,59 +331,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp >= kConsumers) {
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    if (warp > kConsumers) return;
+    const int kv = warp - kConsumers;                    // one warp copies K, one V
+    if (kv > 1) return;
+    // The page numbers of 32 boxes are fetched at a time, one a lane, and the
+    // next 32 while those are copied: a fetch for each tile cost 1200 clocks
+    // a tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
     const int boxes = kTile / p.box, copies = boxes * DC;
+    const int page_boxes = p.cache.page_size / p.box;
     const uint32_t ring0 = smem_addr(ring);
-    int s = 0;
+    int s = kv;
     uint32_t par = 1;                                    // slots start empty
     for (; at.valid(); at.next(p)) {
       const int head = at.u / p.blocks;
       const int total = at.len + at.count;
+      const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
+      auto fetch = [&](int window) {
+        const int box = window * 32 + lane, i = box / page_boxes;
+        return box * p.box < total && i < p.cache.max_pages ? table[i] : -1;
+      };
+      int window = at.t0 * boxes / 32;
+      int pages = fetch(window), ahead = fetch(window + 1);
       for (int t = at.t0; t < at.t1; ++t) {
+        if (t * boxes / 32 != window) {
+          pages = ahead;
+          ahead = fetch(++window + 1);
+        }
         // lane = box * DC + chunk; a box without a page, or past the end,
         // is copied from outside the tensor: zeros, and no traffic
         const int box = lane / DC, chunk = lane % DC;
-        int page = int(p.cache.pages), token = 0;
-        bool ok = false;
-        if (lane < copies) {
-          const int slot = t * kTile + box * p.box;
-          if (slot < total) {
-            const int64_t pg = cache_page(p.cache, at.b, slot);
-            if (pg >= 0) {
-              ok = true;
-              page = int(pg);
-              token = slot % p.cache.page_size;
-            }
-          }
-        }
+        const int number = t * boxes + box;
+        int page = __shfl_sync(~0u, pages, number % 32);
+        const bool ok = lane < copies && page >= 0 && page < p.cache.pages;
+        if (!ok) page = int(p.cache.pages);
+        const int token = ok ? number % page_boxes * p.box : 0;
         // one bit for every 16 keys
         uint32_t bits = ok ? ((1u << (p.box / 16)) - 1) << (box * (p.box / 16)) : 0;
         bits = __reduce_or_sync(~0u, bits);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t bar = full0 + 8 * s;
-          wait_phase(empty0 + 8 * s, par, failed, p.error);
-          if (lane == 0) {
-            page_ok[s] = bits;
-            mbar_arrive_expect_tx(bar, L::kSlot);
-          }
-          __syncwarp();
-          if (lane < copies)
-            tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow,
-                   kv ? &vmap : &kmap, chunk * 64, token, head, page, bar);
-          if (++s == NS) {
-            s = 0;
-            par ^= 1;
-          }
+        wait_phase(empty0 + 8 * s, par, failed, p.error);
+        const uint32_t bar = full0 + 8 * s;
+        if (lane == 0) {
+          if (kv == 0) page_ok[s] = bits;
+          mbar_arrive_expect_tx(bar, L::kSlot);
+        }
+        __syncwarp();
+        if (lane < copies)
+          tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow,
+                 kv ? &vmap : &kmap, chunk * 64, token, head, page, bar);
+        if ((s += 2) >= NS) {
+          s = kv;
+          par ^= 1;
         }
       }
     }
     // every copy has been read, so has landed, before the block may end; after
     // a failure they get 10 ms to land
-    for (int k = 0; k < NS; ++k) {
+    for (int k = 0; k < NS / 2; ++k) {
       wait_phase(empty0 + 8 * s, par, failed, p.error);
-      if (++s == NS) {
-        s = 0;
+      if ((s += 2) >= NS) {
+        s = kv;
         par ^= 1;
       }
     }
@@ -477,17 +491,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     // ---------------------------------------------------------------- tiles
     for (int tile = at.t0; tile < at.t1; ++tile, ++tile_no) {
-      if (L::NG == 2 && (tile_no & 1) != uint32_t(grp)) continue;
+      if (tile_no % L::NG != uint32_t(grp)) continue;
       const uint32_t ik = 2 * tile_no, iv = ik + 1;
       const uint32_t sk = ik % NS, sv = iv % NS;
       wait_phase(full0 + 8 * sk, (ik / NS) & 1, failed, p.error);
       const uint32_t ok_bits = page_ok[sk];
 #pragma unroll
       for (int j = 0; j < L::kSub; ++j) {
-        const int key0 = (j * L::KT + kt) * 16;          // within the tile
+        const int key0 = (j * L::KT + kt) * L::SK;       // within the tile
         const uint32_t kb = ring0 + sk * L::kSlot;
-        float sc[2][4] = {}, sd[2][4] = {};
-        uint32_t pf[4];
+        constexpr int SN = L::SK / 8;
+        // 16 keys: a second set of accumulators, for twice the chains
+        constexpr int kSets = L::SK == 16 ? 2 : 1;
+        float sc[kSets][SN][4] = {};
+        uint32_t pf[L::SK / 16][4];
 #pragma unroll
         for (int ks = 0; ks < DC * 4; ++ks) {
           uint32_t a[4];
@@ -497,16 +514,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           } else {
             load_q(a, ks);
           }
-          auto &acc = ks & 1 ? sd : sc;
-          uint32_t b[4];
+          auto &acc = sc[ks % kSets];
           if constexpr (kType == kE4M3) {
             // 16 codes of a key are one 16-byte chunk: matrices (keys 0-7),
             // (keys 8-15) of steps ks and ks + 1 come together
             if ((ks & 1) == 0) {
-              const uint32_t key = key0 + (lane & 15);
-              ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<1>(key, (ks & 3) + (lane >> 4)));
-              mma<kType>(sc[0], a, e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
-              mma<kType>(sc[1], a, e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
               uint32_t a2[4];
               if constexpr (L::kQReg) {
 #pragma unroll
@@ -514,58 +526,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               } else {
                 load_q(a2, ks + 1);
               }
-              mma<kType>(sd[0], a2, e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
-              mma<kType>(sd[1], a2, e4m3_f16(b[3]), e4m3_f16(b[3] >> 16));
+#pragma unroll
+              for (int h = 0; h < L::SK / 16; ++h) {
+                uint32_t b[4];
+                const uint32_t key = key0 + h * 16 + (lane & 15);
+                ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<1>(key, (ks & 3) + (lane >> 4)));
+                mma<kType>(sc[0][2 * h], a, e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
+                mma<kType>(sc[0][2 * h + 1], a, e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
+                mma<kType>(sc[kSets - 1][2 * h], a2, e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
+                mma<kType>(sc[kSets - 1][2 * h + 1], a2, e4m3_f16(b[3]), e4m3_f16(b[3] >> 16));
+              }
             }
           } else {
-            const uint32_t key = key0 + (lane & 7) + ((lane >> 4) << 3);
-            ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<2>(key, (ks & 3) * 2 + ((lane >> 3) & 1)));
-            mma<kType>(acc[0], a, b[0], b[1]);
-            mma<kType>(acc[1], a, b[2], b[3]);
+#pragma unroll
+            for (int h = 0; h < L::SK / 16; ++h) {
+              uint32_t b[4];
+              const uint32_t key = key0 + h * 16 + (lane & 7) + ((lane >> 4) << 3);
+              ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<2>(key, (ks & 3) * 2 + ((lane >> 3) & 1)));
+              mma<kType>(acc[2 * h], a, b[0], b[1]);
+              mma<kType>(acc[2 * h + 1], a, b[2], b[3]);
+            }
           }
         }
         // scores in base 2; masks where a key is not everybody's
         const int s0 = tile * kTile + key0;
-        const bool there = ok_bits >> (key0 / 16) & 1;
-        const bool open = there && s0 + 16 <= at.len;
-        float x[2][4];
+        constexpr uint32_t kAll = (1u << (L::SK / 16)) - 1;
+        const uint32_t there = ok_bits >> (key0 / 16);
+        const bool open = (there & kAll) == kAll && s0 + L::SK <= at.len;
+        float x[SN][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < SN; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[nt][e] = (sc[nt][e] + sd[nt][e]) * cr[e >> 1];
+          for (int e = 0; e < 4; ++e)
+            x[nt][e] = (kSets == 2 ? sc[0][nt][e] + sc[kSets - 1][nt][e] : sc[0][nt][e]) * cr[e >> 1];
         if (!open) {
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < SN; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int rel = s0 + nt * 8 + 2 * t + (e & 1) - at.len;
-              const bool see = there && (rel < 0 || (rel < 64 && (word[e >> 1] >> (rel & 63) & 1)));
+              const bool see = (there >> (nt / 2) & 1) &&
+                               (rel < 0 || (rel < 64 && (word[e >> 1] >> (rel & 63) & 1)));
               if (!see) x[nt][e] = -INFINITY;
             }
         }
+        float m2[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float top = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+          float top = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+#pragma unroll
+          for (int nt = 1; nt < SN; ++nt) top = fmaxf(top, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          const float m2 = fmaxf(m[r], top);
-          // rescale where a row's maximum has moved, which is rare after the first tiles
-          if (__any_sync(~0u, m2 > m[r])) {
-            const float keep = m[r] == -INFINITY ? 0.f : ex2(m[r] - m2);
+          m2[r] = fmaxf(m[r], top);
+        }
+        // rescale where a row's maximum has moved, which is rare after the first tiles
+        if (__any_sync(~0u, m2[0] > m[0] || m2[1] > m[1])) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float keep = m[r] == -INFINITY ? 0.f : ex2(m[r] - m2[r]);
             l[r] *= keep;
 #pragma unroll
             for (int i = 0; i < L::NT; ++i) {
               o[i][2 * r] *= keep;
               o[i][2 * r + 1] *= keep;
             }
+            m[r] = m2[r];
           }
-          m[r] = m2;
-          const float base = m2 == -INFINITY ? 0.f : m2;
+        }
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
+        for (int r = 0; r < 2; ++r) {
+          const float base = m[r] == -INFINITY ? 0.f : m[r] - kLift<kType>;
+#pragma unroll
+          for (int nt = 0; nt < SN; ++nt) {
             const float a0 = ex2(x[nt][2 * r] - base), a1 = ex2(x[nt][2 * r + 1] - base);
             l[r] += a0 + a1;
-            pf[r + 2 * nt] = pack2<kType>(a0, a1);
+            pf[nt / 2][r + 2 * (nt & 1)] = pack2<kType>(a0, a1);
           }
         }
         if (j == L::kSub - 1) {
@@ -578,23 +614,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t vb = ring0 + sv * L::kSlot;
         if (open) {
 #pragma unroll
-          for (int i = 0; i < L::NT / 2; ++i) {
-            uint32_t b[4];
-            if constexpr (kType == kE4M3) {
-              // 16 columns: matrices (keys 0-7), (keys 8-15) of two blocks of 16
-              if ((i & 1) == 0) {
-                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key0 + (lane & 15), (i & 3) + (lane >> 4)));
+          for (int h = 0; h < L::SK / 16; ++h) {
+            const uint32_t key = key0 + h * 16 + (lane & 15);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const uint32_t w0 = prmt(b[2 * k], 0, 0x3120), w1 = prmt(b[2 * k + 1], 0, 0x3120);
-                  mma<kType>(o[2 * (i + k)], pf, e4m3_f16(w0), e4m3_f16(w1));
-                  mma<kType>(o[2 * (i + k) + 1], pf, e4m3_f16(w0 >> 16), e4m3_f16(w1 >> 16));
+            for (int i = 0; i < L::NT / 2; ++i) {
+              uint32_t b[4];
+              if constexpr (kType == kE4M3) {
+                // 16 columns: matrices (keys 0-7), (keys 8-15) of two blocks of 16
+                if ((i & 1) == 0) {
+                  ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key, (i & 3) + (lane >> 4)));
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const uint32_t w0 = prmt(b[2 * k], 0, 0x3120), w1 = prmt(b[2 * k + 1], 0, 0x3120);
+                    mma<kType>(o[2 * (i + k)], pf[h], e4m3_f16(w0), e4m3_f16(w1));
+                    mma<kType>(o[2 * (i + k) + 1], pf[h], e4m3_f16(w0 >> 16), e4m3_f16(w1 >> 16));
+                  }
                 }
+              } else {
+                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key, (i & 3) * 2 + (lane >> 4)));
+                mma<kType>(o[2 * i], pf[h], b[0], b[1]);
+                mma<kType>(o[2 * i + 1], pf[h], b[2], b[3]);
               }
-            } else {
-              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key0 + (lane & 15), (i & 3) * 2 + (lane >> 4)));
-              mma<kType>(o[2 * i], pf, b[0], b[1]);
-              mma<kType>(o[2 * i + 1], pf, b[2], b[3]);
             }
           }
         } else {
@@ -602,35 +642,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // keep an infinity or NaN of v out of the product, so those are
           // left out of it and added to the rows that do attend.
           uint32_t odd = 0;
+#pragma unroll 1
+          for (int h = 0; h < L::SK / 16; ++h) {
+            uint32_t pp[4];
 #pragma unroll
-          for (int i = 0; i < L::NT / 2; ++i) {
-            uint32_t b[4];
-            if constexpr (kType == kE4M3) {
-              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key0 + (lane & 15), i & 3));
-              const uint32_t w0 = prmt(b[0], 0, 0x3120), w1 = prmt(b[1], 0, 0x3120);
-              b[0] = e4m3_f16(w0);
-              b[1] = e4m3_f16(w1);
-              b[2] = e4m3_f16(w0 >> 16);
-              b[3] = e4m3_f16(w1 >> 16);
-            } else {
-              ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key0 + (lane & 15), (i & 3) * 2 + (lane >> 4)));
-            }
+            for (int e = 0; e < 4; ++e) pp[e] = h == 0 ? pf[0][e] : pf[L::SK / 16 - 1][e];
+            const uint32_t key = key0 + h * 16 + (lane & 15);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t keep = finite_mask<kType>(b[e]);
-              odd |= ~keep;
-              b[e] &= keep;
+            for (int i = 0; i < L::NT / 2; ++i) {
+              uint32_t b[4];
+              if constexpr (kType == kE4M3) {
+                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key, i & 3));
+                const uint32_t w0 = prmt(b[0], 0, 0x3120), w1 = prmt(b[1], 0, 0x3120);
+                b[0] = e4m3_f16(w0);
+                b[1] = e4m3_f16(w1);
+                b[2] = e4m3_f16(w0 >> 16);
+                b[3] = e4m3_f16(w1 >> 16);
+              } else {
+                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key, (i & 3) * 2 + (lane >> 4)));
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t keep = finite_mask<kType>(b[e]);
+                odd |= ~keep;
+                b[e] &= keep;
+              }
+              mma<kType>(o[2 * i], pp, b[0], b[1]);
+              mma<kType>(o[2 * i + 1], pp, b[2], b[3]);
             }
-            mma<kType>(o[2 * i], pf, b[0], b[1]);
-            mma<kType>(o[2 * i + 1], pf, b[2], b[3]);
           }
           if (__any_sync(~0u, odd != 0)) {
-            for (int k = 0; k < 16; ++k) {
+#pragma unroll 1
+            for (int k = 0; k < L::SK; ++k) {
               const int rel = s0 + k - at.len;
               const uint32_t key = key0 + k;
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                if (!there || !(rel < 0 || (rel < 64 && (word[r] >> (rel & 63) & 1)))) continue;
+                if (!(there >> (k / 16) & 1) || !(rel < 0 || (rel < 64 && (word[r] >> (rel & 63) & 1))))
+                  continue;
 #pragma unroll
                 for (int i = 0; i < L::NT; ++i)
 #pragma unroll
@@ -736,7 +785,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (c1 < p.d) *reinterpret_cast<uint32_t *>(out + c1) = pack_out(v2, v3, f16);
         }
         if (p.lse && i == 0 && t == 0)
-          p.lse[at_row] = empty ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
+          p.lse[at_row] = empty ? -INFINITY : (mm[r] - kLift<kType> + log2f(ll[r])) * kLn2;
       }
     };
     const bool whole = at.t0 == 0 && at.t1 == at.tiles;
