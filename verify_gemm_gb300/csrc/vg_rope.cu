@@ -8,12 +8,16 @@
 // (an FP32 product is 0.06 radians off at position 10^6).  What remains, a
 // signed fraction of a turn, goes through sincospif in FP32.
 //
-// Bytes bound it for prompts and latency for single tokens.
+// Bytes bound it for prompts and latency for single tokens: a block takes
+// the heads of up to four tokens, so that their angles are worked out once,
+// and 16 elements of a head (two 16-byte loads) are a thread's item; with few
+// tokens the heads are spread over more blocks instead.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "vg_cache.h"
@@ -44,17 +48,21 @@ __device__ __forceinline__ void from_f(__nv_fp8_e4m3 &o, float x) {
   o.__x = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
-// Cosine and sine, times the factor, of pair j at `position`.
-__device__ __forceinline__ float2 turn(const RopeParams &p, int64_t position, int j) {
+// Frequency j as a fraction of a turn in units of 2^-64.
+__device__ __forceinline__ uint64_t turn_step(const RopeParams &p, int j) {
   const double f = p.inv_freq[j] * 0.15915494309189535;      // 1 / 2 pi
-  const uint64_t step = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+  return __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+}
+// Cosine and sine, times the factor, of the angle position * step.
+__device__ __forceinline__ float2 turn(const RopeParams &p, int64_t position, uint64_t step) {
   const int64_t at = int64_t(uint64_t(position) * step);
   float s, c;
   sincospif(__ll2float_rn(at) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63: half turns
   return make_float2(c * p.factor, s * p.factor);
 }
 
-// One pair of elements at a time: right for every size and alignment.
+// One pair of elements at a time: for parts of a head that are no multiple of
+// 16 elements and for inputs that are not 16-byte aligned.
 template <typename T, typename C, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   extern __shared__ float2 angles[];                          // [rot / 2]
@@ -65,7 +73,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const bool used = i < count;
   const int half = p.rot / 2;
   const int64_t position = len + (p.depth ? p.depth[tok] : i);
-  for (int j = threadIdx.x; j < half; j += kRopeThreads) angles[j] = turn(p, position, j);
+  for (int j = threadIdx.x; j < half; j += kRopeThreads) angles[j] = turn(p, position, turn_step(p, j));
   __syncthreads();
   const int64_t slot = len + i;
   const int64_t page = used && slot >= 0 ? cache_page(p.cache, b, slot) : -1;
@@ -109,13 +117,158 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   }
 }
 
-template <typename T, typename C>
-void launch_rope(const RopeParams &p, bool interleaved, cudaStream_t st) {
-  const size_t smem = size_t(p.rot / 2) * sizeof(float2);
-  if (interleaved)
-    rope_kernel<T, C, true><<<unsigned(p.tokens), kRopeThreads, smem, st>>>(p);
-  else
-    rope_kernel<T, C, false><<<unsigned(p.tokens), kRopeThreads, smem, st>>>(p);
+// What a token's append needs, worked out once by its block.
+struct Token {
+  int64_t q, k, v, out, ck, cv;    // element offsets of its first head; ck < 0: nowhere to append
+  int used, pad;
+};
+constexpr int kRopeTokens = 4;
+
+template <typename T>
+__device__ __forceinline__ void unpack8(float (&f)[8], const uint4 &v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    T lo, hi;
+    memcpy(&lo, &w[i], 2);
+    const uint32_t h = w[i] >> 16;
+    memcpy(&hi, &h, 2);
+    f[2 * i] = to_f(lo);
+    f[2 * i + 1] = to_f(hi);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) from_f(t[i], f[i]);
+  uint4 v;
+  memcpy(&v, t, 16);
+  return v;
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float inv) {
+  __nv_fp8_e4m3 t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) from_f(t[i], f[i] * inv);
+  uint2 v;
+  memcpy(&v, t, 8);
+  return v;
+}
+
+// 16 elements at a time.  blockIdx.x: tokens, blockIdx.y: heads.
+template <typename T, typename C, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_vector_kernel(const RopeParams p, int tokens_per_block, int heads_per_block) {
+  extern __shared__ float2 angles[];                          // [tokens][rot / 2], then the steps
+  __shared__ Token tok[kRopeTokens];
+  const int half = p.rot / 2, tid = threadIdx.x;
+  uint64_t *steps = reinterpret_cast<uint64_t *>(angles + tokens_per_block * half);
+  const int64_t first = int64_t(blockIdx.x) * tokens_per_block;
+  const int tokens = int(min(int64_t(tokens_per_block), p.tokens - first));
+  const int h0 = blockIdx.y * heads_per_block;
+  const int heads = min(heads_per_block, p.hq + 2 * p.hkv - h0);
+  for (int j = tid; j < half; j += kRopeThreads) steps[j] = turn_step(p, j);
+  __shared__ int64_t position[kRopeTokens];
+  if (tid < tokens) {
+    const int64_t at = first + tid;
+    const int b = int(at / p.n), i = int(at % p.n);
+    const int64_t len = p.lens[b];
+    const int count = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
+    Token t;
+    t.used = i < count;
+    position[tid] = len + (p.depth ? p.depth[at] : i);
+    const int64_t slot = len + i;
+    const int64_t page = t.used && slot >= 0 ? cache_page(p.cache, b, slot) : -1;
+    const int64_t off = slot % p.cache.page_size;
+    t.q = b * p.qs[0] + i * p.qs[1];
+    t.k = b * p.ks[0] + i * p.ks[1];
+    t.v = b * p.vs[0] + i * p.vs[1];
+    t.out = at * p.hq * p.d;
+    t.ck = page < 0 ? -1 : page * p.cks[0] + off * p.cks[1];
+    t.cv = page * p.cvs[0] + off * p.cvs[1];
+    tok[tid] = t;
+  }
+  __syncthreads();
+  for (int w = tid; w < tokens * half; w += kRopeThreads)
+    angles[w] = turn(p, position[w / half], steps[w % half]);
+  __syncthreads();
+  const int chunks = p.d / 16, turned = p.rot / 16;
+  const int items = tokens * heads * chunks;
+#pragma unroll 2
+  for (int w = tid; w < items; w += kRopeThreads) {
+    const int c = w % chunks, th = w / chunks, h = h0 + th % heads, ti = th / heads;
+    const Token &t = tok[ti];
+    const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
+    const bool turns = c < turned;
+    // "half" pairs lie rot / 2 apart; everything else is 16 elements in a row
+    const bool apart = turns && !kInterleaved;
+    const int e1 = apart ? 8 * c : 16 * c, e2 = apart ? 8 * c + half : 16 * c + 8;
+    const T *src = is_q ? static_cast<const T *>(p.q) + t.q + h * p.qs[2]
+                 : is_v ? static_cast<const T *>(p.v) + t.v + (h - p.hq - p.hkv) * p.vs[2]
+                        : static_cast<const T *>(p.k) + t.k + (h - p.hq) * p.ks[2];
+    const uint4 r1 = *reinterpret_cast<const uint4 *>(src + e1);
+    const uint4 r2 = *reinterpret_cast<const uint4 *>(src + e2);
+    if (!is_q && t.ck < 0) continue;
+    float x1[8], x2[8];
+    unpack8<T>(x1, r1);
+    unpack8<T>(x2, r2);
+    if (turns && !is_v) {
+      const float2 *a = angles + ti * half + 8 * c;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 cs = a[k];
+        if (kInterleaved) {
+          // pair k of the 16 elements: 2k, 2k + 1
+          float &u = k < 4 ? x1[2 * (k & 3)] : x2[2 * (k & 3)];
+          float &v = k < 4 ? x1[2 * (k & 3) + 1] : x2[2 * (k & 3) + 1];
+          const float y = u * cs.x - v * cs.y;
+          v = u * cs.y + v * cs.x;
+          u = y;
+        } else {
+          const float y = x1[k] * cs.x - x2[k] * cs.y;
+          x2[k] = x1[k] * cs.y + x2[k] * cs.x;
+          x1[k] = y;
+        }
+      }
+    }
+    if (is_q) {
+      T *dst = static_cast<T *>(p.q_out) + t.out + h * p.d;
+      if (!t.used) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x1[k] = x2[k] = 0.f;
+      }
+      *reinterpret_cast<uint4 *>(dst + e1) = pack8<T>(x1);
+      *reinterpret_cast<uint4 *>(dst + e2) = pack8<T>(x2);
+    } else {
+      C *dst = is_v ? static_cast<C *>(p.cv) + t.cv + (h - p.hq - p.hkv) * p.cvs[2]
+                    : static_cast<C *>(p.ck) + t.ck + (h - p.hq) * p.cks[2];
+      if constexpr (sizeof(C) == 1) {
+        const float inv = is_v ? p.v_inv : p.k_inv;
+        *reinterpret_cast<uint2 *>(dst + e1) = pack8_e4m3(x1, inv);
+        *reinterpret_cast<uint2 *>(dst + e2) = pack8_e4m3(x2, inv);
+      } else {
+        *reinterpret_cast<uint4 *>(dst + e1) = pack8<T>(x1);
+        *reinterpret_cast<uint4 *>(dst + e2) = pack8<T>(x2);
+      }
+    }
+  }
+}
+
+template <typename T, typename C, bool kInterleaved>
+void launch_rope(const RopeParams &p, bool vector, int sms, cudaStream_t st) {
+  const int half = p.rot / 2;
+  if (!vector) {
+    rope_kernel<T, C, kInterleaved><<<unsigned(p.tokens), kRopeThreads, size_t(half) * sizeof(float2), st>>>(p);
+    return;
+  }
+  // several tokens a block once that leaves eight blocks an SM; under one
+  // block an SM, 256 items a block
+  const int heads = p.hq + 2 * p.hkv;
+  const int tb = p.tokens >= int64_t(sms) * 8 * kRopeTokens ? kRopeTokens : 1;
+  const int hb = p.tokens < 2 * sms ? std::max(1, kRopeThreads / (p.d / 16)) : heads;
+  const dim3 grid(unsigned((p.tokens + tb - 1) / tb), unsigned((heads + hb - 1) / hb));
+  const size_t smem = size_t(tb) * half * sizeof(float2) + size_t(half) * sizeof(uint64_t);
+  rope_vector_kernel<T, C, kInterleaved><<<grid, kRopeThreads, smem, st>>>(p, tb, hb);
 }
 
 bool map_cache(CUtensorMap *map, const vg_kv_cache &c, void *base, const int64_t *stride) {
@@ -220,14 +373,24 @@ extern "C" vg_status vg_rope_append(const vg_rope_desc *d, const vg_kv_cache *ca
   p.factor = d->factor;
   p.k_inv = 1.f / cache->k_scale;
   p.v_inv = 1.f / cache->v_scale;
-  const bool il = d->layout == VG_ROPE_INTERLEAVED, f8 = cache->type == VG_TYPE_E4M3;
+  bool vector = d->rot % 16 == 0 && aligned16(d->q) && aligned16(d->k) && aligned16(d->v) &&
+                aligned16(d->q_out);
+  for (int i = 0; i < 3; ++i)
+    vector = vector && d->q_stride[i] % 8 == 0 && d->k_stride[i] % 8 == 0 && d->v_stride[i] % 8 == 0;
+  const bool f8 = cache->type == VG_TYPE_E4M3;
   cudaStream_t st = as_cuda(stream);
+  auto launch = [&](auto t, auto c) {
+    using T = decltype(t);
+    using C = decltype(c);
+    if (d->layout == VG_ROPE_INTERLEAVED) launch_rope<T, C, true>(p, vector, sms, st);
+    else launch_rope<T, C, false>(p, vector, sms, st);
+  };
   if (d->type == VG_TYPE_BF16) {
-    if (f8) launch_rope<__nv_bfloat16, __nv_fp8_e4m3>(p, il, st);
-    else launch_rope<__nv_bfloat16, __nv_bfloat16>(p, il, st);
+    if (f8) launch(__nv_bfloat16{}, __nv_fp8_e4m3{});
+    else launch(__nv_bfloat16{}, __nv_bfloat16{});
   } else {
-    if (f8) launch_rope<__half, __nv_fp8_e4m3>(p, il, st);
-    else launch_rope<__half, __half>(p, il, st);
+    if (f8) launch(__half{}, __nv_fp8_e4m3{});
+    else launch(__half{}, __half{});
   }
   VG_LAUNCH_CHECK();
   return VG_OK;

@@ -13,70 +13,245 @@ namespace {
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(float x) { return x; }
+
+// ------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Stores 16 bytes at the address that `p` has in block `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(void *p, uint32_t rank, uint64_t a, uint64_t b) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(at)
+      : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(at), "l"(a), "l"(b) : "memory");
+}
+
+// Launches `fn` with `grid` blocks in clusters of `cluster` (which divides it).
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cluster,
+                            cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(cluster);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
 
 // ------------------------------------------------------------ probabilities
-// One block a row: the largest logit and its first place, the sum of
-// exponentials, and the row again, divided.
-constexpr int kProbThreads = 1024;
+// A cluster of blocks a row, the row's logits in registers: each warp takes
+// its largest logit m_w and s_w = sum of 2^((x - m_w) c), c = log2 e / T,
+// every block gets every warp's pair through distributed shared memory, and
+// with M = max m_w, S = sum s_w 2^((m_w - M) c)
+//     out = 2^((x - m_w) c) 2^((m_w - M) c) / S.
+// So a row is read once and written once, with one barrier between, and bytes
+// bound it.  A greedy row (T <= 0) exchanges (m_w, its first index) instead.
+//
+// Elements go by units of 8 on the grid of the whole array, so that loads
+// and stores are aligned whatever the row's length; the units at a row's two
+// ends go element by element.
+constexpr int kProbThreads = 512, kProbWarps = kProbThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <typename T>
+struct Unit {                      // 8 logits as they came
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint4 &v = w[i / 4];
+      return __uint_as_float(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+    } else {
+      const uint32_t v = i / 2 == 0 ? w[0].x : i / 2 == 1 ? w[0].y : i / 2 == 2 ? w[0].z : w[0].w;
+      const uint16_t h = uint16_t(v >> (16 * (i & 1)));
+      T t;
+      memcpy(&t, &h, 2);
+      return to_f(t);
+    }
+  }
+};
+
+// Unit u of a row whose elements are [lo, hi) of the array; elements outside
+// the row read as -infinity.
+template <typename T>
+__device__ __forceinline__ Unit<T> load_unit(const T *x, int64_t u, int64_t lo, int64_t hi) {
+  Unit<T> v;
+  const int64_t e = u * 8;
+  if (e >= lo && e + 8 <= hi) {
+#pragma unroll
+    for (int k = 0; k < int(sizeof(T) / 2); ++k) v.w[k] = __ldg(reinterpret_cast<const uint4 *>(x + e) + k);
+  } else {
+    T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = e + i >= lo && e + i < hi ? x[e + i] : T(-INFINITY);
+    memcpy(v.w, t, sizeof t);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_unit(float *out, int64_t u, int64_t lo, int64_t hi,
+                                           const float (&y)[8]) {
+  const int64_t e = u * 8;
+  if (e >= lo && e + 8 <= hi) {
+    float4 *to = reinterpret_cast<float4 *>(out + e);
+    __stcs(to, make_float4(y[0], y[1], y[2], y[3]));
+    __stcs(to + 1, make_float4(y[4], y[5], y[6], y[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + i >= lo && e + i < hi) out[e + i] = y[i];
+  }
+}
+
+// NV units a thread are kept in registers; NV = 0: a row of any length, read twice.
+template <typename T, int NV>
 __global__ void __launch_bounds__(kProbThreads)
     probabilities_kernel(const T *x, int64_t V, const float *temperature, float *out) {
-  __shared__ float red[32];
-  __shared__ int64_t where[32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  x += row * V;
-  out += row * V;
+  __shared__ __align__(16) ulonglong2 table[kMaxCluster * kProbWarps];
+  const uint32_t rank = cluster_rank(), blocks = cluster_size();
+  const int64_t row = blockIdx.x / blocks;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t lo = row * V, hi = lo + V;
+  const int64_t stride = int64_t(blocks) * kProbThreads;
+  const int64_t u0 = lo / 8 + rank * kProbThreads + threadIdx.x, end = (hi + 7) / 8;
+  Unit<T> kept[NV ? NV : 1];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t u = u0 + k * stride;
+      if (u < end) kept[k] = load_unit(x, u, lo, hi);
+    }
+  }
   const float t = temperature ? temperature[row] : 1.f;
   const bool greedy = t <= 0.f;
-  float m = -INFINITY;
-  int64_t at = V;
-  for (int64_t i = tid; i < V; i += kProbThreads) {
-    const float v = to_f(x[i]);
-    if (v > m) {
-      m = v;
-      at = i;
-    }
-  }
+  const float c = kLog2e / t;
+  auto each = [&](auto &&f) {
+    if constexpr (NV > 0) {
 #pragma unroll
-  for (int w = 16; w; w /= 2) {
-    const float m2 = __shfl_xor_sync(~0u, m, w);
-    const int64_t a2 = __shfl_xor_sync(~0u, at, w);
-    if (m2 > m || (m2 == m && a2 < at)) {
-      m = m2;
-      at = a2;
+      for (int k = 0; k < NV; ++k) {
+        const int64_t u = u0 + k * stride;
+        if (u < end) f(u, kept[k]);
+      }
+    } else {
+      for (int64_t u = u0; u < end; u += stride) {
+        const Unit<T> v = load_unit(x, u, lo, hi);
+        f(u, v);
+      }
     }
-  }
-  if (lane == 0) {
-    red[warp] = m;
-    where[warp] = at;
-  }
-  __syncthreads();
-  for (int w = 0; w < 32; ++w)
-    if (red[w] > m || (red[w] == m && where[w] < at)) {
-      m = red[w];
-      at = where[w];
-    }
-  __syncthreads();
+  };
+  float m = -INFINITY;
+  each([&](int64_t, const Unit<T> &v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v.get(i));
+  });
+#pragma unroll
+  for (int w = 16; w; w /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+  const float base = m == -INFINITY ? 0.f : m;
+  uint64_t second = 0;                         // the sum, or the first index of the maximum
   if (greedy) {
-    for (int64_t i = tid; i < V; i += kProbThreads) out[i] = i == at ? 1.f : 0.f;
+    int64_t at = V;
+    each([&](int64_t u, const Unit<T> &v) {
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (v.get(i) == m && m != -INFINITY) at = min(at, u * 8 + i - lo);
+    });
+#pragma unroll
+    for (int w = 16; w; w /= 2) at = min(at, int64_t(__shfl_xor_sync(~0u, at, w)));
+    second = uint64_t(at);
+  } else {
+    float sum = 0.f;
+    each([&](int64_t, const Unit<T> &v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += ex2((v.get(i) - base) * c);
+    });
+#pragma unroll
+    for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
+    second = __float_as_uint(sum);
+  }
+  // a block of another cluster position must have begun before it is written to
+  if (blocks > 1) cluster_sync();
+  if (lane < int(blocks))
+    cluster_store(&table[rank * kProbWarps + warp], lane, __float_as_uint(m), second);
+  if (blocks > 1) cluster_sync();
+  else __syncthreads();
+  const int entries = int(blocks) * kProbWarps;
+  float top = -INFINITY;
+  for (int i = lane; i < entries; i += 32) top = fmaxf(top, __uint_as_float(uint32_t(table[i].x)));
+#pragma unroll
+  for (int w = 16; w; w /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+  if (greedy) {
+    int64_t at = V;
+    for (int i = lane; i < entries; i += 32)
+      if (__uint_as_float(uint32_t(table[i].x)) == top) at = min(at, int64_t(table[i].y));
+#pragma unroll
+    for (int w = 16; w; w /= 2) at = min(at, int64_t(__shfl_xor_sync(~0u, at, w)));
+    for (int64_t u = u0; u < end; u += stride) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = u * 8 + i - lo == at ? 1.f : 0.f;
+      store_unit(out, u, lo, hi, y);
+    }
     return;
   }
-  const float c = kLog2e / t;
-  if (m == -INFINITY) m = 0.f;
+  const float all = top == -INFINITY ? 0.f : top;
   float sum = 0.f;
-  for (int64_t i = tid; i < V; i += kProbThreads) sum += exp2f((to_f(x[i]) - m) * c);
+  for (int i = lane; i < entries; i += 32) {
+    const float mw = __uint_as_float(uint32_t(table[i].x));
+    // a warp without a finite logit has summed from 0: its sum is 0, or NaN
+    sum += __uint_as_float(uint32_t(table[i].y)) * ex2(((mw == -INFINITY ? all : mw) - all) * c);
+  }
 #pragma unroll
   for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < 32; ++w) sum += red[w];
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int64_t i = tid; i < V; i += kProbThreads) out[i] = exp2f((to_f(x[i]) - m) * c) * inv;
+  const float scale = (sum == 0.f ? 0.f : 1.f / sum) * ex2((m == -INFINITY ? 0.f : base - all) * c);
+  each([&](int64_t u, const Unit<T> &v) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = ex2((v.get(i) - base) * c) * scale;
+    store_unit(out, u, lo, hi, y);
+  });
+}
+
+// Blocks a row: the fewest that hold it with 5 units a thread, and up to 8
+// while the rows leave SMs idle.
+template <typename T>
+cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const float *temperature,
+                                 float *out, int sms, cudaStream_t st) {
+  const int64_t units = V / 8 + 2;
+  int c = 1;
+  while (c < kMaxCluster &&
+         (units > int64_t(5) * kProbThreads * c || (rows * c < sms && units > kProbThreads * c)))
+    c *= 2;
+  const int64_t each = (units + int64_t(c) * kProbThreads - 1) / (int64_t(c) * kProbThreads);
+  const unsigned grid = unsigned(rows) * unsigned(c);
+  auto go = [&](auto fn) {
+    return launch_clusters(fn, grid, kProbThreads, c, st, x, V, temperature, out);
+  };
+  if (each <= 1) return go(&probabilities_kernel<T, 1>);
+  if (each <= 2) return go(&probabilities_kernel<T, 2>);
+  if (each <= 5) return go(&probabilities_kernel<T, 5>);
+  return go(&probabilities_kernel<T, 0>);
 }
 
 // -------------------------------------------------------------- verification
@@ -88,7 +263,12 @@ __global__ void __launch_bounds__(kProbThreads)
 //
 // Fixed point: p, q and the sums S in units of 2^-60 (a row sums to less
 // than 16), a in units of 2^-56 (at most 1 + the number of refusals).
-constexpr int kVerThreads = 1024, kVerWarps = kVerThreads / 32;
+//
+// A cluster of blocks a sequence.  Every warp of it owns one run of the row:
+// it adds up its run, and every block gets every warp's sum through
+// distributed shared memory, so that each walks the tree by itself and alike;
+// the warp whose run holds the drawn index finds it.
+constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32;
 constexpr int kMaxNodes = 1024;
 constexpr float kUnit = 1152921504606846976.f;                 // 2^60
 
@@ -129,13 +309,28 @@ struct VerifyParams {
   int n, q_rows;
 };
 
+// Four consecutive entries of a row, those at or past `last` as 0.
+template <bool kVector>
+__device__ __forceinline__ float4 load4(const float *row, int64_t e, int64_t last) {
+  if (kVector) return e < last ? __ldg(reinterpret_cast<const float4 *>(row + e)) : make_float4(0, 0, 0, 0);
+  float4 v;
+  v.x = e < last ? __ldg(row + e) : 0.f;
+  v.y = e + 1 < last ? __ldg(row + e + 1) : 0.f;
+  v.z = e + 2 < last ? __ldg(row + e + 2) : 0.f;
+  v.w = e + 3 < last ? __ldg(row + e + 3) : 0.f;
+  return v;
+}
+
+// kVector: vocab % 4 == 0, so every row is 16-byte aligned.
+template <bool kVector>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams v) {
   __shared__ float pt[kMaxNodes], qt[kMaxNodes], su[kMaxNodes];
   __shared__ int16_t par[kMaxNodes];             // -1: no node to try
-  __shared__ uint64_t sums[kVerWarps];
+  __shared__ __align__(16) ulonglong2 table[2][kMaxCluster * kVerWarps];
   __shared__ uint64_t s_a;
-  __shared__ int s_cur, s_more;
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  __shared__ int s_cur, s_more, s_kept;
+  const uint32_t rank = cluster_rank(), blocks = cluster_size();
+  const int b = blockIdx.x / blocks, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t V = v.V;
   const int n = v.counts ? min(max(v.counts[b], 0), v.n) : v.n;
   const float *prow = v.p + int64_t(b) * v.n * V;
@@ -145,7 +340,6 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   for (int i = tid; i < v.n; i += kVerThreads) {
     su[i] = v.u[int64_t(b) * v.n + i];
     par[i] = -1;
-    path[i] = -1;
     if (i > 0 && i < n) {
       const int f = v.parents[int64_t(b) * v.n + i], t = tokens[i];
       if (f >= 0 && f < i && f < v.q_rows && t >= 0 && t < V) {
@@ -155,15 +349,17 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
       }
     }
   }
-  for (int i = tid; i <= v.n; i += kVerThreads) out[i] = -1;
-  __syncthreads();
-  // each warp sums one run of the row: the warps' sums in order are the
-  // running sum at the runs' ends
-  const int64_t run = ((V + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;
-  const int64_t first = min(run * warp, V), last = min(first + run, V);
+  // Runs are whole steps of 128 entries (4 a lane) and follow each other in
+  // the order of the warps: the sums of the warps before are the running sum.
+  const int runs = int(blocks) * kVerWarps, mine = int(rank) * kVerWarps + warp;
+  const int64_t run = ((V + runs - 1) / runs + 127) / 128 * 128;
+  const int64_t first = min(run * mine, V), last = min(first + run, V);
   int i = 1, cur = 0, kept = 0;                  // thread 0's walk
   uint64_t a = 0, S = 1ull << 60, total = 0;
   bool summed = false;
+  uint32_t pass = 0;
+  if (blocks > 1) cluster_sync();                // every block has begun
+  else __syncthreads();
   while (true) {
     if (tid == 0) {
       s_more = 0;
@@ -173,8 +369,11 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
         const uint64_t r = a ? residual(pt[i], qt[i], a) : 0;
         const bool ok = a ? left < double(r) : left < double(pt[i]) * double(1ull << 60);
         if (ok) {
-          path[kept] = i;
-          out[kept++] = tokens[i];
+          if (rank == 0) {
+            path[kept] = i;
+            out[kept] = tokens[i];
+          }
+          ++kept;
           cur = i;
           a = 0;
           S = 1ull << 60;
@@ -193,22 +392,42 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
       }
       s_cur = cur;
       s_a = a;
+      s_kept = kept;
     }
     __syncthreads();
     const int more = s_more, node = s_cur;
     const uint64_t aa = s_a;
     const float *pr = prow + node * V;
     const float *qr = qrow + (node < v.q_rows ? node : 0) * V;
+    // sum of four entries' residuals
+    auto four = [&](const float4 &p4, const float4 &q4) {
+      return residual(p4.x, q4.x, aa) + residual(p4.y, q4.y, aa) + residual(p4.z, q4.z, aa) +
+             residual(p4.w, q4.w, aa);
+    };
+    const float4 none = make_float4(0, 0, 0, 0);
     if (more) {
+      ++pass;
       uint64_t sum = 0;
-      for (int64_t e = first + lane; e < last; e += 32)
-        sum += residual(pr[e], aa ? qr[e] : 0.f, aa);
+      for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
+        float4 p4[4], q4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t e = e0 + k * 128 + lane * 4;
+          p4[k] = load4<kVector>(pr, e, last);
+          q4[k] = aa ? load4<kVector>(qr, e, last) : none;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += four(p4[k], q4[k]);
+      }
       sum = warp_sum(sum);
-      if (lane == 0) sums[warp] = sum;
-      __syncthreads();
-      if (tid == 0) {
-        total = 0;
-        for (int w = 0; w < kVerWarps; ++w) total += sums[w];
+      // two tables in turn: a block may still read the one before
+      if (lane < int(blocks)) cluster_store(&table[pass & 1][mine], lane, sum, 0);
+      if (blocks > 1) cluster_sync();
+      else __syncthreads();
+      if (warp == 0) {
+        uint64_t x = 0;
+        for (int k = lane; k < runs; k += 32) x += table[pass & 1][k].x;
+        total = warp_sum(x);
         S = total;
         summed = true;
       }
@@ -216,30 +435,62 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     }
     // draw: the warp whose run the threshold falls into looks it up
     uint64_t whole = 0, before = 0;
-    for (int w = 0; w < kVerWarps; ++w) {
-      if (w < warp) before += sums[w];
-      whole += sums[w];
+    for (int k = lane; k < runs; k += 32) {
+      const uint64_t x = table[pass & 1][k].x;
+      whole += x;
+      if (k < mine) before += x;
     }
+    whole = warp_sum(whole);
+    before = warp_sum(before);
     const float u0 = fminf(fmaxf(su[0], 0.f), 0x1.fffffep-1f);
     const uint64_t mark = __umul64hi(uint64_t(double(u0) * 18446744073709551616.0), whole);
-    if (tid == 0) v.accepted[b] = kept, s_cur = kept;
-    __syncthreads();
-    if (whole != 0 && before <= mark && mark - before < sums[warp]) {
+    const int at = s_kept;
+    if (rank == 0) {
+      if (tid == 0) v.accepted[b] = at;
+      for (int k = at + tid; k < v.n; k += kVerThreads) path[k] = -1;
+      for (int k = at + 1 + tid; k <= v.n; k += kVerThreads) out[k] = -1;
+      if (tid == 0 && whole == 0) out[at] = -1;
+    }
+    if (whole != 0 && before <= mark && mark - before < table[pass & 1][mine].x) {
       uint64_t c = before;
-      for (int64_t e0 = first; e0 < last; e0 += 32) {
-        const int64_t e = e0 + lane;
-        uint64_t x = e < last ? residual(pr[e], aa ? qr[e] : 0.f, aa) : 0;
+      for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
+        float4 p4[4], q4[4];
 #pragma unroll
-        for (int w = 1; w < 32; w *= 2) {
-          const uint64_t y = __shfl_up_sync(~0u, x, w);
-          if (lane >= w) x += y;
+        for (int k = 0; k < 4; ++k) {
+          const int64_t e = e0 + k * 128 + lane * 4;
+          p4[k] = load4<kVector>(pr, e, last);
+          q4[k] = aa ? load4<kVector>(qr, e, last) : none;
         }
-        const uint32_t over = __ballot_sync(~0u, c + x > mark);
-        if (over) {
-          if (lane == 0) out[s_cur] = int32_t(e0 + __ffs(over) - 1);
-          break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t own = four(p4[k], q4[k]);
+          uint64_t x = own;
+#pragma unroll
+          for (int w = 1; w < 32; w *= 2) {
+            const uint64_t y = __shfl_up_sync(~0u, x, w);
+            if (lane >= w) x += y;
+          }
+          const uint32_t over = __ballot_sync(~0u, c + x > mark);
+          if (over) {
+            if (lane == __ffs(over) - 1) {
+              // one of this lane's four
+              uint64_t y = c + x - own;
+              const float pv[4] = {p4[k].x, p4[k].y, p4[k].z, p4[k].w};
+              const float qv[4] = {q4[k].x, q4[k].y, q4[k].z, q4[k].w};
+              int hit = 3;
+#pragma unroll
+              for (int j = 2; j >= 0; --j) {
+                uint64_t z = y;
+#pragma unroll
+                for (int jj = 0; jj <= j; ++jj) z += residual(pv[jj], qv[jj], aa);
+                if (z > mark) hit = j;
+              }
+              out[at] = int32_t(e0 + k * 128 + lane * 4 + hit);
+            }
+            return;
+          }
+          c += __shfl_sync(~0u, x, 31);
         }
-        c += __shfl_sync(~0u, x, 31);
       }
     }
     return;
@@ -261,16 +512,15 @@ extern "C" vg_status vg_probabilities(const void *x, int type, int64_t rows, int
   int sms = 0;
   if (vg_status s = device_sms(&sms)) return s;
   cudaStream_t st = as_cuda(stream);
-  const unsigned grid = unsigned(rows);
   if (type == VG_TYPE_BF16)
-    probabilities_kernel<<<grid, kProbThreads, 0, st>>>(static_cast<const __nv_bfloat16 *>(x),
-                                                        vocab, temperature, out);
+    VG_CUDA(launch_probabilities(static_cast<const __nv_bfloat16 *>(x), rows, vocab, temperature,
+                                 out, sms, st));
   else if (type == VG_TYPE_FP16)
-    probabilities_kernel<<<grid, kProbThreads, 0, st>>>(static_cast<const __half *>(x), vocab,
-                                                        temperature, out);
+    VG_CUDA(launch_probabilities(static_cast<const __half *>(x), rows, vocab, temperature, out, sms,
+                                 st));
   else
-    probabilities_kernel<<<grid, kProbThreads, 0, st>>>(static_cast<const float *>(x), vocab,
-                                                        temperature, out);
+    VG_CUDA(launch_probabilities(static_cast<const float *>(x), rows, vocab, temperature, out, sms,
+                                 st));
   VG_LAUNCH_CHECK();
   return VG_OK;
 }
@@ -300,7 +550,12 @@ extern "C" vg_status vg_verify_tree(const float *p, const float *q, const int32_
   v.V = vocab;
   v.n = n;
   v.q_rows = q_rows;
-  verify_kernel<<<unsigned(batch), kVerThreads, 0, as_cuda(stream)>>>(v);
+  // blocks a sequence: enough to fill the device, each with a few steps to do
+  int c = kMaxCluster;
+  while (c > 1 && (int64_t(c) * batch > 4 * sms || vocab < int64_t(c) * kVerWarps * 128)) c /= 2;
+  const unsigned grid = unsigned(batch) * unsigned(c);
+  VG_CUDA(launch_clusters(vocab % 4 ? &verify_kernel<false> : &verify_kernel<true>, grid,
+                          kVerThreads, c, as_cuda(stream), v));
   VG_LAUNCH_CHECK();
   return VG_OK;
 }
