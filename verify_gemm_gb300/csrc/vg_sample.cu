@@ -4,7 +4,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "vg_internal.h"
 
@@ -29,6 +31,15 @@ __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
+// The two halves of the barrier: what is done between them overlaps the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // Stores 16 bytes at the address that `p` has in block `rank` of the cluster.
 __device__ __forceinline__ void cluster_store(void *p, uint32_t rank, uint64_t a, uint64_t b) {
   uint32_t at;
@@ -40,11 +51,12 @@ __device__ __forceinline__ void cluster_store(void *p, uint32_t rank, uint64_t a
 
 // Launches `fn` with `grid` blocks in clusters of `cluster` (which divides it).
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cluster,
+cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cluster, int smem,
                             cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -56,25 +68,36 @@ cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cl
 }
 
 // ------------------------------------------------------------ probabilities
-// A cluster of blocks a row, the row's logits in registers: each warp takes
-// its largest logit m_w and s_w = sum of 2^((x - m_w) c), c = log2 e / T,
-// every block gets every warp's pair through distributed shared memory, and
-// with M = max m_w, S = sum s_w 2^((m_w - M) c)
-//     out = 2^((x - m_w) c) 2^((m_w - M) c) / S.
-// So a row is read once and written once, with one barrier between, and bytes
-// bound it.  A greedy row (T <= 0) exchanges (m_w, its first index) instead.
+// A cluster of blocks a row.  Each thread copies its share of the row to
+// shared memory (asynchronously, so every block of an SM has its whole share
+// in flight) and reads it from there three times: each warp takes its largest
+// logit m_w and, with c = log2 e / T and b_w = m_w c, s_w = sum 2^(x c - b_w);
+// every block gets every warp's pair through distributed shared memory; and
+// with B = max b_w, S = sum s_w 2^(b_w - B)
+//     out = 2^(x c - b_w) 2^(b_w - B) / S.
+// (b_w is one rounded number for the whole warp, so its rounding cancels.)
+// A row is read once and written once, with one barrier of the cluster
+// between, and bytes bound it.  A greedy row (T <= 0) exchanges (m_w, its
+// first index) instead.
 //
 // Elements go by units of 8 on the grid of the whole array, so that loads
 // and stores are aligned whatever the row's length; the units at a row's two
 // ends go element by element.
-constexpr int kProbThreads = 512, kProbWarps = kProbThreads / 32;
+constexpr int kProbThreads = 256, kProbWarps = kProbThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kProbShare = 40 * 1024;          // bytes of a row a block holds at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from)
+               : "memory");
 }
 
 template <typename T>
@@ -125,10 +148,12 @@ __device__ __forceinline__ void store_unit(float *out, int64_t u, int64_t lo, in
   }
 }
 
-// NV units a thread are kept in registers; NV = 0: a row of any length, read twice.
-template <typename T, int NV>
+// kHeld: the block's share fits its shared memory; otherwise it is read from
+// memory each time (rows of any length).
+template <typename T, bool kHeld>
 __global__ void __launch_bounds__(kProbThreads)
     probabilities_kernel(const T *x, int64_t V, const float *temperature, float *out) {
+  extern __shared__ __align__(16) uint8_t held[];
   __shared__ __align__(16) ulonglong2 table[kMaxCluster * kProbWarps];
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
   const int64_t row = blockIdx.x / blocks;
@@ -136,29 +161,41 @@ __global__ void __launch_bounds__(kProbThreads)
   const int64_t lo = row * V, hi = lo + V;
   const int64_t stride = int64_t(blocks) * kProbThreads;
   const int64_t u0 = lo / 8 + rank * kProbThreads + threadIdx.x, end = (hi + 7) / 8;
-  Unit<T> kept[NV ? NV : 1];
-  if constexpr (NV > 0) {
+  // a block must have begun before others write to it: said here, waited for there
+  if (blocks > 1) cluster_arrive();
+  constexpr int kPart = sizeof(T) / 2;          // 16-byte parts of a unit, apart in shared memory
+  Unit<T> *units = reinterpret_cast<Unit<T> *>(held);
+  uint4 *parts = reinterpret_cast<uint4 *>(units) + threadIdx.x;
+  if constexpr (kHeld) {
+    uint4 *to = parts;
+    for (int64_t u = u0; u < end; u += stride, to += kPart * kProbThreads) {
+      if (u * 8 >= lo && u * 8 + 8 <= hi) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int64_t u = u0 + k * stride;
-      if (u < end) kept[k] = load_unit(x, u, lo, hi);
+        for (int k = 0; k < kPart; ++k)
+          copy16(to + k * kProbThreads, reinterpret_cast<const uint4 *>(x + u * 8) + k);
+      } else {
+        const Unit<T> v = load_unit(x, u, lo, hi);
+#pragma unroll
+        for (int k = 0; k < kPart; ++k) to[k * kProbThreads] = v.w[k];
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // a thread reads only what it copied
   }
   const float t = temperature ? temperature[row] : 1.f;
   const bool greedy = t <= 0.f;
   const float c = kLog2e / t;
   auto each = [&](auto &&f) {
-    if constexpr (NV > 0) {
+    const uint4 *from = parts;
+#pragma unroll 2
+    for (int64_t u = u0; u < end; u += stride, from += kPart * kProbThreads) {
+      Unit<T> v;
+      if constexpr (kHeld) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int64_t u = u0 + k * stride;
-        if (u < end) f(u, kept[k]);
+        for (int k = 0; k < kPart; ++k) v.w[k] = from[k * kProbThreads];
+      } else {
+        v = load_unit(x, u, lo, hi);
       }
-    } else {
-      for (int64_t u = u0; u < end; u += stride) {
-        const Unit<T> v = load_unit(x, u, lo, hi);
-        f(u, v);
-      }
+      f(u, v);
     }
   };
   float m = -INFINITY;
@@ -183,15 +220,16 @@ __global__ void __launch_bounds__(kProbThreads)
   } else {
     float sum = 0.f;
     each([&](int64_t, const Unit<T> &v) {
+      float part[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += ex2((v.get(i) - base) * c);
+      for (int i = 0; i < 8; ++i) part[i] = ex2((v.get(i) - base) * c);
+      sum += ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
     });
 #pragma unroll
     for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
     second = __float_as_uint(sum);
   }
-  // a block of another cluster position must have begun before it is written to
-  if (blocks > 1) cluster_sync();
+  if (blocks > 1) cluster_wait();
   if (lane < int(blocks))
     cluster_store(&table[rank * kProbWarps + warp], lane, __float_as_uint(m), second);
   if (blocks > 1) cluster_sync();
@@ -224,7 +262,7 @@ __global__ void __launch_bounds__(kProbThreads)
   }
 #pragma unroll
   for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
-  const float scale = (sum == 0.f ? 0.f : 1.f / sum) * ex2((m == -INFINITY ? 0.f : base - all) * c);
+  const float scale = (sum == 0.f ? 0.f : 1.f / sum) * ex2(m == -INFINITY ? 0.f : (base - all) * c);
   each([&](int64_t u, const Unit<T> &v) {
     float y[8];
 #pragma unroll
@@ -233,25 +271,23 @@ __global__ void __launch_bounds__(kProbThreads)
   });
 }
 
-// Blocks a row: the fewest that hold it with 5 units a thread, and up to 8
-// while the rows leave SMs idle.
+// Blocks a row: as few as hold it, and up to 8 while the rows leave SMs idle.
 template <typename T>
 cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const float *temperature,
                                  float *out, int sms, cudaStream_t st) {
-  const int64_t units = V / 8 + 2;
+  const int64_t units = V / 8 + 2, size = 8 * sizeof(T);
   int c = 1;
   while (c < kMaxCluster &&
-         (units > int64_t(5) * kProbThreads * c || (rows * c < sms && units > kProbThreads * c)))
+         (units * size > int64_t(kProbShare) * c || (rows * c < 2 * sms && units > kProbThreads * c)))
     c *= 2;
   const int64_t each = (units + int64_t(c) * kProbThreads - 1) / (int64_t(c) * kProbThreads);
+  const int64_t share = each * kProbThreads * size;
   const unsigned grid = unsigned(rows) * unsigned(c);
-  auto go = [&](auto fn) {
-    return launch_clusters(fn, grid, kProbThreads, c, st, x, V, temperature, out);
-  };
-  if (each <= 1) return go(&probabilities_kernel<T, 1>);
-  if (each <= 2) return go(&probabilities_kernel<T, 2>);
-  if (each <= 5) return go(&probabilities_kernel<T, 5>);
-  return go(&probabilities_kernel<T, 0>);
+  if (share > kProbShare + 8192)
+    return launch_clusters(&probabilities_kernel<T, false>, grid, kProbThreads, c, 0, st, x, V,
+                           temperature, out);
+  return launch_clusters(&probabilities_kernel<T, true>, grid, kProbThreads, c, int(share), st, x, V,
+                         temperature, out);
 }
 
 // -------------------------------------------------------------- verification
@@ -269,29 +305,45 @@ cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const floa
 // distributed shared memory, so that each walks the tree by itself and alike;
 // the warp whose run holds the drawn index finds it.
 constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32;
+constexpr int kVerCluster = 16;                  // most blocks a sequence
 constexpr int kMaxNodes = 1024;
-constexpr float kUnit = 1152921504606846976.f;                 // 2^60
 
-__device__ __forceinline__ float as_probability(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
-__device__ __forceinline__ uint64_t to_fixed(float x) { return __float2ull_rz(x * kUnit); }
-
-// a q in units of 2^-60, rounded down; all ones where it does not fit.
-__device__ __forceinline__ uint64_t scaled(uint64_t a, float q) {
-  const uint32_t bits = __float_as_uint(q), e = bits >> 23;
-  if (e == 0) return 0;                                        // 0, or below 2^-126
-  const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u;           // q = m 2^(e - 150)
-  const uint64_t lo = m * a, hi = __umul64hi(m, a);
-  const uint32_t s = 146u - e;                                 // 19..145, as q <= 1
-  if (s >= 128) return 0;
-  if (s >= 64) return hi >> (s - 64);
-  if (hi >> s) return ~0ull;
-  return (hi << (64 - s)) | (lo >> s);
+// To [0, 1], NaN to 0.
+__device__ __forceinline__ float as_probability(float x) { return __saturatef(x); }
+// ... in units of 2^-60, rounded down: x = m 2^(e - 150), so m 2^37 >> (127 - e).
+// (A conversion to 64 bits runs at 2 a clock and SM here: 13 us for a run of
+// 25 000 entries.)
+__device__ __forceinline__ uint64_t to_fixed(float x) {
+  const uint32_t bits = __float_as_uint(as_probability(x)), e = bits >> 23;
+  const uint64_t m = uint64_t(((bits & 0x7FFFFFu) | 0x800000u) << 5) << 32;
+  uint64_t y;
+  asm("shr.b64 %0, %1, %2;" : "=l"(y) : "l"(m), "r"(127u - e));   // 0 from 64 on
+  return y;
 }
 
+constexpr uint64_t kOne = 1ull << 56;            // a = 1
+
+// max(p - a q, 0) in units of 2^-60.  Modes: a = 0; a = 1; a < 8, where both
+// factors of (y a) >> 56 fit 64 bits with the shift made beforehand; any a.
+template <int kMode>
 __device__ __forceinline__ uint64_t residual(float p, float q, uint64_t a) {
-  const uint64_t x = to_fixed(as_probability(p));
-  const uint64_t y = a ? scaled(a, as_probability(q)) : 0;
+  const uint64_t x = to_fixed(p);
+  if (kMode == 0) return x;
+  uint64_t y = to_fixed(q);
+  if (kMode == 2) y = __umul64hi(y << 3, a << 5);
+  if (kMode == 3) {
+    const uint64_t hi = __umul64hi(y, a), lo = y * a;
+    y = hi >> 56 ? ~0ull : (hi << 8) | (lo >> 56);
+  }
   return x > y ? x - y : 0;
+}
+// Calls f with the mode of `a` as a constant.
+template <typename F>
+__device__ __forceinline__ auto with_mode(uint64_t a, F &&f) {
+  if (a == 0) return f(std::integral_constant<int, 0>{});
+  if (a == kOne) return f(std::integral_constant<int, 1>{});
+  if (a < 8 * kOne) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 3>{});
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -321,12 +373,18 @@ __device__ __forceinline__ float4 load4(const float *row, int64_t e, int64_t las
   return v;
 }
 
+template <int kMode>
+__device__ __forceinline__ uint64_t four(const float4 &p, const float4 &q, uint64_t a) {
+  return residual<kMode>(p.x, q.x, a) + residual<kMode>(p.y, q.y, a) +
+         residual<kMode>(p.z, q.z, a) + residual<kMode>(p.w, q.w, a);
+}
+
 // kVector: vocab % 4 == 0, so every row is 16-byte aligned.
 template <bool kVector>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams v) {
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyParams v) {
   __shared__ float pt[kMaxNodes], qt[kMaxNodes], su[kMaxNodes];
   __shared__ int16_t par[kMaxNodes];             // -1: no node to try
-  __shared__ __align__(16) ulonglong2 table[2][kMaxCluster * kVerWarps];
+  __shared__ __align__(16) ulonglong2 table[2][kVerCluster * kVerWarps];
   __shared__ uint64_t s_a;
   __shared__ int s_cur, s_more, s_kept;
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
@@ -337,6 +395,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   const float *qrow = v.q + int64_t(b) * v.q_rows * V;
   const int32_t *tokens = v.tokens + int64_t(b) * v.n;
   int32_t *path = v.path + int64_t(b) * v.n, *out = v.out + int64_t(b) * (v.n + 1);
+  if (blocks > 1) cluster_arrive();
   for (int i = tid; i < v.n; i += kVerThreads) {
     su[i] = v.u[int64_t(b) * v.n + i];
     par[i] = -1;
@@ -354,19 +413,19 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   const int runs = int(blocks) * kVerWarps, mine = int(rank) * kVerWarps + warp;
   const int64_t run = ((V + runs - 1) / runs + 127) / 128 * 128;
   const int64_t first = min(run * mine, V), last = min(first + run, V);
+  if (blocks > 1) cluster_wait();                // every block has begun
+  else __syncthreads();
   int i = 1, cur = 0, kept = 0;                  // thread 0's walk
   uint64_t a = 0, S = 1ull << 60, total = 0;
   bool summed = false;
   uint32_t pass = 0;
-  if (blocks > 1) cluster_sync();                // every block has begun
-  else __syncthreads();
   while (true) {
     if (tid == 0) {
       s_more = 0;
       for (; i < n; ++i) {
         if (par[i] != cur) continue;
         const double left = double(su[i]) * double(qt[i]) * double(S);
-        const uint64_t r = a ? residual(pt[i], qt[i], a) : 0;
+        const uint64_t r = a ? residual<3>(pt[i], qt[i], a) : 0;
         const bool ok = a ? left < double(r) : left < double(pt[i]) * double(1ull << 60);
         if (ok) {
           if (rank == 0) {
@@ -379,7 +438,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
           S = 1ull << 60;
           summed = false;
         } else {
-          a = a ? a + (S >> 4) : 1ull << 56;
+          a = a ? a + (S >> 4) : kOne;
           s_more = 1;
           ++i;
           break;
@@ -399,26 +458,24 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     const uint64_t aa = s_a;
     const float *pr = prow + node * V;
     const float *qr = qrow + (node < v.q_rows ? node : 0) * V;
-    // sum of four entries' residuals
-    auto four = [&](const float4 &p4, const float4 &q4) {
-      return residual(p4.x, q4.x, aa) + residual(p4.y, q4.y, aa) + residual(p4.z, q4.z, aa) +
-             residual(p4.w, q4.w, aa);
-    };
-    const float4 none = make_float4(0, 0, 0, 0);
     if (more) {
       ++pass;
-      uint64_t sum = 0;
-      for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
-        float4 p4[4], q4[4];
+      uint64_t sum = with_mode(aa, [&](auto mode) {
+        constexpr int kMode = decltype(mode)::value;
+        uint64_t sum = 0;
+        for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
+          float4 p4[4], q4[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t e = e0 + k * 128 + lane * 4;
-          p4[k] = load4<kVector>(pr, e, last);
-          q4[k] = aa ? load4<kVector>(qr, e, last) : none;
+          for (int k = 0; k < 4; ++k) {
+            const int64_t e = e0 + k * 128 + lane * 4;
+            p4[k] = load4<kVector>(pr, e, last);
+            q4[k] = kMode ? load4<kVector>(qr, e, last) : make_float4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum += four<kMode>(p4[k], q4[k], aa);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += four(p4[k], q4[k]);
-      }
+        return sum;
+      });
       sum = warp_sum(sum);
       // two tables in turn: a block may still read the one before
       if (lane < int(blocks)) cluster_store(&table[pass & 1][mine], lane, sum, 0);
@@ -452,46 +509,47 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
       if (tid == 0 && whole == 0) out[at] = -1;
     }
     if (whole != 0 && before <= mark && mark - before < table[pass & 1][mine].x) {
-      uint64_t c = before;
-      for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
-        float4 p4[4], q4[4];
+      const int64_t found = with_mode(aa, [&](auto mode) -> int64_t {
+        constexpr int kMode = decltype(mode)::value;
+        uint64_t c = before;
+        for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
+          float4 p4[4], q4[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t e = e0 + k * 128 + lane * 4;
-          p4[k] = load4<kVector>(pr, e, last);
-          q4[k] = aa ? load4<kVector>(qr, e, last) : none;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t own = four(p4[k], q4[k]);
-          uint64_t x = own;
-#pragma unroll
-          for (int w = 1; w < 32; w *= 2) {
-            const uint64_t y = __shfl_up_sync(~0u, x, w);
-            if (lane >= w) x += y;
+          for (int k = 0; k < 4; ++k) {
+            const int64_t e = e0 + k * 128 + lane * 4;
+            p4[k] = load4<kVector>(pr, e, last);
+            q4[k] = kMode ? load4<kVector>(qr, e, last) : make_float4(0, 0, 0, 0);
           }
-          const uint32_t over = __ballot_sync(~0u, c + x > mark);
-          if (over) {
-            if (lane == __ffs(over) - 1) {
-              // one of this lane's four
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t own = four<kMode>(p4[k], q4[k], aa);
+            uint64_t x = own;
+#pragma unroll
+            for (int w = 1; w < 32; w *= 2) {
+              const uint64_t y = __shfl_up_sync(~0u, x, w);
+              if (lane >= w) x += y;
+            }
+            const uint32_t over = __ballot_sync(~0u, c + x > mark);
+            if (over) {
+              // one of the four of the first lane that is over
               uint64_t y = c + x - own;
               const float pv[4] = {p4[k].x, p4[k].y, p4[k].z, p4[k].w};
               const float qv[4] = {q4[k].x, q4[k].y, q4[k].z, q4[k].w};
-              int hit = 3;
+              int hit = 0;
 #pragma unroll
-              for (int j = 2; j >= 0; --j) {
-                uint64_t z = y;
-#pragma unroll
-                for (int jj = 0; jj <= j; ++jj) z += residual(pv[jj], qv[jj], aa);
-                if (z > mark) hit = j;
+              for (int j = 0; j < 3; ++j) {
+                y += residual<kMode>(pv[j], qv[j], aa);
+                if (y <= mark) hit = j + 1;
               }
-              out[at] = int32_t(e0 + k * 128 + lane * 4 + hit);
+              return e0 + k * 128 + lane * 4 + __shfl_sync(~0u, hit, __ffs(over) - 1) +
+                     4 * (__ffs(over) - 1 - lane);
             }
-            return;
+            c += __shfl_sync(~0u, x, 31);
           }
-          c += __shfl_sync(~0u, x, 31);
         }
-      }
+        return -1;
+      });
+      if (lane == 0) out[at] = int32_t(found);
     }
     return;
   }
@@ -551,11 +609,16 @@ extern "C" vg_status vg_verify_tree(const float *p, const float *q, const int32_
   v.n = n;
   v.q_rows = q_rows;
   // blocks a sequence: enough to fill the device, each with a few steps to do
-  int c = kMaxCluster;
-  while (c > 1 && (int64_t(c) * batch > 4 * sms || vocab < int64_t(c) * kVerWarps * 128)) c /= 2;
+  // (16 is more than a portable cluster, and only one such fits a group of SMs
+  // that holds two smaller ones)
+  int64_t c = batch * 16 <= sms ? kVerCluster : std::min<int64_t>(8, 2 * sms / batch);
+  c = std::max<int64_t>(1, std::min(c, vocab / (kVerWarps * 128)));
   const unsigned grid = unsigned(batch) * unsigned(c);
-  VG_CUDA(launch_clusters(vocab % 4 ? &verify_kernel<false> : &verify_kernel<true>, grid,
-                          kVerThreads, c, as_cuda(stream), v));
+  void (*fn)(VerifyParams) = vocab % 4 ? &verify_kernel<false> : &verify_kernel<true>;
+  if (c > 8)
+    VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  VG_CUDA(launch_clusters(fn, grid, kVerThreads, int(c), 0, as_cuda(stream), v));
   VG_LAUNCH_CHECK();
   return VG_OK;
 }

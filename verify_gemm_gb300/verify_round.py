@@ -23,25 +23,32 @@ _TYPES = {torch.bfloat16: VG_TYPE_BF16, torch.float16: VG_TYPE_FP16, torch.float
 _LAYOUTS = {"half": VG_ROPE_HALF, "interleaved": VG_ROPE_INTERLEAVED}
 
 
-def _stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, device):
+    """The stream's handle; that of the current stream comes straight from
+    torch's table, without the Stream object (3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+_int32_t = torch.int32
 
 
 def _int32(t, shape, name):
-    """Address of a contiguous CUDA int32 tensor of that shape (None: 0)."""
-    if t is None:
-        return None
-    if not (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()) or t.shape != shape:
-        raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of shape {tuple(shape)}")
-    return t.data_ptr()
+    """Address of a contiguous CUDA int32 tensor of that shape."""
+    if t.dtype is _int32_t and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of shape {shape}")
 
 
 def _heads(t, name):
-    """A CUDA tensor [batch, n, heads, head_dim] with contiguous heads."""
-    if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+    """Strides (batch, node, head) of a CUDA tensor [batch, n, heads,
+    head_dim] with contiguous heads."""
+    s = t.stride()
+    if not t.is_cuda or len(s) != 4 or s[3] != 1:
         raise ValueError(f"{name}: expected a CUDA tensor [batch, n, heads, head_dim] whose last "
                          "dimension is contiguous")
-    return t
+    return s[:3]
 
 
 class KVCache:
@@ -129,9 +136,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
     depth[b, i] (depth None: i).  The first 2 * inv_freq.numel() elements of a
     head turn: pairs (j, j + rot/2) for layout "half", (2j, 2j + 1) for
     "interleaved".  Nodes past counts[b] append nothing and give 0."""
-    _heads(q, "q")
-    _heads(k, "k")
-    _heads(v, "v")
+    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
     B, n, hq, d = q.shape
     if B != cache.batch or d != cache.head_dim or k.shape != (B, n, cache.heads, d) \
             or v.shape != k.shape:
@@ -148,11 +153,11 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
               and q_out.is_contiguous()):
         raise ValueError("q_out: expected a contiguous CUDA tensor like q")
     desc = vg_rope_desc(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                        q.stride()[:3], k.stride()[:3], v.stride()[:3], inv_freq.data_ptr(),
-                        _int32(lens, (B,), "lens"), _int32(depth, (B, n), "depth"),
-                        _int32(counts, (B,), "counts"), _TYPES.get(q.dtype, -1), _LAYOUTS[layout],
+                        qs, ks, vs, inv_freq.data_ptr(),
+                        _int32(lens, (B,), "lens"), _int32(depth, (B, n), "depth") if depth is not None else None,
+                        _int32(counts, (B,), "counts") if counts is not None else None, _TYPES.get(q.dtype, -1), _LAYOUTS[layout],
                         n, hq, 2 * inv_freq.numel(), factor)
-    s = _lib.vg_rope_append(ctypes.byref(desc), cache._ref, _stream(stream))
+    s = _lib.load().vg_rope_append(ctypes.byref(desc), cache._ref, _stream(stream, q.get_device()))
     if s:
         _lib.check(s, "vg_rope_append")
     return q_out
@@ -181,7 +186,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     q_heads], written if given.  workspace: from tree_attention_workspace,
     made anew by each call that is given none; calls that share one must not
     overlap."""
-    _heads(q, "q")
+    qs = _heads(q, "q")
     B, n, hq, d = q.shape
     if B != cache.batch or d != cache.head_dim:
         raise ValueError("q and the cache do not fit together")
@@ -199,11 +204,11 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     if workspace is None:
         workspace = tree_attention_workspace(q, cache)
     desc = vg_attention_desc(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                             _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts"),
-                             tree.data_ptr() if tree is not None else None, q.stride()[:3],
+                             _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts") if counts is not None else None,
+                             tree.data_ptr() if tree is not None else None, qs,
                              _TYPES.get(q.dtype, -1), n, hq, d ** -0.5 if scale is None else scale)
-    s = _lib.vg_tree_attention(ctypes.byref(desc), cache._ref, workspace.data_ptr(),
-                               workspace.numel(), _stream(stream))
+    s = _lib.load().vg_tree_attention(ctypes.byref(desc), cache._ref, workspace.data_ptr(),
+                               workspace.numel(), _stream(stream, q.get_device()))
     if s:
         _lib.check(s, "vg_tree_attention")
     return out
@@ -228,9 +233,9 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
     elif not (out.is_cuda and out.shape == logits.shape and out.dtype == torch.float32
               and out.is_contiguous()):
         raise ValueError("out: expected a contiguous CUDA float32 tensor like logits")
-    s = _lib.vg_probabilities(logits.data_ptr(), _TYPES.get(logits.dtype, -1), rows, vocab,
+    s = _lib.load().vg_probabilities(logits.data_ptr(), _TYPES.get(logits.dtype, -1), rows, vocab,
                               temperature.data_ptr() if temperature is not None else None,
-                              out.data_ptr(), _stream(stream))
+                              out.data_ptr(), _stream(stream, logits.get_device()))
     if s:
         _lib.check(s, "vg_probabilities")
     return out
@@ -260,11 +265,11 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
     accepted, path, out = flat.split_with_sizes((B, B * n, B * (n + 1)))
     path, out = path.view(B, n), out.view(B, n + 1)
     at = flat.data_ptr()
-    s = _lib.vg_verify_tree(p.data_ptr(), q.data_ptr() if q is not None else None,
+    s = _lib.load().vg_verify_tree(p.data_ptr(), q.data_ptr() if q is not None else None,
                             _int32(tokens, (B, n), "tokens"), _int32(parents, (B, n), "parents"),
-                            _int32(counts, (B,), "counts"), u.data_ptr(), B, n,
+                            _int32(counts, (B,), "counts") if counts is not None else None, u.data_ptr(), B, n,
                             q.shape[1] if q is not None else 0, V, at, at + 4 * B,
-                            at + 4 * B * (n + 1), _stream(stream))
+                            at + 4 * B * (n + 1), _stream(stream, p.get_device()))
     if s:
         _lib.check(s, "vg_verify_tree")
     return accepted, path, out
