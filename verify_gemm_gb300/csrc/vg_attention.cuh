@@ -71,7 +71,7 @@ struct AttnParams {
   float *partial;                   // [grid][2] of (rows x (head_dim padded) + 2 rows)
   int batch, n, hq, hkv, d, q_f16;
   int rows, blocks;                 // rows that share a cache head, row blocks of a unit
-  int box, slots;                   // tokens of a TMA box, ring slots
+  int box, least;                   // tokens of a TMA box, tiles of a run at least
   float c, v_scale;                 // scale * k_scale * log2 e
 };
 
@@ -96,7 +96,10 @@ struct Cfg {
   static constexpr int kQRow = D * 2 + 16;               // q row in shared memory, padded
   static constexpr int kQBytes = kRows * kQRow;
   static constexpr int kWarpState = NT * 32 * 16;        // one warp's o
-  static constexpr int kScratch = (KW / 2) * RW * kWarpState;
+  // every warp's o is laid open for the joining, at most 64 KB at a time
+  static constexpr int kPasses = DC == 4 && KW > 1 ? 2 : 1;
+  static constexpr int kScratch = KW == 1 ? 0 : kConsumers * kWarpState / kPasses;
+  static constexpr int TPW = NT / KW;                    // tiles that a warp joins
   static constexpr int kState = kConsumers * 16 * 8;     // m, l of each warp's rows
   // header: barriers, flags and the tiles' page bits
   static constexpr int kMaxSlots = 16;
@@ -234,7 +237,9 @@ struct Line {
 #pragma unroll
     for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
     total = sum * units;
-    runs = min(int64_t(gridDim.x), total);
+    // a unit is cut into runs of at least 128 KB: shorter ones cost more in the
+    // joining than they save
+    runs = min(int64_t(gridDim.x), max(total / p.least, int64_t(p.batch) * units));
     const int64_t mine = min(int64_t(blockIdx.x), runs);
     at = total * mine / runs;
     end = mine < runs ? total * (mine + 1) / runs : at;
@@ -289,6 +294,29 @@ struct Line {
     return int(((x + 1) * runs + total - 1) / total) - 1;
   }
 };
+
+// Joins another result of the same rows, o2 (tile i), (m2, l2), to o, m, l.
+template <int NT, typename F>
+__device__ __forceinline__ void merge(float (&o)[NT][4], float (&m)[2], float (&l)[2],
+                                      const float2 (&other)[2], F &&o2) {
+  float wa[2], wb[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float top = fmaxf(m[r], other[r].x);
+    wa[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
+    wb[r] = other[r].x == -INFINITY ? 0.f : ex2(other[r].x - top);
+    l[r] = l[r] * wa[r] + other[r].y * wb[r];
+    m[r] = top;
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const float4 v = o2(i);
+    o[i][0] = o[i][0] * wa[0] + v.x * wb[0];
+    o[i][1] = o[i][1] * wa[0] + v.y * wb[0];
+    o[i][2] = o[i][2] * wa[1] + v.z * wb[1];
+    o[i][3] = o[i][3] * wa[1] + v.w * wb[1];
+  }
+}
 
 // Column of element e of output tile nt in thread t of a quad.  E4M3: the
 // transposed load hands out pairs of columns, tile 2k has the even ones.
@@ -707,113 +735,99 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(empty0 + 8 * sv);
     }
 
-    // -------------------------------------------------- join the key warps
+    // ------------------------------------- join the key warps, then the blocks
+    const int first = at.block_of(at.unit0), final = at.block_of(at.unit0 + at.tiles - 1);
+    const bool whole = first == final;
+    // a block's partial result: its unit's first block has it in its second place
+    auto place = [&](int block) {
+      return p.partial + (int64_t(block) * 2 + (block == first ? 1 : 0)) * L::kPartial;
+    };
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
     }
-    float4 *box = reinterpret_cast<float4 *>(scratch);
+    // Every warp lays its result open in shared memory, and each then joins
+    // a share of the columns of its row group: TPW output tiles, all key warps'.
+    constexpr int TPW = L::TPW, NT = L::NT;
+    float res[TPW][4], mj[2] = {m[0], m[1]}, lj[2] = {l[0], l[1]};
+    if constexpr (L::KW == 1) {
 #pragma unroll
-    for (int half = L::KW / 2; half >= 1; half /= 2) {
-      if (kg >= half && kg < 2 * half) {
-        float4 *to = box + ((kg - half) * RW + rw) * (L::NT * 32);
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < L::NT; ++i)
-          to[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        if (t == 0) {
-          state[warp * 16 + g] = make_float2(m[0], l[0]);
-          state[warp * 16 + g + 8] = make_float2(m[1], l[1]);
-        }
-      }
-      named_bar(1, kConsumers * 32);
-      if (kg < half) {
-        const float4 *from = box + (kg * RW + rw) * (L::NT * 32);
-        float wa[2], wb[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 other = state[(warp + half) * 16 + g + 8 * r];
-          const float m2 = fmaxf(m[r], other.x);
-          wa[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - m2);
-          wb[r] = other.x == -INFINITY ? 0.f : ex2(other.x - m2);
-          l[r] = l[r] * wa[r] + other.y * wb[r];
-          m[r] = m2;
-        }
-#pragma unroll
-        for (int i = 0; i < L::NT; ++i) {
-          const float4 v = from[i * 32 + lane];
-          o[i][0] = o[i][0] * wa[0] + v.x * wb[0];
-          o[i][1] = o[i][1] * wa[0] + v.y * wb[0];
-          o[i][2] = o[i][2] * wa[1] + v.z * wb[1];
-          o[i][3] = o[i][3] * wa[1] + v.w * wb[1];
-        }
-      }
-      if (half > 1) named_bar(1, kConsumers * 32);
-    }
-
-    // -------------------------------------------------------------- results
-    auto finish = [&](int rw_, const float (&mm)[2], const float (&ll)[2], int i, const float4 &a,
-                      const float4 &b2) {
-      // output tiles i and i + 1 of row group rw_, this lane's share
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = row0 + rw_ * 16 + g + 8 * r, node = row / group;
-        if (row >= p.rows) continue;
-        const int h = head * group + row % group;
-        const bool empty = node >= at.count || mm[r] == -INFINITY;
-        const float inv = empty ? 0.f : p.v_scale / ll[r];
-        const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
-        uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
-        float v0 = r ? a.z : a.x, v1 = r ? a.w : a.y, v2 = r ? b2.z : b2.x, v3 = r ? b2.w : b2.y;
-        if (empty) {
-          v0 = v1 = v2 = v3 = 0.f;
-        } else {
-          v0 *= inv;
-          v1 *= inv;
-          v2 *= inv;
-          v3 *= inv;
-        }
-        const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
-        if constexpr (kType == kE4M3) {
-          const int col = 8 * i + 4 * t;                 // i is even
-          if (col < p.d)
-            *reinterpret_cast<uint2 *>(out + col) =
-                make_uint2(pack_out(v0, v2, f16), pack_out(v1, v3, f16));
-        } else {
-          const int c0 = 8 * i + 2 * t, c1 = c0 + 8;
-          if (c0 < p.d) *reinterpret_cast<uint32_t *>(out + c0) = pack_out(v0, v1, f16);
-          if (c1 < p.d) *reinterpret_cast<uint32_t *>(out + c1) = pack_out(v2, v3, f16);
-        }
-        if (p.lse && i == 0 && t == 0)
-          p.lse[at_row] = empty ? -INFINITY : (mm[r] - kLift<kType> + log2f(ll[r])) * kLn2;
-      }
-    };
-    const bool whole = at.t0 == 0 && at.t1 == at.tiles;
-    if (whole) {
-      if (kg == 0) {
-#pragma unroll
-        for (int i = 0; i < L::NT; i += 2)
-          finish(rw, m, l, i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]),
-                 make_float4(o[i + 1][0], o[i + 1][1], o[i + 1][2], o[i + 1][3]));
-      }
+        for (int e = 0; e < 4; ++e) res[i][e] = o[i][e];
     } else {
-      const int first = at.block_of(at.unit0), final = at.block_of(at.unit0 + at.tiles - 1);
-      auto slot_of = [&](int block) {
-        return p.partial + (int64_t(block) * 2 + (block == first ? 1 : 0)) * L::kPartial;
-      };
-      if (kg == 0) {
-        float *mine = slot_of(blockIdx.x);
-        float4 *to = reinterpret_cast<float4 *>(mine) + rw * (L::NT * 32);
-#pragma unroll
-        for (int i = 0; i < L::NT; ++i)
-          to[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        if (t == 0) {
-          float2 *st = reinterpret_cast<float2 *>(mine + RW * L::NT * 32 * 4) + rw * 16;
-          st[g] = make_float2(m[0], l[0]);
-          st[g + 8] = make_float2(m[1], l[1]);
-        }
-        __threadfence();
+      float4 *box = reinterpret_cast<float4 *>(scratch);
+      constexpr int NP = NT / L::kPasses;                // tiles of a pass
+      if (t == 0) {
+        state[warp * 16 + g] = make_float2(m[0], l[0]);
+        state[warp * 16 + g + 8] = make_float2(m[1], l[1]);
       }
+      float w[L::KW][2];
+#pragma unroll
+      for (int pass = 0; pass < L::kPasses; ++pass) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const auto &x = o[pass * NP + i];
+          box[(warp * NP + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        named_bar(1, kConsumers * 32);
+        if (pass == 0) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float2 st[L::KW];
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < L::KW; ++k) {
+              st[k] = state[(rw * L::KW + k) * 16 + g + 8 * r];
+              top = fmaxf(top, st[k].x);
+            }
+#pragma unroll
+            for (int k = 0; k < L::KW; ++k) {
+              w[k][r] = st[k].x == -INFINITY ? 0.f : ex2(st[k].x - top);
+              sum += st[k].y * w[k][r];
+            }
+            mj[r] = top;
+            lj[r] = sum;
+          }
+        }
+        constexpr int TP = TPW / L::kPasses;             // this warp's tiles of a pass
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+          float (&y)[4] = res[pass * TP + i];
+          y[0] = y[1] = y[2] = y[3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < L::KW; ++k) {
+            const float4 v = box[((rw * L::KW + k) * NP + kg * TP + i) * 32 + lane];
+            y[0] += v.x * w[k][0];
+            y[1] += v.y * w[k][0];
+            y[2] += v.z * w[k][1];
+            y[3] += v.w * w[k][1];
+          }
+        }
+        if (pass + 1 < L::kPasses) named_bar(1, kConsumers * 32);
+      }
+    }
+    // tile of the head's columns that res[i] is
+    auto tile_of = [&](int i) {
+      constexpr int TP = TPW / L::kPasses;
+      return (i / TP) * (NT / L::kPasses) + kg * TP + i % TP;
+    };
+    bool done = whole;
+    if (!whole) {
+      // Of a unit that several blocks share, the block that arrives last joins
+      // the blocks' results, in their order.
+      float *mine = place(blockIdx.x);
+      float4 *to = reinterpret_cast<float4 *>(mine) + rw * (NT * 32) + lane;
+#pragma unroll
+      for (int i = 0; i < TPW; ++i)
+        to[tile_of(i) * 32] = make_float4(res[i][0], res[i][1], res[i][2], res[i][3]);
+      if (kg == 0 && t == 0) {
+        float2 *st = reinterpret_cast<float2 *>(mine + RW * NT * 32 * 4) + rw * 16;
+        st[g] = make_float2(mj[0], lj[0]);
+        st[g + 8] = make_float2(mj[1], lj[1]);
+      }
+      __threadfence();
       named_bar(1, kConsumers * 32);
       if (tid == 0) {
         const uint32_t before = atomicAdd(p.arrived + first, 1u);
@@ -822,39 +836,74 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __threadfence();
       }
       named_bar(1, kConsumers * 32);
-      if (*last) {
-        __threadfence();
-        // pairs of output tiles are shared out over the warps
-        for (int w = warp; w < RW * L::NT / 2; w += kConsumers) {
-          const int rw_ = w / (L::NT / 2), i = w % (L::NT / 2) * 2;
-          float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};
-          float4 a = make_float4(0, 0, 0, 0), b2 = a;
-          for (int blk = first; blk <= final; ++blk) {
-            const float *part = slot_of(blk);
-            const float2 *st = reinterpret_cast<const float2 *>(part + RW * L::NT * 32 * 4) + rw_ * 16;
-            const float4 *from = reinterpret_cast<const float4 *>(part) + (rw_ * L::NT + i) * 32 + lane;
-            const float2 s[2] = {__ldcg(st + g), __ldcg(st + g + 8)};
-            const float4 va = __ldcg(from), vb = __ldcg(from + 32);
-            float wa[2], wb[2];
+      done = *last;
+      if (done) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float m2 = fmaxf(mm[r], s[r].x);
-              wa[r] = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - m2);
-              wb[r] = s[r].x == -INFINITY ? 0.f : ex2(s[r].x - m2);
-              ll[r] = ll[r] * wa[r] + s[r].y * wb[r];
-              mm[r] = m2;
-            }
-            a.x = a.x * wa[0] + va.x * wb[0];
-            a.y = a.y * wa[0] + va.y * wb[0];
-            a.z = a.z * wa[1] + va.z * wb[1];
-            a.w = a.w * wa[1] + va.w * wb[1];
-            b2.x = b2.x * wa[0] + vb.x * wb[0];
-            b2.y = b2.y * wa[0] + vb.y * wb[0];
-            b2.z = b2.z * wa[1] + vb.z * wb[1];
-            b2.w = b2.w * wa[1] + vb.w * wb[1];
+        for (int i = 0; i < TPW; ++i) res[i][0] = res[i][1] = res[i][2] = res[i][3] = 0.f;
+        mj[0] = mj[1] = -INFINITY;
+        lj[0] = lj[1] = 0.f;
+        constexpr int kAhead = TPW <= 2 ? 8 : TPW <= 4 ? 4 : 2;   // blocks fetched at a time
+#pragma unroll 1
+        for (int blk = first; blk <= final; blk += kAhead) {
+          float4 v[kAhead][TPW];
+          float2 st[kAhead][2];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const float *part = place(min(blk + k, final));
+            const float2 *sp = reinterpret_cast<const float2 *>(part + RW * NT * 32 * 4) + rw * 16;
+            st[k][0] = __ldcg(sp + g);
+            st[k][1] = __ldcg(sp + g + 8);
+            const float4 *from = reinterpret_cast<const float4 *>(part) + rw * (NT * 32) + lane;
+#pragma unroll
+            for (int i = 0; i < TPW; ++i) v[k][i] = __ldcg(from + tile_of(i) * 32);
           }
-          finish(rw_, mm, ll, i, a, b2);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (blk + k > final) break;
+            merge<TPW>(res, mj, lj, st[k], [&](int i) { return v[k][i]; });
+          }
         }
+      }
+    }
+
+    // -------------------------------------------------------------- results
+    if (done) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + rw * 16 + g + 8 * r, node = row / group;
+        if (row >= p.rows) continue;
+        const int h = head * group + row % group;
+        // NaN is not nothing
+        const bool empty = node >= at.count || (mj[r] == -INFINITY && lj[r] == 0.f);
+        const float inv = empty ? 0.f : p.v_scale / lj[r];
+        const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
+        const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) {
+          const int nt = tile_of(i);
+          const float v0 = empty ? 0.f : res[i][2 * r] * inv, v1 = empty ? 0.f : res[i][2 * r + 1] * inv;
+          if constexpr (kType == kE4M3) {
+            // columns 4t + 2e of even tiles, 4t + 2e + 1 of odd ones: an even
+            // tile's lane stores for both where it has both
+            if constexpr (TPW >= 2) {
+              if (i % 2 == 0 && 8 * nt < p.d) {
+                const float u0 = empty ? 0.f : res[i + 1][2 * r] * inv;
+                const float u1 = empty ? 0.f : res[i + 1][2 * r + 1] * inv;
+                *reinterpret_cast<uint2 *>(out + 8 * nt + 4 * t) =
+                    make_uint2(pack_out(v0, u0, f16), pack_out(v1, u1, f16));
+              }
+            } else if (8 * (nt & ~1) < p.d) {
+              const uint32_t both = pack_out(v0, v1, f16);
+              out[out_col<kType>(nt, t, 0)] = uint16_t(both);
+              out[out_col<kType>(nt, t, 1)] = uint16_t(both >> 16);
+            }
+          } else if (8 * nt < p.d) {
+            *reinterpret_cast<uint32_t *>(out + 8 * nt + 2 * t) = pack_out(v0, v1, f16);
+          }
+        }
+        if (p.lse && t == 0 && kg == 0)
+          p.lse[at_row] = empty ? -INFINITY : (mj[r] - kLift<kType> + log2f(lj[r])) * kLn2;
       }
     }
     named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
