@@ -87,7 +87,10 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   p.rows = rows;
   p.blocks = (rows + v.rows - 1) / v.rows;
   p.box = cache_box_tokens(cache->page_size);
-  p.least = std::max(1, 131072 / (2 * kTile * p.d * (type == kE4M3 ? 1 : 2)));
+  // a unit costs about 3 us beside its tiles, which come at 45 GB/s a block
+  const int tile_bytes = 2 * kTile * p.d * (type == kE4M3 ? 1 : 2);
+  p.least = std::max(1, 131072 / tile_bytes);
+  p.extra = std::max(1, 131072 / tile_bytes);
   p.c = d->scale * cache->k_scale * kLog2e;
   p.v_scale = cache->v_scale;
   // no more blocks than there can be tiles

@@ -71,7 +71,7 @@ struct AttnParams {
   float *partial;                   // [grid][2] of (rows x (head_dim padded) + 2 rows)
   int batch, n, hq, hkv, d, q_f16;
   int rows, blocks;                 // rows that share a cache head, row blocks of a unit
-  int box, least;                   // tokens of a TMA box, tiles of a run at least
+  int box, least, extra;            // tokens of a TMA box; tiles: of a run at least, a unit costs
   float c, v_scale;                 // scale * k_scale * log2 e
 };
 
@@ -79,9 +79,13 @@ struct AttnParams {
 template <int kType, int DC, int RW>
 struct Cfg {
   static constexpr int kSize = kType == kE4M3 ? 1 : 2;
-  static constexpr int kRow = 64 * kSize;                // bytes of a key's 64-element chunk
+  // a key's row comes in chunks of 128 bytes (64 for E4M3 heads of 64): half
+  // as many of twice the size move an E4M3 tile faster
+  static constexpr int kRow = kType == kE4M3 && DC == 1 ? 64 : 128;
+  static constexpr int kElems = kRow / kSize;
+  static constexpr int kChunks = DC * 64 / kElems;
   static constexpr int kChunk = kTile * kRow;
-  static constexpr int kSlot = DC * kChunk;              // one tile of K or of V
+  static constexpr int kSlot = kChunks * kChunk;         // one tile of K or of V
   static constexpr int D = DC * 64;
   static constexpr int kRows = 16 * RW;
   // keys of a step: 32 halve the maxima, shuffles and waits of a key against
@@ -164,11 +168,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ uint32_t pack_out(float a, float b, bool f16) {
   return f16 ? pack2<kF16>(a, b) : pack2<kBf16>(a, b);
 }
-// Whether a half of a 16-bit pair is infinite or NaN.
+// Nonzero where one of the cache's elements in a word is infinite or NaN: x 0
+// is a NaN then, else a zero; of E4M3 codes only 0x7F and 0xFF are.
 template <int kType>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  constexpr uint32_t e = kType == kBf16 ? 0x7F80u : 0x7C00u;
-  return (w & e) == e || ((w >> 16) & e) == e;
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+  uint32_t y;
+  if constexpr (kType == kE4M3) {
+    y = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return y;
+  } else if constexpr (kType == kBf16) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %2;" : "=r"(y) : "r"(w), "r"(0u));
+  } else {
+    asm("fma.rn.f16x2 %0, %1, %2, %2;" : "=r"(y) : "r"(w), "r"(0u));
+  }
+  return y & 0x7FFF7FFFu;
 }
 template <int kType>
 __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
@@ -176,11 +189,14 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
   return ((w & e) == e ? 0u : 0xFFFFu) | (((w >> 16) & e) == e ? 0u : 0xFFFF0000u);
 }
 
-// Byte offset of 16-byte chunk `ch` of key `key` inside a 64-element chunk:
-// TMA's 128-byte (16-bit types) or 64-byte (E4M3) swizzle.
-template <int kSize>
-__device__ __forceinline__ uint32_t swz(uint32_t key, uint32_t ch) {
-  return kSize == 2 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4);
+// Byte offset in a slot of 16-byte piece `c` + `more` of key `key` (`more`
+// stays in the chunk of `c`): TMA's 128-byte or 64-byte swizzle.
+template <typename L>
+__device__ __forceinline__ uint32_t spot(uint32_t key, uint32_t c, uint32_t more = 0) {
+  constexpr uint32_t N = L::kRow / 16;
+  const uint32_t in = c % N + more;
+  return c / N * L::kChunk +
+         (N == 8 ? key * 128 + ((in ^ (key & 7)) << 4) : key * 64 + ((in ^ ((key >> 1) & 3)) << 4));
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int x, int token,
@@ -209,12 +225,15 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 
 // ------------------------------------------------------------------ the line
-// Where a block is on the line of tiles: unit u (= head * blocks + row block)
-// of sequence b, its tiles, and those of them that are the block's.
+// Where a block is on the line: unit u (= head * blocks + row block) of
+// sequence b, and the unit's tiles [t0, t1) that are the block's.  A unit's
+// place on the line is `extra` + its tiles long, as beginning and joining a
+// unit costs about as much as `extra` tiles: without that, blocks with a
+// second unit ended 7 us after the others (39 us in all).
 struct Line {
-  int64_t total, at, end, unit0;    // tiles in all, the block's run, the unit's first
-  int64_t runs;                     // blocks that have a run: no more than tiles
-  int b, u, units, tiles, t0, t1;   // units per sequence; this unit's tiles [t0, t1)
+  int64_t total, end, unit0;        // the line's length, the run's end, where the unit begins
+  int64_t runs;                     // blocks that have a run
+  int b, u, units, extra, tiles, t0, t1;
   int len, count;
 
   __device__ __forceinline__ static int used(const AttnParams &p, int b, int &len) {
@@ -232,23 +251,33 @@ struct Line {
   __device__ void init(const AttnParams &p, int units_) {
     const int lane = threadIdx.x % 32;
     units = units_;
-    int64_t sum = 0;
-    for (int i = lane; i < p.batch; i += 32) sum += tiles_of(p, i);
+    extra = p.extra;
+    auto long_of = [&](int i) { return i < p.batch ? tiles_of(p, i) + extra : 0; };
+    const int own = long_of(lane);              // of the first 32 sequences
+    int64_t sum = own;
+    for (int i = 32 + lane; i < p.batch; i += 32) sum += long_of(i);
 #pragma unroll
     for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
     total = sum * units;
     // a unit is cut into runs of at least 128 KB: shorter ones cost more in the
     // joining than they save
-    runs = min(int64_t(gridDim.x), max(total / p.least, int64_t(p.batch) * units));
+    const int64_t wanted = total < int64_t(1) << 32 ? uint32_t(total) / uint32_t(p.least) : total / p.least;
+    runs = min(int64_t(gridDim.x), max(wanted, int64_t(p.batch) * units));
     const int64_t mine = min(int64_t(blockIdx.x), runs);
-    at = total * mine / runs;
-    end = mine < runs ? total * (mine + 1) / runs : at;
-    // the sequence that holds tile `at`
+    int64_t at;
+    if (total * runs < int64_t(1) << 32) {      // 64-bit divisions are slow
+      at = uint32_t(total * mine) / uint32_t(runs);
+      end = mine < runs ? uint32_t(total * (mine + 1)) / uint32_t(runs) : at;
+    } else {
+      at = total * mine / runs;
+      end = mine < runs ? total * (mine + 1) / runs : at;
+    }
+    // the sequence that holds place `at`
     int64_t before = 0;
+    int length = 1;
     b = 0;
-    tiles = 1;
     for (int i0 = 0; i0 < p.batch; i0 += 32) {
-      const int each = i0 + lane < p.batch ? tiles_of(p, i0 + lane) : 0;
+      const int each = i0 ? long_of(i0 + lane) : own;
       int64_t run = each;
 #pragma unroll
       for (int w = 1; w < 32; w *= 2) {
@@ -258,40 +287,42 @@ struct Line {
       const uint32_t over = __ballot_sync(~0u, (before + run) * units > at);
       if (over) {
         const int f = __ffs(over) - 1;
-        tiles = __shfl_sync(~0u, each, f);
+        length = __shfl_sync(~0u, each, f);
         b = i0 + f;
-        before += __shfl_sync(~0u, run, f) - tiles;
+        before += __shfl_sync(~0u, run, f) - length;
         break;
       }
       before += __shfl_sync(~0u, run, 31);
     }
     const int64_t in = at - before * units;
-    u = int(in / tiles);
-    t0 = int(in % tiles);
-    unit0 = at - t0;
+    u = in < int64_t(1) << 32 ? int(uint32_t(in) / uint32_t(length)) : int(in / length);
+    tiles = length - extra;
+    const int off = int(in - int64_t(u) * length);
+    unit0 = at - off;
+    t0 = max(0, off - extra);
     fill(p);
   }
   __device__ __forceinline__ void fill(const AttnParams &p) {
-    t1 = int(min(int64_t(tiles), t0 + (end - at)));
-    if (at < end) count = used(p, b, len);
+    t1 = int(min(int64_t(tiles), end - unit0 - extra));
+    if (t0 < t1) count = used(p, b, len);
   }
-  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ bool valid() const { return t0 < t1; }
   __device__ __forceinline__ void next(const AttnParams &p) {
-    at += t1 - t0;
-    unit0 = at;
+    unit0 += tiles + extra;
     t0 = 0;
-    if (at < end) {
-      if (++u == units) {
-        u = 0;
-        ++b;
-        tiles = tiles_of(p, b);
-      }
+    t1 = 0;
+    if (unit0 + extra >= end) return;
+    if (++u == units) {
+      u = 0;
+      ++b;
+      tiles = tiles_of(p, b);
     }
     fill(p);
   }
-  // The block that holds tile x of the line.
-  __device__ __forceinline__ int block_of(int64_t x) const {
-    return int(((x + 1) * runs + total - 1) / total) - 1;
+  // The block that holds tile t of the unit.
+  __device__ __forceinline__ int block_of(int t) const {
+    const int64_t x = (unit0 + extra + t + 1) * runs + total - 1;
+    return (x < int64_t(1) << 32 ? int(uint32_t(x) / uint32_t(total)) : int(x / total)) - 1;
   }
 };
 
@@ -345,6 +376,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + L::kMaxSlots);
   if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     *failed = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -364,7 +397,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // The page numbers of 32 boxes are fetched at a time, one a lane, and the
     // next 32 while those are copied: a fetch for each tile cost 1200 clocks
     // a tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
-    const int boxes = kTile / p.box, copies = boxes * DC;
+    const int boxes = kTile / p.box, copies = boxes * L::kChunks;
     const int page_boxes = p.cache.page_size / p.box;
     const uint32_t ring0 = smem_addr(ring);
     int s = kv;
@@ -384,9 +417,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           pages = ahead;
           ahead = fetch(++window + 1);
         }
-        // lane = box * DC + chunk; a box without a page, or past the end,
+        // lane = box * chunks + chunk; a box without a page, or past the end,
         // is copied from outside the tensor: zeros, and no traffic
-        const int box = lane / DC, chunk = lane % DC;
+        const int box = lane / L::kChunks, chunk = lane % L::kChunks;
         const int number = t * boxes + box;
         int page = __shfl_sync(~0u, pages, number % 32);
         const bool ok = lane < copies && page >= 0 && page < p.cache.pages;
@@ -404,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         if (lane < copies)
           tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow,
-                 kv ? &vmap : &kmap, chunk * 64, token, head, page, bar);
+                 kv ? &vmap : &kmap, chunk * L::kElems, token, head, page, bar);
         if ((s += 2) >= NS) {
           s = kv;
           par ^= 1;
@@ -558,7 +591,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               for (int h = 0; h < L::SK / 16; ++h) {
                 uint32_t b[4];
                 const uint32_t key = key0 + h * 16 + (lane & 15);
-                ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<1>(key, (ks & 3) + (lane >> 4)));
+                ldsm4(b, kb + spot<L>(key, ks, lane >> 4));
                 mma<kType>(sc[0][2 * h], a, e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
                 mma<kType>(sc[0][2 * h + 1], a, e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
                 mma<kType>(sc[kSets - 1][2 * h], a2, e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
@@ -570,7 +603,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int h = 0; h < L::SK / 16; ++h) {
               uint32_t b[4];
               const uint32_t key = key0 + h * 16 + (lane & 7) + ((lane >> 4) << 3);
-              ldsm4(b, kb + (ks >> 2) * L::kChunk + swz<2>(key, (ks & 3) * 2 + ((lane >> 3) & 1)));
+              ldsm4(b, kb + spot<L>(key, 2 * ks, (lane >> 3) & 1));
               mma<kType>(acc[2 * h], a, b[0], b[1]);
               mma<kType>(acc[2 * h + 1], a, b[2], b[3]);
             }
@@ -587,16 +620,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             x[nt][e] = (kSets == 2 ? sc[0][nt][e] + sc[kSets - 1][nt][e] : sc[0][nt][e]) * cr[e >> 1];
+        // bit k of sees[r]: row r attends to key s0 + k
+        uint32_t sees[2] = {~0u, ~0u};
         if (!open) {
+          const int rel = s0 - at.len;                   // of the first key to the drafted ones
+          uint32_t exist = 0;
 #pragma unroll
-          for (int nt = 0; nt < SN; ++nt)
+          for (int h = 0; h < L::SK / 16; ++h) exist |= (there >> h & 1) ? 0xFFFFu << (16 * h) : 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int rel = s0 + nt * 8 + 2 * t + (e & 1) - at.len;
-              const bool see = (there >> (nt / 2) & 1) &&
-                               (rel < 0 || (rel < 64 && (word[e >> 1] >> (rel & 63) & 1)));
-              if (!see) x[nt][e] = -INFINITY;
-            }
+          for (int r = 0; r < 2; ++r) {
+            uint32_t w = rel <= -32 ? ~0u
+                       : rel < 0   ? (uint32_t(word[r]) << -rel) | ((1u << -rel) - 1)
+                       : rel < 64  ? uint32_t(word[r] >> rel) : 0u;
+            sees[r] = w & exist;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t w = sees[r] >> (2 * t);
+#pragma unroll
+            for (int nt = 0; nt < SN; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!(w >> (8 * nt + e) & 1)) x[nt][2 * r + e] = -INFINITY;
+          }
         }
         float m2[2];
 #pragma unroll
@@ -640,7 +686,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ----------------------------------------------------------- p . v
         if (j == 0) wait_phase(full0 + 8 * sv, (iv / NS) & 1, failed, p.error);
         const uint32_t vb = ring0 + sv * L::kSlot;
-        if (open) {
+        // Keys that some row does not attend to: a weight of 0 does not keep an
+        // infinity or NaN of v out of the product, so v is looked through first
+        bool plain = true;
+        if (!open) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int h = 0; h < L::SK / 16; ++h)
+#pragma unroll
+            for (int c = 0; c < L::kChunks * (L::kRow / 16); c += 2) {
+              uint32_t b[4];
+              ldsm4(b, vb + spot<L>(key0 + h * 16 + (lane & 15), c, lane >> 4));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= nonfinite_bits<kType>(b[e]);
+            }
+          plain = !__any_sync(~0u, odd != 0);
+        }
+        if (plain) {
 #pragma unroll
           for (int h = 0; h < L::SK / 16; ++h) {
             const uint32_t key = key0 + h * 16 + (lane & 15);
@@ -650,7 +712,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if constexpr (kType == kE4M3) {
                 // 16 columns: matrices (keys 0-7), (keys 8-15) of two blocks of 16
                 if ((i & 1) == 0) {
-                  ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key, (i & 3) + (lane >> 4)));
+                  ldsm4t(b, vb + spot<L>(key, i, lane >> 4));
 #pragma unroll
                   for (int k = 0; k < 2; ++k) {
                     const uint32_t w0 = prmt(b[2 * k], 0, 0x3120), w1 = prmt(b[2 * k + 1], 0, 0x3120);
@@ -659,17 +721,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   }
                 }
               } else {
-                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key, (i & 3) * 2 + (lane >> 4)));
+                ldsm4t(b, vb + spot<L>(key, 2 * i, lane >> 4));
                 mma<kType>(o[2 * i], pf[h], b[0], b[1]);
                 mma<kType>(o[2 * i + 1], pf[h], b[2], b[3]);
               }
             }
           }
         } else {
-          // Keys that some row does not attend to.  A weight of 0 does not
-          // keep an infinity or NaN of v out of the product, so those are
-          // left out of it and added to the rows that do attend.
-          uint32_t odd = 0;
+          // ... and what is not finite is left out of the product and added to
+          // the rows that do attend to it
 #pragma unroll 1
           for (int h = 0; h < L::SK / 16; ++h) {
             uint32_t pp[4];
@@ -680,53 +740,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int i = 0; i < L::NT / 2; ++i) {
               uint32_t b[4];
               if constexpr (kType == kE4M3) {
-                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<1>(key, i & 3));
+                ldsm4t(b, vb + spot<L>(key, i));
                 const uint32_t w0 = prmt(b[0], 0, 0x3120), w1 = prmt(b[1], 0, 0x3120);
                 b[0] = e4m3_f16(w0);
                 b[1] = e4m3_f16(w1);
                 b[2] = e4m3_f16(w0 >> 16);
                 b[3] = e4m3_f16(w1 >> 16);
               } else {
-                ldsm4t(b, vb + (i >> 2) * L::kChunk + swz<2>(key, (i & 3) * 2 + (lane >> 4)));
+                ldsm4t(b, vb + spot<L>(key, 2 * i, lane >> 4));
               }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t keep = finite_mask<kType>(b[e]);
-                odd |= ~keep;
-                b[e] &= keep;
-              }
+              for (int e = 0; e < 4; ++e) b[e] &= finite_mask<kType>(b[e]);
               mma<kType>(o[2 * i], pp, b[0], b[1]);
               mma<kType>(o[2 * i + 1], pp, b[2], b[3]);
             }
           }
-          if (__any_sync(~0u, odd != 0)) {
 #pragma unroll 1
-            for (int k = 0; k < L::SK; ++k) {
-              const int rel = s0 + k - at.len;
-              const uint32_t key = key0 + k;
+          for (int k = 0; k < L::SK; ++k) {
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                if (!(there >> (k / 16) & 1) || !(rel < 0 || (rel < 64 && (word[r] >> (rel & 63) & 1))))
-                  continue;
+            for (int r = 0; r < 2; ++r) {
+              if (!(sees[r] >> k & 1)) continue;
 #pragma unroll
-                for (int i = 0; i < L::NT; ++i)
+              for (int i = 0; i < L::NT; ++i)
 #pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int col = out_col<kType>(i, t, e);
-                    const uint8_t *chunk = ring + sv * L::kSlot + (col / 64) * L::kChunk;
-                    float v;
-                    if constexpr (kType == kE4M3) {
-                      const uint32_t c = chunk[swz<1>(key, (col % 64) / 16) + col % 16];
-                      v = __half2float(__ushort_as_half(uint16_t(e4m3_f16(c))));
-                    } else {
-                      const uint16_t c = *reinterpret_cast<const uint16_t *>(
-                          chunk + swz<2>(key, (col % 64) / 8) + (col % 8) * 2);
-                      v = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(c))
-                                         : __half2float(__ushort_as_half(c));
-                    }
-                    if (!(fabsf(v) < INFINITY)) o[i][2 * r + e] += v;
+                for (int e = 0; e < 2; ++e) {
+                  const int col = out_col<kType>(i, t, e);
+                  const uint8_t *at16 = ring + sv * L::kSlot + spot<L>(key0 + k, col * L::kSize / 16);
+                  float v;
+                  if constexpr (kType == kE4M3) {
+                    v = __half2float(__ushort_as_half(uint16_t(e4m3_f16(at16[col % 16]))));
+                  } else {
+                    const uint16_t c = *reinterpret_cast<const uint16_t *>(at16 + (col % 8) * 2);
+                    v = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(c))
+                                       : __half2float(__ushort_as_half(c));
                   }
-              }
+                  if (!(fabsf(v) < INFINITY)) o[i][2 * r + e] += v;
+                }
             }
           }
         }
@@ -736,7 +785,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 
     // ------------------------------------- join the key warps, then the blocks
-    const int first = at.block_of(at.unit0), final = at.block_of(at.unit0 + at.tiles - 1);
+    const int first = at.block_of(0), final = at.block_of(at.tiles - 1);
     const bool whole = first == final;
     // a block's partial result: its unit's first block has it in its second place
     auto place = [&](int block) {

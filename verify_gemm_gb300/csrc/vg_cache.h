@@ -10,9 +10,12 @@ namespace vg {
 // then a mark over the fields that were checked.
 constexpr int kCacheMapWords = 16;            // 128 bytes each
 constexpr int kCacheMark = 32;                // opaque[32]
-// Boxes of the maps: 64 elements (128 bytes; 64 bytes of E4M3) of the
-// largest power of two of tokens, at most 64, that divides the page.
-constexpr int kCacheBoxElems = 64;
+// Boxes of the maps: 128 bytes of a head (64 bytes of E4M3 heads up to 64
+// elements) of the largest power of two of tokens, at most 64, that divides
+// the page.
+inline int cache_box_bytes(const vg_kv_cache &c) {
+  return c.type == VG_TYPE_E4M3 && c.head_dim <= 64 ? 64 : 128;
+}
 inline int cache_box_tokens(int page_size) {
   int t = 16;
   while (t < 64 && page_size % (2 * t) == 0) t *= 2;

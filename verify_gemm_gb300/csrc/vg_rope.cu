@@ -280,12 +280,12 @@ bool map_cache(CUtensorMap *map, const vg_kv_cache &c, void *base, const int64_t
                               cuuint64_t(c.pages)};
   const cuuint64_t strides[3] = {cuuint64_t(stride[1]) * size, cuuint64_t(stride[2]) * size,
                                  cuuint64_t(stride[0]) * size};
-  const cuuint32_t box[4] = {cuuint32_t(kCacheBoxElems), cuuint32_t(cache_box_tokens(c.page_size)),
+  const cuuint32_t box[4] = {cuuint32_t(cache_box_bytes(c)) / cuuint32_t(size), cuuint32_t(cache_box_tokens(c.page_size)),
                              1u, 1u};
   const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
   return fn(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, dims,
             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            cache_box_bytes(c) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
