@@ -19,8 +19,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libvgemm.so")
 SOURCES = ["vg_api.cu", "vg_pack.cu", "vg_gemv.cu", "vg_noalloc.cu", "vg_probe.cu", "vg_rope.cu",
            "vg_attention.cu", "vg_attention_bf16.cu", "vg_attention_f16.cu", "vg_attention_e4m3.cu",
-           "vg_sample.cu"]
-HEADERS = ["vg_device.cuh", "vg_internal.h", "vg_cache.h", "vg_attention.cuh"]
+           "vg_attention_wide.cu", "vg_sample.cu"]
+HEADERS = ["vg_device.cuh", "vg_internal.h", "vg_cache.h", "vg_attention.cuh", "vg_attention_wide.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-prec-div=true",
          "-prec-sqrt=true", "-ftz=false", "-fmad=true", f"-I{os.path.join(ROOT, 'include')}"]

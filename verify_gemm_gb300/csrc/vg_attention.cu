@@ -10,11 +10,15 @@ namespace {
 
 using namespace attn;
 
+// tcgen05 where mma.sync would set the pace.
+bool is_wide(int type, int d, int rows) { return type != kE4M3 && d <= 128 && rows > 32; }
+
 // Row groups: the fewest that hold the rows of a head, so that as many warps
 // as can share out the keys; above 128 rows, blocks of 128.
 int row_index(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
 const Variant &pick(int type, int d, int rows) {
+  if (is_wide(type, d, rows)) return kWide[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
   const Variants &of = type == kBf16 ? kVariantsBf16 : type == kF16 ? kVariantsF16 : kVariantsE4M3;
   return of[d <= 64 ? 0 : d <= 128 ? 1 : 2][row_index(rows)];
 }

@@ -326,6 +326,77 @@ struct Line {
   }
 };
 
+// One warp copies the K (kv = 0) or V tiles of the block's run into the ring
+// of NS slots, K and V in turn, and leaves for each tile a bit for every 16
+// keys that there are in page_ok[tile of the run % 16].
+// The page numbers of 32 boxes are fetched at a time, one a lane, and the
+// next 32 while those are copied: a fetch for each tile cost 1200 clocks a
+// tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
+template <typename L, int NS>
+__device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map, int kv,
+                           uint32_t ring0, uint32_t full0, uint32_t empty0, uint32_t *page_ok,
+                           volatile int *failed) {
+  const int lane = threadIdx.x % 32;
+  const int boxes = kTile / p.box, copies = boxes * L::kChunks;
+  const int page_boxes = p.cache.page_size / p.box;
+  int s = kv, n = 0;
+  uint32_t par = 1;                                      // slots start empty
+  for (; at.valid(); at.next(p)) {
+    const int head = at.u / p.blocks;
+    const int total = at.len + at.count;
+    const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
+    auto fetch = [&](int window) {
+      const int box = window * 32 + lane, i = box / page_boxes;
+      return box * p.box < total && i < p.cache.max_pages ? table[i] : -1;
+    };
+    int window = at.t0 * boxes / 32;
+    int pages = fetch(window), ahead = fetch(window + 1);
+    for (int t = at.t0; t < at.t1; ++t, ++n) {
+      if (t * boxes / 32 != window) {
+        pages = ahead;
+        ahead = fetch(++window + 1);
+      }
+      // lane = box * chunks + chunk; a box without a page, or past the end,
+      // is copied from outside the tensor: zeros, and no traffic
+      const int box = lane / L::kChunks, chunk = lane % L::kChunks;
+      const int number = t * boxes + box;
+      int page = __shfl_sync(~0u, pages, number % 32);
+      const bool ok = lane < copies && page >= 0 && page < p.cache.pages;
+      if (!ok) page = int(p.cache.pages);
+      const int token = ok ? number % page_boxes * p.box : 0;
+      uint32_t bits = ok ? ((1u << (p.box / 16)) - 1) << (box * (p.box / 16)) : 0;
+      bits = __reduce_or_sync(~0u, bits);
+      wait_phase(empty0 + 8 * s, par, failed, p.error);
+      const uint32_t bar = full0 + 8 * s;
+      if (lane == 0) {
+        if (kv == 0) page_ok[n % 16] = bits;
+        mbar_arrive_expect_tx(bar, L::kSlot);
+      }
+      __syncwarp();
+      if (lane < copies)
+        tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow, map,
+               chunk * L::kElems, token, head, page, bar);
+      if ((s += 2) >= NS) {
+        s = kv;
+        par ^= 1;
+      }
+    }
+  }
+  // every copy has been read, so has landed, before the block may end; after
+  // a failure they get 10 ms to land
+  for (int k = 0; k < NS / 2; ++k) {
+    wait_phase(empty0 + 8 * s, par, failed, p.error);
+    if ((s += 2) >= NS) {
+      s = kv;
+      par ^= 1;
+    }
+  }
+  if (*failed) {
+    const uint64_t end = globaltimer() + 10000000;
+    while (globaltimer() < end) __nanosleep(1000);
+  }
+}
+
 // Joins another result of the same rows, o2 (tile i), (m2, l2), to o, m, l.
 template <int NT, typename F>
 __device__ __forceinline__ void merge(float (&o)[NT][4], float (&m)[2], float (&l)[2],
@@ -394,69 +465,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     const int kv = warp - kConsumers;                    // one warp copies K, one V
     if (kv > 1) return;
-    // The page numbers of 32 boxes are fetched at a time, one a lane, and the
-    // next 32 while those are copied: a fetch for each tile cost 1200 clocks
-    // a tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
-    const int boxes = kTile / p.box, copies = boxes * L::kChunks;
-    const int page_boxes = p.cache.page_size / p.box;
-    const uint32_t ring0 = smem_addr(ring);
-    int s = kv;
-    uint32_t par = 1;                                    // slots start empty
-    for (; at.valid(); at.next(p)) {
-      const int head = at.u / p.blocks;
-      const int total = at.len + at.count;
-      const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
-      auto fetch = [&](int window) {
-        const int box = window * 32 + lane, i = box / page_boxes;
-        return box * p.box < total && i < p.cache.max_pages ? table[i] : -1;
-      };
-      int window = at.t0 * boxes / 32;
-      int pages = fetch(window), ahead = fetch(window + 1);
-      for (int t = at.t0; t < at.t1; ++t) {
-        if (t * boxes / 32 != window) {
-          pages = ahead;
-          ahead = fetch(++window + 1);
-        }
-        // lane = box * chunks + chunk; a box without a page, or past the end,
-        // is copied from outside the tensor: zeros, and no traffic
-        const int box = lane / L::kChunks, chunk = lane % L::kChunks;
-        const int number = t * boxes + box;
-        int page = __shfl_sync(~0u, pages, number % 32);
-        const bool ok = lane < copies && page >= 0 && page < p.cache.pages;
-        if (!ok) page = int(p.cache.pages);
-        const int token = ok ? number % page_boxes * p.box : 0;
-        // one bit for every 16 keys
-        uint32_t bits = ok ? ((1u << (p.box / 16)) - 1) << (box * (p.box / 16)) : 0;
-        bits = __reduce_or_sync(~0u, bits);
-        wait_phase(empty0 + 8 * s, par, failed, p.error);
-        const uint32_t bar = full0 + 8 * s;
-        if (lane == 0) {
-          if (kv == 0) page_ok[s] = bits;
-          mbar_arrive_expect_tx(bar, L::kSlot);
-        }
-        __syncwarp();
-        if (lane < copies)
-          tma_4d(ring0 + s * L::kSlot + chunk * L::kChunk + box * p.box * L::kRow,
-                 kv ? &vmap : &kmap, chunk * L::kElems, token, head, page, bar);
-        if ((s += 2) >= NS) {
-          s = kv;
-          par ^= 1;
-        }
-      }
-    }
-    // every copy has been read, so has landed, before the block may end; after
-    // a failure they get 10 ms to land
-    for (int k = 0; k < NS / 2; ++k) {
-      wait_phase(empty0 + 8 * s, par, failed, p.error);
-      if ((s += 2) >= NS) {
-        s = kv;
-        par ^= 1;
-      }
-    }
-    if (*failed) {
-      const uint64_t end = globaltimer() + 10000000;
-      while (globaltimer() < end) __nanosleep(1000);
-    }
+    copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
     return;
   }
 
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t ik = 2 * tile_no, iv = ik + 1;
       const uint32_t sk = ik % NS, sv = iv % NS;
       wait_phase(full0 + 8 * sk, (ik / NS) & 1, failed, p.error);
-      const uint32_t ok_bits = page_ok[sk];
+      const uint32_t ok_bits = page_ok[tile_no % 16];
 #pragma unroll
       for (int j = 0; j < L::kSub; ++j) {
         const int key0 = (j * L::KT + kt) * L::SK;       // within the tile
@@ -977,6 +986,11 @@ Variant variant() {
 // groups 1, 2, 4, 8: a translation unit each.
 using Variants = Variant[3][4];
 extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
+
+// The tcgen05 kernel (vg_attention_wide.cuh): BF16 and FP16, head_dim up to 64
+// and 128, one and two row tiles of 128.
+using WideVariants = Variant[2][2][2];
+extern const WideVariants kWide;
 
 #define VG_ATTENTION_ROWS(T, DC) \
   {variant<T, DC, 1>(), variant<T, DC, 2>(), variant<T, DC, 4>(), variant<T, DC, 8>()}
