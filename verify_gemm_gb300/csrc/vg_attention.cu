@@ -92,7 +92,8 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   p.blocks = (rows + v.rows - 1) / v.rows;
   p.box = cache_box_tokens(cache->page_size);
   // a unit costs about 3 us beside its tiles, which come at 45 GB/s a block
-  const int tile_bytes = 2 * kTile * p.d * (type == kE4M3 ? 1 : 2);
+  p.tile_log2 = is_wide(type, p.d, rows) ? 7 : 6;
+  const int tile_bytes = (2 * p.d * (type == kE4M3 ? 1 : 2)) << p.tile_log2;
   p.least = std::max(1, 131072 / tile_bytes);
   p.extra = std::max(1, 131072 / tile_bytes);
   p.c = d->scale * cache->k_scale * kLog2e;

@@ -37,7 +37,7 @@
 namespace vg {
 namespace attn {
 
-constexpr int kTile = 64;                     // keys of a tile
+constexpr int kTile = 64;                     // keys of a tile (mma.sync)
 constexpr int kConsumers = 8;                 // warps
 constexpr int kAttnThreads = (kConsumers + 4) * 32;   // three warpgroups, one warp of the last copies
 // Registers a thread: 168 at the launch (384 x 168 = 64512); the producer's
@@ -71,6 +71,7 @@ struct AttnParams {
   float *partial;                   // [grid][2] of (rows x (head_dim padded) + 2 rows)
   int batch, n, hq, hkv, d, q_f16;
   int rows, blocks;                 // rows that share a cache head, row blocks of a unit
+  int tile_log2;                    // keys of a tile
   int box, least, extra;            // tokens of a TMA box; tiles: of a run at least, a unit costs
   float c, v_scale;                 // scale * k_scale * log2 e
 };
@@ -79,6 +80,7 @@ struct AttnParams {
 template <int kType, int DC, int RW>
 struct Cfg {
   static constexpr int kSize = kType == kE4M3 ? 1 : 2;
+  static constexpr int kKeys = kTile;
   // a key's row comes in chunks of 128 bytes (64 for E4M3 heads of 64): half
   // as many of twice the size move an E4M3 tile faster
   static constexpr int kRow = kType == kE4M3 && DC == 1 ? 64 : 128;
@@ -245,7 +247,7 @@ struct Line {
   __device__ __forceinline__ static int tiles_of(const AttnParams &p, int b) {
     int len;
     const int count = used(p, b, len);
-    return max(1, (len + count + kTile - 1) / kTile);
+    return max(1, (len + count + (1 << p.tile_log2) - 1) >> p.tile_log2);
   }
   // The whole warp computes it.
   __device__ void init(const AttnParams &p, int units_) {
@@ -337,7 +339,7 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
                            uint32_t ring0, uint32_t full0, uint32_t empty0, uint32_t *page_ok,
                            volatile int *failed) {
   const int lane = threadIdx.x % 32;
-  const int boxes = kTile / p.box, copies = boxes * L::kChunks;
+  const int boxes = L::kKeys / p.box, copies = boxes * L::kChunks;
   const int page_boxes = p.cache.page_size / p.box;
   int s = kv, n = 0;
   uint32_t par = 1;                                      // slots start empty

@@ -1,17 +1,22 @@
 // vg_attention_wide.cuh -- the attention kernel for many rows a cache head:
 // tcgen05 products with the scores, the weights and the output in TMEM.
 //
-// From some 40 rows a head on, mma.sync (0.5 PFLOP/s here) and not the cache's
-// bytes bounds the kernel of vg_attention.cuh.  Here a block takes one or two
-// row tiles of 128 rows through the same keys:
-//     S = Q K^T        128 x 64, both operands in shared memory
+// From some 32 rows a head on, mma.sync (0.5 PFLOP/s here) and not the cache's
+// bytes bounds the kernel of vg_attention.cuh.  Here the products of 128 rows
+// with 128 keys are
+//     S = Q K^T        both operands in shared memory
 //     P = 2^(c S - m)  one thread a row: TMEM -> registers -> TMEM, 16 bits
 //     O = O + P V      P from TMEM, V in shared memory as it lies (its rows
 //                      are the products' k, so it is the transposed operand)
-// One thread issues the products, a warpgroup does each row tile's softmax, a
-// warp each copies K and V.  S has two buffers a row tile, and P takes the
-// place of its S, so that the products of the next keys run under the softmax
-// of these: TMEM holds 2 x 128 columns of O and 4 x 64 of S.
+// One warp issues the products, a warp each copies K and V, and two
+// warpgroups do the softmax of two streams that take the tensor cores in
+// turn: the products of one run under the softmax of the other.  With more
+// than 128 rows the streams are two row tiles of the same keys; with fewer
+// they are the even and the odd tiles of keys, joined at a unit's end (both
+// outputs lie in the lanes of their row, so a thread reads both).
+// TMEM holds S and O of both streams, 4 x 128 columns; P takes the place of S.
+// 128 keys and not 64: an M = 128 product takes 64 clocks at N = 64 and at
+// N = 128 alike (measured; 128 at N = 256).
 // A row's maximum may lag by up to 2^8: O is rescaled, in TMEM by its softmax
 // warpgroup, only when the true maximum is more than 8 above the one in use,
 // and l carries the same factor.
@@ -25,6 +30,9 @@ namespace vg {
 namespace attn {
 
 constexpr int kWideThreads = 384;
+// Registers a thread: 168 at the launch (384 x 168 = 64512), then 256 x 216 +
+// 128 x 72 = 64512: a softmax thread holds a row of 128 scores.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kLag = 8.f;                   // log2 of what a maximum may lag
 // FP16 weights are at most 2^kLag times 2^lift: lifted to 2^15 in all.
 template <int kType>
@@ -33,13 +41,13 @@ constexpr float kWideLift = kType == kBf16 ? 0.f : 7.f;
 template <int DC, int NQ>
 struct WideCfg {
   static constexpr int D = DC * 64;
-  static constexpr int kRow = 128, kElems = 64, kChunks = DC;
-  static constexpr int kChunk = kTile * kRow;            // 8 KB
+  static constexpr int kRow = 128, kElems = 64, kChunks = DC, kKeys = 128;
+  static constexpr int kChunk = kKeys * kRow;            // 16 KB
   static constexpr int kSlot = DC * kChunk;
   static constexpr int kQChunk = 128 * 128;              // 128 rows of 64 elements
   static constexpr int kQTile = DC * kQChunk;
   static constexpr int kRows = 128 * NQ;
-  static constexpr int kFixed = 2048;
+  static constexpr int kFixed = 1024 + 2 * 128 * 8;
   static constexpr int kFit = (227 * 1024 - 1024 - kFixed - NQ * kQTile) / kSlot;
   static constexpr int kSlots = (kFit > 16 ? 16 : kFit) & ~1;
   static constexpr int kSmem = 1024 + kFixed + NQ * kQTile + kSlots * kSlot;
@@ -48,27 +56,35 @@ struct WideCfg {
 };
 
 // ------------------------------------------------------------- tcgen05 pieces
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+// The issuing warp runs as one, with `lead` set in one lane, so that what the
+// instructions take stays in uniform registers: a branch of one thread paid
+// some 80 clocks for each product.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.u32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // D (TMEM) = A B (+ D): A and B in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add,
+                                          uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      "{ .reg .pred p, e; setp.ne.u32 p, %4, 0; setp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(lead)
       : "memory");
 }
 // A in TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add,
+                                          uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      "{ .reg .pred p, e; setp.ne.u32 p, %4, 0; setp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(lead)
       : "memory");
 }
 // Shared-memory operand: 128-byte swizzle; `lead` and `stride` in bytes.
@@ -116,6 +132,20 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// (a0 c + b, a1 c + b), as one instruction.
+__device__ __forceinline__ void fma2(float &y0, float &y1, uint32_t a0, uint32_t a1, float c, float b) {
+  asm("{ .reg .b64 a, c, b, y; mov.b64 a, {%2, %3}; mov.b64 c, {%4, %4}; mov.b64 b, {%5, %5};\n"
+      "fma.rn.f32x2 y, a, c, b; mov.b64 {%0, %1}, y; }"
+      : "=f"(y0), "=f"(y1)
+      : "r"(a0), "r"(a1), "f"(c), "f"(b));
+}
+__device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
+  asm("{ .reg .b64 s, a; mov.b64 s, {%0, %1}; mov.b64 a, {%2, %3};\n"
+      "add.rn.f32x2 s, s, a; mov.b64 {%0, %1}, s; }"
+      : "+f"(s0), "+f"(s1)
+      : "f"(a0), "f"(a1));
+}
+
 template <int kType, int DC, int NQ>
 __global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
@@ -127,33 +157,36 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint8_t *q_smem = smem + L::kSlots * L::kSlot;
   uint8_t *fixed = q_smem + NQ * L::kQTile;
   uint64_t *bars = reinterpret_cast<uint64_t *>(fixed);
-  // barriers: slots full, slots free, scores there, weights there, product done, q there
+  // barriers: slots full, slots free; of each stream: scores there, weights there
+  // (halves), product done; q there; everything done
   const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + 16), s_full = smem_addr(bars + 32),
-                 p_full = smem_addr(bars + 36), o_full = smem_addr(bars + 40), q_full = smem_addr(bars + 44),
-                 finished = smem_addr(bars + 45);
+                 p_full = smem_addr(bars + 34), o_full = smem_addr(bars + 38), q_full = smem_addr(bars + 40),
+                 finished = smem_addr(bars + 41);
   uint32_t *page_ok = reinterpret_cast<uint32_t *>(fixed + 512);        // [16]
   volatile int *failed = reinterpret_cast<volatile int *>(fixed + 576);
   int *last = reinterpret_cast<int *>(fixed + 580);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(fixed + 584);
-  uint32_t *odd_at = reinterpret_cast<uint32_t *>(fixed + 592);         // [tile % 2][2]
-  volatile int *keep_o = reinterpret_cast<volatile int *>(fixed + 608); // [row tile]
+  volatile int *keep_o = reinterpret_cast<volatile int *>(fixed + 588); // [stream]
+  uint32_t *odd_at = reinterpret_cast<uint32_t *>(fixed + 608);         // [2][4]: bits of keys
+  float2 *state = reinterpret_cast<float2 *>(fixed + 1024);             // [row]: (m, l) of the other stream
   constexpr int NS = L::kSlots;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     *failed = 0;
-    odd_at[0] = odd_at[1] = odd_at[2] = odd_at[3] = 0;
+    for (int i = 0; i < 8; ++i) odd_at[i] = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 128);
+      mbar_init(p_full + 16 * i, 128);
+      mbar_init(p_full + 16 * i + 8, 128);
       mbar_init(o_full + 8 * i, 1);
     }
-    mbar_init(q_full, 128 * NQ);
+    mbar_init(q_full, 256);
     mbar_init(finished, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -171,95 +204,113 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   at.init(p, p.hkv * p.blocks);
   const int group = p.hq / p.hkv;
 
-  if (warp == 8 || warp == 10) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------- copies
     const int kv = warp == 10;
     copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
-  } else if (warp == 9) {
+    } else if (warp == 9) {
     // ----------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t kFmt = kType == kBf16 ? 1 : 0;
-      constexpr uint32_t kIdesc = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u / 16) << 24;
-      constexpr uint32_t kQk = kIdesc | (uint32_t(kTile) / 8) << 17;
-      constexpr uint32_t kPv = kIdesc | 1u << 16 | (uint32_t(L::D) / 8) << 17;   // V: n runs along its rows
-      const uint32_t ring0 = smem_addr(ring), q0 = smem_addr(q_smem);
-      uint32_t n = 0, q_par = 0;                         // tiles so far
-      auto scores = [&](uint32_t i) {                    // S of tile i, every row tile
-        const uint32_t s = 2 * i % NS;
-        wait_phase(full0 + 8 * s, (2 * i / NS) & 1, failed, p.error);
-        tc_after();
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const uint32_t d = tmem + L::kS + (q * 2 + (i & 1)) * kTile;
-#pragma unroll
-          for (int ks = 0; ks < DC * 4; ++ks)
-            tc_mma_ss(d, tc_desc(q0 + q * L::kQTile + (ks / 4) * L::kQChunk + (ks % 4) * 32, 16, 1024),
-                      tc_desc(ring0 + s * L::kSlot + (ks / 4) * L::kChunk + (ks % 4) * 32, 16, 1024), kQk,
-                      ks > 0);
-          tc_commit(s_full + 8 * (q * 2 + (i & 1)));
+    // Step w of a unit is stream w % 2's: tile w / 2 or, with the keys split, w.
+    constexpr uint32_t kFmt = kType == kBf16 ? 1 : 0;
+    constexpr uint32_t kIdesc = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u / 16) << 24;
+    constexpr uint32_t kQk = kIdesc | uint32_t(L::kKeys / 8) << 17;
+    constexpr uint32_t kPv = kIdesc | 1u << 16 | uint32_t(L::D / 8) << 17;   // V: n runs along its rows
+    const uint32_t lead = lane == 0;
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint64_t k_ring = tc_desc(smem_addr(ring), 16, 1024), q_desc = tc_desc(smem_addr(q_smem), 16, 1024);
+    const uint64_t v_ring = tc_desc(smem_addr(ring), L::kChunk, 1024);
+    uint32_t n = 0, q_par = 0, c0 = 0, c1 = 0;           // tiles, units; steps of the streams so far
+    for (; at.valid(); at.next(p)) {
+      wait_phase(q_full, q_par, failed, p.error);
+      q_par ^= 1;
+      tc_after();
+      const uint32_t tiles = __shfl_sync(~0u, uint32_t(at.t1 - at.t0), 0);
+      const uint32_t steps = NQ == 2 ? 2 * tiles : tiles;
+      auto scores = [&](uint32_t w) {
+        const uint32_t q = w & 1, i = n + (NQ == 2 ? w / 2 : w), s = 2 * i % NS;
+        if (NQ == 1 || q == 0) {
+          wait_phase(full0 + 8 * s, (2 * i / NS) & 1, failed, p.error);
+          tc_after();
         }
-        tc_commit(empty0 + 8 * s);
+        const uint64_t kd = k_ring + s * (L::kSlot / 16);
+        const uint64_t qd = q_desc + (NQ == 2 ? q : 0) * (L::kQTile / 16);
+#pragma unroll
+        for (int ks = 0; ks < DC * 4; ++ks)
+          tc_mma_ss(tm + L::kS + q * 128, qd + ((ks / 4) * L::kQChunk + (ks % 4) * 32) / 16,
+                    kd + ((ks / 4) * L::kChunk + (ks % 4) * 32) / 16, kQk, ks > 0, lead);
+        tc_commit(s_full + 8 * q, lead);
+        if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s, lead);
       };
-      for (; at.valid(); at.next(p)) {
-        wait_phase(q_full, q_par, failed, p.error);
-        q_par ^= 1;
+      scores(0);
+      if (steps > 1) scores(1);
+      for (uint32_t w = 0; w < steps; ++w) {
+        const uint32_t q = w & 1, i = n + (NQ == 2 ? w / 2 : w), s = (2 * i + 1) % NS;
+        if (NQ == 1 || q == 0) wait_phase(full0 + 8 * s, ((2 * i + 1) / NS) & 1, failed, p.error);
+        const uint32_t c = q ? c1++ : c0++;
+        const uint64_t vd = v_ring + s * (L::kSlot / 16);
+        // the first half of the weights goes ahead of the second
+        wait_phase(p_full + 16 * q, c & 1, failed, p.error);
         tc_after();
-        const uint32_t end = n + uint32_t(at.t1 - at.t0);
-        scores(n);
-        for (uint32_t i = n; i < end; ++i) {
-          if (i + 1 < end) scores(i + 1);
-          const uint32_t s = (2 * i + 1) % NS;
-          wait_phase(full0 + 8 * s, ((2 * i + 1) / NS) & 1, failed, p.error);
+        const bool fresh = w < 2 && !keep_o[q];          // O begins with this product
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const uint32_t buf = q * 2 + (i & 1);
-            wait_phase(p_full + 8 * buf, (i / 2) & 1, failed, p.error);
-            tc_after();
-            const bool fresh = i == n && !keep_o[q];     // O begins with this product
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv,
+                    !fresh || ks > 0, lead);
+        wait_phase(p_full + 16 * q + 8, c & 1, failed, p.error);
+        tc_after();
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              tc_mma_ts(tmem + L::kO + q * 128, tmem + L::kS + buf * kTile + ks * 8,
-                        tc_desc(ring0 + s * L::kSlot + ks * 2048, L::kChunk, 1024), kPv,
-                        !fresh || ks > 0);
-            tc_commit(o_full + 8 * buf);
-          }
-          tc_commit(empty0 + 8 * s);
-        }
-        n = end;
+        for (int ks = 4; ks < 8; ++ks)
+          tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv, true,
+                    lead);
+        if (w + 2 >= steps) tc_commit(o_full + 8 * q, lead);   // the stream's last of the unit
+        if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s, lead);
+        if (w + 2 < steps) scores(w + 2);
       }
-      // nothing is in flight when TMEM is given back
-      tc_commit(finished);
-      const uint64_t limit = globaltimer() + 10000000;
-      while (!mbar_try_wait(finished, 0) && globaltimer() < limit) {
-      }
+      n += tiles;
+    }
+    // nothing is in flight when TMEM is given back
+    tc_commit(finished, lead);
+    const uint64_t limit = globaltimer() + 10000000;
+    while (!mbar_try_wait(finished, 0) && globaltimer() < limit) {
     }
     __syncwarp();
-  } else if (warp < 4 * NQ) {
+    }
+  } else {
     // ------------------------------------------------------------- softmax
-    const int q = warp / 4, row_in = tid % 128;          // row tile, lane of TMEM
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int q = warp / 4, row_in = tid % 128;          // stream, lane of TMEM
     const uint32_t lanes = tmem + (uint32_t(warp % 4 * 32) << 16);
-    const uint32_t o_at = lanes + L::kO + q * 128;
-    uint32_t n = 0;
-    auto sync_rows = [&] { named_bar(1, 128 * NQ); };
+    const uint32_t o_at = lanes + L::kO + q * 128, s_at = lanes + L::kS + q * 128;
+    // c > 0: its sign goes into q, so that the largest product is the largest score
+    const float c = fmaxf(fabsf(p.c), 1e-30f);
+    const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
+    uint32_t n = 0, steps = 0, units = 0;                // tiles, this stream's steps and units so far
+    auto sync_rows = [&] { named_bar(1, 256); };
     for (; at.valid(); at.next(p)) {
       const int head = at.u / p.blocks, rb = at.u % p.blocks;
-      const int row0 = rb * L::kRows, row = row0 + q * 128 + row_in;
+      const int row0 = rb * L::kRows, row = row0 + (NQ == 2 ? q * 128 : 0) + row_in;
       const int node = row / group, h = head * group + row % group;
       const bool real = row < p.rows;
       // q to shared memory, sixteen lanes a row
       {
         const int piece = lane % 16;
 #pragma unroll 4
-        for (int r = warp % 4 * 2 + lane / 16; r < 128; r += 8) {
-          const int rw = row0 + q * 128 + r;
+        for (int r = warp * 2 + lane / 16; r < L::kRows; r += 16) {
+          const int rw = row0 + r;
           uint4 v = make_uint4(0, 0, 0, 0);
           if (rw < p.rows && piece * 8 < p.d)
             v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at.b * p.qs[0] +
                                                  (rw / group) * p.qs[1] +
                                                  (head * group + rw % group) * p.qs[2] + piece * 8);
+          v.x ^= flip;
+          v.y ^= flip;
+          v.z ^= flip;
+          v.w ^= flip;
           if (piece < DC * 8)
-            *reinterpret_cast<uint4 *>(q_smem + q * L::kQTile + (piece / 8) * L::kQChunk + r * 128 +
-                                       (((piece % 8) ^ (r & 7)) << 4)) = v;
+            *reinterpret_cast<uint4 *>(q_smem + (r / 128) * L::kQTile + (piece / 8) * L::kQChunk +
+                                       (r % 128) * 128 + (((piece % 8) ^ (r & 7)) << 4)) = v;
         }
         fence_proxy_async();
         mbar_arrive(q_full);
@@ -269,64 +320,122 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         word = (at.count >= 64 ? ~0ull : (1ull << at.count) - 1) &
                (p.tree ? p.tree[int64_t(at.b) * p.n + node] : ~0ull >> (63 - node));
       float m = -INFINITY, l = 0.f;                      // the maximum in use
+      const int tiles = at.t1 - at.t0;
 
-      for (int tile = at.t0; tile < at.t1; ++tile, ++n) {
-        const uint32_t buf = q * 2 + (n & 1), s_at = lanes + L::kS + buf * kTile;
-        const uint32_t sv = (2 * n + 1) % NS;
-        wait_phase(s_full + 8 * buf, (n / 2) & 1, failed, p.error);
+      for (int k0 = NQ == 2 ? 0 : q; k0 < tiles; k0 += NQ == 2 ? 1 : 2, ++steps) {
+        const int tile = at.t0 + k0;
+        const uint32_t i = n + k0, sv = (2 * i + 1) % NS;
+        const bool begin = k0 < (NQ == 2 ? 1 : 2);       // O has nothing yet
+        wait_phase(s_full + 8 * q, steps & 1, failed, p.error);
         tc_after();
-        const uint32_t ok_bits = page_ok[n % 16];
-        uint32_t x[2][32];
-        tc_ld32(x[0], s_at);
-        tc_ld32(x[1], s_at + 32);
-        const int rel = tile * kTile - at.len;           // of the first key to the drafted ones
-        const bool open = ok_bits == 15u && rel <= -kTile;
-        uint64_t sees = ~0ull;
-        if (!open) {
-          uint64_t exist = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) exist |= (ok_bits >> k & 1) ? 0xFFFFull << (16 * k) : 0;
-          sees = exist & (rel <= -64 ? ~0ull
-                          : rel < 0  ? (word << -rel) | ((1ull << -rel) - 1)
-                          : rel < 64 ? word >> rel : 0);
-        }
-        tc_wait_ld(x[0]);
-        tc_wait_ld(x[1]);
-        float top = -INFINITY;
+        const uint32_t ok_bits = page_ok[i % 16];
+        const int rel = tile * L::kKeys - at.len;        // of the first key to the drafted ones
+        const bool open = ok_bits == 255u && rel <= -L::kKeys;
+        uint64_t sees[2] = {~0ull, ~0ull};
         if (!open) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float f = __uint_as_float(x[k / 32][k % 32]) * p.c;
-            x[k / 32][k % 32] = __float_as_uint((sees >> k & 1) ? f : -INFINITY);
-            top = fmaxf(top, __uint_as_float(x[k / 32][k % 32]));
-          }
-        } else {
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int k = 0; k < 2; ++k) {
+            uint64_t exist = 0;
+            const int rk = rel + 64 * k;
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float f = __uint_as_float(x[k / 32][k % 32]) * p.c;
-            x[k / 32][k % 32] = __float_as_uint(f);
-            t4[k % 4] = fmaxf(t4[k % 4], f);
+            for (int b = 0; b < 4; ++b) exist |= (ok_bits >> (4 * k + b) & 1) ? 0xFFFFull << (16 * b) : 0;
+            sees[k] = exist & (rk <= -64 ? ~0ull
+                               : rk < 0  ? (word << -rk) | ((1ull << -rk) - 1)
+                               : rk < 64 ? word >> rk : 0);
           }
-          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         }
+        if (begin && row_in == 0) keep_o[q] = 0;
+        if (!open) {
+          // Keys that some row does not attend to: a weight of 0 does not keep an
+          // infinity or NaN of v out of the product.  They are looked for, added
+          // to the rows that attend to them and set to 0.  With two row tiles
+          // both streams come here together; with the keys split, each alone.
+          uint32_t *odd_keys = odd_at + (NQ == 2 ? i & 1 : q) * 4;
+          auto sync_tile = [&] { named_bar(NQ == 2 ? 1 : 2 + q, NQ == 2 ? 256 : 128); };
+          const int first = NQ == 2 ? tid : row_in;
+          wait_phase(full0 + 8 * sv, ((2 * i + 1) / NS) & 1, failed, p.error);
+          uint8_t *slot = ring + sv * L::kSlot;
+          for (int k = first; k < L::kKeys * DC * 8; k += 128 * NQ) {
+            const int key = k / (DC * 8);
+            const uint4 v = *reinterpret_cast<const uint4 *>(slot + spot<L>(key, k % (DC * 8)));
+            if (nonfinite_bits<kType>(v.x) | nonfinite_bits<kType>(v.y) | nonfinite_bits<kType>(v.z) |
+                nonfinite_bits<kType>(v.w))
+              atomicOr(odd_keys + key / 32, 1u << (key % 32));
+          }
+          sync_tile();
+          const uint32_t odd[4] = {odd_keys[0], odd_keys[1], odd_keys[2], odd_keys[3]};
+          if (NQ == 1) sync_tile();                      // the words are read before they change again
+          if (odd[0] | odd[1] | odd[2] | odd[3]) {
+            if (begin && row_in == 0) keep_o[q] = 1;
+#pragma unroll 1
+            for (int k = 0; k < L::D; k += 32) {
+              uint32_t y[32];
+              if (!begin) {
+                tc_ld32(y, o_at + k);
+                tc_wait_ld(y);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = 0;
+              }
+#pragma unroll 1
+              for (int key = 0; key < L::kKeys; ++key) {
+                const uint32_t word32 = key < 32 ? odd[0] : key < 64 ? odd[1] : key < 96 ? odd[2] : odd[3];
+                if (!(word32 >> (key % 32) & 1) || !((key < 64 ? sees[0] : sees[1]) >> (key % 64) & 1)) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const uint16_t b = *reinterpret_cast<const uint16_t *>(
+                      slot + spot<L>(key, (k + e) / 8) + (k + e) % 8 * 2);
+                  const float f = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(b))
+                                                 : __half2float(__ushort_as_half(b));
+                  if (!(fabsf(f) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + f);
+                }
+              }
+              __syncwarp();
+              tc_st32(o_at + k, y);
+            }
+            tc_wait_st();
+            sync_tile();
+            for (int k = first; k < L::kKeys * DC * 8; k += 128 * NQ) {
+              uint4 *v = reinterpret_cast<uint4 *>(slot + spot<L>(k / (DC * 8), k % (DC * 8)));
+              v->x &= finite_mask<kType>(v->x);
+              v->y &= finite_mask<kType>(v->y);
+              v->z &= finite_mask<kType>(v->z);
+              v->w &= finite_mask<kType>(v->w);
+            }
+            fence_proxy_async();
+            if (first < 4) odd_keys[first] = 0;
+            sync_tile();
+          }
+        }
+        uint32_t x[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_ld32(x[k], s_at + 32 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_wait_ld(x[k]);
+        if (!open) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (!(sees[k / 64] >> (k % 64) & 1)) x[k / 32][k % 32] = 0xFF800000u;
+        }
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; ++k) t4[k % 4] = fmaxf(t4[k % 4], __uint_as_float(x[k / 32][k % 32]));
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
         const bool raise = top > m + kLag || (m == -INFINITY && top > m);
         // (all lanes of the warp take part in the TMEM accesses)
         if (__any_sync(~0u, raise)) {
           const float m2 = raise ? top : m;
           const float keep = m == m2 ? 1.f : m == -INFINITY ? 0.f : ex2(m - m2);
-          if (tile > at.t0) {
-            // the product before has been made, the next waits for these weights
-            wait_phase(o_full + 8 * (q * 2 + ((n - 1) & 1)), ((n - 1) / 2) & 1, failed, p.error);
-            tc_after();
+          if (!begin) {
+            // (the product before was made before these scores)
 #pragma unroll 1
-            for (int c = 0; c < L::D; c += 32) {
+            for (int k = 0; k < L::D; k += 32) {
               uint32_t y[32];
-              tc_ld32(y, o_at + c);
+              tc_ld32(y, o_at + k);
               tc_wait_ld(y);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * keep);
-              tc_st32(o_at + c, y);
+              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+              tc_st32(o_at + k, y);
             }
             tc_wait_st();
           }
@@ -335,88 +444,66 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         const float base = m == -INFINITY ? 0.f : m - kWideLift<kType>;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float a = ex2(__uint_as_float(x[k / 16][k % 16 * 2]) - base);
-          const float b = ex2(__uint_as_float(x[k / 16][k % 16 * 2 + 1]) - base);
-          l4[k % 4] += a + b;
-          w[k] = pack2<kType>(a, b);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t *xs = &x[2 * half + k / 16][k % 16 * 2];
+            float a, b;
+            fma2(a, b, xs[0], xs[1], c, -base);
+            a = ex2(a);
+            b = ex2(b);
+            add2(l4[k % 2 * 2], l4[k % 2 * 2 + 1], a, b);
+            w[k] = pack2<kType>(a, b);
+          }
+          tc_st32(s_at + 32 * half, w);
+          tc_wait_st();
+          tc_before();
+          mbar_arrive(p_full + 16 * q + 8 * half);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        tc_st32(s_at, w);
-        if (tile == at.t0 && row_in == 0) keep_o[q] = 0;
-        if (!open) {
-          uint32_t *odd_keys = odd_at + (n & 1) * 2;
-          // Keys that some row does not attend to: a weight of 0 does not keep an
-          // infinity or NaN of v out of the product.  They are looked for, added
-          // to the rows that attend to them and set to 0.
-          wait_phase(full0 + 8 * sv, ((2 * n + 1) / NS) & 1, failed, p.error);
-          uint8_t *slot = ring + sv * L::kSlot;
-          for (int k = tid; k < kTile * DC * 8; k += 128 * NQ) {
-            const int key = k / (DC * 8);
-            const uint4 v = *reinterpret_cast<const uint4 *>(slot + spot<L>(key, k % (DC * 8)));
-            if (nonfinite_bits<kType>(v.x) | nonfinite_bits<kType>(v.y) | nonfinite_bits<kType>(v.z) |
-                nonfinite_bits<kType>(v.w))
-              atomicOr(odd_keys + key / 32, 1u << (key % 32));
-          }
-          sync_rows();
-          const uint64_t odd = uint64_t(odd_keys[1]) << 32 | odd_keys[0];
-          if (odd) {
-            if (tile > at.t0) {
-              wait_phase(o_full + 8 * (q * 2 + ((n - 1) & 1)), ((n - 1) / 2) & 1, failed, p.error);
-              tc_after();
-            } else if (row_in == 0) {
-              keep_o[q] = 1;
-            }
-            const uint64_t mine = odd & sees;
-#pragma unroll 1
-            for (int c = 0; c < L::D; c += 32) {
-              uint32_t y[32];
-              if (tile > at.t0) {
-                tc_ld32(y, o_at + c);
-                tc_wait_ld(y);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] = 0;
-              }
-#pragma unroll 1
-              for (int key = 0; key < kTile; ++key) {
-                if (!(mine >> key & 1)) continue;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const uint16_t e = *reinterpret_cast<const uint16_t *>(
-                      slot + spot<L>(key, (c + k) / 8) + (c + k) % 8 * 2);
-                  const float f = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(e))
-                                                 : __half2float(__ushort_as_half(e));
-                  if (!(fabsf(f) < INFINITY)) y[k] = __float_as_uint(__uint_as_float(y[k]) + f);
-                }
-              }
-              __syncwarp();
-              tc_st32(o_at + c, y);
-            }
-            tc_wait_st();
-            sync_rows();
-            for (int k = tid; k < kTile * DC * 8; k += 128 * NQ) {
-              uint4 *v = reinterpret_cast<uint4 *>(slot + spot<L>(k / (DC * 8), k % (DC * 8)));
-              v->x &= finite_mask<kType>(v->x);
-              v->y &= finite_mask<kType>(v->y);
-              v->z &= finite_mask<kType>(v->z);
-              v->w &= finite_mask<kType>(v->w);
-            }
-            fence_proxy_async();
-            if (tid == 0) odd_keys[0] = odd_keys[1] = 0;
-            sync_rows();
-          }
-        }
-        tc_wait_st();
-        tc_before();
-        mbar_arrive(p_full + 8 * buf);
       }
+      n += tiles;
 
       // ----------------------------------------------------------- results
-      wait_phase(o_full + 8 * (q * 2 + ((n - 1) & 1)), ((n - 1) / 2) & 1, failed, p.error);
-      tc_after();
+      const bool some = NQ == 2 || q == 0 || tiles > 1;  // whether the stream had a tile
+      if (some) {
+        wait_phase(o_full + 8 * q, units & 1, failed, p.error);
+        ++units;
+        tc_after();
+      }
+      float w0 = 1.f, w1 = 0.f;                          // weights of the streams' outputs
+      if constexpr (NQ == 1) {
+        state[tid] = make_float2(m, l);
+        tc_before();
+        sync_rows();
+        tc_after();
+        const float2 a = state[row_in], b = state[128 + row_in];
+        const float both = fmaxf(a.x, b.x);
+        w0 = a.x == -INFINITY ? 0.f : ex2(a.x - both);
+        w1 = b.x == -INFINITY ? 0.f : ex2(b.x - both);
+        l = a.y * w0 + b.y * w1;
+        m = both;
+      }
+      // this thread's columns of its row: all, or its stream's half of them
+      const int col0 = NQ == 2 ? 0 : q * (L::D / 2), col1 = NQ == 2 ? L::D : col0 + L::D / 2;
+      auto load = [&](int k, uint32_t (&y)[32]) {
+        tc_ld32(y, lanes + L::kO + (NQ == 2 ? q * 128 : 0) + k);
+        tc_wait_ld(y);
+        if constexpr (NQ == 1) {
+          // (a NaN of a stream whose rows weigh nothing is kept, too)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * w0);
+          if (tiles > 1) {
+            uint32_t z[32];
+            tc_ld32(z, lanes + L::kO + 128 + k);
+            tc_wait_ld(z);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(fmaf(__uint_as_float(z[e]), w1, __uint_as_float(y[e])));
+          }
+        }
+      };
       const int first = at.block_of(0), final = at.block_of(at.tiles - 1);
       const bool whole = first == final;
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
@@ -435,41 +522,43 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
       };
       auto store_lse = [&](float mm, float ll, bool empty) {
-        if (p.lse && real)
+        if (p.lse && real && (NQ == 2 || q == 0))
           p.lse[at_row] = empty ? -INFINITY : (mm - kWideLift<kType> + log2f(ll)) * kLn2;
       };
       if (whole) {
         const bool empty = node >= at.count || (m == -INFINITY && l == 0.f);   // NaN is not nothing
         const float inv = empty ? 0.f : p.v_scale / l;
 #pragma unroll 1
-        for (int c = 0; c < L::D; c += 32) {
+        for (int k = col0; k < col1; k += 32) {
           uint32_t y[32];
-          tc_ld32(y, o_at + c);
-          tc_wait_ld(y);
+          load(k, y);
           float f[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(y[k]);
-          store(c, f, inv, empty);
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(y[e]);
+          store(k, f, inv, empty);
         }
         store_lse(m, l, empty);
       } else {
         // partial results: [4 columns][row], then (m, l) of each row
-        const int mine_row = q * 128 + row_in;
+        const int mine_row = (NQ == 2 ? q * 128 : 0) + row_in;
         auto place = [&](int block) {
           return p.partial + (int64_t(block) * 2 + (block == first ? 1 : 0)) * L::kPartial;
         };
+        auto state_of = [&](int block) {
+          return __ldcg(reinterpret_cast<const float2 *>(place(block) + L::kRows * L::D) + mine_row);
+        };
         float *mine = place(blockIdx.x);
 #pragma unroll 1
-        for (int c = 0; c < L::D; c += 32) {
+        for (int k = col0; k < col1; k += 32) {
           uint32_t y[32];
-          tc_ld32(y, o_at + c);
-          tc_wait_ld(y);
+          load(k, y);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            reinterpret_cast<uint4 *>(mine)[(c + k) / 4 * L::kRows + mine_row] =
-                make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+          for (int e = 0; e < 32; e += 4)
+            reinterpret_cast<uint4 *>(mine)[(k + e) / 4 * L::kRows + mine_row] =
+                make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
-        reinterpret_cast<float2 *>(mine + L::kRows * L::D)[mine_row] = make_float2(m, l);
+        if (NQ == 2 || q == 0)
+          reinterpret_cast<float2 *>(mine + L::kRows * L::D)[mine_row] = make_float2(m, l);
         __threadfence();
         sync_rows();
         if (tid == 0) {
@@ -481,40 +570,42 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         sync_rows();
         if (*last) {
           float top = -INFINITY, sum = 0.f;
-          for (int blk = first; blk <= final; ++blk)
-            top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(place(blk) + L::kRows * L::D) + mine_row).x);
+#pragma unroll 4
+          for (int blk = first; blk <= final; ++blk) top = fmaxf(top, state_of(blk).x);
+#pragma unroll 4
           for (int blk = first; blk <= final; ++blk) {
-            const float2 st = __ldcg(reinterpret_cast<const float2 *>(place(blk) + L::kRows * L::D) + mine_row);
+            const float2 st = state_of(blk);
             sum += st.y * (st.x == -INFINITY ? 0.f : ex2(st.x - top));
           }
           const bool empty = node >= at.count || (top == -INFINITY && sum == 0.f);
           const float inv = empty ? 0.f : p.v_scale / sum;
 #pragma unroll 1
-          for (int c = 0; c < L::D; c += 32) {
+          for (int k = col0; k < col1; k += 32) {
             float f[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = 0.f;
+            for (int e = 0; e < 32; ++e) f[e] = 0.f;
 #pragma unroll 2
             for (int blk = first; blk <= final; ++blk) {
-              const float *part = place(blk);
-              const float mm = __ldcg(reinterpret_cast<const float2 *>(part + L::kRows * L::D) + mine_row).x;
+              const float mm = state_of(blk).x;
               const float wt = mm == -INFINITY ? 0.f : ex2(mm - top);
+              const float4 *part = reinterpret_cast<const float4 *>(place(blk)) + mine_row;
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part) + (c + k) / 4 * L::kRows + mine_row);
-                f[k] += v.x * wt;
-                f[k + 1] += v.y * wt;
-                f[k + 2] += v.z * wt;
-                f[k + 3] += v.w * wt;
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(part + (k + e) / 4 * L::kRows);
+                f[e] += v.x * wt;
+                f[e + 1] += v.y * wt;
+                f[e + 2] += v.z * wt;
+                f[e + 3] += v.w * wt;
               }
             }
-            store(c, f, inv, empty);
+            store(k, f, inv, empty);
           }
           store_lse(top, sum, empty);
         }
-        sync_rows();                                     // *last is free again
       }
+      // the outputs are read and *last is free before the next unit begins
       tc_before();
+      sync_rows();
     }
   }
   tc_before();
