@@ -56,35 +56,36 @@ struct WideCfg {
 };
 
 // ------------------------------------------------------------- tcgen05 pieces
-// The issuing warp runs as one, with `lead` set in one lane, so that what the
-// instructions take stays in uniform registers: a branch of one thread paid
-// some 80 clocks for each product.
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead) {
-  asm volatile(
-      "{ .reg .pred e; setp.ne.u32 e, %1, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
-      "r"(lead)
-      : "memory");
+// True in one lane of the warp, the same each time.  Products are issued in a
+// branch on this: under it the compiler keeps what they take in uniform
+// registers and a product takes some 15 clocks to issue; under a branch on
+// the lane's number it took 60, as long as the product itself.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(y));
+  return y != 0;
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // D (TMEM) = A B (+ D): A and B in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add,
-                                          uint32_t lead) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.u32 p, %4, 0; setp.ne.u32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(lead)
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
       : "memory");
 }
 // A in TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add,
-                                          uint32_t lead) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.u32 p, %4, 0; setp.ne.u32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(lead)
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
       : "memory");
 }
 // Shared-memory operand: 128-byte swizzle; `lead` and `stride` in bytes.
@@ -217,7 +218,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr uint32_t kIdesc = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u / 16) << 24;
     constexpr uint32_t kQk = kIdesc | uint32_t(L::kKeys / 8) << 17;
     constexpr uint32_t kPv = kIdesc | 1u << 16 | uint32_t(L::D / 8) << 17;   // V: n runs along its rows
-    const uint32_t lead = lane == 0;
     const uint32_t tm = __shfl_sync(~0u, tmem, 0);
     const uint64_t k_ring = tc_desc(smem_addr(ring), 16, 1024), q_desc = tc_desc(smem_addr(q_smem), 16, 1024);
     const uint64_t v_ring = tc_desc(smem_addr(ring), L::kChunk, 1024);
@@ -236,12 +236,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         const uint64_t kd = k_ring + s * (L::kSlot / 16);
         const uint64_t qd = q_desc + (NQ == 2 ? q : 0) * (L::kQTile / 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < DC * 4; ++ks)
-          tc_mma_ss(tm + L::kS + q * 128, qd + ((ks / 4) * L::kQChunk + (ks % 4) * 32) / 16,
-                    kd + ((ks / 4) * L::kChunk + (ks % 4) * 32) / 16, kQk, ks > 0, lead);
-        tc_commit(s_full + 8 * q, lead);
-        if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s, lead);
+          for (int ks = 0; ks < DC * 4; ++ks)
+            tc_mma_ss(tm + L::kS + q * 128, qd + ((ks / 4) * L::kQChunk + (ks % 4) * 32) / 16,
+                      kd + ((ks / 4) * L::kChunk + (ks % 4) * 32) / 16, kQk, ks > 0);
+          tc_commit(s_full + 8 * q);
+          if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s);
+        }
+        __syncwarp();
       };
       scores(0);
       if (steps > 1) scores(1);
@@ -254,24 +257,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wait_phase(p_full + 16 * q, c & 1, failed, p.error);
         tc_after();
         const bool fresh = w < 2 && !keep_o[q];          // O begins with this product
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv,
-                    !fresh || ks > 0, lead);
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv,
+                      !fresh || ks > 0);
+        }
+        __syncwarp();
         wait_phase(p_full + 16 * q + 8, c & 1, failed, p.error);
         tc_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 4; ks < 8; ++ks)
-          tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv, true,
-                    lead);
-        if (w + 2 >= steps) tc_commit(o_full + 8 * q, lead);   // the stream's last of the unit
-        if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s, lead);
+          for (int ks = 4; ks < 8; ++ks)
+            tc_mma_ts(tm + L::kO + q * 128, tm + L::kS + q * 128 + ks * 8, vd + ks * 2048 / 16, kPv, true);
+          if (w + 2 >= steps) tc_commit(o_full + 8 * q);       // the stream's last of the unit
+          if (NQ == 1 || q == 1) tc_commit(empty0 + 8 * s);
+        }
+        __syncwarp();
         if (w + 2 < steps) scores(w + 2);
       }
       n += tiles;
     }
     // nothing is in flight when TMEM is given back
-    tc_commit(finished, lead);
+    if (elect_one()) tc_commit(finished);
+    __syncwarp();
     const uint64_t limit = globaltimer() + 10000000;
     while (!mbar_try_wait(finished, 0) && globaltimer() < limit) {
     }
