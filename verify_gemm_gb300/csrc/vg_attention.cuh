@@ -72,7 +72,7 @@ struct AttnParams {
   int batch, n, hq, hkv, d, q_f16;
   int rows, blocks;                 // rows that share a cache head, row blocks of a unit
   int tile_log2;                    // keys of a tile
-  int box, least, extra;            // tokens of a TMA box; tiles: of a run at least, a unit costs
+  int box, least, extra, snap;      // tokens of a TMA box; tiles: of a run at least, a unit costs, a cut moves
   float c, v_scale;                 // scale * k_scale * log2 e
 };
 
@@ -231,11 +231,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 // sequence b, and the unit's tiles [t0, t1) that are the block's.  A unit's
 // place on the line is `extra` + its tiles long, as beginning and joining a
 // unit costs about as much as `extra` tiles: without that, blocks with a
-// second unit ended 7 us after the others (39 us in all).
+// second unit ended 7 us after the others (39 us in all).  A cut less than
+// `snap` places from a unit's end moves there: it would cost a joining.
 struct Line {
   int64_t total, end, unit0;        // the line's length, the run's end, where the unit begins
   int64_t runs;                     // blocks that have a run
-  int b, u, units, extra, tiles, t0, t1;
+  int b, u, units, extra, snap, tiles, t0, t1;
   int len, count;
 
   __device__ __forceinline__ static int used(const AttnParams &p, int b, int &len) {
@@ -254,6 +255,7 @@ struct Line {
     const int lane = threadIdx.x % 32;
     units = units_;
     extra = p.extra;
+    snap = p.snap;
     auto long_of = [&](int i) { return i < p.batch ? tiles_of(p, i) + extra : 0; };
     const int own = long_of(lane);              // of the first 32 sequences
     int64_t sum = own;
@@ -301,11 +303,16 @@ struct Line {
     tiles = length - extra;
     const int off = int(in - int64_t(u) * length);
     unit0 = at - off;
-    t0 = max(0, off - extra);
-    fill(p);
+    t0 = off <= snap ? 0 : max(0, off - extra);
+    if (off > snap && length - off <= snap)
+      next(p);                                  // the run begins with the unit after
+    else
+      fill(p);
   }
   __device__ __forceinline__ void fill(const AttnParams &p) {
-    t1 = int(min(int64_t(tiles), end - unit0 - extra));
+    const int64_t cut = end - unit0;            // where the run ends, from the unit's beginning
+    const int length = tiles + extra;
+    t1 = cut >= length ? tiles : cut <= snap ? 0 : length - cut <= snap ? tiles : max(0, int(cut) - extra);
     if (t0 < t1) count = used(p, b, len);
   }
   __device__ __forceinline__ bool valid() const { return t0 < t1; }
@@ -313,7 +320,7 @@ struct Line {
     unit0 += tiles + extra;
     t0 = 0;
     t1 = 0;
-    if (unit0 + extra >= end) return;
+    if (unit0 >= end) return;
     if (++u == units) {
       u = 0;
       ++b;
@@ -321,9 +328,17 @@ struct Line {
     }
     fill(p);
   }
-  // The block that holds tile t of the unit.
-  __device__ __forceinline__ int block_of(int t) const {
-    const int64_t x = (unit0 + extra + t + 1) * runs + total - 1;
+  // The blocks that hold the unit's first tile and its last: a cut up to
+  // max(snap, extra) begins a run at tile 0, and one in the last `snap` places
+  // at the next unit.
+  __device__ __forceinline__ int first() const { return block_of(unit0 + min(max(snap, extra), latest())); }
+  __device__ __forceinline__ int final() const { return block_of(unit0 + latest()); }
+  __device__ __forceinline__ int latest() const {
+    return min(tiles + extra - 1, max(snap, tiles + extra - snap - 1));
+  }
+  // The last block whose run, before its cuts are moved, begins at place x or before.
+  __device__ __forceinline__ int block_of(int64_t place) const {
+    const int64_t x = (place + 1) * runs + total - 1;
     return (x < int64_t(1) << 32 ? int(uint32_t(x) / uint32_t(total)) : int(x / total)) - 1;
   }
 };
@@ -796,7 +811,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 
     // ------------------------------------- join the key warps, then the blocks
-    const int first = at.block_of(0), final = at.block_of(at.tiles - 1);
+    const int first = at.first(), final = at.final();
     const bool whole = first == final;
     // a block's partial result: its unit's first block has it in its second place
     auto place = [&](int block) {

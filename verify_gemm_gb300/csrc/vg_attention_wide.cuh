@@ -297,33 +297,51 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
     uint32_t n = 0, steps = 0, units = 0;                // tiles, this stream's steps and units so far
     auto sync_rows = [&] { named_bar(1, 256); };
-    for (; at.valid(); at.next(p)) {
+    // q to shared memory, sixteen lanes a row, by way of registers: the next
+    // unit's q is fetched and stored, and its first scores made, while this
+    // unit's output is still written
+    constexpr int kQn = L::kRows / 16;
+    uint4 qv[kQn];
+    const int piece = lane % 16;
+    auto row_of = [&](int k) {                           // with two row tiles, the stream's own
+      return NQ == 2 ? q * 128 + k * 8 + warp % 4 * 2 + lane / 16 : k * 16 + warp * 2 + lane / 16;
+    };
+    auto fetch_q = [&](const Line &u) {
+      const int head = u.u / p.blocks, row0 = u.u % p.blocks * L::kRows;
+#pragma unroll
+      for (int k = 0; k < kQn; ++k) {
+        const int rw = row0 + row_of(k);
+        qv[k] = make_uint4(0, 0, 0, 0);
+        if (rw < p.rows && piece * 8 < p.d)
+          qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
+                                                   (rw / group) * p.qs[1] +
+                                                   (head * group + rw % group) * p.qs[2] + piece * 8);
+      }
+    };
+    auto store_q = [&] {
+#pragma unroll
+      for (int k = 0; k < kQn; ++k) {
+        const int r = row_of(k);
+        if (piece < DC * 8)
+          *reinterpret_cast<uint4 *>(q_smem + (r / 128) * L::kQTile + (piece / 8) * L::kQChunk +
+                                     (r % 128) * 128 + (((piece % 8) ^ (r & 7)) << 4)) =
+              make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip);
+      }
+      fence_proxy_async();
+      mbar_arrive(q_full);
+    };
+    uint32_t other = 0;                                  // the other stream's steps so far
+    if (at.valid()) {
+      fetch_q(at);
+      store_q();
+    }
+    for (; at.valid();) {
+      Line after = at;
+      after.next(p);
       const int head = at.u / p.blocks, rb = at.u % p.blocks;
       const int row0 = rb * L::kRows, row = row0 + (NQ == 2 ? q * 128 : 0) + row_in;
       const int node = row / group, h = head * group + row % group;
       const bool real = row < p.rows;
-      // q to shared memory, sixteen lanes a row
-      {
-        const int piece = lane % 16;
-#pragma unroll 4
-        for (int r = warp * 2 + lane / 16; r < L::kRows; r += 16) {
-          const int rw = row0 + r;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (rw < p.rows && piece * 8 < p.d)
-            v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at.b * p.qs[0] +
-                                                 (rw / group) * p.qs[1] +
-                                                 (head * group + rw % group) * p.qs[2] + piece * 8);
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
-          if (piece < DC * 8)
-            *reinterpret_cast<uint4 *>(q_smem + (r / 128) * L::kQTile + (piece / 8) * L::kQChunk +
-                                       (r % 128) * 128 + (((piece % 8) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async();
-        mbar_arrive(q_full);
-      }
       uint64_t word = 0;
       if (real)
         word = (at.count >= 64 ? ~0ull : (1ull << at.count) - 1) &
@@ -474,6 +492,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       }
       n += tiles;
+      if (NQ == 1) other += uint32_t(q ? (tiles + 1) / 2 : tiles / 2);
+      if (after.valid()) {
+        fetch_q(after);
+        // both streams read the one row tile: the other's scores are made, too
+        if (NQ == 1 && other) wait_phase(s_full + 8 * (1 - q), (other - 1) & 1, failed, p.error);
+        store_q();
+      }
 
       // ----------------------------------------------------------- results
       const bool some = NQ == 2 || q == 0 || tiles > 1;  // whether the stream had a tile
@@ -513,7 +538,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
       };
-      const int first = at.block_of(0), final = at.block_of(at.tiles - 1);
+      const int first = at.first(), final = at.final();
       const bool whole = first == final;
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
       uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
@@ -615,6 +640,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // the outputs are read and *last is free before the next unit begins
       tc_before();
       sync_rows();
+      at = after;
     }
   }
   tc_before();
