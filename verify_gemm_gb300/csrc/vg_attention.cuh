@@ -152,11 +152,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 codes (the low 16 bits) as FP16, exact.
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
-  uint32_t y;
-  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(y) : "r"(w));
-  return y;
+// Four E4M3 codes as FP16 pairs, exact.
+__device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2;\n"
+      "cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 template <int kType>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -618,10 +619,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 uint32_t b[4];
                 const uint32_t key = key0 + h * 16 + (lane & 15);
                 ldsm4(b, kb + spot<L>(key, ks, lane >> 4));
-                mma<kType>(sc[0][2 * h], a, e4m3_f16(b[0]), e4m3_f16(b[0] >> 16));
-                mma<kType>(sc[0][2 * h + 1], a, e4m3_f16(b[1]), e4m3_f16(b[1] >> 16));
-                mma<kType>(sc[kSets - 1][2 * h], a2, e4m3_f16(b[2]), e4m3_f16(b[2] >> 16));
-                mma<kType>(sc[kSets - 1][2 * h + 1], a2, e4m3_f16(b[3]), e4m3_f16(b[3] >> 16));
+                uint32_t k0[4], k1[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) e4m3_f16(b[e], k0[e], k1[e]);
+                mma<kType>(sc[0][2 * h], a, k0[0], k1[0]);
+                mma<kType>(sc[0][2 * h + 1], a, k0[1], k1[1]);
+                mma<kType>(sc[kSets - 1][2 * h], a2, k0[2], k1[2]);
+                mma<kType>(sc[kSets - 1][2 * h + 1], a2, k0[3], k1[3]);
               }
             }
           } else {
@@ -741,9 +745,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   ldsm4t(b, vb + spot<L>(key, i, lane >> 4));
 #pragma unroll
                   for (int k = 0; k < 2; ++k) {
-                    const uint32_t w0 = prmt(b[2 * k], 0, 0x3120), w1 = prmt(b[2 * k + 1], 0, 0x3120);
-                    mma<kType>(o[2 * (i + k)], pf[h], e4m3_f16(w0), e4m3_f16(w1));
-                    mma<kType>(o[2 * (i + k) + 1], pf[h], e4m3_f16(w0 >> 16), e4m3_f16(w1 >> 16));
+                    uint32_t v0[2], v1[2];
+                    e4m3_f16(prmt(b[2 * k], 0, 0x3120), v0[0], v1[0]);
+                    e4m3_f16(prmt(b[2 * k + 1], 0, 0x3120), v0[1], v1[1]);
+                    mma<kType>(o[2 * (i + k)], pf[h], v0[0], v0[1]);
+                    mma<kType>(o[2 * (i + k) + 1], pf[h], v1[0], v1[1]);
                   }
                 }
               } else {
@@ -767,11 +773,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               uint32_t b[4];
               if constexpr (kType == kE4M3) {
                 ldsm4t(b, vb + spot<L>(key, i));
-                const uint32_t w0 = prmt(b[0], 0, 0x3120), w1 = prmt(b[1], 0, 0x3120);
-                b[0] = e4m3_f16(w0);
-                b[1] = e4m3_f16(w1);
-                b[2] = e4m3_f16(w0 >> 16);
-                b[3] = e4m3_f16(w1 >> 16);
+                e4m3_f16(prmt(b[0], 0, 0x3120), b[0], b[2]);
+                e4m3_f16(prmt(b[1], 0, 0x3120), b[1], b[3]);
               } else {
                 ldsm4t(b, vb + spot<L>(key, 2 * i, lane >> 4));
               }
@@ -794,7 +797,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   const uint8_t *at16 = ring + sv * L::kSlot + spot<L>(key0 + k, col * L::kSize / 16);
                   float v;
                   if constexpr (kType == kE4M3) {
-                    v = __half2float(__ushort_as_half(uint16_t(e4m3_f16(at16[col % 16]))));
+                    uint32_t lo, hi;
+                    e4m3_f16(at16[col % 16], lo, hi);
+                    v = __half2float(__ushort_as_half(uint16_t(lo)));
                   } else {
                     const uint16_t c = *reinterpret_cast<const uint16_t *>(at16 + (col % 8) * 2);
                     v = kType == kBf16 ? __bfloat162float(__ushort_as_bfloat16(c))
