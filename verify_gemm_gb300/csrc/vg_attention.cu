@@ -27,6 +27,18 @@ int cache_type(const vg_kv_cache &c) {
   return c.type == VG_TYPE_E4M3 ? kE4M3 : c.type == VG_TYPE_FP16 ? kF16 : kBf16;
 }
 
+// Lets the kernel have its shared memory, once for each device.
+vg_status allow_smem(const Variant &v) {
+  int dev = 0;
+  VG_CUDA(cudaGetDevice(&dev));
+  const uint64_t bit = uint64_t(1) << (dev & 63);       // device_sms refuses higher numbers
+  if (v.allowed->load(std::memory_order_relaxed) & bit) return VG_OK;
+  VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(v.fn),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem));
+  v.allowed->fetch_or(bit, std::memory_order_relaxed);
+  return VG_OK;
+}
+
 size_t workspace_bytes_of(const Variant &v, int sms) {
   return kHeader + kMaxGrid * sizeof(uint32_t) + size_t(sms) * 2 * size_t(v.partial) * sizeof(float);
 }
@@ -110,8 +122,7 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   alignas(64) CUtensorMap kmap, vmap;
   std::memcpy(&kmap, cache->opaque, sizeof kmap);
   std::memcpy(&vmap, cache->opaque + kCacheMapWords, sizeof vmap);
-  VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(v.fn),
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem));
+  if (vg_status s = allow_smem(v)) return s;
   v.fn<<<grid, kAttnThreads, size_t(v.smem), as_cuda(stream)>>>(p, kmap, vmap);
   VG_LAUNCH_CHECK();
   return VG_OK;

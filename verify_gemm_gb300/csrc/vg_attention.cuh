@@ -29,6 +29,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "vg_cache.h"
@@ -996,12 +997,15 @@ using Kernel = void (*)(AttnParams, CUtensorMap, CUtensorMap);
 struct Variant {
   Kernel fn;
   int smem, rows, partial;
+  std::atomic<uint64_t> *allowed;   // bit d: device d lets fn have its shared memory
 };
 
 template <int kType, int DC, int RW>
 Variant variant() {
   using L = Cfg<kType, DC, RW>;
-  return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW>), L::kSmem, L::kRows, L::kPartial};
+  static std::atomic<uint64_t> allowed{0};
+  return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW>), L::kSmem, L::kRows, L::kPartial,
+          &allowed};
 }
 
 // The variants of one cache type, by head_dim up to 64, 128, 256 and by row

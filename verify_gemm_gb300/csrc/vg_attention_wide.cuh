@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 template <int kType, int DC, int NQ>
 Variant wide_variant() {
   using L = WideCfg<DC, NQ>;
-  return {reinterpret_cast<Kernel>(&wide_kernel<kType, DC, NQ>), L::kSmem, L::kRows, L::kPartial};
+  static std::atomic<uint64_t> allowed{0};
+  return {reinterpret_cast<Kernel>(&wide_kernel<kType, DC, NQ>), L::kSmem, L::kRows, L::kPartial, &allowed};
 }
 
 }  // namespace attn

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -615,9 +616,19 @@ extern "C" vg_status vg_verify_tree(const float *p, const float *q, const int32_
   c = std::max<int64_t>(1, std::min(c, vocab / (kVerWarps * 128)));
   const unsigned grid = unsigned(batch) * unsigned(c);
   void (*fn)(VerifyParams) = vocab % 4 ? &verify_kernel<false> : &verify_kernel<true>;
-  if (c > 8)
-    VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  if (c > 8) {
+    // once for each device and kernel
+    static std::atomic<uint64_t> allowed[2];
+    int dev = 0;
+    VG_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = uint64_t(1) << (dev & 63);     // device_sms refuses higher numbers
+    std::atomic<uint64_t> &a = allowed[vocab % 4 ? 0 : 1];
+    if (!(a.load(std::memory_order_relaxed) & bit)) {
+      VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+      a.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
   VG_CUDA(launch_clusters(fn, grid, kVerThreads, int(c), 0, as_cuda(stream), v));
   VG_LAUNCH_CHECK();
   return VG_OK;

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -21,6 +22,14 @@ from ._lib import (VG_ROPE_HALF, VG_ROPE_INTERLEAVED, VG_TYPE_BF16, VG_TYPE_E4M3
 _TYPES = {torch.bfloat16: VG_TYPE_BF16, torch.float16: VG_TYPE_FP16, torch.float32: VG_TYPE_FP32,
           torch.float8_e4m3fn: VG_TYPE_E4M3}
 _LAYOUTS = {"half": VG_ROPE_HALF, "interleaved": VG_ROPE_INTERLEAVED}
+_CONTIGUOUS = torch.contiguous_format
+
+# The descriptors as bytes (vg_rope_desc, vg_attention_desc of include/vgemm.h):
+# packing them takes a third of the time that filling a ctypes structure does.
+_ROPE_DESC = struct.Struct("@4P9q4P5if0q")
+_ATTENTION_DESC = struct.Struct("@6P3q3if0q")
+assert _ROPE_DESC.size == ctypes.sizeof(vg_rope_desc)
+assert _ATTENTION_DESC.size == ctypes.sizeof(vg_attention_desc)
 
 
 def _stream(stream, device):
@@ -148,16 +157,17 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
     if layout not in _LAYOUTS:
         raise ValueError("layout: 'half' or 'interleaved'")
     if q_out is None:
-        q_out = torch.empty((B, n, hq, d), dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     elif not (q_out.is_cuda and q_out.shape == q.shape and q_out.dtype == q.dtype
               and q_out.is_contiguous()):
         raise ValueError("q_out: expected a contiguous CUDA tensor like q")
-    desc = vg_rope_desc(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                        qs, ks, vs, inv_freq.data_ptr(),
-                        _int32(lens, (B,), "lens"), _int32(depth, (B, n), "depth") if depth is not None else None,
-                        _int32(counts, (B,), "counts") if counts is not None else None, _TYPES.get(q.dtype, -1), _LAYOUTS[layout],
-                        n, hq, 2 * inv_freq.numel(), factor)
-    s = _lib.load().vg_rope_append(ctypes.byref(desc), cache._ref, _stream(stream, q.get_device()))
+    desc = _ROPE_DESC.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *qs, *ks, *vs,
+        inv_freq.data_ptr(), _int32(lens, (B,), "lens"),
+        _int32(depth, (B, n), "depth") if depth is not None else 0,
+        _int32(counts, (B,), "counts") if counts is not None else 0,
+        _TYPES.get(q.dtype, -1), _LAYOUTS[layout], n, hq, 2 * inv_freq.numel(), factor)
+    s = _lib.load().vg_rope_append(desc, cache._ref, _stream(stream, q.get_device()))
     if s:
         _lib.check(s, "vg_rope_append")
     return q_out
@@ -194,7 +204,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
                                  and tree.is_contiguous() and tree.shape == (B, n)):
         raise ValueError("tree: expected a contiguous CUDA int64 tensor [batch, n]")
     if out is None:
-        out = torch.empty((B, n, hq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     elif not (out.is_cuda and out.shape == q.shape and out.dtype == q.dtype
               and out.is_contiguous()):
         raise ValueError("out: expected a contiguous CUDA tensor like q")
@@ -203,12 +213,13 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
         raise ValueError("lse: expected a contiguous CUDA float32 tensor [batch, n, q_heads]")
     if workspace is None:
         workspace = tree_attention_workspace(q, cache)
-    desc = vg_attention_desc(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                             _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts") if counts is not None else None,
-                             tree.data_ptr() if tree is not None else None, qs,
-                             _TYPES.get(q.dtype, -1), n, hq, d ** -0.5 if scale is None else scale)
-    s = _lib.load().vg_tree_attention(ctypes.byref(desc), cache._ref, workspace.data_ptr(),
-                               workspace.numel(), _stream(stream, q.get_device()))
+    desc = _ATTENTION_DESC.pack(
+        q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
+        _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts") if counts is not None else 0,
+        tree.data_ptr() if tree is not None else 0, *qs, _TYPES.get(q.dtype, -1), n, hq,
+        d ** -0.5 if scale is None else scale)
+    s = _lib.load().vg_tree_attention(desc, cache._ref, workspace.data_ptr(), workspace.numel(),
+                                      _stream(stream, q.get_device()))
     if s:
         _lib.check(s, "vg_tree_attention")
     return out
@@ -229,7 +240,7 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
                                         and temperature.numel() == rows):
         raise ValueError("temperature: expected a contiguous CUDA float32 tensor, one for each row")
     if out is None:
-        out = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+        out = torch.empty_like(logits, dtype=torch.float32)
     elif not (out.is_cuda and out.shape == logits.shape and out.dtype == torch.float32
               and out.is_contiguous()):
         raise ValueError("out: expected a contiguous CUDA float32 tensor like logits")
@@ -260,16 +271,14 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
         raise ValueError("q: expected a contiguous CUDA float32 tensor [batch, rows, vocab]")
     if not (u.is_cuda and u.dtype == torch.float32 and u.is_contiguous() and u.shape == (B, n)):
         raise ValueError("u: expected a contiguous CUDA float32 tensor [batch, n]")
-    # one allocation for the three results
-    flat = torch.empty(B * (2 * n + 2), dtype=torch.int32, device=p.device)
-    accepted, path, out = flat.split_with_sizes((B, B * n, B * (n + 1)))
-    path, out = path.view(B, n), out.view(B, n + 1)
-    at = flat.data_ptr()
-    s = _lib.load().vg_verify_tree(p.data_ptr(), q.data_ptr() if q is not None else None,
-                            _int32(tokens, (B, n), "tokens"), _int32(parents, (B, n), "parents"),
-                            _int32(counts, (B,), "counts") if counts is not None else None, u.data_ptr(), B, n,
-                            q.shape[1] if q is not None else 0, V, at, at + 4 * B,
-                            at + 4 * B * (n + 1), _stream(stream, p.get_device()))
+    accepted, path, out = (torch.empty(shape, dtype=_int32_t, device=p.device)
+                           for shape in ((B,), (B, n), (B, n + 1)))
+    s = _lib.load().vg_verify_tree(
+        p.data_ptr(), q.data_ptr() if q is not None else None, _int32(tokens, (B, n), "tokens"),
+        _int32(parents, (B, n), "parents"),
+        _int32(counts, (B,), "counts") if counts is not None else None, u.data_ptr(), B, n,
+        q.shape[1] if q is not None else 0, V, accepted.data_ptr(), path.data_ptr(), out.data_ptr(),
+        _stream(stream, p.get_device()))
     if s:
         _lib.check(s, "vg_verify_tree")
     return accepted, path, out
