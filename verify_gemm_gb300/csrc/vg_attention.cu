@@ -11,14 +11,14 @@ namespace {
 using namespace attn;
 
 // tcgen05 where mma.sync would set the pace.
-bool is_wide(int type, int d, int rows) { return type != kE4M3 && d <= 128 && rows > 32; }
+bool is_wide(int d, int rows) { return d <= 128 && rows > 32; }
 
 // Row groups: the fewest that hold the rows of a head, so that as many warps
 // as can share out the keys; above 128 rows, blocks of 128.
 int row_index(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
 const Variant &pick(int type, int d, int rows) {
-  if (is_wide(type, d, rows)) return kWide[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
+  if (is_wide(d, rows)) return kWide[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
   const Variants &of = type == kBf16 ? kVariantsBf16 : type == kF16 ? kVariantsF16 : kVariantsE4M3;
   return of[d <= 64 ? 0 : d <= 128 ? 1 : 2][row_index(rows)];
 }
@@ -107,7 +107,7 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   // beside its tiles (512 KB with its outputs of 128 rows and more), and a cut
   // that moves by less saves more than it unbalances (measured over 0 to 12
   // tiles of 32 and of 64 KB).
-  const bool wide = is_wide(type, p.d, rows);
+  const bool wide = is_wide(p.d, rows);
   p.tile_log2 = wide ? 7 : 6;
   const int tile_bytes = (2 * p.d * (type == kE4M3 ? 1 : 2)) << p.tile_log2;
   p.least = std::max(1, 131072 / tile_bytes);
@@ -123,7 +123,7 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   std::memcpy(&kmap, cache->opaque, sizeof kmap);
   std::memcpy(&vmap, cache->opaque + kCacheMapWords, sizeof vmap);
   if (vg_status s = allow_smem(v)) return s;
-  v.fn<<<grid, kAttnThreads, size_t(v.smem), as_cuda(stream)>>>(p, kmap, vmap);
+  v.fn<<<grid, v.threads, size_t(v.smem), as_cuda(stream)>>>(p, kmap, vmap);
   VG_LAUNCH_CHECK();
   return VG_OK;
 }

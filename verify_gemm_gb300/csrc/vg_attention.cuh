@@ -172,6 +172,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ uint32_t pack_out(float a, float b, bool f16) {
   return f16 ? pack2<kF16>(a, b) : pack2<kBf16>(a, b);
 }
+// The power of two that a row of q with this largest magnitude is divided by
+// before it goes to FP16: it brings the row to the top of FP16's range.
+__device__ __forceinline__ int q_exponent(float top) {
+  int e = 0;
+  if (top > 0.f && top < INFINITY) {
+    frexpf(top, &e);
+    e = min(max(e - 14, -100), 120);
+  }
+  return e;
+}
 // Nonzero where one of the cache's elements in a word is infinite or NaN: x 0
 // is a NaN then, else a zero; of E4M3 codes only 0x7F and 0xFF are.
 template <int kType>
@@ -522,11 +532,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
 #pragma unroll
         for (int m = 16; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
-        int e = 0;
-        if (top > 0.f && top < INFINITY) {
-          frexpf(top, &e);
-          e = min(max(e - 14, -100), 120);
-        }
+        const int e = q_exponent(top);
         const float down = ldexpf(1.f, -e);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= down;
@@ -996,7 +1002,7 @@ using Kernel = void (*)(AttnParams, CUtensorMap, CUtensorMap);
 
 struct Variant {
   Kernel fn;
-  int smem, rows, partial;
+  int smem, rows, partial, threads;
   std::atomic<uint64_t> *allowed;   // bit d: device d lets fn have its shared memory
 };
 
@@ -1005,7 +1011,7 @@ Variant variant() {
   using L = Cfg<kType, DC, RW>;
   static std::atomic<uint64_t> allowed{0};
   return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW>), L::kSmem, L::kRows, L::kPartial,
-          &allowed};
+          kAttnThreads, &allowed};
 }
 
 // The variants of one cache type, by head_dim up to 64, 128, 256 and by row
@@ -1013,15 +1019,16 @@ Variant variant() {
 using Variants = Variant[3][4];
 extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
 
-// The tcgen05 kernel (vg_attention_wide.cuh): BF16 and FP16, head_dim up to 64
+// The tcgen05 kernel (vg_attention_wide.cuh): by cache type, head_dim up to 64
 // and 128, one and two row tiles of 128.
-using WideVariants = Variant[2][2][2];
+using WideVariants = Variant[3][2][2];
 extern const WideVariants kWide;
 
-#define VG_ATTENTION_ROWS(T, DC) \
-  {variant<T, DC, 1>(), variant<T, DC, 2>(), variant<T, DC, 4>(), variant<T, DC, 8>()}
-#define VG_ATTENTION_VARIANTS(T) \
-  {VG_ATTENTION_ROWS(T, 1), VG_ATTENTION_ROWS(T, 2), VG_ATTENTION_ROWS(T, 4)}
+// (Heads up to 128 go to the tcgen05 kernel above 32 rows.)
+#define VG_ATTENTION_VARIANTS(T)                      \
+  {{variant<T, 1, 1>(), variant<T, 1, 2>()},          \
+   {variant<T, 2, 1>(), variant<T, 2, 2>()},          \
+   {variant<T, 4, 1>(), variant<T, 4, 2>(), variant<T, 4, 4>(), variant<T, 4, 8>()}}
 
 }  // namespace attn
 }  // namespace vg

@@ -1,12 +1,11 @@
-// vg_attention_wide.cu -- the tcgen05 attention kernel over 16-bit caches.
+// vg_attention_wide.cu -- the tcgen05 attention kernel with its variants.
 #include "vg_attention_wide.cuh"
 
 namespace vg {
 namespace attn {
-const WideVariants kWide = {
-    {{wide_variant<kBf16, 1, 1>(), wide_variant<kBf16, 1, 2>()},
-     {wide_variant<kBf16, 2, 1>(), wide_variant<kBf16, 2, 2>()}},
-    {{wide_variant<kF16, 1, 1>(), wide_variant<kF16, 1, 2>()},
-     {wide_variant<kF16, 2, 1>(), wide_variant<kF16, 2, 2>()}}};
+#define VG_WIDE(T)                                      \
+  {{wide_variant<T, 1, 1>(), wide_variant<T, 1, 2>()},  \
+   {wide_variant<T, 2, 1>(), wide_variant<T, 2, 2>()}}
+const WideVariants kWide = {VG_WIDE(kBf16), VG_WIDE(kF16), VG_WIDE(kE4M3)};
 }  // namespace attn
 }  // namespace vg

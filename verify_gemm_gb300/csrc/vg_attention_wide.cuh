@@ -20,6 +20,9 @@
 // A row's maximum may lag by up to 2^8: O is rescaled, in TMEM by its softmax
 // warpgroup, only when the true maximum is more than 8 above the one in use,
 // and l carries the same factor.
+// Codes of an E4M3 cache are copied as they are and turned into FP16 by a
+// fourth warpgroup, tile by tile, into the slots that the products read; q is
+// brought to FP16 by a power of two for each row, which goes into its c.
 // The cutting of the line, the pages and the joining of blocks are those of
 // vg_attention.cuh.
 #pragma once
@@ -29,28 +32,45 @@
 namespace vg {
 namespace attn {
 
-constexpr int kWideThreads = 384;
-// Registers a thread: 168 at the launch (384 x 168 = 64512), then 256 x 216 +
-// 128 x 72 = 64512: a softmax thread holds a row of 128 scores.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// Threads: two softmax warpgroups, one that copies and issues, and for E4M3
+// one that converts.  Registers a thread: 168 at a launch of 384 (64512 in
+// all), then 256 x 216 + 128 x 72 = 64512: a softmax thread holds a row of 128
+// scores; 128 at a launch of 512 (65536), then 256 x 184 + 128 x 64 + 128 x 80
+// = 65536, and the scores are read from TMEM twice instead.
+template <bool kF8>
+struct WideThreads {
+  static constexpr int kThreads = kF8 ? 512 : 384;
+  static constexpr int kSoftmax = kF8 ? 184 : 216, kOther = kF8 ? 64 : 72, kConvert = 80;
+};
 constexpr float kLag = 8.f;                   // log2 of what a maximum may lag
 // FP16 weights are at most 2^kLag times 2^lift: lifted to 2^15 in all.
 template <int kType>
 constexpr float kWideLift = kType == kBf16 ? 0.f : 7.f;
 
-template <int DC, int NQ>
+template <int kCache, int DC, int NQ>
 struct WideCfg {
+  static constexpr bool kF8 = kCache == kE4M3;
+  static constexpr int kType = kF8 ? kF16 : kCache;      // of the products
   static constexpr int D = DC * 64;
   static constexpr int kRow = 128, kElems = 64, kChunks = DC, kKeys = 128;
   static constexpr int kChunk = kKeys * kRow;            // 16 KB
   static constexpr int kSlot = DC * kChunk;
+  // an E4M3 tile as it is copied
+  struct Stage {
+    static constexpr int kRow = DC == 1 ? 64 : 128, kElems = kRow, kChunks = 1, kKeys = 128;
+    static constexpr int kChunk = kKeys * kRow, kSlot = kChunk;
+  };
   static constexpr int kQChunk = 128 * 128;              // 128 rows of 64 elements
   static constexpr int kQTile = DC * kQChunk;
   static constexpr int kRows = 128 * NQ;
-  static constexpr int kFixed = 1024 + 2 * 128 * 8;
-  static constexpr int kFit = (227 * 1024 - 1024 - kFixed - NQ * kQTile) / kSlot;
-  static constexpr int kSlots = (kFit > 16 ? 16 : kFit) & ~1;
-  static constexpr int kSmem = 1024 + kFixed + NQ * kQTile + kSlots * kSlot;
+  static constexpr int kFixed = 3072;
+  static constexpr int kRoom = 227 * 1024 - kFixed - NQ * kQTile;
+  static constexpr int kFit = kRoom / kSlot;
+  static constexpr int kSlots = kF8 ? 4 : (kFit > 16 ? 16 : kFit) & ~1;
+  static constexpr int kStageFit = (kRoom - kSlots * kSlot) / Stage::kSlot;
+  static constexpr int kStages = kF8 ? (kStageFit > 8 ? 8 : kStageFit) & ~1 : 0;
+  static constexpr int kSmem = kFixed + NQ * kQTile + kSlots * kSlot + kStages * Stage::kSlot;
+  static_assert(!kF8 || kStages >= 2, "room for codes of K and of V");
   static constexpr int kPartial = kRows * (D + 2);       // floats of a partial result
   static constexpr uint32_t kO = 0, kS = 256;            // TMEM columns
 };
@@ -147,29 +167,37 @@ __device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
-template <int kType, int DC, int NQ>
-__global__ void __launch_bounds__(kWideThreads, 1)
+template <int kCache, int DC, int NQ>
+__global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
     wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
-  using L = WideCfg<DC, NQ>;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *ring = smem;
-  uint8_t *q_smem = smem + L::kSlots * L::kSlot;
-  uint8_t *fixed = q_smem + NQ * L::kQTile;
+  using L = WideCfg<kCache, DC, NQ>;
+  using W = WideThreads<L::kF8>;
+  constexpr int kType = L::kType;
+  extern __shared__ __align__(1024) uint8_t wide_smem[];
+  if (smem_addr(wide_smem) & 1023) {                     // the swizzles need it
+    if (threadIdx.x == 0) atomicCAS(p.error, 0, kErrAttnWait);
+    return;
+  }
+  uint8_t *ring = wide_smem;
+  uint8_t *q_smem = ring + L::kSlots * L::kSlot;
+  uint8_t *stage = q_smem + NQ * L::kQTile;
+  uint8_t *fixed = stage + L::kStages * L::Stage::kSlot;
   uint64_t *bars = reinterpret_cast<uint64_t *>(fixed);
   // barriers: slots full, slots free; of each stream: scores there, weights there
   // (halves), product done; q there; everything done
   const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + 16), s_full = smem_addr(bars + 32),
                  p_full = smem_addr(bars + 34), o_full = smem_addr(bars + 38), q_full = smem_addr(bars + 40),
-                 finished = smem_addr(bars + 41);
+                 finished = smem_addr(bars + 41), stage_full = smem_addr(bars + 42),
+                 stage_empty = smem_addr(bars + 50);
   uint32_t *page_ok = reinterpret_cast<uint32_t *>(fixed + 512);        // [16]
   volatile int *failed = reinterpret_cast<volatile int *>(fixed + 576);
   int *last = reinterpret_cast<int *>(fixed + 580);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(fixed + 584);
   volatile int *keep_o = reinterpret_cast<volatile int *>(fixed + 588); // [stream]
   uint32_t *odd_at = reinterpret_cast<uint32_t *>(fixed + 608);         // [2][4]: bits of keys
-  float2 *state = reinterpret_cast<float2 *>(fixed + 1024);             // [row]: (m, l) of the other stream
+  int8_t *q_exp = reinterpret_cast<int8_t *>(fixed + 640);              // E4M3: [unit % 2][row]
+  float2 *state = reinterpret_cast<float2 *>(fixed + 1024);             // keys split: [stream][row]: (m, l)
   constexpr int NS = L::kSlots;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
@@ -178,8 +206,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     *failed = 0;
     for (int i = 0; i < 8; ++i) odd_at[i] = 0;
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, L::kF8 ? 128 : 1);
       mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(stage_full + 8 * s, 1);
+      mbar_init(stage_empty + 8 * s, 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -205,12 +237,55 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   at.init(p, p.hkv * p.blocks);
   const int group = p.hq / p.hkv;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (L::kF8 && warp >= 12) {
+    // -------------------------------------------------------- conversions
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvert));
+    if constexpr (L::kF8) {
+      using G = typename L::Stage;
+      constexpr int kPieces = G::kRow / 16;              // 16 codes each
+      const int me = tid - 384;
+      uint32_t i = 0;                                    // K and V tiles so far
+      for (; at.valid(); at.next(p)) {
+        for (uint32_t n = 2 * uint32_t(at.t1 - at.t0); n; --n, ++i) {
+          const uint32_t from = i % L::kStages, to = i % NS;
+          wait_phase(stage_full + 8 * from, (i / L::kStages) & 1, failed, p.error);
+          wait_phase(empty0 + 8 * to, (i / NS & 1) ^ 1, failed, p.error);
+          const uint8_t *src = stage + from * G::kSlot;
+          uint8_t *dst = ring + to * L::kSlot;
+          // Eight lanes take four pieces of two keys whose numbers differ in bits
+          // 0 and 2: then neither the loads nor the stores, of pieces 2c and
+          // 2c + 1 of one 128-byte chunk, meet in a bank.
+#pragma unroll 4
+          for (int k = 0; k < G::kKeys * kPieces / 128; ++k) {
+            const int set = k * 4 + me / 32;             // 8 keys, 4 pieces
+            const int key = set / (kPieces / 4) * 8 + (lane / 8 ^ (lane & 4 ? 5 : 0));
+            const int c = set % (kPieces / 4) * 4 + lane % 4;
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + spot<G>(key, c));
+            uint4 a, b;
+            e4m3_f16(v.x, a.x, a.y);
+            e4m3_f16(v.y, a.z, a.w);
+            e4m3_f16(v.z, b.x, b.y);
+            e4m3_f16(v.w, b.z, b.w);
+            *reinterpret_cast<uint4 *>(dst + spot<L>(key, 2 * c)) = a;
+            *reinterpret_cast<uint4 *>(dst + spot<L>(key, 2 * c + 1)) = b;
+          }
+          fence_proxy_async();
+          mbar_arrive(full0 + 8 * to);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stage_empty + 8 * from);
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kOther));
     if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------- copies
     const int kv = warp == 10;
-    copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
+    if constexpr (L::kF8)
+      copy_tiles<typename L::Stage, L::kStages>(p, at, kv ? &vmap : &kmap, kv, smem_addr(stage), stage_full,
+                                                stage_empty, page_ok, failed);
+    else
+      copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
     } else if (warp == 9) {
     // ----------------------------------------------------------- products
     // Step w of a unit is stream w % 2's: tile w / 2 or, with the keys split, w.
@@ -288,12 +363,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kSoftmax));
     const int q = warp / 4, row_in = tid % 128;          // stream, lane of TMEM
     const uint32_t lanes = tmem + (uint32_t(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + L::kO + q * 128, s_at = lanes + L::kS + q * 128;
     // c > 0: its sign goes into q, so that the largest product is the largest score
-    const float c = fmaxf(fabsf(p.c), 1e-30f);
+    float c = fmaxf(fabsf(p.c), 1e-30f);
     const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
     uint32_t n = 0, steps = 0, units = 0;                // tiles, this stream's steps and units so far
     auto sync_rows = [&] { named_bar(1, 256); };
@@ -318,10 +393,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                                    (head * group + rw % group) * p.qs[2] + piece * 8);
       }
     };
-    auto store_q = [&] {
+    auto store_q = [&](int8_t *exps) {
 #pragma unroll
       for (int k = 0; k < kQn; ++k) {
         const int r = row_of(k);
+        if constexpr (L::kF8) {
+          float f[8], top = 0.f;
+          const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint16_t x = uint16_t(w[e / 2] >> (16 * (e & 1)));
+            f[e] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
+            top = fmaxf(top, fabsf(f[e]));
+          }
+#pragma unroll
+          for (int m = 8; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+          const int e = q_exponent(top);
+          const float down = ldexpf(1.f, -e);
+          qv[k] = make_uint4(pack2<kF16>(f[0] * down, f[1] * down), pack2<kF16>(f[2] * down, f[3] * down),
+                             pack2<kF16>(f[4] * down, f[5] * down), pack2<kF16>(f[6] * down, f[7] * down));
+          if (piece == 0) exps[r] = int8_t(e);
+        }
         if (piece < DC * 8)
           *reinterpret_cast<uint4 *>(q_smem + (r / 128) * L::kQTile + (piece / 8) * L::kQChunk +
                                      (r % 128) * 128 + (((piece % 8) ^ (r & 7)) << 4)) =
@@ -331,11 +423,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_arrive(q_full);
     };
     uint32_t other = 0;                                  // the other stream's steps so far
+    uint32_t unit = 0;
     if (at.valid()) {
       fetch_q(at);
-      store_q();
+      store_q(q_exp);
+      if (L::kF8) sync_rows();                           // everybody's exponents are there
     }
-    for (; at.valid();) {
+    for (; at.valid(); ++unit) {
+      if constexpr (L::kF8)
+        c = fmaxf(fabsf(p.c) * ldexpf(1.f, q_exp[unit % 2 * L::kRows + (NQ == 2 ? q * 128 : 0) + row_in]),
+                  1e-30f);
       Line after = at;
       after.next(p);
       const int head = at.u / p.blocks, rb = at.u % p.blocks;
@@ -434,19 +531,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sync_tile();
           }
         }
+        // 32 columns of scores, masked
+        auto scores = [&](uint32_t (&x)[32], int k) {
+          if (!open) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(sees[k / 2] >> (32 * (k % 2) + e) & 1)) x[e] = 0xFF800000u;
+          }
+        };
         uint32_t x[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tc_ld32(x[k], s_at + 32 * k);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tc_wait_ld(x[k]);
-        if (!open) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (!(sees[k / 64] >> (k % 64) & 1)) x[k / 32][k % 32] = 0xFF800000u;
-        }
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        constexpr int kAtOnce = L::kF8 ? 2 : 4;          // loads of 32 columns held
 #pragma unroll
-        for (int k = 0; k < 128; ++k) t4[k % 4] = fmaxf(t4[k % 4], __uint_as_float(x[k / 32][k % 32]));
+        for (int k0 = 0; k0 < 4; k0 += kAtOnce) {
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) tc_ld32(x[k], s_at + 32 * (k0 + k));
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) tc_wait_ld(x[k]);
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            scores(x[k], k0 + k);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t4[e % 4] = fmaxf(t4[e % 4], __uint_as_float(x[k][e]));
+          }
+        }
         const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
         const bool raise = top > m + kLag || (m == -INFINITY && top > m);
         // (all lanes of the warp take part in the TMEM accesses)
@@ -473,10 +581,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          if constexpr (L::kF8) {
+            // (the first half's weights lie where its scores were)
+            tc_ld32(x[0], s_at + 64 * half);
+            tc_ld32(x[1], s_at + 64 * half + 32);
+            tc_wait_ld(x[0]);
+            tc_wait_ld(x[1]);
+            scores(x[0], 2 * half);
+            scores(x[1], 2 * half + 1);
+          }
           uint32_t w[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const uint32_t *xs = &x[2 * half + k / 16][k % 16 * 2];
+            const uint32_t *xs = &x[(L::kF8 ? 0 : 2 * half) + k / 16][k % 16 * 2];
             float a, b;
             fma2(a, b, xs[0], xs[1], c, -base);
             a = ex2(a);
@@ -497,7 +614,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         fetch_q(after);
         // both streams read the one row tile: the other's scores are made, too
         if (NQ == 1 && other) wait_phase(s_full + 8 * (1 - q), (other - 1) & 1, failed, p.error);
-        store_q();
+        store_q(q_exp + (unit + 1) % 2 * L::kRows);
       }
 
       // ----------------------------------------------------------- results
@@ -550,9 +667,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             float z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = empty ? 0.f : y[k + e] * inv;
+            const bool f16 = L::kF8 ? p.q_f16 != 0 : kType == kF16;
             *reinterpret_cast<uint4 *>(out + c + k) =
-                make_uint4(pack2<kType>(z[0], z[1]), pack2<kType>(z[2], z[3]),
-                           pack2<kType>(z[4], z[5]), pack2<kType>(z[6], z[7]));
+                make_uint4(pack_out(z[0], z[1], f16), pack_out(z[2], z[3], f16),
+                           pack_out(z[4], z[5], f16), pack_out(z[6], z[7], f16));
           }
       };
       auto store_lse = [&](float mm, float ll, bool empty) {
@@ -651,11 +769,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-template <int kType, int DC, int NQ>
+template <int kCache, int DC, int NQ>
 Variant wide_variant() {
-  using L = WideCfg<DC, NQ>;
+  using L = WideCfg<kCache, DC, NQ>;
   static std::atomic<uint64_t> allowed{0};
-  return {reinterpret_cast<Kernel>(&wide_kernel<kType, DC, NQ>), L::kSmem, L::kRows, L::kPartial, &allowed};
+  return {reinterpret_cast<Kernel>(&wide_kernel<kCache, DC, NQ>), L::kSmem, L::kRows, L::kPartial,
+          WideThreads<L::kF8>::kThreads, &allowed};
 }
 
 }  // namespace attn
