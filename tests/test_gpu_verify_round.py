@@ -237,7 +237,7 @@ def reference_attention(q, k, v, seen, scale):
     """q [r, d], k, v [s, d], seen [r, s] in 64 bits: (o, lse, sum p |v|, weight error, sum |v|)."""
     d = q.shape[1]
     x = (q @ torch.where(torch.isfinite(k), k, 0.0).T) * scale
-    size = (q.abs() @ torch.where(torch.isfinite(k), k, 0.0).abs().T) * scale
+    size = (q.abs() @ torch.where(torch.isfinite(k), k, 0.0).abs().T) * abs(scale)
     x = torch.where(seen, x, -math.inf)
     top = x.amax(-1, keepdim=True) if x.shape[1] else torch.full((len(q), 1), -math.inf, device=DEV).double()
     top = torch.where(top == -math.inf, 0.0, top)
@@ -738,3 +738,46 @@ def test_refusals(vg):
                 lambda: vg.verify_tree(torch.zeros((2, 3, 4), device=DEV), None, lens, lens, lens)):
         with pytest.raises((ValueError, vg.VGError)):
             bad()
+
+
+def test_a_row_without_numbers_stays_without(vg):
+    """A query of NaN gives NaN, and leaves the other rows alone."""
+    g = torch.Generator().manual_seed(15)
+    for n, hq in ((3, 2), (20, 4)):
+        cache, ck, cv, table = build_cache(vg, g, 1, 300, 2, 64, 16, torch.bfloat16, torch.bfloat16)
+        q = randn(g, 1, n, hq, 64, dtype=torch.bfloat16)
+        lens = torch.tensor([200], dtype=torch.int32, device=DEV)
+        want = vg.tree_attention(q, cache, lens)
+        q[0, 1, 0] = math.nan
+        lse = torch.empty((1, n, hq), device=DEV)
+        got = vg.tree_attention(q, cache, lens, lse=lse)
+        assert torch.isnan(got[0, 1, 0]).all() and torch.isnan(lse[0, 1, 0])
+        got[0, 1, 0], want[0, 1, 0] = 0, 0
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(16, 4, 1, 128), (64, 8, 2, 64), (50, 6, 1, 96), (64, 16, 1, 128),
+                                        (12, 24, 4, 80)])
+@pytest.mark.parametrize("dtype,held", [(torch.bfloat16, None), (torch.float16, None), (torch.bfloat16, E4M3)])
+def test_attention_many_rows(vg, n, hq, hkv, d, dtype, held):
+    """More than 32 rows a cache head, at lengths about the tiles' borders, with nodes that
+    are not finite where some rows do not see them."""
+    lens = [0, 1, 127, 128, 129, 255, 1100, 40]
+    check_attention(vg, 41, len(lens), n, hq, hkv, d, dtype, held or dtype, 16, lens, fill="nan", tree="random",
+                    counts=[n, 1, n // 2, n, n, 0, n, n - 1])
+    chain = [[(1 << (i + 1)) - 1 if i < 63 else -1 for i in range(n)] for _ in lens]
+    check_attention(vg, 42, len(lens), n, hq, hkv, d, dtype, held or dtype, 16, lens, fill="nan", tree=chain,
+                    poison=True)
+
+
+def test_attention_negative_and_zero_scale(vg):
+    for n, hq in ((4, 4), (40, 4)):
+        for scale in (-0.2, 0.0):
+            check_attention(vg, 43, 2, n, hq, 2, 128, torch.bfloat16, torch.bfloat16, 16, [300, 9], scale=scale)
+
+
+def test_the_example_runs(vg):
+    import runpy
+    import os
+    from conftest import ROOT
+    runpy.run_path(os.path.join(ROOT, "examples", "verify_round.py"), run_name="__main__")

@@ -36,7 +36,7 @@ __all__ = [
     "int4g_pack", "mxfp8_unpack", "int4g_unpack", "mxfp8_from_canonical",
     "int4g_from_canonical", "VG_FMT_MXFP8", "VG_FMT_INT4G",
     "KVCache", "rope_frequencies", "rope_append", "tree_attention_workspace", "tree_attention",
-    "probabilities", "verify_tree",
+    "probabilities", "verify_tree", "workspace_error",
 ]
 
 
