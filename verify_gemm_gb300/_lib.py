@@ -8,11 +8,14 @@ raises instead of falling back to anything else.  Build it with
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libvgemm.so")
+TORCH_PATH = os.path.join(HERE, "_build", "_vgtorch.so")
 
 VG_OK = 0
 VG_ERR_INVALID_ARG = 1
@@ -132,6 +135,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_torch_module = None
 
 
 class VGError(RuntimeError):
@@ -161,6 +165,26 @@ def load():
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def load_torch():
+    """The verify round's calls from torch tensors (raises if not built)."""
+    global _torch_module
+    load()
+    with _lock:
+        if _torch_module is None:
+            if not os.path.exists(TORCH_PATH):
+                raise RuntimeError(
+                    f"_vgtorch.so not found at {TORCH_PATH}; build it with "
+                    "`python -m verify_gemm_gb300.build` (there is no fallback path)")
+            import torch  # noqa: F401  (its libraries, which the module needs)
+
+            loader = importlib.machinery.ExtensionFileLoader("_vgtorch", TORCH_PATH)
+            spec = importlib.util.spec_from_file_location("_vgtorch", TORCH_PATH, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            _torch_module = module
+    return _torch_module
 
 
 def check(status: int, where: str):

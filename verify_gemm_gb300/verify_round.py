@@ -3,61 +3,43 @@ positions with the append to a paged cache, attention of a tree of drafted
 tokens over that cache, the probabilities of logits and the verification of
 the drafted tokens.
 
-Every step runs in the CUDA kernels of ``libvgemm.so``; this module only
-checks and marshals torch tensors.  Lengths, node counts and page tables are
-read on the device, so a captured graph serves every length.
+Every step runs in the CUDA kernels of ``libvgemm.so``.  The calls go through
+``_vgtorch.so``, which checks the tensors, allocates the outputs and calls the
+C ABI.  Lengths, node counts and page tables are read on the device, so a
+captured graph serves every length.
 """
 from __future__ import annotations
 
 import ctypes
 import math
-import struct
 
 import torch
 
 from . import _lib
 from ._lib import (VG_ROPE_HALF, VG_ROPE_INTERLEAVED, VG_TYPE_BF16, VG_TYPE_E4M3, VG_TYPE_FP16,
-                   VG_TYPE_FP32, vg_attention_desc, vg_kv_cache, vg_rope_desc)
+                   vg_kv_cache)
 
-_TYPES = {torch.bfloat16: VG_TYPE_BF16, torch.float16: VG_TYPE_FP16, torch.float32: VG_TYPE_FP32,
+_TYPES = {torch.bfloat16: VG_TYPE_BF16, torch.float16: VG_TYPE_FP16,
           torch.float8_e4m3fn: VG_TYPE_E4M3}
 _LAYOUTS = {"half": VG_ROPE_HALF, "interleaved": VG_ROPE_INTERLEAVED}
-_CONTIGUOUS = torch.contiguous_format
-
-# The descriptors as bytes (vg_rope_desc, vg_attention_desc of include/vgemm.h):
-# packing them takes a third of the time that filling a ctypes structure does.
-_ROPE_DESC = struct.Struct("@4P9q4P5if0q")
-_ATTENTION_DESC = struct.Struct("@6P3q3if0q")
-assert _ROPE_DESC.size == ctypes.sizeof(vg_rope_desc)
-assert _ATTENTION_DESC.size == ctypes.sizeof(vg_attention_desc)
+_native = None
 
 
-def _stream(stream, device):
-    """The stream's handle; that of the current stream comes straight from
-    torch's table, without the Stream object (3 us)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device)
+def _calls():
+    global _native
+    if _native is None:
+        _native = _lib.load_torch()
+    return _native
 
 
-_int32_t = torch.int32
+def _handle(stream):
+    return stream.cuda_stream if stream is not None else None
 
 
-def _int32(t, shape, name):
-    """Address of a contiguous CUDA int32 tensor of that shape."""
-    if t.dtype is _int32_t and t.is_cuda and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of shape {shape}")
-
-
-def _heads(t, name):
-    """Strides (batch, node, head) of a CUDA tensor [batch, n, heads,
-    head_dim] with contiguous heads."""
-    s = t.stride()
-    if not t.is_cuda or len(s) != 4 or s[3] != 1:
-        raise ValueError(f"{name}: expected a CUDA tensor [batch, n, heads, head_dim] whose last "
-                         "dimension is contiguous")
-    return s[:3]
+def _checked(result, where):
+    if type(result) is int:          # a vg_status
+        _lib.check(result, where)
+    return result
 
 
 class KVCache:
@@ -96,7 +78,7 @@ class KVCache:
         c.k_scale, c.v_scale = k_scale, v_scale
         _lib.check(_lib.vg_kv_cache_init(ctypes.byref(c)), "vg_kv_cache_init")
         self._c = c
-        self._ref = ctypes.byref(c)
+        self._at = ctypes.addressof(c)
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
@@ -145,38 +127,17 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
     depth[b, i] (depth None: i).  The first 2 * inv_freq.numel() elements of a
     head turn: pairs (j, j + rot/2) for layout "half", (2j, 2j + 1) for
     "interleaved".  Nodes past counts[b] append nothing and give 0."""
-    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
-    B, n, hq, d = q.shape
-    if B != cache.batch or d != cache.head_dim or k.shape != (B, n, cache.heads, d) \
-            or v.shape != k.shape:
-        raise ValueError("q, k, v and the cache do not fit together")
-    if not q.dtype == k.dtype == v.dtype:
-        raise ValueError("q, k and v must have the same type")
-    if not (inv_freq.is_cuda and inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()):
-        raise ValueError("inv_freq: expected a contiguous CUDA float64 tensor")
     if layout not in _LAYOUTS:
         raise ValueError("layout: 'half' or 'interleaved'")
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=_CONTIGUOUS)
-    elif not (q_out.is_cuda and q_out.shape == q.shape and q_out.dtype == q.dtype
-              and q_out.is_contiguous()):
-        raise ValueError("q_out: expected a contiguous CUDA tensor like q")
-    desc = _ROPE_DESC.pack(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *qs, *ks, *vs,
-        inv_freq.data_ptr(), _int32(lens, (B,), "lens"),
-        _int32(depth, (B, n), "depth") if depth is not None else 0,
-        _int32(counts, (B,), "counts") if counts is not None else 0,
-        _TYPES.get(q.dtype, -1), _LAYOUTS[layout], n, hq, 2 * inv_freq.numel(), factor)
-    s = _lib.load().vg_rope_append(desc, cache._ref, _stream(stream, q.get_device()))
-    if s:
-        _lib.check(s, "vg_rope_append")
-    return q_out
+    return _checked((_native or _calls()).rope_append(
+        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out,
+        _handle(stream)), "vg_rope_append")
 
 
 def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
     """A zero-filled workspace for tree_attention with q of this shape."""
     n = ctypes.c_size_t()
-    _lib.check(_lib.vg_tree_attention_workspace_size(q.shape[1], q.shape[2], cache._ref,
+    _lib.check(_lib.vg_tree_attention_workspace_size(q.shape[1], q.shape[2], cache._at,
                                                      ctypes.byref(n)),
                "vg_tree_attention_workspace_size")
     return torch.zeros(n.value, dtype=torch.uint8, device=q.device)
@@ -196,33 +157,11 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     q_heads], written if given.  workspace: from tree_attention_workspace,
     made anew by each call that is given none; calls that share one must not
     overlap."""
-    qs = _heads(q, "q")
-    B, n, hq, d = q.shape
-    if B != cache.batch or d != cache.head_dim:
-        raise ValueError("q and the cache do not fit together")
-    if tree is not None and not (tree.is_cuda and tree.dtype == torch.int64
-                                 and tree.is_contiguous() and tree.shape == (B, n)):
-        raise ValueError("tree: expected a contiguous CUDA int64 tensor [batch, n]")
-    if out is None:
-        out = torch.empty_like(q, memory_format=_CONTIGUOUS)
-    elif not (out.is_cuda and out.shape == q.shape and out.dtype == q.dtype
-              and out.is_contiguous()):
-        raise ValueError("out: expected a contiguous CUDA tensor like q")
-    if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32
-                                and lse.is_contiguous() and lse.shape == (B, n, hq)):
-        raise ValueError("lse: expected a contiguous CUDA float32 tensor [batch, n, q_heads]")
     if workspace is None:
         workspace = tree_attention_workspace(q, cache)
-    desc = _ATTENTION_DESC.pack(
-        q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
-        _int32(lens, (B,), "lens"), _int32(counts, (B,), "counts") if counts is not None else 0,
-        tree.data_ptr() if tree is not None else 0, *qs, _TYPES.get(q.dtype, -1), n, hq,
-        d ** -0.5 if scale is None else scale)
-    s = _lib.load().vg_tree_attention(desc, cache._ref, workspace.data_ptr(), workspace.numel(),
-                                      _stream(stream, q.get_device()))
-    if s:
-        _lib.check(s, "vg_tree_attention")
-    return out
+    return _checked((_native or _calls()).tree_attention(
+        q, cache._at, lens, tree, counts, cache.head_dim ** -0.5 if scale is None else scale, out, lse,
+        workspace, _handle(stream)), "vg_tree_attention")
 
 
 def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -231,25 +170,8 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
     float16 or float32), each row over its own temperature (float32, one for
     every row; None: 1).  A temperature <= 0 gives 1 at the row's first
     largest logit."""
-    if not (logits.is_cuda and logits.is_contiguous() and logits.dim() >= 1 and logits.numel()):
-        raise ValueError("logits: expected a contiguous CUDA tensor that is not empty")
-    vocab = logits.shape[-1]
-    rows = logits.numel() // vocab
-    if temperature is not None and not (temperature.is_cuda and temperature.dtype == torch.float32
-                                        and temperature.is_contiguous()
-                                        and temperature.numel() == rows):
-        raise ValueError("temperature: expected a contiguous CUDA float32 tensor, one for each row")
-    if out is None:
-        out = torch.empty_like(logits, dtype=torch.float32)
-    elif not (out.is_cuda and out.shape == logits.shape and out.dtype == torch.float32
-              and out.is_contiguous()):
-        raise ValueError("out: expected a contiguous CUDA float32 tensor like logits")
-    s = _lib.load().vg_probabilities(logits.data_ptr(), _TYPES.get(logits.dtype, -1), rows, vocab,
-                              temperature.data_ptr() if temperature is not None else None,
-                              out.data_ptr(), _stream(stream, logits.get_device()))
-    if s:
-        _lib.check(s, "vg_probabilities")
-    return out
+    return _checked((_native or _calls()).probabilities(logits, temperature, out, _handle(stream)),
+                    "vg_probabilities")
 
 
 def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
@@ -263,22 +185,5 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
     Returns int32 (accepted [batch], path [batch, n], out [batch, n + 1]): how
     many drafts hold, their nodes, and their tokens with the one drawn after
     them; -1 behind.  include/vgemm.h (vg_verify_tree) has the rule."""
-    if not (p.is_cuda and p.dtype == torch.float32 and p.dim() == 3 and p.is_contiguous()):
-        raise ValueError("p: expected a contiguous CUDA float32 tensor [batch, n, vocab]")
-    B, n, V = p.shape
-    if q is not None and not (q.is_cuda and q.dtype == torch.float32 and q.dim() == 3
-                              and q.is_contiguous() and q.shape[0] == B and q.shape[2] == V):
-        raise ValueError("q: expected a contiguous CUDA float32 tensor [batch, rows, vocab]")
-    if not (u.is_cuda and u.dtype == torch.float32 and u.is_contiguous() and u.shape == (B, n)):
-        raise ValueError("u: expected a contiguous CUDA float32 tensor [batch, n]")
-    accepted, path, out = (torch.empty(shape, dtype=_int32_t, device=p.device)
-                           for shape in ((B,), (B, n), (B, n + 1)))
-    s = _lib.load().vg_verify_tree(
-        p.data_ptr(), q.data_ptr() if q is not None else None, _int32(tokens, (B, n), "tokens"),
-        _int32(parents, (B, n), "parents"),
-        _int32(counts, (B,), "counts") if counts is not None else None, u.data_ptr(), B, n,
-        q.shape[1] if q is not None else 0, V, accepted.data_ptr(), path.data_ptr(), out.data_ptr(),
-        _stream(stream, p.get_device()))
-    if s:
-        _lib.check(s, "vg_verify_tree")
-    return accepted, path, out
+    return _checked((_native or _calls()).verify_tree(p, q, tokens, parents, u, counts, _handle(stream)),
+                    "vg_verify_tree")
