@@ -506,42 +506,61 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t ring0 = smem_addr(ring), q0 = smem_addr(q_smem);
   const int group = p.hq / p.hkv;
   uint32_t tile_no = 0;                                  // tiles of the block so far
-  for (; at.valid(); at.next(p)) {
-    const int head = at.u / p.blocks, rb = at.u % p.blocks;
-    const int row0 = rb * L::kRows;
-    // ---------------------------------------------------------- q to shared
-    // a warp a row; E4M3: in FP16, each row brought near the middle of its
-    // range by a power of two, which keeps every bit of a BF16 row that
-    // counts (2^-29 of the row's largest element and more)
-    for (int r = warp; r < L::kRows; r += kConsumers) {
-      const int row = row0 + r, node = row / group, h = head * group + row % group;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const bool live = row < p.rows && lane * 8 < p.d;
-      if (live)
-        v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at.b * p.qs[0] +
-                                             node * p.qs[1] + h * p.qs[2] + lane * 8);
+  // A unit's q goes to shared memory by way of registers, a warp a row.  With
+  // up to 32 rows the next unit's is fetched before this one's results are
+  // joined: under load a fetch takes 3 us.
+  constexpr int kQn = L::kRows / kConsumers;
+  // (E4M3 has no registers for it: 156 -> 170 us over 262001 keys.)
+  constexpr bool kAheadQ = L::kRows <= 32 && kType != kE4M3;
+  uint4 qv[kQn];
+  auto fetch_q = [&](const Line &u) {
+    const int head = u.u / p.blocks, row0 = u.u % p.blocks * L::kRows;
+#pragma unroll
+    for (int k = 0; k < kQn; ++k) {
+      const int row = row0 + k * kConsumers + warp;
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (row < p.rows && lane * 8 < p.d)
+        qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
+                                                 (row / group) * p.qs[1] +
+                                                 (head * group + row % group) * p.qs[2] + lane * 8);
+    }
+  };
+  // E4M3: in FP16, each row brought to the top of its range by a power of two,
+  // which keeps every bit of a BF16 row that counts (2^-29 of the row's
+  // largest element and more)
+  auto store_q = [&] {
+#pragma unroll
+    for (int k = 0; k < kQn; ++k) {
+      const int r = k * kConsumers + warp;
       if constexpr (kType == kE4M3) {
         float f[8];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
         float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint16_t x = uint16_t(w[k / 2] >> (16 * (k & 1)));
-          f[k] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
-          top = fmaxf(top, fabsf(f[k]));
+        for (int e = 0; e < 8; ++e) {
+          const uint16_t x = uint16_t(w[e / 2] >> (16 * (e & 1)));
+          f[e] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
+          top = fmaxf(top, fabsf(f[e]));
         }
 #pragma unroll
         for (int m = 16; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
         const int e = q_exponent(top);
         const float down = ldexpf(1.f, -e);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= down;
-        v = make_uint4(pack2<kF16>(f[0], f[1]), pack2<kF16>(f[2], f[3]), pack2<kF16>(f[4], f[5]),
-                       pack2<kF16>(f[6], f[7]));
+        qv[k] = make_uint4(pack2<kF16>(f[0] * down, f[1] * down), pack2<kF16>(f[2] * down, f[3] * down),
+                           pack2<kF16>(f[4] * down, f[5] * down), pack2<kF16>(f[6] * down, f[7] * down));
         if (lane == 0) q_unit[r] = ldexpf(1.f, e);
       }
-      if (lane * 8 < L::D) *reinterpret_cast<uint4 *>(q_smem + r * L::kQRow + lane * 16) = v;
+      if (lane * 8 < L::D) *reinterpret_cast<uint4 *>(q_smem + r * L::kQRow + lane * 16) = qv[k];
     }
+  };
+  if (kAheadQ && at.valid()) fetch_q(at);
+  for (; at.valid();) {
+    Line after = at;
+    after.next(p);
+    const int head = at.u / p.blocks, rb = at.u % p.blocks;
+    const int row0 = rb * L::kRows;
+    if (!kAheadQ) fetch_q(at);
+    store_q();
     named_bar(1, kConsumers * 32);
 
     uint32_t qf[L::kQReg ? DC * 4 : 1][4];
@@ -822,6 +841,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(empty0 + 8 * sv);
     }
 
+    if (kAheadQ && after.valid()) fetch_q(after);
+
     // ------------------------------------- join the key warps, then the blocks
     const int first = at.first(), final = at.final();
     const bool whole = first == final;
@@ -994,6 +1015,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
     named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
+    at = after;
   }
 }
 
