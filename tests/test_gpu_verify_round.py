@@ -463,6 +463,18 @@ def test_probabilities(vg, dtype, rows, vocab):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_probabilities_at_every_share_of_a_row(vg, dtype):
+    """Vocabularies whose share of a block takes every multiple of 4 KB of its shared
+    memory, up to those that do not fit: each against a sum in 64 bits."""
+    g = torch.Generator().manual_seed(3)
+    for vocab in list(range(9000, 420000, 15361)) + [98000, 98304, 190000, 196607, 393000, 786432, 800011]:
+        x = randn(g, 2, vocab, dtype=dtype, scale=2.0)
+        y = vg.probabilities(x).double()
+        want = torch.softmax(x.double(), -1)
+        assert ((y - want).abs() <= want * (2.0 ** -16 + 40 * 2.0 ** -22) + 1e-37).all(), vocab
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_probabilities_of_masked_rows(vg, dtype):
     low = torch.finfo(dtype).min
     V = 5003

@@ -68,6 +68,21 @@ cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cl
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
+// Lets `fn` have `bytes` of dynamic shared memory, once for each device (its
+// bit in `allowed`; device_sms refuses devices above 63).
+template <typename F>
+cudaError_t allow_smem(F *fn, int bytes, std::atomic<uint64_t> &allowed) {
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
+    return e;
+  allowed.fetch_or(bit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 // ------------------------------------------------------------ probabilities
 // A cluster of blocks a row.  Each thread copies its share of the row to
 // shared memory (asynchronously, so every block of an SM has its whole share
@@ -86,7 +101,8 @@ cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cl
 // ends go element by element.
 constexpr int kProbThreads = 256, kProbWarps = kProbThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kProbShare = 40 * 1024;          // bytes of a row a block holds at most
+constexpr int kProbShare = 40 * 1024;          // bytes of a row a block should hold at most ...
+constexpr int kProbShareMax = 96 * 1024;       // ... and may
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -284,9 +300,12 @@ cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const floa
   const int64_t each = (units + int64_t(c) * kProbThreads - 1) / (int64_t(c) * kProbThreads);
   const int64_t share = each * kProbThreads * size;
   const unsigned grid = unsigned(rows) * unsigned(c);
-  if (share > kProbShare + 8192)
+  if (share > kProbShareMax)
     return launch_clusters(&probabilities_kernel<T, false>, grid, kProbThreads, c, 0, st, x, V,
                            temperature, out);
+  // more than 48 KB, the kernel's own words included, have to be asked for
+  static std::atomic<uint64_t> allowed{0};
+  if (const cudaError_t e = allow_smem(&probabilities_kernel<T, true>, kProbShareMax, allowed)) return e;
   return launch_clusters(&probabilities_kernel<T, true>, grid, kProbThreads, c, int(share), st, x, V,
                          temperature, out);
 }
