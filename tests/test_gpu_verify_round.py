@@ -782,6 +782,15 @@ def test_attention_many_rows(vg, n, hq, hkv, d, dtype, held):
                     poison=True)
 
 
+@pytest.mark.parametrize("n,hq,d,length", [(26, 8, 128, 20601), (64, 2, 64, 9001), (20, 8, 192, 9001),
+                                           (8, 2, 256, 12345), (1, 1, 128, 30000)])
+@pytest.mark.parametrize("held", [torch.bfloat16, E4M3])
+def test_attention_of_few_units_over_long_caches(vg, n, hq, d, length, held):
+    """Units that most of the device's blocks have a part in."""
+    check_attention(vg, 47, 1, n, hq, 1, d, torch.bfloat16, held, 64, [length], tree="random")
+    check_attention(vg, 48, 3, n, hq, 1, d, torch.bfloat16, held, 16, [length // 2, 0, length], counts=[n, 1, n])
+
+
 def test_attention_negative_and_zero_scale(vg):
     for n, hq in ((4, 4), (40, 4)):
         for scale in (-0.2, 0.0):

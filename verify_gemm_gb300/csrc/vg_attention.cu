@@ -40,7 +40,7 @@ vg_status allow_smem(const Variant &v) {
 }
 
 size_t workspace_bytes_of(const Variant &v, int sms) {
-  return kHeader + kMaxGrid * sizeof(uint32_t) + size_t(sms) * 2 * size_t(v.partial) * sizeof(float);
+  return kHeader + 3 * kMaxGrid * sizeof(uint32_t) + size_t(sms) * 2 * size_t(v.partial) * sizeof(float);
 }
 
 }  // namespace
@@ -93,7 +93,7 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.error = reinterpret_cast<int *>(ws);
   p.arrived = reinterpret_cast<uint32_t *>(ws + kHeader);
-  p.partial = reinterpret_cast<float *>(ws + kHeader + kMaxGrid * sizeof(uint32_t));
+  p.partial = reinterpret_cast<float *>(ws + kHeader + 3 * kMaxGrid * sizeof(uint32_t));
   p.batch = cache->batch;
   p.n = d->n;
   p.hq = d->q_heads;
@@ -101,17 +101,23 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   p.d = cache->head_dim;
   p.q_f16 = d->type == VG_TYPE_FP16;
   p.rows = rows;
+  p.group = d->q_heads / cache->heads;
+  p.group_magic = p.group == 1 ? 0 : uint32_t((uint64_t(1) << 32) / uint64_t(p.group)) + 1;
   p.blocks = (rows + v.rows - 1) / v.rows;
   p.box = cache_box_tokens(cache->page_size);
-  // In the time that a block's 45 GB/s take for them: a unit costs 256 KB
-  // beside its tiles (512 KB with its outputs of 128 rows and more), and a cut
-  // that moves by less saves more than it unbalances (measured over 0 to 12
-  // tiles of 32 and of 64 KB).
+  // What a unit costs beside its tiles, in tiles, and half of it as the cut that
+  // moves: less saves more than it unbalances.  Beginning and joining a unit
+  // takes some 4 us.  The tcgen05 kernel's tiles are bound by their exponentials,
+  // whatever their bytes; the other's by their bytes (45 GB/s a block) but for
+  // the smallest ones, and by the products from 64 rows on.  Measured over 1 to
+  // 16 tiles of ragged batches: 18 sequences of 304 rows of 128, 6 tiles 100 us,
+  // 8 106, 16 114; 30 units of 55 rows of 64 in E4M3, 26 us, 27, 32 and 40 with
+  // 32; 50 units of 128 rows of 256, 2 tiles 36 us, 4 41.
   const bool wide = is_wide(p.d, rows);
   p.tile_log2 = wide ? 7 : 6;
   const int tile_bytes = (2 * p.d * (type == kE4M3 ? 1 : 2)) << p.tile_log2;
   p.least = std::max(1, 131072 / tile_bytes);
-  p.extra = std::max(1, (wide ? 524288 : 262144) / tile_bytes);
+  p.extra = wide ? 6 : std::max(1, std::min({8, 16 * 16 / v.rows, 262144 / tile_bytes}));
   p.snap = p.extra / 2;
   p.c = d->scale * cache->k_scale * kLog2e;
   p.v_scale = cache->v_scale;

@@ -9,12 +9,26 @@
 //     m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + v 2^(x - m').
 //
 // Keys and values are read once from HBM, which bounds the kernel for up to
-// about 64 rows a head.  One block per SM: a producer warp copies tiles by
-// TMA (a box of a page at a time, 128-byte swizzle) into a ring of slots,
-// K and V in turn; eight consumer warps share out rows (RW groups of 16) and
-// keys (16 at a time), each with a softmax state of its own, and are joined
-// in shared memory at the end of a unit.  mma.sync carries the products:
-// at 16 rows they take a fifth of the time that the bytes take.
+// about 16 rows a head.  One block per SM, because a ring that fills its
+// shared memory is what keeps HBM busy: two warps, one for K and one for V,
+// copy tiles by TMA (a box of a page at a time, 128-byte swizzle) into its
+// slots; eight consumer warps share out rows (RW groups of 16) and keys (32 at
+// a time, 16 for heads of 256), each with a softmax state of its own, and are
+// joined in shared memory at the end of a unit.  Keys and not only rows are
+// shared out because a chain of 8 nodes with 2 query heads a cache head has 16
+// rows in all, one fragment of mma.sync, which carries the products: at
+// 16 rows they take a fifth of the time that the bytes take.
+//
+// A warp that waits for a step's dependent chain (scores, maximum, weights,
+// output) leaves its slots held, so with more rows the warps' latency and not
+// the bytes sets the pace.  Measured (heads of 128, a kernel by itself):
+//     8003 keys of 40 heads, 8 rows, BF16        164 MB   34.5 us  4.75 TB/s
+//     262001 keys of 8 heads, 20 rows, E4M3      537 MB  155 us    3.5 TB/s
+//     131000 keys of 8 heads, 20 rows, BF16      537 MB   93 us    5.8 TB/s
+//     130 keys of 8 heads of 64, 4 rows: 6.6 us, a launch and a chain of waits
+// (With 16 keys a step, one copying warp and a page number fetched for each
+// tile the second took 227 us.  Two row groups a warp, which read each key once
+// and not twice for 20 rows, made it 194 us: q no longer stays in registers.)
 //
 // The tiles of all units form one line that is cut into equal runs, one a
 // block, from the lengths in device memory: ragged lengths and long single
@@ -45,7 +59,7 @@ constexpr int kAttnThreads = (kConsumers + 4) * 32;   // three warpgroups, one w
 // warpgroup gives up what the consumers' two take, 128 x 56 + 256 x 224 = 64512.
 constexpr int kProducerRegs = 56, kConsumerRegs = 224;
 constexpr int kHeader = 256;                  // workspace: error word, then ...
-constexpr int kMaxGrid = 512;                 // ... a counter for each block
+constexpr int kMaxGrid = 512;                 // ... three counters for each block
 constexpr uint64_t kWaitNs = 2000000000ull;   // bound of every wait
 constexpr int kErrAttnWait = 16;              // the error word of a wait that ran out
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,14 +82,62 @@ struct AttnParams {
   int64_t qs[3];
   CacheView cache;
   int *error;
-  uint32_t *arrived;                // [grid]
+  uint32_t *arrived;                // [3][kMaxGrid]: units', and groups' by their first block's place
   float *partial;                   // [grid][2] of (rows x (head_dim padded) + 2 rows)
   int batch, n, hq, hkv, d, q_f16;
   int rows, blocks;                 // rows that share a cache head, row blocks of a unit
+  int group;                        // query heads that share a cache head
+  uint32_t group_magic;             // 2^32 / group + 1
   int tile_log2;                    // keys of a tile
   int box, least, extra, snap;      // tokens of a TMA box; tiles: of a run at least, a unit costs, a cut moves
   float c, v_scale;                 // scale * k_scale * log2 e
 };
+
+// Divisions by numbers that only the launch knows take some 150 clocks, and a
+// unit's beginning and end are a chain of them.
+// row / group, exact for row < 2^32 / group (rows are below 2^20 / 4).
+__device__ __forceinline__ int node_of(const AttnParams &p, int row) {
+  return p.group == 1 ? row : int(__umulhi(uint32_t(row), p.group_magic));
+}
+// Cache head and row block of unit u of a sequence.
+__device__ __forceinline__ int head_of(const AttnParams &p, int u) { return p.blocks == 1 ? u : u / p.blocks; }
+__device__ __forceinline__ int block_of_rows(const AttnParams &p, int u) { return p.blocks == 1 ? 0 : u % p.blocks; }
+
+// ------------------------------------------------------------------ joining
+// The blocks first .. final of a cut unit leave partial results, and the one
+// that arrives last joins them in the blocks' order.  Where that is much to
+// read for one block (some 120 GB/s), groups of about the square root of them
+// are joined first, each by its last, into its first block's place: 80 blocks
+// of 256 rows, 10.6 MB, took 110 us to join.  A second step costs what half a
+// megabyte does.
+struct Join {
+  int lo, hi, step;                 // the blocks that are joined now
+  int group, first, final;          // blocks of a group (all, when there is one step)
+  __device__ __forceinline__ Join(int first_, int final_, int block, int most)
+      : first(first_), final(final_) {
+    const int count = final - first + 1;
+    group = count;
+    if (count > most)
+      for (group = 2; group * group < count;) ++group;
+    lo = first + (block - first) / group * group;
+    hi = min(lo + group - 1, final);
+    step = 1;
+  }
+  __device__ __forceinline__ bool last() const { return lo == first && hi == final; }
+  __device__ __forceinline__ void next() {
+    lo = first;
+    hi = final;
+    step = group;
+  }
+  __device__ __forceinline__ uint32_t members() const { return uint32_t((hi - lo) / step) + 1; }
+  // A block has a part in at most one unit that it is the first block of and
+  // in one that it is not.
+  __device__ __forceinline__ uint32_t *counter(const AttnParams &p) const {
+    return p.arrived + (last() ? 0 : lo == first ? kMaxGrid : 2 * kMaxGrid) + lo;
+  }
+};
+template <typename L>
+constexpr int kJoinAtOnce = 131072 / L::kPartial > 12 ? 131072 / L::kPartial : 12;
 
 // ----------------------------------------------------------------- layout
 template <int kType, int DC, int RW>
@@ -257,10 +319,13 @@ struct Line {
     len = int(min(int64_t(max(p.lens[b], 0)), room));
     return p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   }
+  __device__ __forceinline__ static int tiles_for(const AttnParams &p, int tokens) {
+    return max(1, (tokens + (1 << p.tile_log2) - 1) >> p.tile_log2);
+  }
   __device__ __forceinline__ static int tiles_of(const AttnParams &p, int b) {
     int len;
     const int count = used(p, b, len);
-    return max(1, (len + count + (1 << p.tile_log2) - 1) >> p.tile_log2);
+    return tiles_for(p, len + count);
   }
   // The whole warp computes it.
   __device__ void init(const AttnParams &p, int units_) {
@@ -313,6 +378,7 @@ struct Line {
     const int64_t in = at - before * units;
     u = in < int64_t(1) << 32 ? int(uint32_t(in) / uint32_t(length)) : int(in / length);
     tiles = length - extra;
+    count = b < p.batch ? used(p, b, len) : 0;
     const int off = int(in - int64_t(u) * length);
     unit0 = at - off;
     t0 = off <= snap ? 0 : max(0, off - extra);
@@ -325,9 +391,9 @@ struct Line {
     const int64_t cut = end - unit0;            // where the run ends, from the unit's beginning
     const int length = tiles + extra;
     t1 = cut >= length ? tiles : cut <= snap ? 0 : length - cut <= snap ? tiles : max(0, int(cut) - extra);
-    if (t0 < t1) count = used(p, b, len);
   }
   __device__ __forceinline__ bool valid() const { return t0 < t1; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
   __device__ __forceinline__ void next(const AttnParams &p) {
     unit0 += tiles + extra;
     t0 = 0;
@@ -336,7 +402,8 @@ struct Line {
     if (++u == units) {
       u = 0;
       ++b;
-      tiles = tiles_of(p, b);
+      count = used(p, b, len);
+      tiles = tiles_for(p, len + count);
     }
     fill(p);
   }
@@ -371,7 +438,7 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
   int s = kv, n = 0;
   uint32_t par = 1;                                      // slots start empty
   for (; at.valid(); at.next(p)) {
-    const int head = at.u / p.blocks;
+    const int head = head_of(p, at.u);
     const int total = at.len + at.count;
     const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
     auto fetch = [&](int window) {
@@ -504,7 +571,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int rw = warp / L::KW, kg = warp % L::KW;        // row group, key warp
   const int grp = kg / L::KT, kt = kg % L::KT;
   const uint32_t ring0 = smem_addr(ring), q0 = smem_addr(q_smem);
-  const int group = p.hq / p.hkv;
   uint32_t tile_no = 0;                                  // tiles of the block so far
   // A unit's q goes to shared memory by way of registers, a warp a row.  With
   // up to 32 rows the next unit's is fetched before this one's results are
@@ -514,15 +580,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr bool kAheadQ = L::kRows <= 32 && kType != kE4M3;
   uint4 qv[kQn];
   auto fetch_q = [&](const Line &u) {
-    const int head = u.u / p.blocks, row0 = u.u % p.blocks * L::kRows;
+    const int head = head_of(p, u.u), row0 = block_of_rows(p, u.u) * L::kRows;
 #pragma unroll
     for (int k = 0; k < kQn; ++k) {
-      const int row = row0 + k * kConsumers + warp;
+      const int row = row0 + k * kConsumers + warp, node = node_of(p, row);
       qv[k] = make_uint4(0, 0, 0, 0);
       if (row < p.rows && lane * 8 < p.d)
         qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
-                                                 (row / group) * p.qs[1] +
-                                                 (head * group + row % group) * p.qs[2] + lane * 8);
+                                                 node * p.qs[1] +
+                                                 (head * p.group + row - node * p.group) * p.qs[2] + lane * 8);
     }
   };
   // E4M3: in FP16, each row brought to the top of its range by a power of two,
@@ -557,8 +623,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   for (; at.valid();) {
     Line after = at;
     after.next(p);
-    const int head = at.u / p.blocks, rb = at.u % p.blocks;
-    const int row0 = rb * L::kRows;
+    const int head = head_of(p, at.u), row0 = block_of_rows(p, at.u) * L::kRows;
     if (!kAheadQ) fetch_q(at);
     store_q();
     named_bar(1, kConsumers * 32);
@@ -591,7 +656,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint64_t used = at.count >= 64 ? ~0ull : (1ull << at.count) - 1;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int node = (row0 + rw * 16 + g + 8 * r) / group;
+      const int node = node_of(p, row0 + rw * 16 + g + 8 * r);
       word[r] = 0;
       if (node < p.n)
         word[r] = used & (p.tree ? p.tree[int64_t(at.b) * p.n + node] : ~0ull >> (63 - node));
@@ -844,8 +909,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (kAheadQ && after.valid()) fetch_q(after);
 
     // ------------------------------------- join the key warps, then the blocks
-    const int first = at.first(), final = at.final();
-    const bool whole = first == final;
+    const bool whole = at.whole();
+    const int first = whole ? 0 : at.first(), final = whole ? 0 : at.final();
     // a block's partial result: its unit's first block has it in its second place
     auto place = [&](int block) {
       return p.partial + (int64_t(block) * 2 + (block == first ? 1 : 0)) * L::kPartial;
@@ -923,41 +988,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     bool done = whole;
     if (!whole) {
-      // Of a unit that several blocks share, the block that arrives last joins
-      // the blocks' results, in their order.
-      float *mine = place(blockIdx.x);
-      float4 *to = reinterpret_cast<float4 *>(mine) + rw * (NT * 32) + lane;
+      Join join(first, final, blockIdx.x, kJoinAtOnce<L>);
+      float *to = place(blockIdx.x);
+#pragma unroll 1
+      while (true) {
+        float4 *cols = reinterpret_cast<float4 *>(to) + rw * (NT * 32) + lane;
 #pragma unroll
-      for (int i = 0; i < TPW; ++i)
-        to[tile_of(i) * 32] = make_float4(res[i][0], res[i][1], res[i][2], res[i][3]);
-      if (kg == 0 && t == 0) {
-        float2 *st = reinterpret_cast<float2 *>(mine + RW * NT * 32 * 4) + rw * 16;
-        st[g] = make_float2(mj[0], lj[0]);
-        st[g + 8] = make_float2(mj[1], lj[1]);
-      }
-      __threadfence();
-      named_bar(1, kConsumers * 32);
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(p.arrived + first, 1u);
-        *last = before == uint32_t(final - first);
-        if (*last) p.arrived[first] = 0;
+        for (int i = 0; i < TPW; ++i)
+          cols[tile_of(i) * 32] = make_float4(res[i][0], res[i][1], res[i][2], res[i][3]);
+        if (kg == 0 && t == 0) {
+          float2 *st = reinterpret_cast<float2 *>(to + RW * NT * 32 * 4) + rw * 16;
+          st[g] = make_float2(mj[0], lj[0]);
+          st[g + 8] = make_float2(mj[1], lj[1]);
+        }
         __threadfence();
-      }
-      named_bar(1, kConsumers * 32);
-      done = *last;
-      if (done) {
+        named_bar(1, kConsumers * 32);
+        if (tid == 0) {
+          uint32_t *counter = join.counter(p);
+          *last = atomicAdd(counter, 1u) + 1 == join.members();
+          if (*last) *counter = 0;
+          __threadfence();
+        }
+        named_bar(1, kConsumers * 32);
+        if (!*last) break;
 #pragma unroll
         for (int i = 0; i < TPW; ++i) res[i][0] = res[i][1] = res[i][2] = res[i][3] = 0.f;
         mj[0] = mj[1] = -INFINITY;
         lj[0] = lj[1] = 0.f;
         constexpr int kAhead = TPW <= 2 ? 8 : TPW <= 4 ? 4 : 2;   // blocks fetched at a time
 #pragma unroll 1
-        for (int blk = first; blk <= final; blk += kAhead) {
+        for (int blk = join.lo; blk <= join.hi; blk += kAhead * join.step) {
           float4 v[kAhead][TPW];
           float2 st[kAhead][2];
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
-            const float *part = place(min(blk + k, final));
+            const int from_block = blk + k * join.step;
+            const float *part = place(from_block <= join.hi ? from_block : blk);
             const float2 *sp = reinterpret_cast<const float2 *>(part + RW * NT * 32 * 4) + rw * 16;
             st[k][0] = __ldcg(sp + g);
             st[k][1] = __ldcg(sp + g + 8);
@@ -967,10 +1033,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
-            if (blk + k > final) break;
+            if (blk + k * join.step > join.hi) break;
             merge<TPW>(res, mj, lj, st[k], [&](int i) { return v[k][i]; });
           }
         }
+        done = join.last();
+        if (done) break;
+        named_bar(1, kConsumers * 32);                   // everybody has read the group's
+        to = place(join.lo);
+        join.next();
       }
     }
 
@@ -978,9 +1049,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (done) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = row0 + rw * 16 + g + 8 * r, node = row / group;
+        const int row = row0 + rw * 16 + g + 8 * r, node = node_of(p, row);
         if (row >= p.rows) continue;
-        const int h = head * group + row % group;
+        const int h = head * p.group + row - node * p.group;
         // NaN is not nothing
         const bool empty = node >= at.count || (mj[r] == -INFINITY && lj[r] == 0.f);
         const float inv = empty ? 0.f : p.v_scale / lj[r];

@@ -25,6 +25,18 @@
 // brought to FP16 by a power of two for each row, which goes into its c.
 // The cutting of the line, the pages and the joining of blocks are those of
 // vg_attention.cuh.
+//
+// Measured (heads of 128, a kernel by itself):
+//     8 sequences of 8190 keys, 64 nodes, 8 query heads a cache head, BF16
+//         512 rows: 127 us, 1.09 PFLOP/s (tensor pipe busy 47 % of the time;
+//         the rest is the softmax that no product covers, at a unit's first
+//         and last tiles most of all)
+//     48 sequences of 1200 to 6007 keys, 16 nodes, 4 query heads a cache head
+//         64 rows: 734 MB of FP16 in 133 us, 5.5 TB/s
+//     the same over an E4M3 cache, half the bytes: 143 us, bound by the
+//         warps that convert codes (two codes an instruction)
+// The kernel of vg_attention.cuh took 458 us and 184 us for the first two, and
+// 222 us for the third.
 #pragma once
 
 #include "vg_attention.cuh"
@@ -63,7 +75,7 @@ struct WideCfg {
   static constexpr int kQChunk = 128 * 128;              // 128 rows of 64 elements
   static constexpr int kQTile = DC * kQChunk;
   static constexpr int kRows = 128 * NQ;
-  static constexpr int kFixed = 3072;
+  static constexpr int kFixed = 3 * 1024;
   static constexpr int kRoom = 227 * 1024 - kFixed - NQ * kQTile;
   static constexpr int kFit = kRoom / kSlot;
   static constexpr int kSlots = kF8 ? 4 : (kFit > 16 ? 16 : kFit) & ~1;
@@ -235,7 +247,6 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
   const uint32_t tmem = *tmem_at;
   Line at;
   at.init(p, p.hkv * p.blocks);
-  const int group = p.hq / p.hkv;
 
   if (L::kF8 && warp >= 12) {
     // -------------------------------------------------------- conversions
@@ -382,15 +393,15 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       return NQ == 2 ? q * 128 + k * 8 + warp % 4 * 2 + lane / 16 : k * 16 + warp * 2 + lane / 16;
     };
     auto fetch_q = [&](const Line &u) {
-      const int head = u.u / p.blocks, row0 = u.u % p.blocks * L::kRows;
+      const int head = head_of(p, u.u), row0 = block_of_rows(p, u.u) * L::kRows;
 #pragma unroll
       for (int k = 0; k < kQn; ++k) {
-        const int rw = row0 + row_of(k);
+        const int rw = row0 + row_of(k), node = node_of(p, rw);
         qv[k] = make_uint4(0, 0, 0, 0);
         if (rw < p.rows && piece * 8 < p.d)
           qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
-                                                   (rw / group) * p.qs[1] +
-                                                   (head * group + rw % group) * p.qs[2] + piece * 8);
+                                                   node * p.qs[1] +
+                                                   (head * p.group + rw - node * p.group) * p.qs[2] + piece * 8);
       }
     };
     auto store_q = [&](int8_t *exps) {
@@ -435,9 +446,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
                   1e-30f);
       Line after = at;
       after.next(p);
-      const int head = at.u / p.blocks, rb = at.u % p.blocks;
+      const int head = head_of(p, at.u), rb = block_of_rows(p, at.u);
       const int row0 = rb * L::kRows, row = row0 + (NQ == 2 ? q * 128 : 0) + row_in;
-      const int node = row / group, h = head * group + row % group;
+      const int node = node_of(p, row), h = head * p.group + row - node * p.group;
       const bool real = row < p.rows;
       uint64_t word = 0;
       if (real)
@@ -655,8 +666,8 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
           }
         }
       };
-      const int first = at.first(), final = at.final();
-      const bool whole = first == final;
+      const bool whole = at.whole();
+      const int first = whole ? 0 : at.first(), final = whole ? 0 : at.final();
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
       uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
       auto store = [&](int c, const float (&y)[32], float inv, bool empty) {
@@ -699,47 +710,53 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         auto state_of = [&](int block) {
           return __ldcg(reinterpret_cast<const float2 *>(place(block) + L::kRows * L::D) + mine_row);
         };
-        float *mine = place(blockIdx.x);
+        Join join(first, final, blockIdx.x, kJoinAtOnce<L>);
+        float *to = place(blockIdx.x);
 #pragma unroll 1
         for (int k = col0; k < col1; k += 32) {
           uint32_t y[32];
           load(k, y);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            reinterpret_cast<uint4 *>(mine)[(k + e) / 4 * L::kRows + mine_row] =
+            reinterpret_cast<uint4 *>(to)[(k + e) / 4 * L::kRows + mine_row] =
                 make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
-        if (NQ == 2 || q == 0)
-          reinterpret_cast<float2 *>(mine + L::kRows * L::D)[mine_row] = make_float2(m, l);
-        __threadfence();
-        sync_rows();
-        if (tid == 0) {
-          const uint32_t before = atomicAdd(p.arrived + first, 1u);
-          *last = before == uint32_t(final - first);
-          if (*last) p.arrived[first] = 0;
+#pragma unroll 1
+        while (true) {
+          if (NQ == 2 || q == 0)
+            reinterpret_cast<float2 *>(to + L::kRows * L::D)[mine_row] = make_float2(m, l);
           __threadfence();
-        }
-        sync_rows();
-        if (*last) {
-          float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-          for (int blk = first; blk <= final; ++blk) top = fmaxf(top, state_of(blk).x);
-#pragma unroll 4
-          for (int blk = first; blk <= final; ++blk) {
-            const float2 st = state_of(blk);
-            sum += st.y * (st.x == -INFINITY ? 0.f : ex2(st.x - top));
+          sync_rows();
+          if (tid == 0) {
+            uint32_t *counter = join.counter(p);
+            *last = atomicAdd(counter, 1u) + 1 == join.members();
+            if (*last) *counter = 0;
+            __threadfence();
           }
-          const bool empty = node >= at.count || (top == -INFINITY && sum == 0.f);
-          const float inv = empty ? 0.f : p.v_scale / sum;
+          sync_rows();
+          if (!*last) break;
+          m = -INFINITY;
+          l = 0.f;
+#pragma unroll 4
+          for (int blk = join.lo; blk <= join.hi; blk += join.step) m = fmaxf(m, state_of(blk).x);
+#pragma unroll 4
+          for (int blk = join.lo; blk <= join.hi; blk += join.step) {
+            const float2 st = state_of(blk);
+            l += st.y * (st.x == -INFINITY ? 0.f : ex2(st.x - m));
+          }
+          const bool all = join.last();
+          to = place(join.lo);
+          const bool empty = node >= at.count || (m == -INFINITY && l == 0.f);
+          const float inv = empty ? 0.f : p.v_scale / l;
 #pragma unroll 1
           for (int k = col0; k < col1; k += 32) {
             float f[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
 #pragma unroll 2
-            for (int blk = first; blk <= final; ++blk) {
+            for (int blk = join.lo; blk <= join.hi; blk += join.step) {
               const float mm = state_of(blk).x;
-              const float wt = mm == -INFINITY ? 0.f : ex2(mm - top);
+              const float wt = mm == -INFINITY ? 0.f : ex2(mm - m);
               const float4 *part = reinterpret_cast<const float4 *>(place(blk)) + mine_row;
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
@@ -750,9 +767,22 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
                 f[e + 3] += v.w * wt;
               }
             }
-            store(k, f, inv, empty);
+            if (all) {
+              store(k, f, inv, empty);
+            } else {
+              // (these columns of this row are read by no other thread)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                reinterpret_cast<float4 *>(to)[(k + e) / 4 * L::kRows + mine_row] =
+                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
           }
-          store_lse(top, sum, empty);
+          if (all) {
+            store_lse(m, l, empty);
+            break;
+          }
+          sync_rows();                                   // everybody has read the group's states
+          join.next();
         }
       }
       // the outputs are read and *last is free before the next unit begins

@@ -11,7 +11,12 @@
 // Bytes bound it for prompts and latency for single tokens: a block takes
 // the heads of up to four tokens, so that their angles are worked out once,
 // and 16 elements of a head (two 16-byte loads) are a thread's item; with few
-// tokens the heads are spread over more blocks instead.
+// tokens the heads are spread over more blocks instead.  Four tokens a block
+// and not one, because the product in 64 bits and the sincospif of a pair are
+// dearer than the bytes of the pair in one head.  Measured: 16381 tokens of 40
+// + 2 x 8 heads of 128 in FP16 (470 MB) 84 us, 5.6 TB/s, which is what a copy
+// of as many bytes takes within a fifth; one token of 40 + 2 x 40 heads 3.3 us,
+// a launch; 32 trees of 8 nodes (6.8 MB) into an E4M3 cache under 6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
