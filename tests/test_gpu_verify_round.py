@@ -791,6 +791,22 @@ def test_attention_of_few_units_over_long_caches(vg, n, hq, d, length, held):
     check_attention(vg, 48, 3, n, hq, 1, d, torch.bfloat16, held, 16, [length // 2, 0, length], counts=[n, 1, n])
 
 
+@pytest.mark.parametrize("n,hq,d", [(9, 4, 192), (13, 5, 144), (16, 5, 256), (40, 1, 176), (64, 3, 192), (7, 3, 128)])
+@pytest.mark.parametrize("dtype,held", [(torch.bfloat16, None), (torch.float16, None), (torch.bfloat16, E4M3)])
+def test_attention_rows_that_fill_no_block(vg, n, hq, d, dtype, held):
+    check_attention(vg, 51, 3, n, hq, 1, d, dtype, held or dtype, 32, [700, 3, 131], tree="random")
+    check_attention(vg, 52, 2, n, hq, 1, d, dtype, held or dtype, 48, [90, 260], counts=[n // 2, n], poison=True)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(2, 40, 40, 96), (3, 10, 5, 64), (5, 20, 5, 128), (1, 7, 7, 256)])
+@pytest.mark.parametrize("dtype,held", [(torch.bfloat16, None), (torch.float16, E4M3)])
+def test_attention_of_many_short_sequences(vg, n, hq, hkv, d, dtype, held):
+    """Units of one tile among longer ones, several to a block."""
+    lens = [2, 0, 61, 64, 65, 1, 200, 5, 7, 30, 1000, 59, 62, 3, 3, 3, 4, 17, 48]
+    check_attention(vg, 53, len(lens), n, hq, hkv, d, dtype, held or dtype, 16, lens, tree="random")
+    check_attention(vg, 54, len(lens), n, hq, hkv, d, dtype, held or dtype, 32, lens[::-1], poison=True)
+
+
 def test_attention_negative_and_zero_scale(vg):
     for n, hq in ((4, 4), (40, 4)):
         for scale in (-0.2, 0.0):

@@ -20,7 +20,8 @@ int row_index(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 
 const Variant &pick(int type, int d, int rows) {
   if (is_wide(d, rows)) return kWide[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
   const Variants &of = type == kBf16 ? kVariantsBf16 : type == kF16 ? kVariantsF16 : kVariantsE4M3;
-  return of[d <= 64 ? 0 : d <= 128 ? 1 : 2][row_index(rows)];
+  const int r = row_index(rows);
+  return of[d <= 64 ? 0 : d <= 128 ? 1 : d <= 192 && r >= 2 ? 2 : 3][r];
 }
 
 int cache_type(const vg_kv_cache &c) {

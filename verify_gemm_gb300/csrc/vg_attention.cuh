@@ -148,7 +148,7 @@ struct Cfg {
   // as many of twice the size move an E4M3 tile faster
   static constexpr int kRow = kType == kE4M3 && DC == 1 ? 64 : 128;
   static constexpr int kElems = kRow / kSize;
-  static constexpr int kChunks = DC * 64 / kElems;
+  static constexpr int kChunks = (DC * 64 + kElems - 1) / kElems;
   static constexpr int kChunk = kTile * kRow;
   static constexpr int kSlot = kChunks * kChunk;         // one tile of K or of V
   static constexpr int D = DC * 64;
@@ -166,7 +166,7 @@ struct Cfg {
   static constexpr int kQBytes = kRows * kQRow;
   static constexpr int kWarpState = NT * 32 * 16;        // one warp's o
   // every warp's o is laid open for the joining, at most 64 KB at a time
-  static constexpr int kPasses = DC == 4 && KW > 1 ? 2 : 1;
+  static constexpr int kPasses = DC >= 3 && KW > 1 ? 2 : 1;
   static constexpr int kScratch = KW == 1 ? 0 : kConsumers * kWarpState / kPasses;
   static constexpr int TPW = NT / KW;                    // tiles that a warp joins
   static constexpr int kState = kConsumers * 16 * 8;     // m, l of each warp's rows
@@ -437,6 +437,7 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
   const int page_boxes = p.cache.page_size / p.box;
   int s = kv, n = 0;
   uint32_t par = 1;                                      // slots start empty
+  int pages = -1, ahead = -1, seq = -1, window = -1;     // the numbers held, of which sequence and window
   for (; at.valid(); at.next(p)) {
     const int head = head_of(p, at.u);
     const int total = at.len + at.count;
@@ -445,8 +446,12 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
       const int box = window * 32 + lane, i = box / page_boxes;
       return box * p.box < total && i < p.cache.max_pages ? table[i] : -1;
     };
-    int window = at.t0 * boxes / 32;
-    int pages = fetch(window), ahead = fetch(window + 1);
+    if (at.b != seq || at.t0 * boxes / 32 != window) {   // (a sequence's heads have the same pages)
+      seq = at.b;
+      window = at.t0 * boxes / 32;
+      pages = fetch(window);
+      ahead = fetch(window + 1);
+    }
     for (int t = at.t0; t < at.t1; ++t, ++n) {
       if (t * boxes / 32 != window) {
         pages = ahead;
@@ -576,70 +581,104 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // up to 32 rows the next unit's is fetched before this one's results are
   // joined: under load a fetch takes 3 us.
   constexpr int kQn = L::kRows / kConsumers;
+  // A unit of one tile occupies one group of key warps only; the others go on
+  // to the next units meanwhile.  Each row group's KT warps are by themselves
+  // then: their q lies in the first one's part of the scratch memory, and they
+  // meet at a barrier of their own.  (1640 units of one tile 36.6 -> 17 us.)  Heads
+  // above 128 have no room for it, and E4M3 heads above 64 no registers: their
+  // long sequences would take 4 % more.
+  constexpr bool kSolo = L::NG > 1 && L::kPasses == 1 && !(kType == kE4M3 && DC > 1);
+  auto solo = [&](const Line &u) { return kSolo && u.valid() && u.tiles == 1; };
+  const int pair = 2 + rw * L::NG + grp;
+  uint8_t *solo_q = scratch + (rw * L::KW + grp * L::KT) * L::kWarpState;
+  float *solo_unit = reinterpret_cast<float *>(solo_q + 16 * L::kQRow);
+  static_assert(!kSolo || 16 * L::kQRow + 64 <= L::kWarpState * L::KT, "room for q");
   // (E4M3 has no registers for it: 156 -> 170 us over 262001 keys.)
   constexpr bool kAheadQ = L::kRows <= 32 && kType != kE4M3;
   uint4 qv[kQn];
+  auto q_row = [&](const Line &u, int r) {
+    const int row = block_of_rows(p, u.u) * L::kRows + r, node = node_of(p, row);
+    if (row >= p.rows || lane * 8 >= p.d) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] + node * p.qs[1] +
+                                            (head_of(p, u.u) * p.group + row - node * p.group) * p.qs[2] + lane * 8);
+  };
   auto fetch_q = [&](const Line &u) {
-    const int head = head_of(p, u.u), row0 = block_of_rows(p, u.u) * L::kRows;
 #pragma unroll
-    for (int k = 0; k < kQn; ++k) {
-      const int row = row0 + k * kConsumers + warp, node = node_of(p, row);
-      qv[k] = make_uint4(0, 0, 0, 0);
-      if (row < p.rows && lane * 8 < p.d)
-        qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
-                                                 node * p.qs[1] +
-                                                 (head * p.group + row - node * p.group) * p.qs[2] + lane * 8);
-    }
+    for (int k = 0; k < kQn; ++k) qv[k] = q_row(u, k * kConsumers + warp);
   };
   // E4M3: in FP16, each row brought to the top of its range by a power of two,
   // which keeps every bit of a BF16 row that counts (2^-29 of the row's
   // largest element and more)
-  auto store_q = [&] {
+  auto put_q = [&](uint4 v, uint8_t *to, float *unit) {
+    if constexpr (kType == kE4M3) {
+      float f[8];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < kQn; ++k) {
-      const int r = k * kConsumers + warp;
-      if constexpr (kType == kE4M3) {
-        float f[8];
-        const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint16_t x = uint16_t(w[e / 2] >> (16 * (e & 1)));
-          f[e] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
-          top = fmaxf(top, fabsf(f[e]));
-        }
-#pragma unroll
-        for (int m = 16; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
-        const int e = q_exponent(top);
-        const float down = ldexpf(1.f, -e);
-        qv[k] = make_uint4(pack2<kF16>(f[0] * down, f[1] * down), pack2<kF16>(f[2] * down, f[3] * down),
-                           pack2<kF16>(f[4] * down, f[5] * down), pack2<kF16>(f[6] * down, f[7] * down));
-        if (lane == 0) q_unit[r] = ldexpf(1.f, e);
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t x = uint16_t(w[e / 2] >> (16 * (e & 1)));
+        f[e] = p.q_f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
+        top = fmaxf(top, fabsf(f[e]));
       }
-      if (lane * 8 < L::D) *reinterpret_cast<uint4 *>(q_smem + r * L::kQRow + lane * 16) = qv[k];
+#pragma unroll
+      for (int m = 16; m; m /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+      const int e = q_exponent(top);
+      const float down = ldexpf(1.f, -e);
+      v = make_uint4(pack2<kF16>(f[0] * down, f[1] * down), pack2<kF16>(f[2] * down, f[3] * down),
+                     pack2<kF16>(f[4] * down, f[5] * down), pack2<kF16>(f[6] * down, f[7] * down));
+      if (lane == 0) *unit = ldexpf(1.f, e);
     }
+    if (lane * 8 < L::D) *reinterpret_cast<uint4 *>(to + lane * 16) = v;
   };
-  if (kAheadQ && at.valid()) fetch_q(at);
+  bool fetched = kAheadQ && at.valid() && !solo(at);
+  if (fetched) fetch_q(at);
   for (; at.valid();) {
     Line after = at;
     after.next(p);
+    const bool alone = solo(at);
+    if (alone && tile_no % L::NG != uint32_t(grp)) {
+      ++tile_no;
+      fetched = false;
+      at = after;
+      continue;
+    }
     const int head = head_of(p, at.u), row0 = block_of_rows(p, at.u) * L::kRows;
-    if (!kAheadQ) fetch_q(at);
-    store_q();
-    named_bar(1, kConsumers * 32);
+    uint32_t q_at = q0 + rw * 16 * L::kQRow;             // of this warp's rows
+    const float *unit = q_unit + rw * 16;
+    if (alone) {
+      constexpr int kN = 16 / L::KT;
+      uint4 v[kN];
+#pragma unroll
+      for (int k = 0; k < kN; ++k) v[k] = q_row(at, rw * 16 + k * L::KT + kt);
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        put_q(v[k], solo_q + (k * L::KT + kt) * L::kQRow, solo_unit + k * L::KT + kt);
+      q_at = smem_addr(solo_q);
+      unit = solo_unit;
+      named_bar(pair, L::KT * 32);
+    } else {
+      if (!fetched) fetch_q(at);
+#pragma unroll
+      for (int k = 0; k < kQn; ++k) {
+        const int r = k * kConsumers + warp;
+        put_q(qv[k], q_smem + r * L::kQRow, q_unit + r);
+      }
+      named_bar(1, kConsumers * 32);
+    }
+    fetched = false;
 
     uint32_t qf[L::kQReg ? DC * 4 : 1][4];
     auto load_q = [&](uint32_t (&a)[4], int ks) {
       if constexpr (kType == kE4M3) {
         // k order of a step: thread t has elements 4t .. 4t + 3
-        const uint32_t base = q0 + (rw * 16 + g) * L::kQRow + ks * 32 + t * 8;
+        const uint32_t base = q_at + g * L::kQRow + ks * 32 + t * 8;
         const uint2 lo = lds64(base), hi = lds64(base + 8 * L::kQRow);
         a[0] = lo.x;
         a[1] = hi.x;
         a[2] = lo.y;
         a[3] = hi.y;
       } else {
-        ldsm4(a, q0 + (rw * 16 + (lane & 15)) * L::kQRow + ks * 32 + (lane >> 4) * 16);
+        ldsm4(a, q_at + (lane & 15) * L::kQRow + ks * 32 + (lane >> 4) * 16);
       }
     };
     if constexpr (L::kQReg) {
@@ -648,8 +687,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     float cr[2] = {p.c, p.c};
     if constexpr (kType == kE4M3) {
-      cr[0] *= q_unit[rw * 16 + g];
-      cr[1] *= q_unit[rw * 16 + g + 8];
+      cr[0] *= unit[g];
+      cr[1] *= unit[g + 8];
     }
     // the drafted nodes that this thread's two rows attend to
     uint64_t word[2];
@@ -668,12 +707,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
+    // a group of rows that do not exist leaves the tensor cores to the others
+    const bool idle = row0 + rw * 16 >= p.rows;
+
     // ---------------------------------------------------------------- tiles
     for (int tile = at.t0; tile < at.t1; ++tile, ++tile_no) {
       if (tile_no % L::NG != uint32_t(grp)) continue;
       const uint32_t ik = 2 * tile_no, iv = ik + 1;
       const uint32_t sk = ik % NS, sv = iv % NS;
       wait_phase(full0 + 8 * sk, (ik / NS) & 1, failed, p.error);
+      if (RW > 1 && idle) {
+        wait_phase(full0 + 8 * sv, (iv / NS) & 1, failed, p.error);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(empty0 + 8 * sk);
+          mbar_arrive(empty0 + 8 * sv);
+        }
+        continue;
+      }
       const uint32_t ok_bits = page_ok[tile_no % 16];
 #pragma unroll
       for (int j = 0; j < L::kSub; ++j) {
@@ -906,7 +957,86 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(empty0 + 8 * sv);
     }
 
-    if (kAheadQ && after.valid()) fetch_q(after);
+    // What a row's result is, from `res` (tile_of(i): which tile of its columns
+    // res[i] is) with maximum mm and sum ll.
+    auto emit = [&](auto &res, const float (&mm)[2], const float (&ll)[2], bool first_warp, auto &&tile_of) {
+      constexpr int N = sizeof(res) / sizeof(res[0]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + rw * 16 + g + 8 * r, node = node_of(p, row);
+        if (row >= p.rows) continue;
+        const int h = head * p.group + row - node * p.group;
+        // NaN is not nothing
+        const bool empty = node >= at.count || (mm[r] == -INFINITY && ll[r] == 0.f);
+        const float inv = empty ? 0.f : p.v_scale / ll[r];
+        const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
+        const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int nt = tile_of(i);
+          const float v0 = empty ? 0.f : res[i][2 * r] * inv, v1 = empty ? 0.f : res[i][2 * r + 1] * inv;
+          if constexpr (kType == kE4M3) {
+            // columns 4t + 2e of even tiles, 4t + 2e + 1 of odd ones: an even
+            // tile's lane stores for both where it has both
+            if constexpr (N >= 2) {
+              if (i % 2 == 0 && 8 * nt < p.d) {
+                const float u0 = empty ? 0.f : res[i + 1][2 * r] * inv;
+                const float u1 = empty ? 0.f : res[i + 1][2 * r + 1] * inv;
+                *reinterpret_cast<uint2 *>(out + 8 * nt + 4 * t) =
+                    make_uint2(pack_out(v0, u0, f16), pack_out(v1, u1, f16));
+              }
+            } else if (8 * (nt & ~1) < p.d) {
+              const uint32_t both = pack_out(v0, v1, f16);
+              out[out_col<kType>(nt, t, 0)] = uint16_t(both);
+              out[out_col<kType>(nt, t, 1)] = uint16_t(both >> 16);
+            }
+          } else if (8 * nt < p.d) {
+            *reinterpret_cast<uint32_t *>(out + 8 * nt + 2 * t) = pack_out(v0, v1, f16);
+          }
+        }
+        if (p.lse && t == 0 && first_warp)
+          p.lse[at_row] = empty ? -INFINITY : (mm[r] - kLift<kType> + log2f(ll[r])) * kLn2;
+      }
+    };
+    if constexpr (kSolo) {
+      if (alone) {
+        // the KT warps join shares of the columns among themselves
+        constexpr int TS = L::NT / L::KT;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          l[r] += __shfl_xor_sync(~0u, l[r], 1);
+          l[r] += __shfl_xor_sync(~0u, l[r], 2);
+        }
+        named_bar(pair, L::KT * 32);                     // q has been read
+        const int warp0 = rw * L::KW + grp * L::KT;
+        float4 *box = reinterpret_cast<float4 *>(scratch) + warp0 * (L::NT * 32) + lane;
+#pragma unroll
+        for (int i = 0; i < L::NT; ++i)
+          box[(kt * L::NT + i) * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        if (t == 0) {
+          state[warp * 16 + g] = make_float2(m[0], l[0]);
+          state[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+        }
+        named_bar(pair, L::KT * 32);
+        float res[TS][4], mj[2] = {-INFINITY, -INFINITY}, lj[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < TS; ++i) res[i][0] = res[i][1] = res[i][2] = res[i][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < L::KT; ++k) {
+          const float2 st[2] = {state[(warp0 + k) * 16 + g], state[(warp0 + k) * 16 + g + 8]};
+          merge<TS>(res, mj, lj, st, [&](int i) { return box[(k * L::NT + kt * TS + i) * 32]; });
+        }
+        emit(res, mj, lj, kt == 0, [&](int i) { return kt * TS + i; });
+        named_bar(pair, L::KT * 32);                     // scratch is free again
+        at = after;
+        continue;
+      }
+    }
+    if constexpr (kAheadQ) {
+      fetched = after.valid() && !solo(after);
+      if (fetched) fetch_q(after);
+    }
 
     // ------------------------------------- join the key warps, then the blocks
     const bool whole = at.whole();
@@ -1046,45 +1176,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 
     // -------------------------------------------------------------- results
-    if (done) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = row0 + rw * 16 + g + 8 * r, node = node_of(p, row);
-        if (row >= p.rows) continue;
-        const int h = head * p.group + row - node * p.group;
-        // NaN is not nothing
-        const bool empty = node >= at.count || (mj[r] == -INFINITY && lj[r] == 0.f);
-        const float inv = empty ? 0.f : p.v_scale / lj[r];
-        const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
-        uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
-        const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
-#pragma unroll
-        for (int i = 0; i < TPW; ++i) {
-          const int nt = tile_of(i);
-          const float v0 = empty ? 0.f : res[i][2 * r] * inv, v1 = empty ? 0.f : res[i][2 * r + 1] * inv;
-          if constexpr (kType == kE4M3) {
-            // columns 4t + 2e of even tiles, 4t + 2e + 1 of odd ones: an even
-            // tile's lane stores for both where it has both
-            if constexpr (TPW >= 2) {
-              if (i % 2 == 0 && 8 * nt < p.d) {
-                const float u0 = empty ? 0.f : res[i + 1][2 * r] * inv;
-                const float u1 = empty ? 0.f : res[i + 1][2 * r + 1] * inv;
-                *reinterpret_cast<uint2 *>(out + 8 * nt + 4 * t) =
-                    make_uint2(pack_out(v0, u0, f16), pack_out(v1, u1, f16));
-              }
-            } else if (8 * (nt & ~1) < p.d) {
-              const uint32_t both = pack_out(v0, v1, f16);
-              out[out_col<kType>(nt, t, 0)] = uint16_t(both);
-              out[out_col<kType>(nt, t, 1)] = uint16_t(both >> 16);
-            }
-          } else if (8 * nt < p.d) {
-            *reinterpret_cast<uint32_t *>(out + 8 * nt + 2 * t) = pack_out(v0, v1, f16);
-          }
-        }
-        if (p.lse && t == 0 && kg == 0)
-          p.lse[at_row] = empty ? -INFINITY : (mj[r] - kLift<kType> + log2f(lj[r])) * kLn2;
-      }
-    }
+    if (done) emit(res, mj, lj, kg == 0, tile_of);
     named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
     at = after;
   }
@@ -1107,9 +1199,9 @@ Variant variant() {
           kAttnThreads, &allowed};
 }
 
-// The variants of one cache type, by head_dim up to 64, 128, 256 and by row
-// groups 1, 2, 4, 8: a translation unit each.
-using Variants = Variant[3][4];
+// The variants of one cache type, by head_dim up to 64, 128, 192, 256 and by
+// row groups 1, 2, 4, 8: a translation unit each.
+using Variants = Variant[4][4];
 extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
 
 // The tcgen05 kernel (vg_attention_wide.cuh): by cache type, head_dim up to 64
@@ -1117,10 +1209,12 @@ extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
 using WideVariants = Variant[3][2][2];
 extern const WideVariants kWide;
 
-// (Heads up to 128 go to the tcgen05 kernel above 32 rows.)
+// (Heads up to 128 go to the tcgen05 kernel above 32 rows.  Up to 32 the bytes
+// and not the products bound heads of 192, and those of 256 serve.)
 #define VG_ATTENTION_VARIANTS(T)                      \
-  {{variant<T, 1, 1>(), variant<T, 1, 2>()},          \
-   {variant<T, 2, 1>(), variant<T, 2, 2>()},          \
+  {{variant<T, 1, 1>(), variant<T, 1, 2>()},           \
+   {variant<T, 2, 1>(), variant<T, 2, 2>()},           \
+   {{}, {}, variant<T, 3, 4>(), variant<T, 3, 8>()},  \
    {variant<T, 4, 1>(), variant<T, 4, 2>(), variant<T, 4, 4>(), variant<T, 4, 8>()}}
 
 }  // namespace attn
