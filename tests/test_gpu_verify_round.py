@@ -714,6 +714,37 @@ def test_work_runs_on_the_given_stream(vg):
     assert torch.equal(out, want)
 
 
+def test_what_a_call_makes_belongs_to_its_stream(vg):
+    """The outputs and the workspace that a call is not given are made on the stream that it is
+    given: a current stream that is held up delays none of it."""
+    g = torch.Generator().manual_seed(15)
+    cache, ck, cv, table = build_cache(vg, g, 2, 5000, 2, 128, 16, torch.bfloat16, torch.bfloat16)
+    q = randn(g, 2, 8, 4, 128, dtype=torch.bfloat16)
+    lens = torch.tensor([4900, 17], dtype=torch.int32, device=DEV)
+    logits = randn(g, 3, 5001)
+    p = torch.softmax(randn(g, 2, 4, 999), -1).contiguous()
+    tokens = torch.zeros((2, 4), dtype=torch.int32, device=DEV)
+    parents = torch.arange(-1, 3, dtype=torch.int32, device=DEV).expand(2, 4).contiguous()
+    rnd = torch.full((2, 4), 0.5, device=DEV)
+
+    def calls(stream):
+        return [vg.tree_attention(q, cache, lens, stream=stream), vg.probabilities(logits, stream=stream),
+                *vg.verify_tree(p, p, tokens, parents, rnd, stream=stream)]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(400_000_000)                       # some 0.2 s
+    held = torch.cuda.Event()
+    held.record()
+    got = calls(side)
+    side.synchronize()
+    early = not held.query()
+    torch.cuda.synchronize()
+    assert early
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_refusals(vg):
     g = torch.Generator().manual_seed(14)
     cache, ck, cv, table = build_cache(vg, g, 2, 64, 2, 64, 16, torch.bfloat16, torch.bfloat16)

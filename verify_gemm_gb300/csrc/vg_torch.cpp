@@ -81,8 +81,8 @@ float number(PyObject *o) {
 
 const vg_kv_cache *cache_of(PyObject *o) { return reinterpret_cast<const vg_kv_cache *>(integer(o)); }
 
-vg_stream_t stream_of(PyObject *o, const Tensor &t) {
-  if (given(o)) return reinterpret_cast<vg_stream_t>(integer(o));
+// Work and the tensors made for it go to the current stream.
+vg_stream_t stream_of(const Tensor &t) {
   return reinterpret_cast<vg_stream_t>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
 }
 
@@ -111,9 +111,9 @@ PyObject *result(vg_status s, const Tensor &t) {
   }                                                                                   \
   END_HANDLE_TH_ERRORS
 
-// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out, stream
+// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(12)
+  VG_BEGIN(11)
   vg_rope_desc d;
   const Tensor &q = heads(a[0], "q", d.q_stride), &k = heads(a[1], "k", d.k_stride),
                &v = heads(a[2], "v", d.v_stride), &f = tensor(a[3], "inv_freq");
@@ -143,13 +143,13 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   d.q_heads = int32_t(q.size(2));
   d.rot = int32_t(2 * f.numel());
   d.factor = number(a[9]);
-  return result(vg_rope_append(&d, cache, stream_of(a[11], q)), out);
+  return result(vg_rope_append(&d, cache, stream_of(q)), out);
   VG_END
 }
 
-// q, cache, lens, tree, counts, scale, out, lse, workspace, stream
+// q, cache, lens, tree, counts, scale, out, lse, workspace
 PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(10)
+  VG_BEGIN(9)
   vg_attention_desc d;
   const Tensor &q = heads(a[0], "q", d.q_stride);
   const vg_kv_cache *cache = cache_of(a[1]);
@@ -170,13 +170,13 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   d.n = int32_t(n);
   d.q_heads = int32_t(hq);
   d.scale = number(a[5]);
-  return result(vg_tree_attention(&d, cache, ws.data_ptr(), size_t(ws.numel()), stream_of(a[9], q)), out);
+  return result(vg_tree_attention(&d, cache, ws.data_ptr(), size_t(ws.numel()), stream_of(q)), out);
   VG_END
 }
 
-// logits, temperature, out, stream
+// logits, temperature, out
 PyObject *probabilities(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(4)
+  VG_BEGIN(3)
   const Tensor &x = tensor(a[0], "logits");
   if (x.dim() < 1 || !x.numel() || !x.is_contiguous())
     throw Bad{"logits: expected a contiguous CUDA tensor that is not empty"};
@@ -190,14 +190,14 @@ PyObject *probabilities(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   }
   const Tensor out = output(a[2], x, at::kFloat, "out");
   return result(vg_probabilities(x.const_data_ptr(), type_of(x), rows, vocab, t,
-                                 static_cast<float *>(out.data_ptr()), stream_of(a[3], x)),
+                                 static_cast<float *>(out.data_ptr()), stream_of(x)),
                 out);
   VG_END
 }
 
-// p, q, tokens, parents, u, counts, stream -> (accepted, path, out)
+// p, q, tokens, parents, u, counts -> (accepted, path, out)
 PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(7)
+  VG_BEGIN(6)
   const Tensor &p = tensor(a[0], "p");
   if (p.scalar_type() != at::kFloat || p.dim() != 3 || !p.is_contiguous())
     throw Bad{"p: expected a contiguous CUDA float32 tensor [batch, n, vocab]"};
@@ -222,7 +222,7 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const vg_status s = vg_verify_tree(
       static_cast<const float *>(p.const_data_ptr()), q, tokens, parents, counts, u, int(B), int(n),
       int(rows), V, static_cast<int32_t *>(accepted.data_ptr()), static_cast<int32_t *>(path.data_ptr()),
-      static_cast<int32_t *>(out.data_ptr()), stream_of(a[6], p));
+      static_cast<int32_t *>(out.data_ptr()), stream_of(p));
   if (s) return PyLong_FromLong(s);
   PyObject *r = PyTuple_New(3);
   if (!r) return nullptr;

@@ -32,10 +32,6 @@ def _calls():
     return _native
 
 
-def _handle(stream):
-    return stream.cuda_stream if stream is not None else None
-
-
 def _checked(result, where):
     if type(result) is int:          # a vg_status
         _lib.check(result, where)
@@ -127,11 +123,14 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
     depth[b, i] (depth None: i).  The first 2 * inv_freq.numel() elements of a
     head turn: pairs (j, j + rot/2) for layout "half", (2j, 2j + 1) for
     "interleaved".  Nodes past counts[b] append nothing and give 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):      # q_out, too, is made there
+            return rope_append(q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out)
     if layout not in _LAYOUTS:
         raise ValueError("layout: 'half' or 'interleaved'")
     return _checked((_native or _calls()).rope_append(
-        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out,
-        _handle(stream)), "vg_rope_append")
+        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out),
+        "vg_rope_append")
 
 
 def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
@@ -157,11 +156,14 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     q_heads], written if given.  workspace: from tree_attention_workspace,
     made anew by each call that is given none; calls that share one must not
     overlap."""
+    if stream is not None:
+        with torch.cuda.stream(stream):      # out and a new workspace, too, are made there
+            return tree_attention(q, cache, lens, tree, counts, scale, out, lse, workspace)
     if workspace is None:
         workspace = tree_attention_workspace(q, cache)
     return _checked((_native or _calls()).tree_attention(
         q, cache._at, lens, tree, counts, cache.head_dim ** -0.5 if scale is None else scale, out, lse,
-        workspace, _handle(stream)), "vg_tree_attention")
+        workspace), "vg_tree_attention")
 
 
 def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -170,8 +172,10 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
     float16 or float32), each row over its own temperature (float32, one for
     every row; None: 1).  A temperature <= 0 gives 1 at the row's first
     largest logit."""
-    return _checked((_native or _calls()).probabilities(logits, temperature, out, _handle(stream)),
-                    "vg_probabilities")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return probabilities(logits, temperature, out)
+    return _checked((_native or _calls()).probabilities(logits, temperature, out), "vg_probabilities")
 
 
 def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
@@ -185,5 +189,7 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
     Returns int32 (accepted [batch], path [batch, n], out [batch, n + 1]): how
     many drafts hold, their nodes, and their tokens with the one drawn after
     them; -1 behind.  include/vgemm.h (vg_verify_tree) has the rule."""
-    return _checked((_native or _calls()).verify_tree(p, q, tokens, parents, u, counts, _handle(stream)),
-                    "vg_verify_tree")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_tree(p, q, tokens, parents, u, counts)
+    return _checked((_native or _calls()).verify_tree(p, q, tokens, parents, u, counts), "vg_verify_tree")
