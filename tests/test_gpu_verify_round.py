@@ -211,6 +211,35 @@ def test_rope_far_positions(vg, past):
     assert ((out.double().cpu()[0, :, 0] - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("B,n,hq,hkv,d", [(3, 5001, 2, 1, 64), (77, 13, 4, 4, 64), (11, 333, 3, 1, 128)])
+def test_rope_many_tokens_of_few_heads(vg, B, n, hq, hkv, d):
+    """Blocks of several tokens, of more than one sequence, the last of them not full."""
+    counts = [n - (7 * b) % n for b in range(B)]
+    check_rope(vg, 7, B, n, hq, hkv, d, d, "half", torch.bfloat16, E4M3, 32, 3, counts=counts)
+    check_rope(vg, 8, B, n, hq, hkv, d, 16, "interleaved", torch.float16, torch.float16, 16, 40)
+
+
+def test_rope_any_frequency(vg):
+    """Frequencies of either sign, of many turns a position, tiny ones and none."""
+    inv = [0.0, -0.0, 1.0, -1.0, 0.3, -0.7, 2.0, 6.283185307179586, 12.5, 1e3 + 0.1, -123456.789, 1e-3, 1e-9,
+           -1e-12, 2.0 ** -60, 2.0 ** -80, 1e-300, 5e-324, 2.0 ** 20, -2.0 ** 33, 3.14159, 1e6, 0.999999, -1e-6]
+    d, n = 48, 5
+    g = torch.Generator().manual_seed(9)
+    cache, *_ = build_cache(vg, g, 1, 16, 1, d, 16, torch.float16, torch.float16)
+    q = randn(g, 1, n, 1, d, dtype=torch.float16)
+    f = torch.tensor(inv, dtype=torch.float64, device=DEV)
+    lens = torch.full((1,), 1000, dtype=torch.int32, device=DEV)
+    out = vg.rope_append(q, q, q, f, cache, lens).double().cpu()[0, :, 0]
+    pos = (1000 + torch.arange(n, dtype=torch.float64))[:, None]
+    a = pos * f.cpu()
+    x1, x2 = q.double().cpu()[0, :, 0].split(d // 2, -1)
+    want = torch.cat((x1 * a.cos() - x2 * a.sin(), x1 * a.sin() + x2 * a.cos()), -1)
+    # the reference's product is off by 2^-53 of the angle, as is each of its values' argument
+    size = torch.cat((x1.abs() + x2.abs(),) * 2, -1)
+    tol = (2e-6 + 4 * a.abs().repeat(1, 2) * 2.0 ** -53) * size + u(torch.float16) * want.abs() + 2.0 ** -25
+    assert ((out - want).abs() <= tol).all()
+
+
 def test_rope_drops_what_has_no_page(vg):
     g = torch.Generator().manual_seed(6)
     B, n, h, d, page = 4, 20, 2, 64, 16

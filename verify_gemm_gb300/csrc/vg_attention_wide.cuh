@@ -28,9 +28,10 @@
 //
 // Measured (heads of 128, a kernel by itself):
 //     8 sequences of 8190 keys, 64 nodes, 8 query heads a cache head, BF16
-//         512 rows: 127 us, 1.09 PFLOP/s (tensor pipe busy 47 % of the time;
-//         the rest is the softmax that no product covers, at a unit's first
-//         and last tiles most of all)
+//         512 rows: 124 us, 1.12 PFLOP/s.  Within a unit the tensor cores are
+//         busy two thirds of the time (a stream's step takes 3094 clocks, the
+//         two streams' products 2048); 9 us pass before the first scores and
+//         12 in writing and joining the results of units that are cut
 //     48 sequences of 1200 to 6007 keys, 16 nodes, 4 query heads a cache head
 //         64 rows: 734 MB of FP16 in 133 us, 5.5 TB/s
 //     the same over an E4M3 cache, half the bytes: 143 us, bound by the

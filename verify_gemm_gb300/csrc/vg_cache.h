@@ -59,10 +59,10 @@ inline CacheView cache_view(const vg_kv_cache &c) {
 }
 
 #ifdef __CUDACC__
-// Page of slot `s` (>= 0) of sequence b, or -1.
+// Page of slot `s` (below 2^32) of sequence b, or -1.
 __device__ __forceinline__ int64_t cache_page(const CacheView &c, int b, int64_t s) {
-  const int64_t i = s / c.page_size;
-  if (i >= c.max_pages) return -1;
+  const uint32_t i = uint32_t(s) / uint32_t(c.page_size);
+  if (i >= uint32_t(c.max_pages)) return -1;
   const int32_t p = c.table[b * c.table_stride + i];
   return p >= 0 && p < c.pages ? p : -1;
 }

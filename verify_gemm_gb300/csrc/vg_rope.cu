@@ -9,14 +9,11 @@
 // signed fraction of a turn, goes through sincospif in FP32.
 //
 // Bytes bound it for prompts and latency for single tokens: a block takes
-// the heads of up to four tokens, so that their angles are worked out once,
+// the heads of up to 16 tokens, so that their angles are worked out once,
 // and 16 elements of a head (two 16-byte loads) are a thread's item; with few
-// tokens the heads are spread over more blocks instead.  Four tokens a block
-// and not one, because the product in 64 bits and the sincospif of a pair are
-// dearer than the bytes of the pair in one head.  Measured: 16381 tokens of 40
-// + 2 x 8 heads of 128 in FP16 (470 MB) 84 us, 5.6 TB/s, which is what a copy
-// of as many bytes takes within a fifth; one token of 40 + 2 x 40 heads 3.3 us,
-// a launch; 32 trees of 8 nodes (6.8 MB) into an E4M3 cache under 6 us.
+// tokens the heads are spread over more blocks instead.  Measured: 16381 tokens
+// of 40 + 2 x 8 heads of 128 in FP16 (470 MB) 78 us, 6.0 TB/s, 0.89 of a copy's
+// rate; one token of 40 + 2 x 40 heads 3.0 us, a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -44,6 +41,7 @@ struct RopeParams {
 };
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBlocks = 6;     // of an SM at once: 42 registers a thread (5 blocks: 82 us for 78)
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -53,16 +51,30 @@ __device__ __forceinline__ void from_f(__nv_fp8_e4m3 &o, float x) {
   o.__x = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
-// Frequency j as a fraction of a turn in units of 2^-64.
+// Frequency j, m 2^e with an m of 53 bits, as a fraction of a turn in units of
+// 2^-64: m (2^66 / 2 pi) 2^(e - 2), of which whole turns fall off at the top.
+// (Integers: this GPU does two FP64 operations a clock and SM, and a block of
+// few heads waited for them.)
 __device__ __forceinline__ uint64_t turn_step(const RopeParams &p, int j) {
-  const double f = p.inv_freq[j] * 0.15915494309189535;      // 1 / 2 pi
-  return __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+  const uint64_t bits = uint64_t(__double_as_longlong(p.inv_freq[j]));
+  const int field = int(bits >> 52 & 0x7FF);
+  if (field == 0) return 0;                                  // below 2^-1022
+  const uint64_t m = (bits & ((uint64_t(1) << 52) - 1)) | uint64_t(1) << 52;
+  constexpr uint64_t kTurn = 0xA2F9836E4E441529ull;           // 2^66 / 2 pi
+  const uint64_t lo = m * kTurn, hi = __umul64hi(m, kTurn);
+  const int right = 1077 - field;                            // 2 - e
+  const uint64_t r = right <= 0    ? (right > -64 ? lo << -right : 0)
+                     : right < 64  ? hi << (64 - right) | lo >> right
+                     : right < 128 ? hi >> (right - 64)
+                                   : 0;
+  return bits >> 63 ? -r : r;
 }
-// Cosine and sine, times the factor, of the angle position * step.
+// Cosine and sine, times the factor, of the angle position * step: of its
+// upper 32 bits, 2^-32 turns.
 __device__ __forceinline__ float2 turn(const RopeParams &p, int64_t position, uint64_t step) {
-  const int64_t at = int64_t(uint64_t(position) * step);
+  const int32_t at = int32_t(uint64_t(position) * step >> 32);
   float s, c;
-  sincospif(__ll2float_rn(at) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63: half turns
+  sincospif(__int2float_rn(at) * 4.6566128730773926e-10f, &s, &c);   // * 2^-31: half turns
   return make_float2(c * p.factor, s * p.factor);
 }
 
@@ -127,7 +139,7 @@ struct Token {
   int64_t q, k, v, out, ck, cv;    // element offsets of its first head; ck < 0: nowhere to append
   int used, pad;
 };
-constexpr int kRopeTokens = 4;
+constexpr int kRopeTokens = 16;
 
 template <typename T>
 __device__ __forceinline__ void unpack8(float (&f)[8], const uint4 &v) {
@@ -162,7 +174,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float inv) {
 
 // 16 elements at a time.  blockIdx.x: tokens, blockIdx.y: heads.
 template <typename T, typename C, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_vector_kernel(const RopeParams p, int tokens_per_block, int heads_per_block) {
   extern __shared__ float2 angles[];                          // [tokens][rot / 2], then the steps
   __shared__ Token tok[kRopeTokens];
@@ -176,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   __shared__ int64_t position[kRopeTokens];
   if (tid < tokens) {
     const int64_t at = first + tid;
-    const int b = int(at / p.n), i = int(at % p.n);
+    const int b = int(uint32_t(at) / uint32_t(p.n)), i = int(at - int64_t(b) * p.n);   // tokens are below 2^31
     const int64_t len = p.lens[b];
     const int count = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
     Token t;
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     position[tid] = len + (p.depth ? p.depth[at] : i);
     const int64_t slot = len + i;
     const int64_t page = t.used && slot >= 0 ? cache_page(p.cache, b, slot) : -1;
-    const int64_t off = slot % p.cache.page_size;
+    const int64_t off = uint32_t(slot) % uint32_t(p.cache.page_size);
     t.q = b * p.qs[0] + i * p.qs[1];
     t.k = b * p.ks[0] + i * p.ks[1];
     t.v = b * p.vs[0] + i * p.vs[1];
@@ -266,10 +278,15 @@ void launch_rope(const RopeParams &p, bool vector, int sms, cudaStream_t st) {
     rope_kernel<T, C, kInterleaved><<<unsigned(p.tokens), kRopeThreads, size_t(half) * sizeof(float2), st>>>(p);
     return;
   }
-  // several tokens a block once that leaves eight blocks an SM; under one
-  // block an SM, 256 items a block
+  // as many tokens a block as fit the device at once, up to 2048 items, eight
+  // a thread: what a block waits for before its first item (lengths, pages,
+  // angles) is as long for one token as for sixteen.  Under one block an SM,
+  // 256 items a block.  19005 tokens of 10 heads of 128 take 32 us with 4 tokens
+  // a block and 25 with 16; 1001 tokens of 12 heads of 64 5.3 with 1 and 3.5 with 2.
   const int heads = p.hq + 2 * p.hkv;
-  const int tb = p.tokens >= int64_t(sms) * 8 * kRopeTokens ? kRopeTokens : 1;
+  const int64_t resident = int64_t(kRopeBlocks) * sms;
+  const int tb = int(std::max<int64_t>(
+      1, std::min({int64_t(kRopeTokens), int64_t(2048 / (heads * (p.d / 16))), (p.tokens + resident - 1) / resident})));
   const int hb = p.tokens < 2 * sms ? std::max(1, kRopeThreads / (p.d / 16)) : heads;
   const dim3 grid(unsigned((p.tokens + tb - 1) / tb), unsigned((heads + hb - 1) / hb));
   const size_t smem = size_t(tb) * half * sizeof(float2) + size_t(half) * sizeof(uint64_t);
