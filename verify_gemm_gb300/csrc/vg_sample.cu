@@ -68,17 +68,19 @@ cudaError_t launch_clusters(void (*fn)(P...), unsigned grid, int threads, int cl
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
-// Lets `fn` have `bytes` of dynamic shared memory, once for each device (its
-// bit in `allowed`; device_sms refuses devices above 63).
+// Lets `fn` have `bytes` of dynamic shared memory and clusters of more than
+// eight blocks, once for each device (its bit in `allowed`; device_sms refuses
+// devices above 63).
 template <typename F>
-cudaError_t allow_smem(F *fn, int bytes, std::atomic<uint64_t> &allowed) {
+cudaError_t allow(F *fn, int bytes, std::atomic<uint64_t> &allowed) {
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  if (const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
-    return e;
+  const void *f = reinterpret_cast<const void *>(fn);
+  if (const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+  if (bytes)
+    if (const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
   allowed.fetch_or(bit, std::memory_order_relaxed);
   return cudaSuccess;
 }
@@ -97,17 +99,16 @@ cudaError_t allow_smem(F *fn, int bytes, std::atomic<uint64_t> &allowed) {
 // first index) instead.
 //
 // 256 rows of 151936 BF16 logits (233 MB read and written): 52 us, 4.5 TB/s.
-// With five blocks on an SM half of its warps are resident and they issue 58 %
-// of the time (an exponential is taken twice an element, which costs less than
-// 4 bytes more of shared memory for each): latency and issue share the bound.
-// 512 threads a block, shares of 80 KB and stores that stay in L2 measured the
-// same.  One row: 7.1 us, of which the launch and the exchange are most.
+// An exponential is taken twice an element, which costs less than 4 bytes more
+// of shared memory for each.  Shares of 80 KB, 512 threads a block and stores
+// that stay in L2 measured the same, shares of 20 KB 60 us.  One row: 4.6 us, of
+// which the launch and the exchange are most.
 //
 // Elements go by units of 8 on the grid of the whole array, so that loads
 // and stores are aligned whatever the row's length; the units at a row's two
 // ends go element by element.
 constexpr int kProbThreads = 256, kProbWarps = kProbThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kProbShare = 40 * 1024;          // bytes of a row a block should hold at most ...
 constexpr int kProbShareMax = 96 * 1024;       // ... and may
 constexpr float kLog2e = 1.4426950408889634f;
@@ -124,21 +125,75 @@ __device__ __forceinline__ void copy16(void *to, const void *from) {
                : "memory");
 }
 
+// a + b and a * b, two at a time.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+
 template <typename T>
 struct Unit {                      // 8 logits as they came
   uint4 w[sizeof(T) / 2];
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (sizeof(T) == 4) {
-      const uint4 &v = w[i / 4];
-      return __uint_as_float(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+  __device__ __forceinline__ uint32_t word(int k) const {
+    const uint4 &v = w[k / 4];
+    return k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w;
+  }
+  __device__ __forceinline__ float2 pair(int k) const {       // logits 2k and 2k + 1
+    if constexpr (std::is_same_v<T, float>) {
+      return make_float2(__uint_as_float(word(2 * k)), __uint_as_float(word(2 * k + 1)));
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      return make_float2(__uint_as_float(word(k) << 16), __uint_as_float(word(k) & 0xFFFF0000u));
     } else {
-      const uint32_t v = i / 2 == 0 ? w[0].x : i / 2 == 1 ? w[0].y : i / 2 == 2 ? w[0].z : w[0].w;
-      const uint16_t h = uint16_t(v >> (16 * (i & 1)));
-      T t;
-      memcpy(&t, &h, 2);
-      return to_f(t);
+      __half2 h;
+      const uint32_t v = word(k);
+      memcpy(&h, &v, 4);
+      return __half22float2(h);
     }
   }
+};
+// The largest of units, 16-bit logits two at a time.  (A NaN counts for nothing.)
+template <typename T>
+struct Largest {
+  using Pair = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+  Pair top[2];
+  __device__ __forceinline__ Largest() {
+    const T low = T(-INFINITY);
+    const T both[2] = {low, low};
+    memcpy(&top[0], both, 4);
+    top[1] = top[0];
+  }
+  __device__ __forceinline__ void take(const Unit<T> &v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      Pair x;
+      const uint32_t w = v.word(k);
+      memcpy(&x, &w, 4);
+      top[k % 2] = __hmax2(top[k % 2], x);
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    const Pair x = __hmax2(top[0], top[1]);
+    return fmaxf(to_f(x.x), to_f(x.y));
+  }
+};
+template <>
+struct Largest<float> {
+  float top = -INFINITY;
+  __device__ __forceinline__ void take(const Unit<float> &v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(v.pair(k).x, v.pair(k).y));
+  }
+  __device__ __forceinline__ float value() const { return top; }
 };
 
 // Unit u of a row whose elements are [lo, hi) of the array; elements outside
@@ -158,17 +213,16 @@ __device__ __forceinline__ Unit<T> load_unit(const T *x, int64_t u, int64_t lo, 
   }
   return v;
 }
-__device__ __forceinline__ void store_unit(float *out, int64_t u, int64_t lo, int64_t hi,
-                                           const float (&y)[8]) {
-  const int64_t e = u * 8;
-  if (e >= lo && e + 8 <= hi) {
-    float4 *to = reinterpret_cast<float4 *>(out + e);
-    __stcs(to, make_float4(y[0], y[1], y[2], y[3]));
-    __stcs(to + 1, make_float4(y[4], y[5], y[6], y[7]));
+// Stores elements r .. r + 7 of a row of V.
+__device__ __forceinline__ void store_unit(float *row, int r, int V, const float2 (&y)[4]) {
+  if (r >= 0 && r + 8 <= V) {
+    float4 *to = reinterpret_cast<float4 *>(row + r);
+    __stcs(to, make_float4(y[0].x, y[0].y, y[1].x, y[1].y));
+    __stcs(to + 1, make_float4(y[2].x, y[2].y, y[3].x, y[3].y));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e + i >= lo && e + i < hi) out[e + i] = y[i];
+      if (r + i >= 0 && r + i < V) row[r + i] = i % 2 ? y[i / 2].y : y[i / 2].x;
   }
 }
 
@@ -208,47 +262,58 @@ __global__ void __launch_bounds__(kProbThreads)
   const float t = temperature ? temperature[row] : 1.f;
   const bool greedy = t <= 0.f;
   const float c = kLog2e / t;
+  // units by the place of their first element in the row (-7 and up)
+  const int first = int(u0 * 8 - lo), count = int(V), step = int(stride) * 8;
   auto each = [&](auto &&f) {
     const uint4 *from = parts;
 #pragma unroll 2
-    for (int64_t u = u0; u < end; u += stride, from += kPart * kProbThreads) {
+    for (int r = first; r < count; r += step, from += kPart * kProbThreads) {
       Unit<T> v;
       if constexpr (kHeld) {
 #pragma unroll
         for (int k = 0; k < kPart; ++k) v.w[k] = from[k * kProbThreads];
       } else {
-        v = load_unit(x, u, lo, hi);
+        v = load_unit(x, (lo + r) / 8, lo, hi);
       }
-      f(u, v);
+      f(r, v);
     }
   };
-  float m = -INFINITY;
-  each([&](int64_t, const Unit<T> &v) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, v.get(i));
-  });
+  Largest<T> largest;
+  each([&](int, const Unit<T> &v) { largest.take(v); });
+  float m = largest.value();
 #pragma unroll
   for (int w = 16; w; w /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
   const float base = m == -INFINITY ? 0.f : m;
+  // 2^((x - base) c) of a unit; the difference first, as x c may overflow
+  auto weigh = [&](const Unit<T> &v, float2 (&e)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 d = mul2(add2(v.pair(k), make_float2(-base, -base)), make_float2(c, c));
+      e[k] = make_float2(ex2(d.x), ex2(d.y));
+    }
+  };
   uint64_t second = 0;                         // the sum, or the first index of the maximum
   if (greedy) {
-    int64_t at = V;
-    each([&](int64_t u, const Unit<T> &v) {
+    int at = count;
+    each([&](int r, const Unit<T> &v) {
 #pragma unroll
-      for (int i = 7; i >= 0; --i)
-        if (v.get(i) == m && m != -INFINITY) at = min(at, u * 8 + i - lo);
+      for (int k = 3; k >= 0; --k) {
+        const float2 p = v.pair(k);
+        if (p.y == m && m != -INFINITY) at = min(at, r + 2 * k + 1);
+        if (p.x == m && m != -INFINITY) at = min(at, r + 2 * k);
+      }
     });
 #pragma unroll
-    for (int w = 16; w; w /= 2) at = min(at, int64_t(__shfl_xor_sync(~0u, at, w)));
+    for (int w = 16; w; w /= 2) at = min(at, __shfl_xor_sync(~0u, at, w));
     second = uint64_t(at);
   } else {
-    float sum = 0.f;
-    each([&](int64_t, const Unit<T> &v) {
-      float part[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) part[i] = ex2((v.get(i) - base) * c);
-      sum += ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+    float2 sums = make_float2(0.f, 0.f);
+    each([&](int, const Unit<T> &v) {
+      float2 e[4];
+      weigh(v, e);
+      sums = add2(sums, add2(add2(e[0], e[1]), add2(e[2], e[3])));
     });
+    float sum = sums.x + sums.y;
 #pragma unroll
     for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
     second = __float_as_uint(sum);
@@ -264,16 +329,17 @@ __global__ void __launch_bounds__(kProbThreads)
 #pragma unroll
   for (int w = 16; w; w /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
   if (greedy) {
-    int64_t at = V;
+    int at = count;
     for (int i = lane; i < entries; i += 32)
-      if (__uint_as_float(uint32_t(table[i].x)) == top) at = min(at, int64_t(table[i].y));
+      if (__uint_as_float(uint32_t(table[i].x)) == top) at = min(at, int(table[i].y));
 #pragma unroll
-    for (int w = 16; w; w /= 2) at = min(at, int64_t(__shfl_xor_sync(~0u, at, w)));
-    for (int64_t u = u0; u < end; u += stride) {
-      float y[8];
+    for (int w = 16; w; w /= 2) at = min(at, __shfl_xor_sync(~0u, at, w));
+    for (int r = first; r < count; r += step) {
+      float2 y[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = u * 8 + i - lo == at ? 1.f : 0.f;
-      store_unit(out, u, lo, hi, y);
+      for (int k = 0; k < 4; ++k)
+        y[k] = make_float2(r + 2 * k == at ? 1.f : 0.f, r + 2 * k + 1 == at ? 1.f : 0.f);
+      store_unit(out + lo, r, count, y);
     }
     return;
   }
@@ -287,34 +353,37 @@ __global__ void __launch_bounds__(kProbThreads)
 #pragma unroll
   for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
   const float scale = (sum == 0.f ? 0.f : 1.f / sum) * ex2(m == -INFINITY ? 0.f : (base - all) * c);
-  each([&](int64_t u, const Unit<T> &v) {
-    float y[8];
+  each([&](int r, const Unit<T> &v) {
+    float2 y[4];
+    weigh(v, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = ex2((v.get(i) - base) * c) * scale;
-    store_unit(out, u, lo, hi, y);
+    for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], make_float2(scale, scale));
+    store_unit(out + lo, r, count, y);
   });
 }
 
-// Blocks a row: as few as hold it, and up to 8 while the rows leave SMs idle.
+// Blocks a row: as few as hold it, up to 8 while the rows leave SMs idle, and
+// 16, more than a portable cluster, for a few rows (151936 BF16 logits: one row
+// 4.6 us against 5.9 with 8, eight rows 7.3 against 6.5).
 template <typename T>
 cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const float *temperature,
                                  float *out, int sms, cudaStream_t st) {
   const int64_t units = V / 8 + 2, size = 8 * sizeof(T);
   int c = 1;
-  while (c < kMaxCluster &&
+  while (c < 8 &&
          (units * size > int64_t(kProbShare) * c || (rows * c < 2 * sms && units > kProbThreads * c)))
     c *= 2;
+  if (c == 8 && units > 8 * kProbThreads && rows * 32 <= sms) c = kMaxCluster;
   const int64_t each = (units + int64_t(c) * kProbThreads - 1) / (int64_t(c) * kProbThreads);
   const int64_t share = each * kProbThreads * size;
   const unsigned grid = unsigned(rows) * unsigned(c);
-  if (share > kProbShareMax)
-    return launch_clusters(&probabilities_kernel<T, false>, grid, kProbThreads, c, 0, st, x, V,
-                           temperature, out);
-  // more than 48 KB, the kernel's own words included, have to be asked for
-  static std::atomic<uint64_t> allowed{0};
-  if (const cudaError_t e = allow_smem(&probabilities_kernel<T, true>, kProbShareMax, allowed)) return e;
-  return launch_clusters(&probabilities_kernel<T, true>, grid, kProbThreads, c, int(share), st, x, V,
-                         temperature, out);
+  // (more than 48 KB, the kernel's own words included, have to be asked for)
+  static std::atomic<uint64_t> allowed[2];
+  const bool held = share <= kProbShareMax;
+  void (*fn)(const T *, int64_t, const float *, float *) =
+      held ? &probabilities_kernel<T, true> : &probabilities_kernel<T, false>;
+  if (const cudaError_t e = allow(fn, held ? kProbShareMax : 0, allowed[held])) return e;
+  return launch_clusters(fn, grid, kProbThreads, c, held ? int(share) : 0, st, x, V, temperature, out);
 }
 
 // -------------------------------------------------------------- verification
@@ -654,19 +723,8 @@ extern "C" vg_status vg_verify_tree(const float *p, const float *q, const int32_
   c = std::max<int64_t>(1, std::min(c, vocab / (kVerWarps * 128)));
   const unsigned grid = unsigned(batch) * unsigned(c);
   void (*fn)(VerifyParams) = vocab % 4 ? &verify_kernel<false> : &verify_kernel<true>;
-  if (c > 8) {
-    // once for each device and kernel
-    static std::atomic<uint64_t> allowed[2];
-    int dev = 0;
-    VG_CUDA(cudaGetDevice(&dev));
-    const uint64_t bit = uint64_t(1) << (dev & 63);     // device_sms refuses higher numbers
-    std::atomic<uint64_t> &a = allowed[vocab % 4 ? 0 : 1];
-    if (!(a.load(std::memory_order_relaxed) & bit)) {
-      VG_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-      a.fetch_or(bit, std::memory_order_relaxed);
-    }
-  }
+  static std::atomic<uint64_t> allowed[2];
+  VG_CUDA(allow(fn, 0, allowed[vocab % 4 ? 0 : 1]));
   VG_CUDA(launch_clusters(fn, grid, kVerThreads, int(c), 0, as_cuda(stream), v));
   VG_LAUNCH_CHECK();
   return VG_OK;
