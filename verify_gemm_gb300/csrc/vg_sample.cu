@@ -101,8 +101,10 @@ cudaError_t allow(F *fn, int bytes, std::atomic<uint64_t> &allowed) {
 // 256 rows of 151936 BF16 logits (233 MB read and written): 52 us, 4.5 TB/s.
 // An exponential is taken twice an element, which costs less than 4 bytes more
 // of shared memory for each.  Shares of 80 KB, 512 threads a block and stores
-// that stay in L2 measured the same, shares of 20 KB 60 us.  One row: 4.6 us, of
-// which the launch and the exchange are most.
+// that stay in L2 measured the same, shares of 20 KB 60 us: all blocks of a wave
+// copy, compute and store together, and HBM waits while they compute.  Stores
+// of whole sectors, by way of shuffles, took 50 us, but one row 6.6.  One row:
+// 4.6 us, of which the launch and the exchange are most.
 //
 // Elements go by units of 8 on the grid of the whole array, so that loads
 // and stores are aligned whatever the row's length; the units at a row's two
