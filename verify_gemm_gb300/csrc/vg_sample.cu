@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
   const int runs = int(blocks) * kVerWarps, mine = int(rank) * kVerWarps + warp;
   const int64_t run = ((V + runs - 1) / runs + 127) / 128 * 128;
   const int64_t first = min(run * mine, V), last = min(first + run, V);
-  if (blocks > 1) cluster_wait();                // every block has begun
-  else __syncthreads();
+  if (blocks > 1) cluster_wait();                // every block has begun ...
+  __syncthreads();                               // ... and this one's nodes are there (written after its arrival)
   int i = 1, cur = 0, kept = 0;                  // thread 0's walk
   uint64_t a = 0, S = 1ull << 60, total = 0;
   bool summed = false;
