@@ -77,3 +77,79 @@ def check_long(vg, p, q, tokens, parents, u, again=1):
 def test_verify_a_batch_over_a_real_vocabulary(vg):
     """Twelve sequences, eight blocks each."""
     check_long(vg, *draw_long(5, 12, 8, 151936))
+
+
+def whole_verify(p, q, tokens, u, count):
+    """The rule in whole numbers for children of the root alone: (accepted node or None, the last
+    token).  p [nodes][V], q [V] and u [nodes] in units of 2^-24; the residual and its sum S in
+    units of 2^-(24 + s)."""
+    r, S, s, node = list(p[0]), 1 << 24, 0, None
+    for i in range(1, count):
+        if u[i] * q[tokens[i]] * S < r[tokens[i]] << 48:
+            r, node = p[i], i
+            break
+        r = [max((a << 24) - S * b, 0) for a, b in zip(r, q)]
+        S, s = sum(r), s + 24
+    if sum(r) == 0:
+        r = p[node or 0]
+    run, last = 0, -1
+    for k, x in enumerate(r):
+        run += x
+        if run << 24 > u[0] * sum(r):
+            last = k
+            break
+    return node, last
+
+
+def check_whole(vg, p, q, tokens, u, counts):
+    """p [B, n, V], q [B, V], u [B, n] int64 in units of 2^-24, tokens [B, n]: all of the root's."""
+    B, n, V = p.shape
+    parents = torch.zeros((B, n), dtype=torch.int32)
+    f = [(t.double() * 2.0 ** -24).float().to(DEV) for t in (p, q[:, None], u)]
+    assert all(torch.equal((x.double() * 2 ** 24).long().cpu().view(t.shape), t) for x, t in zip(f, (p, q, u)))
+    acc, path, out = vg.verify_tree(f[0], f[1], tokens.int().to(DEV), parents.to(DEV), f[2],
+                                    counts=torch.tensor(counts, dtype=torch.int32, device=DEV))
+    for b in range(B):
+        node, last = whole_verify(p[b].tolist(), q[b].tolist(), tokens[b].tolist(), u[b].tolist(), counts[b])
+        kept = [] if node is None else [node]
+        assert path[b].tolist() == kept + [-1] * (n - len(kept)), b
+        assert out[b].tolist() == [int(tokens[b, i]) for i in kept] + [last] + [-1] * (n - len(kept)), b
+        assert int(acc[b]) == len(kept)
+
+
+@pytest.mark.parametrize("V", [7, 8])
+def test_verify_of_a_thousand_refusals(vg, V):
+    """Nearly disjoint p and q: what q is weighed with passes 256 after some 350 refusals and
+    reaches 600, while entries with a small q keep a residual."""
+    g = torch.Generator().manual_seed(17)
+    B, n, one = 10, 1024, 1 << 24
+    p = torch.zeros((B, n, V), dtype=torch.long)
+    p[:] = torch.tensor([0.3, 0.25, 0.2, 0.15, 0.1] + [0.0] * (V - 5)).mul(one).long()
+    q = torch.zeros((B, V), dtype=torch.long)
+    q[:, :5] = (torch.rand((B, 5), generator=g) * 0.002 * one).long()
+    q[:, 0] = torch.linspace(0.0001, 0.0006, B).mul(one).long()
+    q[:, V - 1] = one - q.sum(1)
+    tokens = torch.full((B, n), V - 1)
+    u = torch.randint(0, one, (B, n), generator=g)
+    u[:, 0] = torch.linspace(0.01, 0.97, B).mul(one).long()
+    counts = [1024, 350, 360, 400, 513, 700, 900, 1023, 1000, 600]
+    for b in range(0, B, 2):
+        tokens[b, counts[b] - 1] = b // 2 % 4            # the last child may hold
+    check_whole(vg, p, q, tokens, u, counts)
+
+
+def test_verify_of_rows_that_sum_to_nearly_sixteen(vg):
+    g = torch.Generator().manual_seed(18)
+    B, n, V, one = 8, 1000, 36, 1 << 24
+    p = torch.zeros((B, n, V), dtype=torch.long)
+    p[:, :, :16] = (0.99 * one * (1 - 0.01 * torch.rand((B, 1, 16), generator=g))).long()
+    q = torch.zeros((B, V), dtype=torch.long)
+    q[:, 18:34] = int(0.99 * one)
+    q[:, :16] = (10.0 ** -torch.linspace(2, 4.5, 16) * one).long()
+    tokens = torch.randint(18, 34, (B, n), generator=g)
+    u = torch.randint(0, one, (B, n), generator=g)
+    u[:, 0] = torch.linspace(0.01, 0.97, B).mul(one).long()
+    counts = [5, 17, 18, 20, 40, 100, 500, 1000]
+    for b in range(1, B, 2):
+        tokens[b, counts[b] - 1] = 15
+    check_whole(vg, p, q, tokens, u, counts)

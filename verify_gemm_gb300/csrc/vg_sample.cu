@@ -396,7 +396,9 @@ cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const floa
 // one number, and the rows of accepted nodes are never read whole.
 //
 // Fixed point: p, q and the sums S in units of 2^-60 (a row sums to less
-// than 16), a in units of 2^-56 (at most 1 + the number of refusals).
+// than 16), a in units of 2^-56, which hold up to 256.  1023 refusals can bring
+// it to 1 + 16 * 1023, so it is counted beyond that, and from 256 on entries
+// are taken with a in units of 2^-48: a cut of 2^-56 of it at most, as below.
 //
 // A cluster of blocks a sequence.  Every warp of it owns one run of the row:
 // it adds up its run, and every block gets every warp's sum through
@@ -429,22 +431,42 @@ __device__ __forceinline__ uint64_t to_fixed(float x) {
 constexpr uint64_t kOne = 1ull << 56;            // a = 1
 
 // max(p - a q, 0) in units of 2^-60.  Modes: a = 0; a = 1; a < 8, where both
-// factors of (y a) >> 56 fit 64 bits with the shift made beforehand; any a.
+// factors of (y a) >> 56 fit 64 bits with the shift made beforehand; a < 256;
+// any a, in units of 2^-48.
 template <int kMode>
 __device__ __forceinline__ uint64_t residual(float p, float q, uint64_t a) {
   const uint64_t x = to_fixed(p);
   if (kMode == 0) return x;
   uint64_t y = to_fixed(q);
   if (kMode == 2) y = __umul64hi(y << 3, a << 5);
-  if (kMode == 3) {
+  if (kMode >= 3) {
+    constexpr int kShift = kMode == 3 ? 56 : 48;
     const uint64_t hi = __umul64hi(y, a), lo = y * a;
-    y = hi >> 56 ? ~0ull : (hi << 8) | (lo >> 56);
+    y = hi >> kShift ? ~0ull : (hi << (64 - kShift)) | (lo >> kShift);
   }
   return x > y ? x - y : 0;
 }
-// Calls f with the mode of `a` as a constant.
+// a while the tree is walked: whole 256s and the rest in units of 2^-56.
+struct Weight {
+  uint64_t rest = 0;
+  uint32_t whole = 0;
+  __device__ __forceinline__ bool zero() const { return rest == 0 && whole == 0; }
+  // one more refusal, after which the residual summed to S
+  __device__ __forceinline__ void refuse(uint64_t S) {
+    const uint64_t next = zero() ? kOne : rest + (S >> 4);
+    whole += next < rest;
+    rest = next;
+  }
+  // in the units that `residual` takes it in
+  __device__ __forceinline__ uint64_t units() const { return whole ? uint64_t(whole) << 56 | rest >> 8 : rest; }
+  __device__ __forceinline__ uint64_t left(float p, float q) const {
+    return whole ? residual<4>(p, q, units()) : residual<3>(p, q, rest);
+  }
+};
+// Calls f with the mode of `a` (in units of 2^-48: `coarse`) as a constant.
 template <typename F>
-__device__ __forceinline__ auto with_mode(uint64_t a, F &&f) {
+__device__ __forceinline__ auto with_mode(uint64_t a, bool coarse, F &&f) {
+  if (coarse) return f(std::integral_constant<int, 4>{});
   if (a == 0) return f(std::integral_constant<int, 0>{});
   if (a == kOne) return f(std::integral_constant<int, 1>{});
   if (a < 8 * kOne) return f(std::integral_constant<int, 2>{});
@@ -491,7 +513,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
   __shared__ int16_t par[kMaxNodes];             // -1: no node to try
   __shared__ __align__(16) ulonglong2 table[2][kVerCluster * kVerWarps];
   __shared__ uint64_t s_a;
-  __shared__ int s_cur, s_more, s_kept;
+  __shared__ int s_cur, s_more, s_kept, s_coarse;
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
   const int b = blockIdx.x / blocks, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t V = v.V;
@@ -521,7 +543,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
   if (blocks > 1) cluster_wait();                // every block has begun ...
   __syncthreads();                               // ... and this one's nodes are there (written after its arrival)
   int i = 1, cur = 0, kept = 0;                  // thread 0's walk
-  uint64_t a = 0, S = 1ull << 60, total = 0;
+  Weight a;
+  uint64_t S = 1ull << 60, total = 0;
   bool summed = false;
   uint32_t pass = 0;
   while (true) {
@@ -530,8 +553,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
       for (; i < n; ++i) {
         if (par[i] != cur) continue;
         const double left = double(su[i]) * double(qt[i]) * double(S);
-        const uint64_t r = a ? residual<3>(pt[i], qt[i], a) : 0;
-        const bool ok = a ? left < double(r) : left < double(pt[i]) * double(1ull << 60);
+        const bool ok = a.zero() ? left < double(pt[i]) * double(1ull << 60) : left < double(a.left(pt[i], qt[i]));
         if (ok) {
           if (rank == 0) {
             path[kept] = i;
@@ -539,33 +561,35 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
           }
           ++kept;
           cur = i;
-          a = 0;
+          a = Weight{};
           S = 1ull << 60;
           summed = false;
         } else {
-          a = a ? a + (S >> 4) : kOne;
+          a.refuse(S);
           s_more = 1;
           ++i;
           break;
         }
       }
       // the end: the sums of p itself, where none or empty ones are at hand
-      if (!s_more && (!summed || (total == 0 && a != 0))) {
-        a = 0;
+      if (!s_more && (!summed || (total == 0 && !a.zero()))) {
+        a = Weight{};
         s_more = 2;
       }
       s_cur = cur;
-      s_a = a;
+      s_a = a.units();
+      s_coarse = a.whole != 0;
       s_kept = kept;
     }
     __syncthreads();
     const int more = s_more, node = s_cur;
     const uint64_t aa = s_a;
+    const bool coarse = s_coarse;
     const float *pr = prow + node * V;
     const float *qr = qrow + (node < v.q_rows ? node : 0) * V;
     if (more) {
       ++pass;
-      uint64_t sum = with_mode(aa, [&](auto mode) {
+      uint64_t sum = with_mode(aa, coarse, [&](auto mode) {
         constexpr int kMode = decltype(mode)::value;
         uint64_t sum = 0;
         for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
@@ -614,7 +638,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
       if (tid == 0 && whole == 0) out[at] = -1;
     }
     if (whole != 0 && before <= mark && mark - before < table[pass & 1][mine].x) {
-      const int64_t found = with_mode(aa, [&](auto mode) -> int64_t {
+      const int64_t found = with_mode(aa, coarse, [&](auto mode) -> int64_t {
         constexpr int kMode = decltype(mode)::value;
         uint64_t c = before;
         for (int64_t e0 = first; e0 < last; e0 += 4 * 128) {
