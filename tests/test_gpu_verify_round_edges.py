@@ -153,3 +153,29 @@ def test_verify_of_rows_that_sum_to_nearly_sixteen(vg):
     for b in range(1, B, 2):
         tokens[b, counts[b] - 1] = 15
     check_whole(vg, p, q, tokens, u, counts)
+
+
+# -------------------------------------------------------------- probabilities
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [1, 8, 9, 1003, 4096, 20007, 151937])
+def test_probabilities_at_the_ends_of_the_temperatures(vg, dtype, vocab):
+    g = torch.Generator().manual_seed(vocab)
+    temps = [math.inf, 3e38, 1e30, 1e-30, 5e-39, 1e-40, 1e-45, math.inf, 1e-40, math.inf, 1e-45]
+    x = randn(g, len(temps), vocab, dtype=dtype, scale=2.5)
+    x[7:9, 1::3] = -math.inf                             # masked by -infinity ...
+    x[9:, 1::3] = torch.finfo(dtype).min                 # ... and by the lowest value
+    t = torch.tensor(temps, dtype=torch.float32, device=DEV)
+    xd = x.double()
+    z = (xd - xd.amax(-1, keepdim=True)) / t.double()[:, None]
+    z = torch.where(xd == -math.inf, -math.inf, z)       # (over an infinite T, too)
+    want = torch.softmax(z, -1)
+    tol = want * (z.abs().clamp(max=200) * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -17) + 1e-37
+    got = vg.probabilities(x, temperature=t).double()
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() - tol).amax(-1)
+
+
+def test_probabilities_of_a_temperature_that_is_no_number(vg):
+    x = randn(torch.Generator().manual_seed(2), 2, 1003)
+    y = vg.probabilities(x, temperature=torch.tensor([math.nan, 1.0], device=DEV))
+    assert torch.isnan(y[0]).all() and not torch.isnan(y[1]).any()

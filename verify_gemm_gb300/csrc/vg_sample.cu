@@ -263,7 +263,11 @@ __global__ void __launch_bounds__(kProbThreads)
   }
   const float t = temperature ? temperature[row] : 1.f;
   const bool greedy = t <= 0.f;
-  const float c = kLog2e / t;
+  // At the ends of T c is neither 0, which -infinity makes a NaN of, nor infinite,
+  // which the maximum's 0 does: with 2^-149 every finite logit weighs 1, with the
+  // largest number a logit 2^-121 below the maximum nothing.  A T of NaN stays one.
+  float c = kLog2e / t;
+  c = c == 0.f ? __uint_as_float(1) : c == INFINITY ? 0x1.fffffep127f : c;
   // units by the place of their first element in the row (-7 and up)
   const int first = int(u0 * 8 - lo), count = int(V), step = int(stride) * 8;
   auto each = [&](auto &&f) {
