@@ -587,7 +587,8 @@ vg_status vg_tree_attention(const vg_attention_desc *desc, const vg_kv_cache *ca
  * FP32, for contiguous rows of logits (BF16, FP16 or FP32).  temperature:
  * device FP32 [rows], or NULL for 1; a row with T <= 0 gives 1 at its first
  * largest logit and 0 elsewhere.  A logit of -infinity has probability 0; a
- * row of nothing else is all 0.  x and out 16-byte aligned. */
+ * row of nothing else is all 0.  A row with a NaN is all NaN, with T <= 0 all
+ * 0: no logit of it is the largest.  x and out 16-byte aligned. */
 vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
                            const float *temperature, float *out, vg_stream_t stream);
 

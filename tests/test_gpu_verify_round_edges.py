@@ -179,3 +179,23 @@ def test_probabilities_of_a_temperature_that_is_no_number(vg):
     x = randn(torch.Generator().manual_seed(2), 2, 1003)
     y = vg.probabilities(x, temperature=torch.tensor([math.nan, 1.0], device=DEV))
     assert torch.isnan(y[0]).all() and not torch.isnan(y[1]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,vocab", [(1, 5), (3, 1003), (40, 4099), (2, 151937), (4, 800011)])
+def test_probabilities_of_greedy_rows_with_nan(vg, dtype, rows, vocab):
+    """No logit is the largest beside a NaN: the row is 0, as a row without a logit is."""
+    g = torch.Generator().manual_seed(rows)
+    x = randn(g, rows, vocab, dtype=dtype)
+    clean = vg.probabilities(x, temperature=torch.zeros(rows, device=DEV))
+    assert (clean.sum(-1) == 1).all()
+    for at in sorted({0, 1 % vocab, vocab // 2, vocab - 2, vocab - 1}):
+        y = x.clone()
+        row = at % rows
+        y[row, at] = -math.nan if at % 2 else math.nan
+        got = vg.probabilities(y, temperature=torch.zeros(rows, device=DEV))
+        assert (got[row] == 0).all(), at
+        sampled = vg.probabilities(y)
+        assert torch.isnan(sampled[row]).all(), at
+        keep = torch.arange(rows, device=DEV) != row
+        assert torch.equal(got[keep], clean[keep]) and torch.isfinite(sampled[keep]).all()

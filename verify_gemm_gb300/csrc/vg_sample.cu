@@ -163,7 +163,14 @@ struct Unit {                      // 8 logits as they came
     }
   }
 };
-// The largest of units, 16-bit logits two at a time.  (A NaN counts for nothing.)
+// The largest of two, NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// The largest of units, 16-bit logits two at a time; NaN where one of them is, so
+// that the row is: no logit is the largest beside it.
 template <typename T>
 struct Largest {
   using Pair = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
@@ -180,12 +187,12 @@ struct Largest {
       Pair x;
       const uint32_t w = v.word(k);
       memcpy(&x, &w, 4);
-      top[k % 2] = __hmax2(top[k % 2], x);
+      top[k % 2] = __hmax2_nan(top[k % 2], x);
     }
   }
   __device__ __forceinline__ float value() const {
-    const Pair x = __hmax2(top[0], top[1]);
-    return fmaxf(to_f(x.x), to_f(x.y));
+    const Pair x = __hmax2_nan(top[0], top[1]);
+    return max_nan(to_f(x.x), to_f(x.y));
   }
 };
 template <>
@@ -193,7 +200,7 @@ struct Largest<float> {
   float top = -INFINITY;
   __device__ __forceinline__ void take(const Unit<float> &v) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(v.pair(k).x, v.pair(k).y));
+    for (int k = 0; k < 4; ++k) top = max_nan(top, max_nan(v.pair(k).x, v.pair(k).y));
   }
   __device__ __forceinline__ float value() const { return top; }
 };
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kProbThreads)
   each([&](int, const Unit<T> &v) { largest.take(v); });
   float m = largest.value();
 #pragma unroll
-  for (int w = 16; w; w /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+  for (int w = 16; w; w /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, w));
   const float base = m == -INFINITY ? 0.f : m;
   // 2^((x - base) c) of a unit; the difference first, as x c may overflow
   auto weigh = [&](const Unit<T> &v, float2 (&e)[4]) {
@@ -331,9 +338,9 @@ __global__ void __launch_bounds__(kProbThreads)
   else __syncthreads();
   const int entries = int(blocks) * kProbWarps;
   float top = -INFINITY;
-  for (int i = lane; i < entries; i += 32) top = fmaxf(top, __uint_as_float(uint32_t(table[i].x)));
+  for (int i = lane; i < entries; i += 32) top = max_nan(top, __uint_as_float(uint32_t(table[i].x)));
 #pragma unroll
-  for (int w = 16; w; w /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+  for (int w = 16; w; w /= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, w));
   if (greedy) {
     int at = count;
     for (int i = lane; i < entries; i += 32)
