@@ -566,7 +566,8 @@ vg_status vg_rope_append(const vg_rope_desc *desc, const vg_kv_cache *cache, vg_
  *   workspace: vg_tree_attention_workspace_size bytes, 16-byte aligned,
  *   zero-filled once; calls that share one must not overlap on the GPU.  Its
  *   error word (vg_gemv_workspace_check reads and clears it) is set by
- *   bounded waits that run out. */
+ *   bounded waits that run out.  What is then computed, and everything that
+ *   is computed while the word is set, is NaN. */
 typedef struct vg_attention_desc {
     const void *q;
     void *out;

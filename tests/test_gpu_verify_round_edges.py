@@ -199,3 +199,37 @@ def test_probabilities_of_greedy_rows_with_nan(vg, dtype, rows, vocab):
         assert torch.isnan(sampled[row]).all(), at
         keep = torch.arange(rows, device=DEV) != row
         assert torch.equal(got[keep], clean[keep]) and torch.isfinite(sampled[keep]).all()
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("n,hq,hkv,d,held", [
+    (1, 8, 2, 64, None), (3, 10, 2, 64, None), (8, 4, 2, 128, None), (6, 4, 1, 128, E4M3), (20, 1, 1, 256, None),
+    (20, 3, 1, 192, None), (64, 3, 1, 192, E4M3), (16, 8, 2, 128, None), (16, 8, 2, 64, E4M3),
+    (64, 16, 2, 128, None), (64, 16, 2, 128, E4M3)])
+def test_attention_of_a_workspace_whose_error_word_is_set(vg, n, hq, hkv, d, held):
+    """Nothing that a call computes passes for a result before the error has been read and cleared."""
+    g = torch.Generator().manual_seed(n)
+    lens = [9000, 0, 30, 400]
+    cache, *_ = build_cache(vg, g, 4, 9000 + n, hkv, d, 64, torch.bfloat16, held or torch.bfloat16,
+                            (0.03, 0.04) if held else (1.0, 1.0))
+    q = randn(g, 4, n, hq, d, dtype=torch.bfloat16)
+    tl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    counts = torch.tensor([n, n, max(1, n - 1), n], dtype=torch.int32, device=DEV)
+    ws = vg.tree_attention_workspace(q, cache)
+
+    def call():
+        lse = torch.zeros((4, n, hq), device=DEV)
+        return vg.tree_attention(q, cache, tl, counts=counts, lse=lse, workspace=ws), lse
+
+    want = call()
+    ws[:4].view(torch.int32).fill_(16)
+    used = (torch.arange(n, device=DEV)[None, :] < counts[:, None])
+    for _ in range(2):
+        out, lse = call()
+        assert torch.isnan(out[used]).all() and torch.isnan(lse[used]).all()
+        assert (out[~used] == 0).all() and (lse[~used] == -math.inf).all()
+    assert vg.workspace_error(ws) == 16
+    out, lse = call()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert vg.workspace_error(ws) == 0

@@ -292,8 +292,8 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   while (!mbar_try_wait(bar, parity)) {
     if (*failed) return false;
     if (globaltimer() > end) {
-      *failed = 1;
       atomicCAS(error, 0, kErrAttnWait);
+      *failed = 1;
       return false;
     }
   }
@@ -424,15 +424,17 @@ struct Line {
 
 // One warp copies the K (kv = 0) or V tiles of the block's run into the ring
 // of NS slots, K and V in turn, and leaves for each tile a bit for every 16
-// keys that there are in page_ok[tile of the run % 16].
+// keys that there are in page_ok[tile of the run % 16].  What the error word
+// says at the beginning goes to *stale before the first V tile can be seen.
 // The page numbers of 32 boxes are fetched at a time, one a lane, and the
 // next 32 while those are copied: a fetch for each tile cost 1200 clocks a
 // tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
 template <typename L, int NS>
 __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map, int kv,
                            uint32_t ring0, uint32_t full0, uint32_t empty0, uint32_t *page_ok,
-                           volatile int *failed) {
+                           volatile int *failed, volatile int *stale) {
   const int lane = threadIdx.x % 32;
+  const int before = kv == 1 && lane == 0 ? *static_cast<volatile int *>(p.error) : 0;
   const int boxes = L::kKeys / p.box, copies = boxes * L::kChunks;
   const int page_boxes = p.cache.page_size / p.box;
   int s = kv, n = 0;
@@ -471,6 +473,7 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
       const uint32_t bar = full0 + 8 * s;
       if (lane == 0) {
         if (kv == 0) page_ok[n % 16] = bits;
+        else if (n == 0) *stale = before;
         mbar_arrive_expect_tx(bar, L::kSlot);
       }
       __syncwarp();
@@ -540,6 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t *page_ok = reinterpret_cast<uint32_t *>(bars + 2 * L::kMaxSlots);   // [kMaxSlots]
   volatile int *failed = reinterpret_cast<volatile int *>(page_ok + L::kMaxSlots);
   int *last = const_cast<int *>(failed) + 1;
+  volatile int *stale = failed + 2;
   float2 *state = reinterpret_cast<float2 *>(smem + L::kSlots * L::kSlot + 1024);   // [warp][16]
   float *q_unit = reinterpret_cast<float *>(state) + L::kState / 4;                  // [kRows]
   uint8_t *q_smem = reinterpret_cast<uint8_t *>(q_unit + L::kRows);
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
-    *failed = 0;
+    *failed = *stale = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, L::KT * RW);
@@ -566,7 +570,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     const int kv = warp - kConsumers;                    // one warp copies K, one V
     if (kv > 1) return;
-    copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
+    copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed,
+                      stale);
     return;
   }
 
@@ -956,6 +961,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * sv);
     }
+
+    // After a wait that ran out, in this call or in one before whose error nobody
+    // has read, the sums are NaN, and with them what is made of them: the block
+    // that joins other blocks' results, too, must not give out numbers.
+    if (*failed | *stale) l[0] = l[1] = __int_as_float(0x7FFFFFFF);
 
     // What a row's result is, from `res` (tile_of(i): which tile of its columns
     // res[i] is) with maximum mm and sum ll.

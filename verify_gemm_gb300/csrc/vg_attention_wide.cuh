@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
   int *last = reinterpret_cast<int *>(fixed + 580);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(fixed + 584);
   volatile int *keep_o = reinterpret_cast<volatile int *>(fixed + 588); // [stream]
+  volatile int *stale = reinterpret_cast<volatile int *>(fixed + 596);
   uint32_t *odd_at = reinterpret_cast<uint32_t *>(fixed + 608);         // [2][4]: bits of keys
   int8_t *q_exp = reinterpret_cast<int8_t *>(fixed + 640);              // E4M3: [unit % 2][row]
   float2 *state = reinterpret_cast<float2 *>(fixed + 1024);             // keys split: [stream][row]: (m, l)
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
-    *failed = 0;
+    *failed = *stale = 0;
     for (int i = 0; i < 8; ++i) odd_at[i] = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, L::kF8 ? 128 : 1);
@@ -295,9 +296,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
     const int kv = warp == 10;
     if constexpr (L::kF8)
       copy_tiles<typename L::Stage, L::kStages>(p, at, kv ? &vmap : &kmap, kv, smem_addr(stage), stage_full,
-                                                stage_empty, page_ok, failed);
+                                                stage_empty, page_ok, failed, stale);
     else
-      copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed);
+      copy_tiles<L, NS>(p, at, kv ? &vmap : &kmap, kv, smem_addr(ring), full0, empty0, page_ok, failed, stale);
     } else if (warp == 9) {
     // ----------------------------------------------------------- products
     // Step w of a unit is stream w % 2's: tile w / 2 or, with the keys split, w.
@@ -636,6 +637,8 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         ++units;
         tc_after();
       }
+      // after a wait that ran out nothing passes for a number, as in the other kernel
+      if (*failed | *stale) l = __int_as_float(0x7FFFFFFF);
       float w0 = 1.f, w1 = 0.f;                          // weights of the streams' outputs
       if constexpr (NQ == 1) {
         state[tid] = make_float2(m, l);

@@ -155,7 +155,10 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     give 0.  scale: 1 / sqrt(head_dim) by default.  lse: float32 [batch, n,
     q_heads], written if given.  workspace: from tree_attention_workspace,
     made anew by each call that is given none; calls that share one must not
-    overlap."""
+    overlap.  A wait on the GPU that runs out, which should not happen, gives
+    NaN and sets the workspace's error word: while workspace_error has not read
+    and cleared it, calls on that workspace give NaN.  (The word of a workspace
+    that a call made for itself cannot be read.)"""
     if stream is not None:
         with torch.cuda.stream(stream):      # out and a new workspace, too, are made there
             return tree_attention(q, cache, lens, tree, counts, scale, out, lse, workspace)
