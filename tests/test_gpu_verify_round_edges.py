@@ -233,3 +233,27 @@ def test_attention_of_a_workspace_whose_error_word_is_set(vg, n, hq, hkv, d, hel
     out, lse = call()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert vg.workspace_error(ws) == 0
+
+
+def test_dimensions_of_one_may_have_any_stride(vg):
+    """A single sequence, node or head, and a table of one column."""
+    g = torch.Generator().manual_seed(4)
+    d = 64
+    for B, n, h in ((1, 3, 2), (2, 1, 2), (2, 3, 1), (1, 1, 1)):
+        cache, *_ = build_cache(vg, g, B, 60, 1, d, 16, torch.bfloat16, torch.bfloat16)
+        lens = torch.full((B,), 40, dtype=torch.int32, device=DEV)
+        flat = randn(g, B * n * h * d, dtype=torch.bfloat16)
+        q = flat.view(B, n, h, d)
+        odd = torch.as_strided(flat, (B, n, h, d), [s if size > 1 else 7 for s, size in zip(q.stride(), q.shape)])
+        assert torch.equal(odd, q)
+        assert torch.equal(vg.tree_attention(odd, cache, lens), vg.tree_attention(q, cache, lens))
+        kv = randn(g, B, n, 1, d, dtype=torch.bfloat16)
+        inv, _ = vg.rope_frequencies(d, device=DEV)
+        assert torch.equal(vg.rope_append(odd, kv, kv, inv, cache, lens), vg.rope_append(q, kv, kv, inv, cache, lens))
+    k = randn(g, 4, 64, 1, d, dtype=torch.bfloat16)
+    column = torch.as_strided(torch.tensor([2, 0], dtype=torch.int32, device=DEV), (2, 1), (1, 5))
+    plain = column.contiguous().view(2, 1)
+    q = randn(g, 2, 3, 1, d, dtype=torch.bfloat16)
+    lens = torch.tensor([30, 11], dtype=torch.int32, device=DEV)
+    assert torch.equal(vg.tree_attention(q, vg.KVCache(k, k, column), lens),
+                       vg.tree_attention(q, vg.KVCache(k, k, plain), lens))

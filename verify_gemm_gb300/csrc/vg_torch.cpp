@@ -49,13 +49,14 @@ const T *at_of(PyObject *o, at::ScalarType type, at::IntArrayRef shape, const ch
   return given(o) ? static_cast<const T *>(exact(o, type, shape, name).const_data_ptr()) : nullptr;
 }
 
-// [batch, n, heads, head_dim] whose last dimension is contiguous.
+// [batch, n, heads, head_dim] whose last dimension is contiguous.  The stride of a
+// dimension of one is arbitrary: 0 is aligned to everything.
 const Tensor &heads(PyObject *o, const char *name, int64_t (&stride)[3]) {
   const Tensor &t = tensor(o, name);
   if (t.dim() != 4 || t.stride(3) != 1)
     throw Bad{std::string(name) + ": expected a CUDA tensor [batch, n, heads, head_dim] whose last "
                                   "dimension is contiguous"};
-  for (int i = 0; i < 3; ++i) stride[i] = t.stride(i);
+  for (int i = 0; i < 3; ++i) stride[i] = t.size(i) > 1 ? t.stride(i) : 0;
   return t;
 }
 

@@ -56,7 +56,7 @@ class KVCache:
         if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must have the same shape, type and device")
         if not (page_table.device == k.device and page_table.dtype == torch.int32
-                and page_table.dim() == 2 and page_table.stride(1) == 1):
+                and page_table.dim() == 2 and (page_table.stride(1) == 1 or page_table.shape[1] == 1)):
             raise ValueError("page_table: expected a CUDA int32 tensor [batch, max_pages]")
         self.k, self.v, self.page_table = k, v, page_table
         self.batch, self.heads, self.head_dim, self.dtype = (page_table.shape[0], k.shape[2],
