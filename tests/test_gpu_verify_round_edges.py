@@ -257,3 +257,38 @@ def test_dimensions_of_one_may_have_any_stride(vg):
     lens = torch.tensor([30, 11], dtype=torch.int32, device=DEV)
     assert torch.equal(vg.tree_attention(q, vg.KVCache(k, k, column), lens),
                        vg.tree_attention(q, vg.KVCache(k, k, plain), lens))
+
+
+# ------------------------------------------------------- the cache's descriptor
+
+def fake_cache(L, **kw):
+    """A descriptor over addresses that nothing reads: it is only checked."""
+    c = L.vg_kv_cache()
+    c.k, c.v, c.page_table = 0x10000, 0x10000, 0x10000
+    c.type, c.heads, c.head_dim, c.page_size, c.pages = L.VG_TYPE_E4M3, 2, 64, 16, 8
+    for s in (c.k_stride, c.v_stride):
+        s[0], s[1], s[2] = 16 * 128, 128, 64
+    c.table_stride, c.batch, c.max_pages, c.k_scale, c.v_scale = 4, 3, 4, 0.5, 0.5
+    for name, value in kw.items():
+        setattr(c, name, value)
+    return c
+
+
+def test_a_cache_that_has_changed_is_refused(vg):
+    from verify_gemm_gb300 import _lib as L
+
+    n = ctypes.c_size_t()
+    ask = lambda c: L.vg_tree_attention_workspace_size(4, 2, ctypes.byref(c), ctypes.byref(n))  # noqa: E731
+    changes = dict(k=0x20000, v=0x20000, page_table=0x20000, type=L.VG_TYPE_BF16, heads=1, head_dim=32, page_size=32,
+                   pages=9, table_stride=5, batch=2, max_pages=3, k_scale=0.25, v_scale=0.0)
+    for name, value in changes.items():
+        c = fake_cache(L)
+        assert L.vg_kv_cache_init(ctypes.byref(c)) == 0 and ask(c) == 0
+        setattr(c, name, value)
+        assert ask(c) == 1, name
+    for at in range(3):
+        for name in ("k_stride", "v_stride"):
+            c = fake_cache(L)
+            assert L.vg_kv_cache_init(ctypes.byref(c)) == 0
+            getattr(c, name)[at] += 64
+            assert ask(c) == 1, (name, at)

@@ -39,6 +39,10 @@ inline uint64_t cache_mark(const vg_kv_cache &c) {
   }
   add(uint64_t(c.table_stride));
   add(uint64_t(uint32_t(c.batch)) | uint64_t(uint32_t(c.max_pages)) << 32);
+  uint32_t scales[2];
+  std::memcpy(&scales[0], &c.k_scale, 4);
+  std::memcpy(&scales[1], &c.v_scale, 4);
+  add(uint64_t(scales[0]) | uint64_t(scales[1]) << 32);
   return h | 1;
 }
 
