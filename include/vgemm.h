@@ -503,7 +503,8 @@ enum { VG_ROPE_HALF = 0, VG_ROPE_INTERLEAVED = 1 };
  * them and prepares the copies' descriptors; the struct is host memory, is
  * only read by later calls and holds no resource.
  * Limits: head_dim a multiple of 16, at most 256; page_size a multiple of
- * 16; k, v 16-byte aligned, strides multiples of 16 bytes.
+ * 16; max_pages * page_size at most 2^31 - 8192; k, v 16-byte aligned,
+ * strides multiples of 16 bytes.
  * type: VG_TYPE_BF16, VG_TYPE_FP16 (that of q) or VG_TYPE_E4M3, whose codes
  * are worth k_scale (v_scale) times their value; the scales are 1 otherwise.
  * An entry of the table outside 0..pages-1 is no page, and neither is a slot

@@ -292,3 +292,12 @@ def test_a_cache_that_has_changed_is_refused(vg):
             assert L.vg_kv_cache_init(ctypes.byref(c)) == 0
             getattr(c, name)[at] += 64
             assert ask(c) == 1, (name, at)
+
+
+def test_a_table_of_nearly_all_32_bit_slots_is_refused(vg):
+    """A length and its tree's nodes have to fit 32 bits."""
+    from verify_gemm_gb300 import _lib as L
+
+    for slots, status in ((2 ** 31 - 16, 3), (2 ** 31 - 8192 + 16, 3), (2 ** 31 - 8192, 0)):
+        c = fake_cache(L, max_pages=slots // 16, table_stride=slots // 16)
+        assert L.vg_kv_cache_init(ctypes.byref(c)) == status, slots

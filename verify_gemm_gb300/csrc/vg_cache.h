@@ -10,6 +10,9 @@ namespace vg {
 // then a mark over the fields that were checked.
 constexpr int kCacheMapWords = 16;            // 128 bytes each
 constexpr int kCacheMark = 32;                // opaque[32]
+// Slots of a sequence: a length, its tree's nodes and the pages that are fetched
+// ahead of them are counted in 32 bits.
+constexpr int64_t kCacheMaxSlots = (int64_t(1) << 31) - 8192;
 // Boxes of the maps: 128 bytes of a head (64 bytes of E4M3 heads up to 64
 // elements) of the largest power of two of tokens, at most 64, that divides
 // the page.

@@ -326,7 +326,7 @@ extern "C" vg_status vg_kv_cache_init(vg_kv_cache *c) {
   if (c->type != VG_TYPE_BF16 && c->type != VG_TYPE_FP16 && c->type != VG_TYPE_E4M3)
     return VG_ERR_INVALID_ARG;
   if (c->head_dim > 256 || c->pages >= (int64_t(1) << 31) || c->heads > 65535 ||
-      c->batch > 65535 || int64_t(c->max_pages) * c->page_size >= (int64_t(1) << 31))
+      c->batch > 65535 || int64_t(c->max_pages) * c->page_size > kCacheMaxSlots)
     return VG_ERR_UNSUPPORTED;
   const int64_t size = c->type == VG_TYPE_E4M3 ? 1 : 2;
   if (c->type == VG_TYPE_E4M3) {
