@@ -490,7 +490,8 @@ vg_status vg_verify_plan_destroy(vg_verify_plan *plan);
  * kernels, so one captured graph serves every length.
  *
  * Device pointers of this section need the alignment of their type unless
- * a function says otherwise. */
+ * a function says otherwise.  They and the stream belong to the device that
+ * is current in the calling thread. */
 
 enum { VG_TYPE_BF16 = 0, VG_TYPE_FP16 = 1, VG_TYPE_FP32 = 2, VG_TYPE_E4M3 = 3 };
 enum { VG_ROPE_HALF = 0, VG_ROPE_INTERLEAVED = 1 };

@@ -7,9 +7,12 @@
 // Python took 6 to 10 us a call beside the launch, here it takes about 1.
 //
 // A function returns its output, or the vg_status of a call that was refused;
-// a tensor of the wrong kind raises ValueError.
+// a tensor of the wrong kind raises ValueError, and so do tensors of several
+// devices.  libvgemm launches on the current device: a call makes its tensors'
+// device current.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -80,6 +83,25 @@ float number(PyObject *o) {
   return float(v);
 }
 
+// The device of a call's tensors, which must be one; those not given are passed
+// over, but for the first.
+struct Argument {
+  PyObject *o;
+  const char *name;
+};
+c10::DeviceIndex one_device(std::initializer_list<Argument> all, PyObject *cache_device = nullptr) {
+  int64_t device = cache_device ? integer(cache_device) : -1;
+  for (const Argument &x : all) {
+    if (!given(x.o) && &x != all.begin()) continue;
+    const int64_t its = tensor(x.o, x.name).get_device();
+    if (device < 0) device = its;
+    if (its != device)
+      throw Bad{std::string(x.name) + ": on device " + std::to_string(its) + ", and others of the call on device " +
+                std::to_string(device)};
+  }
+  return c10::DeviceIndex(device);
+}
+
 const vg_kv_cache *cache_of(PyObject *o) { return reinterpret_cast<const vg_kv_cache *>(integer(o)); }
 
 // Work and the tensors made for it go to the current stream.
@@ -112,9 +134,11 @@ PyObject *result(vg_status s, const Tensor &t) {
   }                                                                                   \
   END_HANDLE_TH_ERRORS
 
-// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out
+// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out, the cache's device
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(11)
+  VG_BEGIN(12)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[1], "k"}, {a[2], "v"}, {a[3], "inv_freq"}, {a[5], "lens"},
+                                               {a[6], "depth"}, {a[7], "counts"}, {a[10], "q_out"}}, a[11]));
   vg_rope_desc d;
   const Tensor &q = heads(a[0], "q", d.q_stride), &k = heads(a[1], "k", d.k_stride),
                &v = heads(a[2], "v", d.v_stride), &f = tensor(a[3], "inv_freq");
@@ -148,9 +172,11 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   VG_END
 }
 
-// q, cache, lens, tree, counts, scale, out, lse, workspace
+// q, cache, lens, tree, counts, scale, out, lse, workspace, the cache's device
 PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(9)
+  VG_BEGIN(10)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[2], "lens"}, {a[3], "tree"}, {a[4], "counts"},
+                                               {a[6], "out"}, {a[7], "lse"}, {a[8], "workspace"}}, a[9]));
   vg_attention_desc d;
   const Tensor &q = heads(a[0], "q", d.q_stride);
   const vg_kv_cache *cache = cache_of(a[1]);
@@ -178,6 +204,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 // logits, temperature, out
 PyObject *probabilities(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   VG_BEGIN(3)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "logits"}, {a[1], "temperature"}, {a[2], "out"}}));
   const Tensor &x = tensor(a[0], "logits");
   if (x.dim() < 1 || !x.numel() || !x.is_contiguous())
     throw Bad{"logits: expected a contiguous CUDA tensor that is not empty"};
@@ -199,6 +226,8 @@ PyObject *probabilities(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 // p, q, tokens, parents, u, counts -> (accepted, path, out)
 PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   VG_BEGIN(6)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "p"}, {a[1], "q"}, {a[2], "tokens"}, {a[3], "parents"}, {a[4], "u"},
+                                               {a[5], "counts"}}));
   const Tensor &p = tensor(a[0], "p");
   if (p.scalar_type() != at::kFloat || p.dim() != 3 || !p.is_contiguous())
     throw Bad{"p: expected a contiguous CUDA float32 tensor [batch, n, vocab]"};

@@ -32,6 +32,13 @@ def _calls():
     return _native
 
 
+def _on(stream, tensor):
+    """Makes the stream current; it has to be of the tensors' device."""
+    if stream.device != getattr(tensor, "device", None):
+        raise ValueError("the stream and the tensors are on different devices")
+    return torch.cuda.stream(stream)
+
+
 def _checked(result, where):
     if type(result) is int:          # a vg_status
         _lib.check(result, where)
@@ -75,6 +82,7 @@ class KVCache:
         _lib.check(_lib.vg_kv_cache_init(ctypes.byref(c)), "vg_kv_cache_init")
         self._c = c
         self._at = ctypes.addressof(c)
+        self._device = k.device.index
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
@@ -124,17 +132,23 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
     head turn: pairs (j, j + rot/2) for layout "half", (2j, 2j + 1) for
     "interleaved".  Nodes past counts[b] append nothing and give 0."""
     if stream is not None:
-        with torch.cuda.stream(stream):      # q_out, too, is made there
+        with _on(stream, q):                 # q_out, too, is made there
             return rope_append(q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out)
     if layout not in _LAYOUTS:
         raise ValueError("layout: 'half' or 'interleaved'")
     return _checked((_native or _calls()).rope_append(
-        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out),
+        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out,
+        cache._device),
         "vg_rope_append")
 
 
 def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
     """A zero-filled workspace for tree_attention with q of this shape."""
+    if q.device != cache.k.device:
+        raise ValueError("q and the cache are on different devices")
+    if cache._device != torch.cuda.current_device():
+        with torch.cuda.device(cache._device):
+            return tree_attention_workspace(q, cache)
     n = ctypes.c_size_t()
     _lib.check(_lib.vg_tree_attention_workspace_size(q.shape[1], q.shape[2], cache._at,
                                                      ctypes.byref(n)),
@@ -160,13 +174,13 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
     and cleared it, calls on that workspace give NaN.  (The word of a workspace
     that a call made for itself cannot be read.)"""
     if stream is not None:
-        with torch.cuda.stream(stream):      # out and a new workspace, too, are made there
+        with _on(stream, q):                 # out and a new workspace, too, are made there
             return tree_attention(q, cache, lens, tree, counts, scale, out, lse, workspace)
     if workspace is None:
         workspace = tree_attention_workspace(q, cache)
     return _checked((_native or _calls()).tree_attention(
         q, cache._at, lens, tree, counts, cache.head_dim ** -0.5 if scale is None else scale, out, lse,
-        workspace), "vg_tree_attention")
+        workspace, cache._device), "vg_tree_attention")
 
 
 def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -176,7 +190,7 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
     every row; None: 1).  A temperature <= 0 gives 1 at the row's first
     largest logit."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, logits):
             return probabilities(logits, temperature, out)
     return _checked((_native or _calls()).probabilities(logits, temperature, out), "vg_probabilities")
 
@@ -193,6 +207,6 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
     many drafts hold, their nodes, and their tokens with the one drawn after
     them; -1 behind.  include/vgemm.h (vg_verify_tree) has the rule."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, p):
             return verify_tree(p, q, tokens, parents, u, counts)
     return _checked((_native or _calls()).verify_tree(p, q, tokens, parents, u, counts), "vg_verify_tree")
