@@ -3,7 +3,9 @@
 Translation units are compiled in parallel, then linked into
 ``verify_gemm_gb300/_build/libvgemm.so``.  ``_vgtorch.so`` beside it, the calls
 of the verify round from torch tensors, is compiled against the installed
-torch by the host compiler and linked to it.  Run ``python -m
+torch by the host compiler and linked to it.  Where that cannot be done (no
+headers of torch's or Python's) the library is there all the same, with a
+warning, and only the calls that need the binding raise.  Run ``python -m
 verify_gemm_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -14,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -38,13 +41,19 @@ def nvcc() -> str:
     return exe
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
+def _older(target, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [TORCH_SOURCE]]
-    deps.append(os.path.join(ROOT, "include", "vgemm.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in deps + [os.path.join(ROOT, "include", "vgemm.h")])
+
+
+def _stale() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
+
+
+def _binding_stale() -> bool:
+    return _older(TORCH_LIB, [os.path.join(CSRC, TORCH_SOURCE)])
 
 
 def _run(cmd, what):
@@ -87,12 +96,8 @@ def _link_binding(obj):
     os.replace(tmp, TORCH_LIB)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
+def _build_library(verbose):
     exe = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
@@ -106,17 +111,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([exe, *ARCH, "-shared", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+
+
+# Why the binding could not be made: tried once a process.
+_binding_failed = None
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    global _binding_failed
+    library = force or _stale()
+    binding = _binding_failed is None and (force or _binding_stale())
+    if not (library or binding):
+        return LIB
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        obj = ex.submit(_compile_binding) if binding else None
+        if library:
+            _build_library(verbose)
+        if binding:
+            try:
+                _link_binding(obj.result())
+            except Exception as e:
+                _binding_failed = str(e)
+                if os.path.exists(TORCH_LIB):             # one of other headers
+                    os.remove(TORCH_LIB)
+                warnings.warn("the calls of the verify round from torch tensors are not available: "
+                              + _binding_failed, RuntimeWarning, stacklevel=2)
     return LIB
 
 
