@@ -84,3 +84,19 @@ def test_a_finished_build_is_left_alone(box):
     box.again()
     box.module.build()
     assert not box.calls("nvcc") and not box.calls("g++")
+
+
+def test_another_torch_makes_the_binding_anew(box):
+    """The binding is compiled against one torch's headers; the library is not."""
+    box.module.build()
+    box.calls("nvcc"), box.calls("g++")
+    version = os.path.join(box.module._torch_dir(), "version.py")
+    with open(version, "w") as f:
+        f.write("__version__ = '2.11.0'\n")
+    os.utime(version, (1, 1))                             # (an older file than the build, as wheels hold)
+    box.again()
+    box.module.build()
+    assert len(box.calls("g++")) == 2 and not box.calls("nvcc")
+    box.again()
+    box.module.build()
+    assert not box.calls("g++")

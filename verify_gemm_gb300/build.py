@@ -52,7 +52,20 @@ def _stale() -> bool:
     return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
 
 
+def _made_for() -> str:
+    """The torch and the Python whose headers the binding is compiled with."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{_torch_dir()}\n{f.read()}\n{sysconfig.get_config_var('SOABI')}\n"
+
+
 def _binding_stale() -> bool:
+    # (kept beside the binding: an installed torch's files are older than it)
+    try:
+        with open(TORCH_LIB + ".for") as f:
+            if f.read() != _made_for():
+                return True
+    except OSError:
+        return True
     return _older(TORCH_LIB, [os.path.join(CSRC, TORCH_SOURCE)])
 
 
@@ -94,6 +107,8 @@ def _link_binding(obj):
           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{lib}"], "linking the torch binding")
     os.replace(tmp, TORCH_LIB)
+    with open(TORCH_LIB + ".for", "w") as f:
+        f.write(_made_for())
 
 
 def _build_library(verbose):
