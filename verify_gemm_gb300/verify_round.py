@@ -95,7 +95,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     it; "yarn" leaves the pairs that turn more than beta_fast times in the
     original `context`, divides those that turn less than beta_slow times, and
     goes over evenly in the logarithm of the turns between the two, with the
-    attention factor 0.1 ln(factor) + 1."""
+    attention factor 0.1 ln(factor) + 1.  The ramp's ends are taken as they come
+    out; a model trained with a table whose ramp begins and ends at whole pairs
+    (some percent apart within the ramp) needs that table as inv_freq."""
     if rot < 2 or rot % 2 or base <= 1 or factor < 1:
         raise ValueError("rot must be even and positive, base > 1 and factor >= 1")
     j = torch.arange(rot // 2, dtype=torch.float64)
@@ -200,7 +202,9 @@ def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
                 stream=None):
     """Verifies each sequence's drafted tokens: p float32 [batch, n, vocab],
     the target's distribution after each node; q float32 [batch, rows, vocab],
-    the distribution each node's children were drafted from; tokens and
+    the distribution each node's children were drafted from, independently of
+    one another (with children made distinct, by top-k or by draws without
+    replacement, what comes out is not distributed as p); tokens and
     parents int32 [batch, n]; u float32 [batch, n], random numbers in [0, 1).
 
     Returns int32 (accepted [batch], path [batch, n], out [batch, n + 1]): how
