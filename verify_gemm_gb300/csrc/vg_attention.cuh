@@ -441,7 +441,8 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
   int s = kv, n = 0;
   uint32_t par = 1;                                      // slots start empty
   int pages = -1, ahead = -1, seq = -1, window = -1;     // the numbers held, of which sequence and window
-  for (; at.valid(); at.next(p)) {
+  bool going = true;
+  for (; going && at.valid(); at.next(p)) {
     const int head = head_of(p, at.u);
     const int total = at.len + at.count;
     const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
@@ -470,7 +471,9 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
       const int token = ok ? number % page_boxes * p.box : 0;
       uint32_t bits = ok ? ((1u << (p.box / 16)) - 1) << (box * (p.box / 16)) : 0;
       bits = __reduce_or_sync(~0u, bits);
-      wait_phase(empty0 + 8 * s, par, failed, p.error);
+      // a slot that did not become free may still be filled or read: nothing more is copied
+      going = __all_sync(~0u, wait_phase(empty0 + 8 * s, par, failed, p.error));
+      if (!going) break;
       const uint32_t bar = full0 + 8 * s;
       if (lane == 0) {
         if (kv == 0) page_ok[n % 16] = bits;
