@@ -100,3 +100,19 @@ def test_another_torch_makes_the_binding_anew(box):
     box.again()
     box.module.build()
     assert not box.calls("g++")
+
+
+def test_builds_at_the_same_time_make_everything_once(box, tmp_path, monkeypatch):
+    """Processes that build at once (parallel tests, several ranks) do not write one another's objects."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    slow = SCRIPT.replace("while [", "sleep 0.3\nwhile [")
+    for name in ("nvcc", "g++"):
+        path = tmp_path / name
+        path.write_text(slow.format(log=tmp_path / (name + ".log"), fail=""))
+        path.chmod(0o755)
+    monkeypatch.setattr(box.module, "nvcc", lambda: str(tmp_path / "nvcc"))
+    monkeypatch.setattr(box.module, "_cxx", lambda: str(tmp_path / "g++"))
+    with ThreadPoolExecutor(3) as ex:                     # (the lock is a file's: threads and processes wait alike)
+        assert [f.result() for f in [ex.submit(box.module.build) for _ in range(3)]] == [box.module.LIB] * 3
+    assert len(box.calls("nvcc")) == len(box.module.SOURCES) + 1 and len(box.calls("g++")) == 2

@@ -11,6 +11,8 @@ verify_gemm_gb300.build`` or call :func:`build`.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import os
 import shutil
 import subprocess
@@ -133,17 +135,32 @@ def _build_library(verbose):
     os.replace(tmp, LIB)
 
 
+@contextlib.contextmanager
+def _alone():
+    """One build at a time in the folder: a process that waited finds the work done."""
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with open(os.path.join(OUT_DIR, ".lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
+
+
 # Why the binding could not be made: tried once a process.
 _binding_failed = None
 
 
+def _needed(force):
+    return force or _stale(), _binding_failed is None and (force or _binding_stale())
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    if any(_needed(force)):
+        with _alone():
+            _build(*_needed(force), verbose)
+    return LIB
+
+
+def _build(library, binding, verbose):
     global _binding_failed
-    library = force or _stale()
-    binding = _binding_failed is None and (force or _binding_stale())
-    if not (library or binding):
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(1) as ex:
         obj = ex.submit(_compile_binding) if binding else None
         if library:
@@ -156,8 +173,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 if os.path.exists(TORCH_LIB):             # one of other headers
                     os.remove(TORCH_LIB)
                 warnings.warn("the calls of the verify round from torch tensors are not available: "
-                              + _binding_failed, RuntimeWarning, stacklevel=2)
-    return LIB
+                              + _binding_failed, RuntimeWarning, stacklevel=3)
 
 
 if __name__ == "__main__":
