@@ -589,6 +589,48 @@ vg_status vg_tree_attention_workspace_size(int n, int q_heads, const vg_kv_cache
 vg_status vg_tree_attention(const vg_attention_desc *desc, const vg_kv_cache *cache,
                             void *workspace, size_t workspace_bytes, vg_stream_t stream);
 
+/* vg_rope_append with RMS norms of the heads of q and k before they turn, in the
+ * same launch: each head x of q (of k) is replaced by
+ *     x[i] * weight[i] / sqrt(sum_j x[j]^2 / head_dim + eps),
+ * in FP32 up to the rounding of what is stored.  The norm takes the whole head,
+ * what of it does not turn included; v is as in vg_rope_append, and so is
+ * everything else.
+ *   q_weight, k_weight  [head_dim] in weight_type (VG_TYPE_FP32 or that of q), NULL: ones.
+ *   eps  at least 2^-126, finite. */
+typedef struct vg_qk_norm_rope_desc {
+    vg_rope_desc rope;
+    const void *q_weight, *k_weight;
+    int32_t weight_type;
+    float eps;
+} vg_qk_norm_rope_desc;
+
+vg_status vg_qk_norm_rope_append(const vg_qk_norm_rope_desc *desc, const vg_kv_cache *cache,
+                                 vg_stream_t stream);
+
+/* vg_tree_attention of a batch whose sequences begin with the same tokens (a
+ * system prompt, a document): the pages that the prefix fills are read once for
+ * the rows of all sequences, what each has behind them by its own rows, and the two
+ * are joined.  The result is that of vg_tree_attention over page tables that
+ * name the prefix's pages first, but for the order of its sums.
+ *   prefix  device int32: the prefix's tokens P.  Its whole pages, F = P /
+ *     page_size of them, max_prefix_pages at most, are shared; tokens behind
+ *     them lie in pages of each sequence's own.
+ *   prefix_pages  device int32 [max_prefix_pages]: the shared pages.
+ *     Entries outside 0..pages-1 are no pages, as in the table.
+ * A sequence with lens[b] < F * page_size has no part in the prefix: all its slots are
+ * taken from its own row of the table.  Of the others' rows the first F entries
+ * are not read.  Both are read by the kernels, so one captured graph serves every
+ * prefix up to max_prefix_pages.
+ * desc and limits as in vg_tree_attention; batch * n * (q_heads / heads)^2 and
+ * batch * n^2 below 2^32.  workspace: vg_prefix_attention_workspace_size
+ * bytes, under the same rules. */
+vg_status vg_prefix_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
+                                             size_t *bytes);
+vg_status vg_prefix_attention(const vg_attention_desc *desc, const vg_kv_cache *cache,
+                              const int32_t *prefix, const int32_t *prefix_pages,
+                              int max_prefix_pages, void *workspace, size_t workspace_bytes,
+                              vg_stream_t stream);
+
 /* out[r][i] = exp((x[r][i] - max) / T[r]) / sum of the same over the row,
  * FP32, for contiguous rows of logits (BF16, FP16 or FP32).  temperature:
  * device FP32 [rows], or NULL for 1; a row with T <= 0 gives 1 at its first
@@ -597,6 +639,41 @@ vg_status vg_tree_attention(const vg_attention_desc *desc, const vg_kv_cache *ca
  * 0: no logit of it is the largest.  x and out 16-byte aligned. */
 vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
                            const float *temperature, float *out, vg_stream_t stream);
+
+/* Draws from the softmax of logits with a temperature, truncated by top-k, top-p
+ * and min-p, from given random numbers.  A row's tokens are ordered by logit,
+ * the largest first and equal ones by index; kept are
+ *     the first top_k of them (<= 0 or >= vocab: all),
+ *     of these the fewest first ones whose probabilities sum to top_p of theirs
+ *       and more (>= 1 or NaN: all; at least one),
+ *     of these the ones at least min_p times as probable as the first (<= 0 or
+ *       NaN: all; at least one).
+ * A token is the first index whose running sum of probabilities over what is
+ * kept, in the order of the indices, exceeds u times their sum.  Weights are good
+ * to some 2^-29 of themselves and sums are exact in integers, so the same call
+ * gives the same tokens.
+ * With T <= 0 the first largest logit alone is kept.  A logit of -infinity is never
+ * kept.  A row with a NaN, with a T of NaN, or with +infinity and T > 0, and a row of
+ * nothing but -infinity have the token -1.
+ *   x      rows of logits (BF16, FP16 or FP32), row_stride elements apart.
+ *   u      FP32 [rows][draws] in [0, 1) (below: 0, above: the last token).
+ *   temperature, top_p, min_p  FP32 [rows], top_k int32 [rows], or NULL: 1, and none.
+ *   tokens int32 [rows][draws]: independent draws from one distribution.
+ *   out    FP32 [rows][vocab] or NULL: that distribution, 0 for what is not kept: the p
+ *     and the q of vg_verify_tree.  (Rows without a token: NaN, or 0 for one of
+ *     nothing but -infinity and for one with T <= 0.)
+ * x and out 16-byte aligned; vocab < 2^28, rows < 2^26, draws <= 65536. */
+typedef struct vg_sample_desc {
+    const void *x;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *out;
+    int64_t rows, vocab, row_stride;
+    int32_t type, draws;
+} vg_sample_desc;
+
+vg_status vg_sample(const vg_sample_desc *desc, vg_stream_t stream);
 
 /* Verification of a tree of drafted tokens against the target's
  * probabilities, from given random numbers.

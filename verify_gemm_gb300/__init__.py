@@ -25,8 +25,9 @@ import torch
 from . import _lib
 from ._lib import (VG_FMT_FP8_ROWSCALE, VG_FMT_INT4G, VG_FMT_MXFP8, VG_FMT_NVFP4,  # noqa: F401
                    VG_OP_GEMV, VG_OP_RMSNORM, VG_OP_SWIGLU, VGError)
-from .verify_round import (KVCache, probabilities, rope_append, rope_frequencies,  # noqa: F401
-                           tree_attention, tree_attention_workspace, verify_tree)
+from .verify_round import (KVCache, prefix_attention, prefix_attention_workspace,  # noqa: F401
+                           probabilities, qk_norm_rope_append, rope_append, rope_frequencies,
+                           sample, tree_attention, tree_attention_workspace, verify_tree)
 
 __all__ = [
     "NVFP4Weight", "FP8Weight", "nvfp4_pack", "fp8_pack", "nvfp4_unpack", "fp8_unpack",
@@ -36,7 +37,8 @@ __all__ = [
     "int4g_pack", "mxfp8_unpack", "int4g_unpack", "mxfp8_from_canonical",
     "int4g_from_canonical", "VG_FMT_MXFP8", "VG_FMT_INT4G",
     "KVCache", "rope_frequencies", "rope_append", "tree_attention_workspace", "tree_attention",
-    "probabilities", "verify_tree", "workspace_error",
+    "probabilities", "verify_tree", "workspace_error", "qk_norm_rope_append",
+    "prefix_attention_workspace", "prefix_attention", "sample",
 ]
 
 

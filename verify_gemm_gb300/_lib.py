@@ -82,6 +82,17 @@ class vg_attention_desc(ctypes.Structure):
                 ("q_heads", ctypes.c_int32), ("scale", f32)]
 
 
+class vg_qk_norm_rope_desc(ctypes.Structure):
+    _fields_ = [("rope", vg_rope_desc), ("q_weight", P), ("k_weight", P),
+                ("weight_type", ctypes.c_int32), ("eps", f32)]
+
+
+class vg_sample_desc(ctypes.Structure):
+    _fields_ = [("x", P), ("u", P), ("temperature", P), ("top_p", P), ("min_p", P), ("top_k", P),
+                ("tokens", P), ("out", P), ("rows", i64), ("vocab", i64), ("row_stride", i64),
+                ("type", ctypes.c_int32), ("draws", ctypes.c_int32)]
+
+
 SIGNATURES = {
     "vg_status_string": (ctypes.c_char_p, [st]),
     "vg_version": (i32, []),
@@ -127,6 +138,10 @@ SIGNATURES = {
     "vg_verify_plan_destroy": (st, [P]),
     "vg_kv_cache_init": (st, [ctypes.POINTER(vg_kv_cache)]),
     "vg_rope_append": (st, [P, P, P]),
+    "vg_qk_norm_rope_append": (st, [P, P, P]),
+    "vg_prefix_attention_workspace_size": (st, [i32, i32, P, ctypes.POINTER(sz)]),
+    "vg_prefix_attention": (st, [P, P, P, P, i32, P, sz, P]),
+    "vg_sample": (st, [P, P]),
     "vg_tree_attention_workspace_size": (st, [i32, i32, P, ctypes.POINTER(sz)]),
     "vg_tree_attention": (st, [P, P, P, sz, P]),
     "vg_probabilities": (st, [P, i32, i64, i64, P, P, P]),

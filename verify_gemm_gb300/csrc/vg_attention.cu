@@ -40,49 +40,31 @@ vg_status allow_smem(const Variant &v) {
   return VG_OK;
 }
 
-size_t workspace_bytes_of(const Variant &v, int sms) {
-  return kHeader + 3 * kMaxGrid * sizeof(uint32_t) + size_t(sms) * 2 * size_t(v.partial) * sizeof(float);
+size_t workspace_bytes_of(int partial, int sms) {
+  return kHeader + 3 * kMaxGrid * sizeof(uint32_t) + size_t(sms) * 2 * size_t(partial) * sizeof(float);
 }
 
-}  // namespace
-}  // namespace vg
-
-using namespace vg;
-
-extern "C" vg_status vg_tree_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
-                                                      size_t *bytes) {
-  if (!bytes || n < 1 || n > 64 || q_heads < 1) return VG_ERR_INVALID_ARG;
+vg_status check_heads(int n, int q_heads, const vg_kv_cache *cache) {
+  if (n < 1 || n > 64 || q_heads < 1) return VG_ERR_INVALID_ARG;
   if (vg_status s = cache_ready(cache)) return s;
   if (q_heads % cache->heads) return VG_ERR_INVALID_ARG;
-  if (q_heads / cache->heads > 4096) return VG_ERR_UNSUPPORTED;
-  int sms = 0;
-  if (vg_status s = device_sms(&sms)) return s;
-  *bytes = workspace_bytes_of(pick(cache_type(*cache), cache->head_dim, n * (q_heads / cache->heads)), sms);
-  return VG_OK;
+  return q_heads / cache->heads > 4096 ? VG_ERR_UNSUPPORTED : VG_OK;
 }
 
-extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_cache *cache,
-                                       void *workspace, size_t workspace_bytes,
-                                       vg_stream_t stream) {
-  if (!d || d->n < 1 || d->n > 64 || d->q_heads < 1) return VG_ERR_INVALID_ARG;
-  if (vg_status s = cache_ready(cache)) return s;
-  if (d->q_heads % cache->heads) return VG_ERR_INVALID_ARG;
+vg_status check_call(const vg_attention_desc *d, const vg_kv_cache *cache) {
+  if (!d) return VG_ERR_INVALID_ARG;
+  if (vg_status s = check_heads(d->n, d->q_heads, cache)) return s;
   if (!d->q || !d->out || !d->lens || !std::isfinite(d->scale)) return VG_ERR_INVALID_ARG;
   if (d->type != VG_TYPE_BF16 && d->type != VG_TYPE_FP16) return VG_ERR_INVALID_ARG;
   if (cache->type != VG_TYPE_E4M3 && cache->type != d->type) return VG_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
     if (d->q_stride[i] % 8) return VG_ERR_ALIGNMENT;
   if (!aligned16(d->q) || !aligned16(d->out)) return VG_ERR_ALIGNMENT;
-  if (d->q_heads / cache->heads > 4096) return VG_ERR_UNSUPPORTED;
-  int sms = 0;
-  if (vg_status s = device_sms(&sms)) return s;
-  if (sms > kMaxGrid) return VG_ERR_UNSUPPORTED;
-  const int rows = d->n * (d->q_heads / cache->heads);
-  const int type = cache_type(*cache);
-  const Variant &v = pick(type, cache->head_dim, rows);
-  if (!workspace || workspace_bytes < workspace_bytes_of(v, sms)) return VG_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return VG_ERR_ALIGNMENT;
-  AttnParams p;
+  return VG_OK;
+}
+
+AttnParams params_of(const vg_attention_desc *d, const vg_kv_cache *cache, void *workspace) {
+  AttnParams p{};
   p.q = d->q;
   p.out = d->out;
   p.lse = d->lse;
@@ -101,11 +83,18 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   p.hkv = cache->heads;
   p.d = cache->head_dim;
   p.q_f16 = d->type == VG_TYPE_FP16;
-  p.rows = rows;
   p.group = d->q_heads / cache->heads;
   p.group_magic = p.group == 1 ? 0 : uint32_t((uint64_t(1) << 32) / uint64_t(p.group)) + 1;
-  p.blocks = (rows + v.rows - 1) / v.rows;
   p.box = cache_box_tokens(cache->page_size);
+  p.c = d->scale * cache->k_scale * kLog2e;
+  p.v_scale = cache->v_scale;
+  return p;
+}
+
+// One launch over p.batch sequences of p.n nodes.
+vg_status launch(AttnParams p, const Variant &v, int type, const vg_kv_cache *cache, int sms, vg_stream_t stream) {
+  p.rows = p.n * p.group;
+  p.blocks = (p.rows + v.rows - 1) / v.rows;
   // What a unit costs beside its tiles, in tiles, and half of it as the cut that
   // moves: less saves more than it unbalances.  Beginning and joining a unit
   // takes some 4 us.  The tcgen05 kernel's tiles take what a stream's chain of
@@ -114,17 +103,15 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   // 16 tiles of ragged batches: 18 sequences of 304 rows of 128, 6 tiles 100 us,
   // 8 106, 16 114; 30 units of 55 rows of 64 in E4M3, 26 us, 27, 32 and 40 with
   // 32; 50 units of 128 rows of 256, 2 tiles 36 us, 4 41.
-  const bool wide = is_wide(p.d, rows);
+  const bool wide = is_wide(p.d, p.rows);
   p.tile_log2 = wide ? 7 : 6;
   const int tile_bytes = (2 * p.d * (type == kE4M3 ? 1 : 2)) << p.tile_log2;
   p.least = std::max(1, 131072 / tile_bytes);
   p.extra = wide ? 6 : std::max(1, std::min({8, 16 * 16 / v.rows, 262144 / tile_bytes}));
   p.snap = p.extra / 2;
-  p.c = d->scale * cache->k_scale * kLog2e;
-  p.v_scale = cache->v_scale;
   // no more blocks than there can be tiles
-  const int64_t most = int64_t(cache->batch) * cache->heads * p.blocks *
-                       ((int64_t(cache->max_pages) * cache->page_size + d->n + kTile - 1) / kTile);
+  const int64_t most = int64_t(p.batch) * p.hkv * p.blocks *
+                       ((int64_t(p.cache.max_pages) * p.cache.page_size + p.n + kTile - 1) / kTile);
   const unsigned grid = unsigned(std::min<int64_t>(sms, most));
   alignas(64) CUtensorMap kmap, vmap;
   std::memcpy(&kmap, cache->opaque, sizeof kmap);
@@ -133,4 +120,100 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   v.fn<<<grid, v.threads, size_t(v.smem), as_cuda(stream)>>>(p, kmap, vmap);
   VG_LAUNCH_CHECK();
   return VG_OK;
+}
+
+// What prefix attention adds: the kernels of its two launches and their workspace.
+struct Behind {
+  const Variant *prefix, *own;
+  size_t seed_at, bytes;             // the prefix's outputs in the workspace, and its whole
+};
+vg_status behind_prefix(int n, int q_heads, const vg_kv_cache *cache, int sms, Behind &b) {
+  const int group = q_heads / cache->heads, type = cache_type(*cache);
+  const int64_t nodes = int64_t(cache->batch) * n, rows = nodes * group;
+  // (node_of and q_of divide by multiplying)
+  if (rows * group >= int64_t(1) << 32 || nodes * n >= int64_t(1) << 32 || rows >= int64_t(1) << 31)
+    return VG_ERR_UNSUPPORTED;
+  b.prefix = &pick(type, cache->head_dim, int(rows));
+  b.own = &pick(type, cache->head_dim, n * group);
+  const size_t fixed = workspace_bytes_of(std::max(b.prefix->partial, b.own->partial), sms);
+  const size_t lse = (size_t(nodes) * size_t(q_heads) * sizeof(float) + 15) / 16 * 16;
+  b.seed_at = (fixed + 15) / 16 * 16;
+  b.bytes = b.seed_at + lse + size_t(nodes) * size_t(q_heads) * size_t(cache->head_dim) * sizeof(float);
+  return VG_OK;
+}
+
+}  // namespace
+}  // namespace vg
+
+using namespace vg;
+
+extern "C" vg_status vg_tree_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
+                                                      size_t *bytes) {
+  if (!bytes) return VG_ERR_INVALID_ARG;
+  if (vg_status s = check_heads(n, q_heads, cache)) return s;
+  int sms = 0;
+  if (vg_status s = device_sms(&sms)) return s;
+  *bytes = workspace_bytes_of(pick(cache_type(*cache), cache->head_dim, n * (q_heads / cache->heads)).partial, sms);
+  return VG_OK;
+}
+
+extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_cache *cache,
+                                       void *workspace, size_t workspace_bytes,
+                                       vg_stream_t stream) {
+  if (vg_status s = check_call(d, cache)) return s;
+  int sms = 0;
+  if (vg_status s = device_sms(&sms)) return s;
+  if (sms > kMaxGrid) return VG_ERR_UNSUPPORTED;
+  const int type = cache_type(*cache);
+  const Variant &v = pick(type, cache->head_dim, d->n * (d->q_heads / cache->heads));
+  if (!workspace || workspace_bytes < workspace_bytes_of(v.partial, sms)) return VG_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return VG_ERR_ALIGNMENT;
+  return launch(params_of(d, cache, workspace), v, type, cache, sms, stream);
+}
+
+extern "C" vg_status vg_prefix_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
+                                                        size_t *bytes) {
+  if (!bytes) return VG_ERR_INVALID_ARG;
+  if (vg_status s = check_heads(n, q_heads, cache)) return s;
+  int sms = 0;
+  if (vg_status s = device_sms(&sms)) return s;
+  Behind b;
+  if (vg_status s = behind_prefix(n, q_heads, cache, sms, b)) return s;
+  *bytes = b.bytes;
+  return VG_OK;
+}
+
+extern "C" vg_status vg_prefix_attention(const vg_attention_desc *d, const vg_kv_cache *cache,
+                                         const int32_t *prefix, const int32_t *prefix_pages,
+                                         int max_prefix_pages, void *workspace,
+                                         size_t workspace_bytes, vg_stream_t stream) {
+  if (vg_status s = check_call(d, cache)) return s;
+  if (max_prefix_pages < 0 || !prefix || (max_prefix_pages && !prefix_pages)) return VG_ERR_INVALID_ARG;
+  if (int64_t(max_prefix_pages) * cache->page_size > kCacheMaxSlots) return VG_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(prefix) | reinterpret_cast<uintptr_t>(prefix_pages)) & 3) return VG_ERR_ALIGNMENT;
+  int sms = 0;
+  if (vg_status s = device_sms(&sms)) return s;
+  if (sms > kMaxGrid) return VG_ERR_UNSUPPORTED;
+  Behind b;
+  if (vg_status s = behind_prefix(d->n, d->q_heads, cache, sms, b)) return s;
+  if (!workspace || workspace_bytes < b.bytes) return VG_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return VG_ERR_ALIGNMENT;
+  const int type = cache_type(*cache);
+  AttnParams own = params_of(d, cache, workspace);
+  if (max_prefix_pages == 0) return launch(own, *b.own, type, cache, sms, stream);
+  own.pass = kOwn;
+  own.prefix = prefix;
+  own.prefix_pages = max_prefix_pages;
+  own.seed_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.seed_at);
+  own.seed = own.seed_lse + (int64_t(own.batch) * own.n * own.hq + 3) / 4 * 4;
+  AttnParams first = own;
+  first.pass = kPrefix;
+  first.inner = own.n;
+  first.inner_magic = own.n == 1 ? 0 : uint32_t((uint64_t(1) << 32) / uint64_t(own.n)) + 1;
+  first.batch = 1;
+  first.n = own.batch * own.n;
+  first.cache.table = prefix_pages;
+  first.cache.table_stride = first.cache.max_pages = max_prefix_pages;
+  if (vg_status s = launch(first, *b.prefix, type, cache, sms, stream)) return s;
+  return launch(own, *b.own, type, cache, sms, stream);
 }

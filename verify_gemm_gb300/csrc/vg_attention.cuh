@@ -92,14 +92,61 @@ struct AttnParams {
   int tile_log2;                    // keys of a tile
   int box, least, extra, snap;      // tokens of a TMA box; tiles: of a run at least, a unit costs, a cut moves
   float c, v_scale;                 // scale * k_scale * log2 e
+  // Attention behind a shared prefix (vg_prefix_attention) is two launches.  The
+  // first takes the prefix's whole pages as a sequence by themselves, whose nodes
+  // are those of the whole batch, and leaves each row's output and the log2 of
+  // its sum of exponentials in `seed`.  The second takes what each sequence has behind
+  // them and joins the two.  Without a prefix `pass` is kAlone.
+  int pass, inner;                  // kPrefix: nodes of a sequence of the batch
+  uint32_t inner_magic;             // 2^32 / inner + 1
+  const int32_t *prefix;            // tokens of the prefix
+  int prefix_pages;                 // pages there are of it at most
+  float *seed, *seed_lse;           // [batch][n][hq][d], [batch][n][hq]
 };
+enum { kAlone = 0, kPrefix = 1, kOwn = 2 };
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Divisions by numbers that only the launch knows take some 150 clocks, and a
 // unit's beginning and end are a chain of them.
 // row / group, exact for row < 2^32 / group (rows are below 2^20 / 4).
 __device__ __forceinline__ int node_of(const AttnParams &p, int row) {
   return p.group == 1 ? row : int(__umulhi(uint32_t(row), p.group_magic));
 }
+// Where q of node `node` of sequence b begins; the prefix's nodes are those of all sequences.
+__device__ __forceinline__ int64_t q_of(const AttnParams &p, int b, int node) {
+  if (p.pass != kPrefix) return b * p.qs[0] + node * p.qs[1];
+  const int seq = p.inner == 1 ? node : int(__umulhi(uint32_t(node), p.inner_magic));
+  return seq * p.qs[0] + (node - seq * p.inner) * p.qs[1];
+}
+// The drafted nodes that a node attends to, of `count` there are.
+__device__ __forceinline__ uint64_t nodes_seen(const AttnParams &p, int b, int node, int count) {
+  if (p.pass == kPrefix) return 0;
+  return (count >= 64 ? ~0ull : (1ull << count) - 1) &
+         (p.tree ? p.tree[int64_t(b) * p.n + node] : ~0ull >> (63 - node));
+}
+// A row's result without the prefix, o / l = `scale` o, and log2 l as `lse`, joined to
+// the prefix's: out = w_seed seed + w_own scale o.
+struct Seed {
+  const float *at;                  // NULL: nothing to join
+  float w_seed, w_own;
+  __device__ __forceinline__ Seed(const AttnParams &p, int64_t row, bool shares, bool unused, float &lse)
+      : at(nullptr), w_seed(0.f), w_own(1.f) {
+    if (p.pass != kOwn || !shares || unused) return;
+    const float theirs = __ldg(p.seed_lse + row);
+    if (theirs == -INFINITY) return;
+    const float top = fmaxf(theirs, lse);
+    float a = ex2(theirs - top), b = lse == -INFINITY ? 0.f : ex2(lse - top);
+    const float sum = a + b;
+    lse = top + log2f(sum);
+    at = p.seed + row * p.d;
+    w_seed = a / sum;
+    w_own = b / sum;
+  }
+};
 // Cache head and row block of unit u of a sequence.
 __device__ __forceinline__ int head_of(const AttnParams &p, int u) { return p.blocks == 1 ? u : u / p.blocks; }
 __device__ __forceinline__ int block_of_rows(const AttnParams &p, int u) { return p.blocks == 1 ? 0 : u % p.blocks; }
@@ -211,11 +258,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Four E4M3 codes as FP16 pairs, exact.
 __device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
   asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2;\n"
@@ -313,19 +355,32 @@ struct Line {
   int64_t runs;                     // blocks that have a run
   int b, u, units, extra, snap, tiles, t0, t1;
   int len, count;
+  int shared, skip;                 // slots in the prefix's whole pages; of them, those the sequence leaves out
 
-  __device__ __forceinline__ static int used(const AttnParams &p, int b, int &len) {
+  // Committed slots of sequence b that are taken here and, returned, its drafted
+  // nodes.  Slots are counted from `skip` on: a sequence that has the whole of the
+  // prefix begins behind it.
+  __device__ __forceinline__ int used(const AttnParams &p, int b, int &len, int &skip) const {
+    skip = 0;
+    if (p.pass == kPrefix) {
+      len = shared;
+      return 0;
+    }
     // no slot past the table exists: such lengths end with it
     const int64_t room = int64_t(p.cache.max_pages) * p.cache.page_size;
     len = int(min(int64_t(max(p.lens[b], 0)), room));
+    if (p.pass == kOwn && len >= shared) {
+      skip = shared;
+      len -= shared;
+    }
     return p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   }
   __device__ __forceinline__ static int tiles_for(const AttnParams &p, int tokens) {
     return max(1, (tokens + (1 << p.tile_log2) - 1) >> p.tile_log2);
   }
-  __device__ __forceinline__ static int tiles_of(const AttnParams &p, int b) {
-    int len;
-    const int count = used(p, b, len);
+  __device__ __forceinline__ int tiles_of(const AttnParams &p, int b) const {
+    int len, skip;
+    const int count = used(p, b, len, skip);
     return tiles_for(p, len + count);
   }
   // The whole warp computes it.
@@ -334,6 +389,7 @@ struct Line {
     units = units_;
     extra = p.extra;
     snap = p.snap;
+    shared = p.pass == kAlone ? 0 : min(max(*p.prefix, 0) / p.cache.page_size, p.prefix_pages) * p.cache.page_size;
     auto long_of = [&](int i) { return i < p.batch ? tiles_of(p, i) + extra : 0; };
     const int own = long_of(lane);              // of the first 32 sequences
     int64_t sum = own;
@@ -379,7 +435,7 @@ struct Line {
     const int64_t in = at - before * units;
     u = in < int64_t(1) << 32 ? int(uint32_t(in) / uint32_t(length)) : int(in / length);
     tiles = length - extra;
-    count = b < p.batch ? used(p, b, len) : 0;
+    count = b < p.batch ? used(p, b, len, skip) : 0;
     const int off = int(in - int64_t(u) * length);
     unit0 = at - off;
     t0 = off <= snap ? 0 : max(0, off - extra);
@@ -403,7 +459,7 @@ struct Line {
     if (++u == units) {
       u = 0;
       ++b;
-      count = used(p, b, len);
+      count = used(p, b, len, skip);
       tiles = tiles_for(p, len + count);
     }
     fill(p);
@@ -445,10 +501,11 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
   for (; going && at.valid(); at.next(p)) {
     const int head = head_of(p, at.u);
     const int total = at.len + at.count;
-    const int32_t *table = p.cache.table + at.b * p.cache.table_stride;
+    const int skipped = at.skip / p.cache.page_size;
+    const int32_t *table = p.cache.table + at.b * p.cache.table_stride + skipped;
     auto fetch = [&](int window) {
       const int box = window * 32 + lane, i = box / page_boxes;
-      return box * p.box < total && i < p.cache.max_pages ? table[i] : -1;
+      return box * p.box < total && i < p.cache.max_pages - skipped ? table[i] : -1;
     };
     if (at.b != seq || at.t0 * boxes / 32 != window) {   // (a sequence's heads have the same pages)
       seq = at.b;
@@ -608,7 +665,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   auto q_row = [&](const Line &u, int r) {
     const int row = block_of_rows(p, u.u) * L::kRows + r, node = node_of(p, row);
     if (row >= p.rows || lane * 8 >= p.d) return make_uint4(0, 0, 0, 0);
-    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] + node * p.qs[1] +
+    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of(p, u.b, node) +
                                             (head_of(p, u.u) * p.group + row - node * p.group) * p.qs[2] + lane * 8);
   };
   auto fetch_q = [&](const Line &u) {
@@ -701,13 +758,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     // the drafted nodes that this thread's two rows attend to
     uint64_t word[2];
-    const uint64_t used = at.count >= 64 ? ~0ull : (1ull << at.count) - 1;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int node = node_of(p, row0 + rw * 16 + g + 8 * r);
-      word[r] = 0;
-      if (node < p.n)
-        word[r] = used & (p.tree ? p.tree[int64_t(at.b) * p.n + node] : ~0ull >> (63 - node));
+      word[r] = node < p.n ? nodes_seen(p, at.b, node, at.count) : 0;
     }
     float o[L::NT][4];
 #pragma unroll
@@ -984,36 +1038,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (row >= p.rows) continue;
         const int h = head * p.group + row - node * p.group;
         // NaN is not nothing
-        const bool empty = node >= at.count || (mm[r] == -INFINITY && ll[r] == 0.f);
-        const float inv = empty ? 0.f : p.v_scale / ll[r];
+        const bool unused = p.pass != kPrefix && node >= at.count;
+        const bool empty = unused || (mm[r] == -INFINITY && ll[r] == 0.f);
+        float inv = empty ? 0.f : p.v_scale / ll[r];
+        float lse = empty ? -INFINITY : mm[r] - kLift<kType> + log2f(ll[r]);
         const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
+        const Seed seed(p, at_row, at.skip > 0, unused, lse);
+        if (seed.at) inv *= seed.w_own;
+        float *sums = p.pass == kPrefix ? p.seed + at_row * p.d : nullptr;
         uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
         const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
+        // element e of tile i, and what the prefix gives to it
+        auto value = [&](int i, int e, int col) {
+          const float v = empty ? 0.f : res[i][2 * r + e] * inv;
+          return seed.at ? fmaf(seed.at[col], seed.w_seed, v) : v;
+        };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int nt = tile_of(i);
-          const float v0 = empty ? 0.f : res[i][2 * r] * inv, v1 = empty ? 0.f : res[i][2 * r + 1] * inv;
           if constexpr (kType == kE4M3) {
             // columns 4t + 2e of even tiles, 4t + 2e + 1 of odd ones: an even
             // tile's lane stores for both where it has both
             if constexpr (N >= 2) {
               if (i % 2 == 0 && 8 * nt < p.d) {
-                const float u0 = empty ? 0.f : res[i + 1][2 * r] * inv;
-                const float u1 = empty ? 0.f : res[i + 1][2 * r + 1] * inv;
-                *reinterpret_cast<uint2 *>(out + 8 * nt + 4 * t) =
-                    make_uint2(pack_out(v0, u0, f16), pack_out(v1, u1, f16));
+                const int col = 8 * nt + 4 * t;
+                const float v0 = value(i, 0, col), u0 = value(i + 1, 0, col + 1);
+                const float v1 = value(i, 1, col + 2), u1 = value(i + 1, 1, col + 3);
+                if (sums)
+                  *reinterpret_cast<float4 *>(sums + col) = make_float4(v0, u0, v1, u1);
+                else
+                  *reinterpret_cast<uint2 *>(out + col) = make_uint2(pack_out(v0, u0, f16), pack_out(v1, u1, f16));
               }
             } else if (8 * (nt & ~1) < p.d) {
-              const uint32_t both = pack_out(v0, v1, f16);
-              out[out_col<kType>(nt, t, 0)] = uint16_t(both);
-              out[out_col<kType>(nt, t, 1)] = uint16_t(both >> 16);
+              const int col0 = out_col<kType>(nt, t, 0), col1 = out_col<kType>(nt, t, 1);
+              const float v0 = value(i, 0, col0), v1 = value(i, 1, col1);
+              if (sums) {
+                sums[col0] = v0;
+                sums[col1] = v1;
+              } else {
+                const uint32_t both = pack_out(v0, v1, f16);
+                out[col0] = uint16_t(both);
+                out[col1] = uint16_t(both >> 16);
+              }
             }
           } else if (8 * nt < p.d) {
-            *reinterpret_cast<uint32_t *>(out + 8 * nt + 2 * t) = pack_out(v0, v1, f16);
+            const int col = 8 * nt + 2 * t;
+            const float v0 = value(i, 0, col), v1 = value(i, 1, col + 1);
+            if (sums)
+              *reinterpret_cast<float2 *>(sums + col) = make_float2(v0, v1);
+            else
+              *reinterpret_cast<uint32_t *>(out + col) = pack_out(v0, v1, f16);
           }
         }
-        if (p.lse && t == 0 && first_warp)
-          p.lse[at_row] = empty ? -INFINITY : (mm[r] - kLift<kType> + log2f(ll[r])) * kLn2;
+        if (t == 0 && first_warp) {
+          if (sums)
+            p.seed_lse[at_row] = lse;
+          else if (p.lse)
+            p.lse[at_row] = lse * kLn2;
+        }
       }
     };
     if constexpr (kSolo) {

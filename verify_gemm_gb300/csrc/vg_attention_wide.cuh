@@ -404,8 +404,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         const int rw = row0 + row_of(k), node = node_of(p, rw);
         qv[k] = make_uint4(0, 0, 0, 0);
         if (rw < p.rows && piece * 8 < p.d)
-          qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + u.b * p.qs[0] +
-                                                   node * p.qs[1] +
+          qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of(p, u.b, node) +
                                                    (head * p.group + rw - node * p.group) * p.qs[2] + piece * 8);
       }
     };
@@ -455,10 +454,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       const int row0 = rb * L::kRows, row = row0 + (NQ == 2 ? q * 128 : 0) + row_in;
       const int node = node_of(p, row), h = head * p.group + row - node * p.group;
       const bool real = row < p.rows;
-      uint64_t word = 0;
-      if (real)
-        word = (at.count >= 64 ? ~0ull : (1ull << at.count) - 1) &
-               (p.tree ? p.tree[int64_t(at.b) * p.n + node] : ~0ull >> (63 - node));
+      const uint64_t word = real ? nodes_seen(p, at.b, node, at.count) : 0;
       float m = -INFINITY, l = 0.f;                      // the maximum in use
       const int tiles = at.t1 - at.t0;
 
@@ -677,7 +673,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       const int first = whole ? 0 : at.first(), final = whole ? 0 : at.final();
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
       uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
-      auto store = [&](int c, const float (&y)[32], float inv, bool empty) {
+      float *sums = p.pass == kPrefix ? p.seed + at_row * p.d : nullptr;
+      const bool unused = p.pass != kPrefix && node >= at.count;
+      auto store = [&](int c, const float (&y)[32], float inv, bool empty, const Seed &seed) {
         if (!real) return;
 #pragma unroll
         for (int k = 0; k < 32; k += 8)
@@ -685,19 +683,40 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
             float z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = empty ? 0.f : y[k + e] * inv;
+            if (seed.at) {
+              const float4 a = __ldg(reinterpret_cast<const float4 *>(seed.at + c + k));
+              const float4 b = __ldg(reinterpret_cast<const float4 *>(seed.at + c + k + 4));
+              const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] = fmaf(s[e], seed.w_seed, z[e]);
+            }
+            if (sums) {
+              reinterpret_cast<float4 *>(sums + c + k)[0] = make_float4(z[0], z[1], z[2], z[3]);
+              reinterpret_cast<float4 *>(sums + c + k)[1] = make_float4(z[4], z[5], z[6], z[7]);
+              continue;
+            }
             const bool f16 = L::kF8 ? p.q_f16 != 0 : kType == kF16;
             *reinterpret_cast<uint4 *>(out + c + k) =
                 make_uint4(pack_out(z[0], z[1], f16), pack_out(z[2], z[3], f16),
                            pack_out(z[4], z[5], f16), pack_out(z[6], z[7], f16));
           }
       };
-      auto store_lse = [&](float mm, float ll, bool empty) {
-        if (p.lse && real && (NQ == 2 || q == 0))
-          p.lse[at_row] = empty ? -INFINITY : (mm - kWideLift<kType> + log2f(ll)) * kLn2;
+      // the log2 of a row's sum; a row that is none has no seed
+      auto lse_of = [&](float mm, float ll, bool empty) {
+        return empty ? -INFINITY : mm - kWideLift<kType> + log2f(ll);
+      };
+      auto store_lse = [&](float lse) {
+        if (!real || (NQ == 1 && q == 1)) return;
+        if (sums)
+          p.seed_lse[at_row] = lse;
+        else if (p.lse)
+          p.lse[at_row] = lse * kLn2;
       };
       if (whole) {
-        const bool empty = node >= at.count || (m == -INFINITY && l == 0.f);   // NaN is not nothing
-        const float inv = empty ? 0.f : p.v_scale / l;
+        const bool empty = unused || (m == -INFINITY && l == 0.f);   // NaN is not nothing
+        float inv = empty ? 0.f : p.v_scale / l, lse = lse_of(m, l, empty);
+        const Seed seed(p, at_row, at.skip > 0, unused || !real, lse);
+        if (seed.at) inv *= seed.w_own;
 #pragma unroll 1
         for (int k = col0; k < col1; k += 32) {
           uint32_t y[32];
@@ -705,9 +724,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
           float f[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(y[e]);
-          store(k, f, inv, empty);
+          store(k, f, inv, empty, seed);
         }
-        store_lse(m, l, empty);
+        store_lse(lse);
       } else {
         // partial results: [4 columns][row], then (m, l) of each row
         const int mine_row = (NQ == 2 ? q * 128 : 0) + row_in;
@@ -753,8 +772,10 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
           }
           const bool all = join.last();
           to = place(join.lo);
-          const bool empty = node >= at.count || (m == -INFINITY && l == 0.f);
-          const float inv = empty ? 0.f : p.v_scale / l;
+          const bool empty = unused || (m == -INFINITY && l == 0.f);
+          float inv = empty ? 0.f : p.v_scale / l, lse = lse_of(m, l, empty);
+          const Seed seed(p, at_row, all && at.skip > 0, unused || !real, lse);
+          if (seed.at) inv *= seed.w_own;
 #pragma unroll 1
           for (int k = col0; k < col1; k += 32) {
             float f[32];
@@ -775,7 +796,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
               }
             }
             if (all) {
-              store(k, f, inv, empty);
+              store(k, f, inv, empty, seed);
             } else {
               // (these columns of this row are read by no other thread)
 #pragma unroll
@@ -785,7 +806,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
             }
           }
           if (all) {
-            store_lse(m, l, empty);
+            store_lse(lse);
             break;
           }
           sync_rows();                                   // everybody has read the group's states

@@ -135,12 +135,8 @@ PyObject *result(vg_status s, const Tensor &t) {
   }                                                                                   \
   END_HANDLE_TH_ERRORS
 
-// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out, the cache's device
-PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(12)
-  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[1], "k"}, {a[2], "v"}, {a[3], "inv_freq"}, {a[5], "lens"},
-                                               {a[6], "depth"}, {a[7], "counts"}, {a[10], "q_out"}}, a[11]));
-  vg_rope_desc d;
+// Fills `d` from q, k, v, inv_freq, cache, lens, depth, counts, layout, factor and q_out; returns the output.
+Tensor rope_desc(PyObject *const *a, vg_rope_desc &d) {
   const Tensor &q = heads(a[0], "q", d.q_stride), &k = heads(a[1], "k", d.k_stride),
                &v = heads(a[2], "v", d.v_stride), &f = tensor(a[3], "inv_freq");
   const vg_kv_cache *cache = cache_of(a[4]);
@@ -169,24 +165,55 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   d.q_heads = int32_t(q.size(2));
   d.rot = int32_t(2 * f.numel());
   d.factor = number(a[9]);
-  return result(vg_rope_append(&d, cache, stream_of(q)), out);
+  return out;
+}
+
+// q, k, v, inv_freq, cache, lens, depth, counts, layout, factor, q_out, the cache's device
+PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  VG_BEGIN(12)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[1], "k"}, {a[2], "v"}, {a[3], "inv_freq"}, {a[5], "lens"},
+                                               {a[6], "depth"}, {a[7], "counts"}, {a[10], "q_out"}}, a[11]));
+  vg_rope_desc d;
+  const Tensor out = rope_desc(a, d);
+  return result(vg_rope_append(&d, cache_of(a[4]), stream_of(out)), out);
   VG_END
 }
 
-// q, cache, lens, tree, counts, scale, out, lse, workspace, the cache's device
-PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  VG_BEGIN(10)
-  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[2], "lens"}, {a[3], "tree"}, {a[4], "counts"},
-                                               {a[6], "out"}, {a[7], "lse"}, {a[8], "workspace"}}, a[9]));
-  vg_attention_desc d;
+// rope_append's, then q_weight, k_weight, eps
+PyObject *qk_norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  VG_BEGIN(15)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[1], "k"}, {a[2], "v"}, {a[3], "inv_freq"}, {a[5], "lens"},
+                                               {a[6], "depth"}, {a[7], "counts"}, {a[10], "q_out"}, {a[12], "q_weight"},
+                                               {a[13], "k_weight"}}, a[11]));
+  vg_qk_norm_rope_desc d;
+  const Tensor out = rope_desc(a, d.rope);
+  d.weight_type = d.rope.type;
+  d.q_weight = d.k_weight = nullptr;
+  bool some = false;
+  for (const bool k : {false, true}) {
+    const char *name = k ? "k_weight" : "q_weight";
+    if (!given(a[12 + k])) continue;
+    const Tensor &w = tensor(a[12 + k], name);
+    const at::ScalarType type = w.scalar_type() == at::kFloat ? at::kFloat : out.scalar_type();
+    if (w.scalar_type() != type || w.dim() != 1 || w.size(0) != out.size(3) || !w.is_contiguous())
+      throw Bad{std::string(name) + ": expected a contiguous CUDA tensor [head_dim] of float32 or of q's type"};
+    if (some && type_of(w) != d.weight_type) throw Bad{"q_weight and k_weight must have the same type"};
+    some = true;
+    d.weight_type = type_of(w);
+    (k ? d.k_weight : d.q_weight) = w.const_data_ptr();
+  }
+  d.eps = number(a[14]);
+  return result(vg_qk_norm_rope_append(&d, cache_of(a[4]), stream_of(out)), out);
+  VG_END
+}
+
+// Fills `d` from q, cache, lens, tree, counts, scale, out, lse; returns the output.
+Tensor attention_desc(PyObject *const *a, vg_attention_desc &d) {
   const Tensor &q = heads(a[0], "q", d.q_stride);
   const vg_kv_cache *cache = cache_of(a[1]);
   const int64_t B = q.size(0), n = q.size(1), hq = q.size(2);
   if (B != cache->batch || q.size(3) != cache->head_dim) throw Bad{"q and the cache do not fit together"};
   if (n > INT32_MAX || hq > INT32_MAX) throw Bad{"q is too long"};
-  const Tensor &ws = tensor(a[8], "workspace");
-  if (ws.scalar_type() != at::kByte || !ws.is_contiguous())
-    throw Bad{"workspace: expected a tensor from tree_attention_workspace"};
   const Tensor out = output(a[6], q, q.scalar_type(), "out");
   d.q = q.const_data_ptr();
   d.out = out.data_ptr();
@@ -198,7 +225,44 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   d.n = int32_t(n);
   d.q_heads = int32_t(hq);
   d.scale = number(a[5]);
-  return result(vg_tree_attention(&d, cache, ws.data_ptr(), size_t(ws.numel()), stream_of(q)), out);
+  return out;
+}
+
+const Tensor &workspace_of(PyObject *o, const char *maker) {
+  const Tensor &ws = tensor(o, "workspace");
+  if (ws.scalar_type() != at::kByte || !ws.is_contiguous())
+    throw Bad{std::string("workspace: expected a tensor from ") + maker};
+  return ws;
+}
+
+// q, cache, lens, tree, counts, scale, out, lse, workspace, the cache's device
+PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  VG_BEGIN(10)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[2], "lens"}, {a[3], "tree"}, {a[4], "counts"},
+                                               {a[6], "out"}, {a[7], "lse"}, {a[8], "workspace"}}, a[9]));
+  vg_attention_desc d;
+  const Tensor &ws = workspace_of(a[8], "tree_attention_workspace");
+  const Tensor out = attention_desc(a, d);
+  return result(vg_tree_attention(&d, cache_of(a[1]), ws.data_ptr(), size_t(ws.numel()), stream_of(out)), out);
+  VG_END
+}
+
+// tree_attention's, then prefix, prefix_pages
+PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  VG_BEGIN(12)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "q"}, {a[2], "lens"}, {a[3], "tree"}, {a[4], "counts"},
+                                               {a[6], "out"}, {a[7], "lse"}, {a[8], "workspace"}, {a[10], "prefix"},
+                                               {a[11], "prefix_pages"}}, a[9]));
+  vg_attention_desc d;
+  const Tensor &ws = workspace_of(a[8], "prefix_attention_workspace");
+  const Tensor &prefix = exact(a[10], at::kInt, {1}, "prefix"), &pages = tensor(a[11], "prefix_pages");
+  if (pages.scalar_type() != at::kInt || pages.dim() != 1 || !pages.is_contiguous() || pages.numel() > INT32_MAX)
+    throw Bad{"prefix_pages: expected a contiguous CUDA int32 tensor [pages]"};
+  const Tensor out = attention_desc(a, d);
+  return result(vg_prefix_attention(&d, cache_of(a[1]), static_cast<const int32_t *>(prefix.const_data_ptr()),
+                                    static_cast<const int32_t *>(pages.const_data_ptr()), int(pages.numel()),
+                                    ws.data_ptr(), size_t(ws.numel()), stream_of(out)),
+                out);
   VG_END
 }
 
@@ -221,6 +285,46 @@ PyObject *probabilities(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   return result(vg_probabilities(x.const_data_ptr(), type_of(x), rows, vocab, t,
                                  static_cast<float *>(out.data_ptr()), stream_of(x)),
                 out);
+  VG_END
+}
+
+// logits, u, temperature, top_k, top_p, min_p, out -> tokens
+PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  VG_BEGIN(7)
+  const c10::cuda::CUDAGuard guard(one_device({{a[0], "logits"}, {a[1], "u"}, {a[2], "temperature"}, {a[3], "top_k"},
+                                               {a[4], "top_p"}, {a[5], "min_p"}, {a[6], "out"}}));
+  const Tensor &x = tensor(a[0], "logits"), &u = tensor(a[1], "u");
+  const bool one = x.dim() == 1;
+  if (x.dim() < 1 || x.dim() > 2 || !x.numel() || (x.size(-1) > 1 && x.stride(-1) != 1))
+    throw Bad{"logits: expected a CUDA tensor [rows, vocab] or [vocab] that is not empty and whose last dimension is "
+              "contiguous"};
+  vg_sample_desc d;
+  d.rows = one ? 1 : x.size(0);
+  d.vocab = x.size(-1);
+  d.row_stride = d.rows > 1 ? x.stride(0) : d.vocab;
+  // [rows] or [rows, draws], without rows where the logits have none
+  if (u.scalar_type() != at::kFloat || !u.is_contiguous() || (!one && u.dim() < 1) ||
+      u.dim() > (one ? 1 : 2) || (!one && u.size(0) != d.rows) || !u.numel() || u.numel() / d.rows > INT32_MAX)
+    throw Bad{"u: expected a contiguous CUDA float32 tensor [rows] or [rows, draws]"};
+  d.draws = int32_t(u.numel() / d.rows);
+  auto each = [&](PyObject *o, at::ScalarType type, const char *name) -> const void * {
+    if (!given(o)) return nullptr;
+    const Tensor &t = tensor(o, name);
+    if (t.scalar_type() != type || !t.is_contiguous() || t.numel() != d.rows)
+      throw Bad{std::string(name) + ": expected a contiguous CUDA " + c10::toString(type) + " tensor, one for each row"};
+    return t.const_data_ptr();
+  };
+  d.temperature = static_cast<const float *>(each(a[2], at::kFloat, "temperature"));
+  d.top_k = static_cast<const int32_t *>(each(a[3], at::kInt, "top_k"));
+  d.top_p = static_cast<const float *>(each(a[4], at::kFloat, "top_p"));
+  d.min_p = static_cast<const float *>(each(a[5], at::kFloat, "min_p"));
+  d.out = given(a[6]) ? static_cast<float *>(exact(a[6], at::kFloat, x.sizes(), "out").data_ptr()) : nullptr;
+  d.x = x.const_data_ptr();
+  d.u = static_cast<const float *>(u.const_data_ptr());
+  d.type = type_of(x);
+  const Tensor tokens = at::empty(u.sizes(), u.options().dtype(at::kInt));
+  d.tokens = static_cast<int32_t *>(tokens.data_ptr());
+  return result(vg_sample(&d, stream_of(x)), tokens);
   VG_END
 }
 
@@ -266,7 +370,8 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 
 #define VG_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {VG_METHOD(rope_append), VG_METHOD(tree_attention), VG_METHOD(probabilities),
-                         VG_METHOD(verify_tree), {nullptr, nullptr, 0, nullptr}};
+                         VG_METHOD(verify_tree), VG_METHOD(qk_norm_rope_append), VG_METHOD(prefix_attention),
+                         VG_METHOD(sample), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_vgtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -144,6 +144,27 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: tor
         "vg_rope_append")
 
 
+def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                        inv_freq: torch.Tensor, cache: KVCache, lens: torch.Tensor,
+                        depth: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                        eps: float = 1e-6, layout: str = "half", factor: float = 1.0,
+                        q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """rope_append of q and k whose heads are normed first, in the same launch:
+    x * weight / sqrt(mean(x ** 2) + eps) over each whole head, in float32 up to
+    what is stored.  q_weight, k_weight [head_dim]: float32 or q's type, both the
+    same, None: ones.  eps at least 2 ** -126."""
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, cache, lens, depth, counts, eps,
+                                       layout, factor, q_out)
+    if layout not in _LAYOUTS:
+        raise ValueError("layout: 'half' or 'interleaved'")
+    return _checked((_native or _calls()).qk_norm_rope_append(
+        q, k, v, inv_freq, cache._at, lens, depth, counts, _LAYOUTS[layout], factor, q_out,
+        cache._device, q_weight, k_weight, eps), "vg_qk_norm_rope_append")
+
+
 def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
     """A zero-filled workspace for tree_attention with q of this shape."""
     if q.device != cache.k.device:
@@ -151,10 +172,12 @@ def tree_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
     if cache._device != torch.cuda.current_device():
         with torch.cuda.device(cache._device):
             return tree_attention_workspace(q, cache)
+    return _workspace("vg_tree_attention_workspace_size", q, cache)
+
+
+def _workspace(query, q, cache):
     n = ctypes.c_size_t()
-    _lib.check(_lib.vg_tree_attention_workspace_size(q.shape[1], q.shape[2], cache._at,
-                                                     ctypes.byref(n)),
-               "vg_tree_attention_workspace_size")
+    _lib.check(getattr(_lib, query)(q.shape[1], q.shape[2], cache._at, ctypes.byref(n)), query)
     return torch.zeros(n.value, dtype=torch.uint8, device=q.device)
 
 
@@ -185,6 +208,43 @@ def tree_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor,
         workspace, cache._device), "vg_tree_attention")
 
 
+def prefix_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
+    """A zero-filled workspace for prefix_attention with q of this shape."""
+    if q.device != cache.k.device:
+        raise ValueError("q and the cache are on different devices")
+    if cache._device != torch.cuda.current_device():
+        with torch.cuda.device(cache._device):
+            return prefix_attention_workspace(q, cache)
+    return _workspace("vg_prefix_attention_workspace_size", q, cache)
+
+
+def prefix_attention(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, prefix: torch.Tensor,
+                     prefix_pages: torch.Tensor, tree: torch.Tensor | None = None,
+                     counts: torch.Tensor | None = None, scale: float | None = None,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """tree_attention of sequences that begin with the same tokens: the pages
+    that the prefix fills are read once for the whole batch.
+
+    prefix int32 [1]: its tokens.  Its first prefix // page_size pages (as many as
+    prefix_pages, int32 [pages], has at most) are shared; what it has behind
+    them lies in each sequence's own pages.  lens counts the prefix's tokens, too, and
+    the row of the page table of a sequence that shares has its own pages from
+    there on (the entries before are not read).  A sequence shorter than the shared pages has no
+    part in them and takes all its slots from its own row.  The result is that of
+    tree_attention over tables that begin with the shared pages, but for the
+    order of its sums; everything else is as there.  workspace: from
+    prefix_attention_workspace."""
+    if stream is not None:
+        with _on(stream, q):                 # out and a new workspace, too, are made there
+            return prefix_attention(q, cache, lens, prefix, prefix_pages, tree, counts, scale, out, lse, workspace)
+    if workspace is None:
+        workspace = prefix_attention_workspace(q, cache)
+    return _checked((_native or _calls()).prefix_attention(
+        q, cache._at, lens, tree, counts, cache.head_dim ** -0.5 if scale is None else scale, out, lse,
+        workspace, cache._device, prefix, prefix_pages), "vg_prefix_attention")
+
+
 def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """float32 softmax over the last dimension of contiguous logits (bfloat16,
@@ -195,6 +255,32 @@ def probabilities(logits: torch.Tensor, temperature: torch.Tensor | None = None,
         with _on(stream, logits):
             return probabilities(logits, temperature, out)
     return _checked((_native or _calls()).probabilities(logits, temperature, out), "vg_probabilities")
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+           min_p: torch.Tensor | None = None, out: torch.Tensor | None = None,
+           stream=None) -> torch.Tensor:
+    """Tokens drawn from the softmax of logits [rows, vocab] (bfloat16, float16 or
+    float32; rows may lie apart), truncated: int32, one for each number of u
+    (float32 [rows] or [rows, draws], in [0, 1)).
+
+    Each row has its own temperature, top_p, min_p (float32) and top_k (int32), or
+    all none (None: 1, and no limit).  In the order of the logits, equal ones by
+    index, the first top_k tokens are kept (<= 0: all), of these the fewest
+    whose probabilities sum to top_p of theirs (>= 1: all), of these the ones
+    min_p times as probable as the first; one at least.  The token is the first
+    index whose running sum over what is kept exceeds u of the whole.  A
+    temperature <= 0 keeps the first largest logit.  A row without a
+    distribution (a NaN, or nothing but -infinity) has the token -1.
+
+    out, float32 like logits and contiguous, receives the truncated distribution itself, which
+    verify_tree takes as p and, for drafts drawn from it, as q.
+    include/vgemm.h (vg_sample) has the rule."""
+    if stream is not None:
+        with _on(stream, logits):
+            return sample(logits, u, temperature, top_k, top_p, min_p, out)
+    return _checked((_native or _calls()).sample(logits, u, temperature, top_k, top_p, min_p, out), "vg_sample")
 
 
 def verify_tree(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor,
