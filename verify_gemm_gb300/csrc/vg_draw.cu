@@ -4,21 +4,24 @@
 // A row's tokens are ordered by logit, the largest first, equal ones by index.
 // What a row keeps is a beginning of that order: at most k tokens, of these the
 // fewest whose weights 2^-z, z = (max - x) log2 e / T, sum to p times theirs,
-// of these the ones that weigh min_p and more.  So it is given by the last kept
-// logit x_f and how many of the logits equal to it are kept, m_f, the first by
-// index.  The token drawn is the first index whose running sum over what is
-// kept exceeds u times the whole.
+// of these the ones that weigh min_p and more.  So it is given by its last token:
+// logit x_f, index i_f.  The token drawn is the first index whose running sum
+// over what is kept exceeds u times the whole.
 //
-// Sums are integers (a weight of 1 is 2^s with sums below 2^62), so that no order
+// Sums are integers (a weight of 1 is 2^bits with sums below 2^62), so that no order
 // of addition changes what is kept or drawn, and weights are exact to some
 // 2^-29 of themselves: a draw is a comparison of u with the boundaries of 150000
 // tokens, and with sums good to 2^-22 one row in some hundred would end on the
 // neighbour.
 //
 // A cluster of blocks a row; a block holds a run of it in shared memory, and
-// each warp a run of that, so that the warps' order is the index order.  x_f is
-// looked for in histograms of 2048 bins over the logits' codes (ordered as
-// integers): a level narrows the range to the codes of one bin.
+// each warp a run of that, so that the warps' order is the index order.  The
+// last token is looked for in two steps: a histogram over z, 2048 bins of 1/64 of
+// an octave, says in which bin it lies (of counts for top-k, of weights for
+// top-p), and the tokens of that bin alone are sorted.  Up to 256 tokens of
+// top-k are found from each thread's largest logit alone: the k-th largest of
+// those is at most the k-th largest of all, so that all that is kept, and little
+// else, lies in the bins down to it.
 #include <algorithm>
 #include <cmath>
 
@@ -29,8 +32,13 @@ namespace {
 
 constexpr int kDrawThreads = 512, kDrawWarps = kDrawThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kDrawShare = 72 * 1024;         // bytes of a row a block should hold at most ...
+constexpr int kDrawShare = 76 * 1024;         // bytes of a row a block should hold at most ...
 constexpr int kDrawShareMax = 160 * 1024;     // ... and may
+constexpr int kLocal = 1024, kSorted = 2048;  // tokens of a block, of the row, that a list holds
+constexpr int kSmallK = 256;
+constexpr int kByThread = 16384;              // from this vocabulary on each thread's largest stands for its logits
+constexpr int kListBytes = (kLocal + kSorted) * 8;   // (and the bins, which are read before a list is made)
+static_assert(kListBytes >= 2 * kBins * 4, "room for the bins");
 
 struct DrawParams {
   const void *x;
@@ -54,31 +62,49 @@ struct Scale {
   float top, c, c_low, cap;          // c as two floats; differences beyond cap weigh nothing
 };
 
-// The weight of logit x: 2^-z in units of 2^-bits (up = bits - 30).  With z = (k + r) / 32, k
-// whole, |r| <= 1/2, it is 2^-(k / 32) from a table times 2^-(r / 32) by its series.
-// max - x is exact in FP32 for 16-bit logits but for those that are 2^-16 of
-// the largest or less; for FP32 ones what it loses is carried along.
+// The weight of logit x is w 2^(up - (bin >> 6)) (up = bits - 30, and w some 2^30).  With
+// z = (k + r) / 32, k whole, |r| <= 1/2, it is 2^-(k / 32) from a table times
+// 2^-(r / 32) by its series.  max - x is exact in FP32 for 16-bit logits but for
+// those that are 2^-16 of the largest or less; for FP32 ones what it loses is
+// carried along.  The bin is z in units of 1/64: the larger logit never has the
+// larger bin, as it goes by the rounded difference alone.
 template <typename T>
-__device__ __forceinline__ uint64_t weight(const Scale &s, const uint32_t *powers, float x, int up) {
-  constexpr float kMagic = 12582912.f;         // 1.5 2^23: what is added to it is rounded to a whole number
-  const float d = fminf(s.top - x, s.cap);
-  float low = d * s.c_low;
-  if constexpr (std::is_same_v<T, float>) {
-    const float a = s.top - x, b = a - s.top;
-    const float e = (s.top - (a - b)) + (-x - b);
-    low = a < s.cap ? fmaf(e, s.c, low) : low;
+struct Weight {
+  int w, k, half;
+  __device__ __forceinline__ Weight(const Scale &s, const uint32_t *powers, float x) {
+    constexpr float kMagic = 12582912.f;       // 1.5 2^23: what is added to it is rounded to a whole number
+    const float d = fminf(s.top - x, s.cap);
+    float low = d * s.c_low;
+    if constexpr (std::is_same_v<T, float>) {
+      const float a = s.top - x, b = a - s.top;
+      const float e = (s.top - (a - b)) + (-x - b);
+      low = a < s.cap ? fmaf(e, s.c, low) : low;
+    }
+    const float t = fmaf(d, s.c, kMagic);
+    k = __float_as_int(t) - __float_as_int(kMagic);
+    float r = fmaf(d, s.c, -(t - kMagic));
+    half = r >= 0.f;
+    r += low;
+    // 2^28 (2^-(r / 32) - 1)
+    float q = fmaf(r, 2.46224105f, -454.689658f);
+    q = fmaf(r, q, 62973.9374f);
+    q = fmaf(r, q, -5814539.98f);
+    const int f = __float_as_int(fmaf(r, q, kMagic)) - __float_as_int(kMagic);
+    const int p = int(powers[k & 31]);
+    w = p + __mulhi(p, f << 4);
+    if (x == -INFINITY) k = 2048;
   }
-  const float t = fmaf(d, s.c, kMagic);
+  __device__ __forceinline__ uint64_t value(int up) const { return uint64_t(uint32_t(w)) << up >> min(k >> 5, 63); }
+  __device__ __forceinline__ uint32_t bin() const { return min(uint32_t(2 * k + half), uint32_t(kBins - 1)); }
+  // w in the units of its bin: the last one has all weights below 2^-32
+  __device__ __forceinline__ uint32_t in_bin() const { return uint32_t(w) >> min(max((k >> 5) - 31, 0), 31); }
+};
+// Its bin alone.
+__device__ __forceinline__ uint32_t bin_of(const Scale &s, float x) {
+  constexpr float kMagic = 12582912.f;
+  const float d = fminf(s.top - x, s.cap), t = fmaf(d, s.c, kMagic);
   const int k = __float_as_int(t) - __float_as_int(kMagic);
-  const float r = fmaf(d, s.c, -(t - kMagic)) + low;
-  // 2^28 (2^-(r / 32) - 1)
-  float q = fmaf(r, 2.46224105f, -454.689658f);
-  q = fmaf(r, q, 62973.9374f);
-  q = fmaf(r, q, -5814539.98f);
-  const int f = __float_as_int(fmaf(r, q, kMagic)) - __float_as_int(kMagic);
-  const int w = int(powers[k & 31]);
-  const uint64_t v = uint64_t(uint32_t(w + __mulhi(w, f << 4))) << up;
-  return x == -INFINITY ? 0 : v >> min(k >> 5, 63);
+  return x == -INFINITY ? kBins - 1 : min(uint32_t(2 * k + (fmaf(d, s.c, -(t - kMagic)) >= 0.f)), uint32_t(kBins - 1));
 }
 
 // Logits' codes in their order; logits of 16 bits have as many codes.
@@ -125,7 +151,33 @@ __device__ __forceinline__ uint64_t scan_up(uint64_t v, int lane) {
   return v;
 }
 
-// Where a search is: codes [lo, hi], bins of 2^shift of them from hi down, the last
+// Sorts n (a power of two, at least 64) entries, the smallest first; the whole block.
+__device__ __forceinline__ void sort_up(uint64_t *v, int n) {
+  for (int size = 2; size <= n; size *= 2)
+    for (int stride = size / 2; stride; stride /= 2) {
+      // (pairs at most 32 apart stay within a warp's 64 entries)
+      if (stride > 16) __syncthreads();
+      else __syncwarp();
+      for (int q = threadIdx.x; q < n / 2; q += kDrawThreads) {
+        const int a = 2 * q - (q & (stride - 1)), b = a + stride;
+        const uint64_t x = v[a], y = v[b];
+        if ((x > y) == ((a & size) == 0)) {
+          v[a] = y;
+          v[b] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// What the first block of a row tells the others.
+struct Found {
+  uint32_t bin, code;                // the last token's bin; its logit
+  int32_t index, state;              // its index
+  uint64_t target, whole;            // the count or weight wanted of the bin; the weight of what is kept
+};
+enum { kGo = 0, kAll = 1, kTooMany = 2 };      // state; kAll: nothing is left out
+// Where a search by codes is: codes [lo, hi], bins of 2^shift of them from hi down, the last
 // bin with all that is below; what is wanted of them.
 struct Search {
   uint32_t hi, lo;
@@ -139,17 +191,21 @@ __device__ __forceinline__ int shift_for(uint32_t span) {
 }
 
 template <typename T, bool kHeld>
-__global__ void __launch_bounds__(kDrawThreads, 1) sample_kernel(const __grid_constant__ DrawParams p) {
+__global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_constant__ DrawParams p) {
   extern __shared__ __align__(16) uint8_t draw_smem[];
   __shared__ __align__(16) ulonglong2 tops[kMaxCluster * kDrawWarps];
   __shared__ __align__(16) ulonglong2 sums[kMaxCluster * kDrawWarps];
-  __shared__ __align__(16) Search told;
+  __shared__ __align__(16) Found told;
+  __shared__ __align__(16) Search told_search;
   __shared__ uint32_t powers[32];
   __shared__ Scale told_scale;
   __shared__ double min_at;          // T ln(min_p)
   __shared__ uint64_t scan[kDrawWarps];
+  __shared__ uint32_t listed;
+  __shared__ int n_keep;
   uint32_t *bin_lo = reinterpret_cast<uint32_t *>(draw_smem), *bin_hi = bin_lo + kBins;
-  uint4 *held = reinterpret_cast<uint4 *>(bin_hi + kBins);
+  uint64_t *local = reinterpret_cast<uint64_t *>(draw_smem), *list = local + kLocal;
+  uint4 *held = reinterpret_cast<uint4 *>(draw_smem + kListBytes);
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
   const int64_t row = blockIdx.x / blocks;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -201,7 +257,8 @@ __global__ void __launch_bounds__(kDrawThreads, 1) sample_kernel(const __grid_co
       return load_unit(x, w0 + i, lo, hi);
     }
   };
-  // f(i, logits 8 i .. 8 i + 7 of the warp's run), 0 for -0; all lanes come along
+  const int64_t base = w0 * 8 - lo;                      // index of the warp's first element in the row
+  // f(index of the first, 8 logits, 0 for -0), over the warp's run; all lanes come along
   auto each = [&](auto &&f) {
 #pragma unroll 1
     for (int i0 = 0; i0 < mine; i0 += 32) {
@@ -218,20 +275,21 @@ __global__ void __launch_bounds__(kDrawThreads, 1) sample_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = -INFINITY;
       }
-      f(i, y);
+      f(int(base) + i * 8, y);
     }
+  };
+  auto sync_all = [&] {
+    if (blocks > 1) cluster_sync();
+    else __syncthreads();
   };
 
   // ------------------------------------------------------------- the largest
   Largest<T> largest;
   for (int i = lane; i < mine; i += 32) largest.take(unit(i));
-  float m = largest.value();
+  const float my_top = largest.value();
+  float m = my_top;
 #pragma unroll
   for (int w = 16; w; w /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, w));
-  auto sync_all = [&] {
-    if (blocks > 1) cluster_sync();
-    else __syncthreads();
-  };
   if (blocks > 1) cluster_wait();
   if (lane < int(blocks)) cluster_store(&tops[rank * kDrawWarps + warp], lane, __float_as_uint(m), 0);
   sync_all();
@@ -241,293 +299,23 @@ __global__ void __launch_bounds__(kDrawThreads, 1) sample_kernel(const __grid_co
 #pragma unroll
   for (int w = 16; w; w /= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, w));
   top += 0.f;
-  const bool greedy = temperature <= 0.f;
   float *out = p.out ? p.out + row * p.V : nullptr;
   // no token: a NaN, an infinity that weighs all, nothing but -infinity
-  const bool bad = isnan(top) || isnan(temperature) || (top == INFINITY && !greedy);
+  const bool cold = temperature <= 0.f;
+  const bool bad = isnan(top) || isnan(temperature) || (top == INFINITY && !cold);
   if (bad || top == -INFINITY) {
     if (rank == 0)
       for (int i = tid; i < p.draws; i += kDrawThreads) p.tokens[row * p.draws + i] = -1;
     if (out) {
-      const float v = bad && !greedy ? __int_as_float(0x7FFFFFFF) : 0.f;
+      const float v = bad && !cold ? __int_as_float(0x7FFFFFFF) : 0.f;
       for (int64_t i = rank * kDrawThreads + tid; i < p.V; i += int64_t(blocks) * kDrawThreads) out[i] = v;
     }
     return;
   }
-  Scale scale = told_scale;
-  scale.top = top;
-  const int up = p.bits - 30;
-  auto weigh = [&](float y) { return weight<T>(scale, powers, y, up); };
-
-  // ---------------------------------------------------------- what is kept
-  // Kept are logits above x_f and the first m_f equal to it.
-  float x_f = -INFINITY;
-  uint64_t m_f = 0;
-  // Looks for the logit at which the running count (kMass: weight) of the order reaches the
-  // target, among those above `floor`; kMass: the target is top_p of their sum and
-  // `beyond`, the weight of what is kept of those equal to the floor.
-  auto search = [&](auto mass, float floor, uint64_t target, uint64_t beyond) {
-    constexpr bool kMass = decltype(mass)::value;
-    Search s;
-    s.hi = code_of<T>(top);
-    s.lo = code_of<T>(floor) + 1;
-    // (beyond 40 octaves of weight the bins need not tell codes apart)
-    const uint32_t guess = code_of<T>(fmaxf(top - 1280.f / scale.c, floor));
-    s.shift = shift_for(s.hi - min(guess, s.hi));
-    s.target = target;
-    s.done = 0;
-    bool first = true;
-    while (true) {
-      for (int i = tid; i < 2 * kBins; i += kDrawThreads) bin_lo[i] = 0;
-      __syncthreads();
-      each([&](int, const float (&y)[8]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t code = code_of<T>(y[k]);
-          if (code > s.hi || code < s.lo) continue;
-          const uint32_t b = min((s.hi - code) >> s.shift, uint32_t(kBins - 1));
-          if constexpr (kMass) {
-            const uint64_t w = weigh(y[k]);
-            const uint32_t low = uint32_t(w);
-            const uint32_t old = atomicAdd(bin_lo + b, low);
-            const uint32_t more = uint32_t(w >> 32) + (old + low < old);
-            if (more) atomicAdd(bin_hi + b, more);
-          } else {
-            atomicAdd(bin_lo + b, 1u);
-          }
-        }
-      });
-      sync_all();
-      if (rank == 0) {
-        // four bins a thread, of all blocks
-        constexpr int kEach = kBins / kDrawThreads;
-        uint64_t v[kEach] = {};
-        for (uint32_t r = 0; r < blocks; ++r)
-#pragma unroll
-          for (int k = 0; k < kEach; ++k) {
-            uint32_t a, b;
-            const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(bin_lo + tid * kEach + k));
-            asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %2, %3; ld.shared::cluster.u32 %0, [at];\n"
-                         "ld.shared::cluster.u32 %1, [at + %4]; }"
-                         : "=&r"(a), "=&r"(b)
-                         : "r"(here), "r"(r), "n"(kBins * 4)
-                         : "memory");
-            v[k] += uint64_t(b) << 32 | a;
-          }
-        uint64_t sum = 0;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) sum += v[k];
-        uint64_t run = scan_up(sum, lane);
-        if (lane == 31) scan[warp] = run;
-        __syncthreads();
-        uint64_t whole = 0;
-#pragma unroll
-        for (int w = 0; w < kDrawWarps; ++w) {
-          if (w < warp) run += scan[w];
-          whole += scan[w];
-        }
-        uint64_t before = run - sum;
-        Search next = s;
-        if (kMass && first) {
-          bool exact;
-          next.target = part_of(top_p, whole + beyond, exact);
-          next.target = max(next.target + !exact, uint64_t(1));
-        }
-        if (next.target > whole) {
-          if (tid == 0) {
-            next.done = 2;
-            next.target -= whole;
-            told = next;
-          }
-        } else if (before < next.target && next.target <= run) {
-          int b = 0;
-#pragma unroll
-          for (int k = 0; k < kEach - 1; ++k)
-            if (b == k && before + v[k] < next.target) {
-              before += v[k];
-              ++b;
-            }
-          const uint32_t bin = uint32_t(tid * kEach + b);
-          next.target -= before;
-          const uint32_t above = s.hi - (bin << s.shift);
-          if (bin < kBins - 1) {
-            next.done = s.shift == 0;
-            next.lo = max(s.lo, above - ((1u << s.shift) - 1));
-          }
-          next.hi = above;
-          next.shift = shift_for(next.hi - next.lo);
-          if (next.done) {
-            const uint64_t w = kMass ? weigh(logit_of<T>(above)) : 1;
-            next.ties = (next.target + w - 1) / w;
-          }
-          told = next;
-        }
-        __syncthreads();
-        // to the other blocks
-        if (blocks > 1 && tid < int(blocks)) {
-          const uint64_t *from = reinterpret_cast<const uint64_t *>(&told);
-          if (tid)
-#pragma unroll
-            for (int k = 0; k < int(sizeof(Search) / 16); ++k)
-              cluster_store(reinterpret_cast<ulonglong2 *>(&told) + k, uint32_t(tid), from[2 * k], from[2 * k + 1]);
-        }
-      }
-      sync_all();
-      s = told;
-      first = false;
-      if (s.done) return s;
-    }
-  };
-  if (greedy) {
-    x_f = top;
-    m_f = 1;
-  } else {
-    if (top_k > 0 && top_k < p.V) {
-      const Search s = search(std::false_type{}, -INFINITY, uint64_t(top_k), 0);
-      if (s.done == 1) {
-        x_f = logit_of<T>(s.hi);
-        m_f = s.ties;
-      }
-    }
-    if (top_p < 1.f) {
-      const uint64_t w = m_f ? weigh(x_f) : 0;
-      const Search s = search(std::true_type{}, x_f, 0, m_f * w);
-      if (s.done == 1) {
-        x_f = logit_of<T>(s.hi);
-        m_f = s.ties;
-      } else if (w) {
-        m_f = min(m_f, (s.target + w - 1) / w);
-      }
-    }
-    if (min_p > 0.f) {
-      // the smallest logit that weighs min_p: those below are left out
-      const double least = double(top) + min_at;
-      float f = __double2float_ru(least);
-      if (!(f < top)) {
-        if (f > top) m_f = x_f == top ? min(m_f, uint64_t(1)) : 1;   // (min_p above 1: the first token alone)
-        else if (x_f < top) m_f = uint64_t(p.V);
-        x_f = top;
-      } else if (f > x_f) {
-        x_f = f;
-        m_f = uint64_t(p.V);
-      }
-    }
-  }
-
-  // ---------------------------------------------------------------- the draw
-  // of each warp: the weight above x_f and how many are equal to it
-  uint64_t mass = 0;
-  uint32_t ties = 0;
-  each([&](int, const float (&y)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (y[k] > x_f) mass += weigh(y[k]);
-      ties += y[k] == x_f;
-    }
-  });
-#pragma unroll
-  for (int w = 16; w; w /= 2) {
-    mass += __shfl_xor_sync(~0u, mass, w);
-    ties += __shfl_xor_sync(~0u, ties, w);
-  }
-  if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, mass, ties);
-  sync_all();
-  const uint64_t w_f = x_f == top ? uint64_t(1) << p.bits : m_f ? weigh(x_f) : 0;
-  // entries a lane: a run of the warps; how many ties and how much weight lie before it
-  const int per = (entries + 31) / 32, first = lane * per;
-  uint64_t t = 0;
-  for (int i = first; i < min(first + per, entries); ++i) t += sums[i].y;
-  const uint64_t t_before = scan_up(t, lane) - t;
-  auto kept_ties = [&](uint64_t before, uint64_t n) { return before >= m_f ? 0 : min(n, m_f - before); };
-  uint64_t here = 0, ties_run = t_before;
-  for (int i = first; i < min(first + per, entries); ++i) {
-    here += sums[i].x + kept_ties(ties_run, sums[i].y) * w_f;
-    ties_run += sums[i].y;
-  }
-  const uint64_t upto = scan_up(here, lane);
-  const uint64_t whole = __shfl_sync(~0u, upto, 31);
-  // what lies before this warp
-  const int me = rank * kDrawWarps + warp;
-  uint64_t my_ties = t_before, my_mass = upto - here;
-  for (int i = first; i < min(first + per, me); ++i) {
-    my_mass += sums[i].x + kept_ties(my_ties, sums[i].y) * w_f;
-    my_ties += sums[i].y;
-  }
-  my_ties = __shfl_sync(~0u, my_ties, me / per);
-  my_mass = __shfl_sync(~0u, my_mass, me / per);
-  const uint64_t my_end = my_mass + mass + kept_ties(my_ties, ties) * w_f;
-  const int64_t base = w0 * 8 - lo;                      // index of the run's first element
-  for (int d = 0; d < p.draws; ++d) {
-    float u = p.u[row * p.draws + d];
-    u = u >= 1.f ? 0x1.fffffep-1f : u;
-    bool exact;
-    const uint64_t want = part_of(u, whole, exact);      // the first running sum above it
-    if (want < my_mass || want >= my_end) continue;
-    uint64_t run = my_mass, tie = my_ties;
-    bool found = false;
-    each([&](int i, const float (&y)[8]) {
-      if (found) return;
-      uint32_t n = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) n += y[k] == x_f;
-      uint32_t n_before = n;
-#pragma unroll
-      for (int w = 1; w < 32; w *= 2) {
-        const uint32_t z = __shfl_up_sync(~0u, n_before, w);
-        if (lane >= w) n_before += z;
-      }
-      const uint32_t n_all = __shfl_sync(~0u, n_before, 31);
-      uint64_t t0 = tie + n_before - n, sum = 0, each_w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        each_w[k] = y[k] > x_f ? weigh(y[k]) : 0;
-        if (y[k] == x_f && t0++ < m_f) each_w[k] = w_f;
-        sum += each_w[k];
-      }
-      const uint64_t to = scan_up(sum, lane);
-      uint64_t from = run + to - sum;
-      if (want >= from && want < run + to) {
-        int at8 = 0;
-        for (int k = 0; k < 8; ++k) {
-          if (want >= from + each_w[k]) at8 = k + 1;
-          else break;
-          from += each_w[k];
-        }
-        p.tokens[row * p.draws + d] = int32_t(base + int64_t(i) * 8 + at8);
-      }
-      run += __shfl_sync(~0u, to, 31);
-      tie += n_all;
-      found = run > want;
-    });
-  }
-  if (!out) return;
-  // ------------------------------------------------------- the distribution
-  const float c = scale.c * (1.f / 32), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
-  uint64_t tie = my_ties;
+  // stores the 8 probabilities v of elements r .. r + 7
   const bool aligned = ((row * p.V + base) & 3) == 0;
-  each([&](int i, const float (&y)[8]) {
-    uint32_t n = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) n += y[k] == x_f;
-    uint32_t n_before = n;
-    if (__any_sync(~0u, n != 0)) {
-#pragma unroll
-      for (int w = 1; w < 32; w *= 2) {
-        const uint32_t z = __shfl_up_sync(~0u, n_before, w);
-        if (lane >= w) n_before += z;
-      }
-    }
-    uint64_t t0 = tie + n_before - n;
-    tie += __shfl_sync(~0u, n_before, 31);
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool kept = y[k] > x_f || (y[k] == x_f && t0 < m_f && y[k] > -INFINITY);
-      t0 += y[k] == x_f;
-      v[k] = kept ? (y[k] == top ? 1.f : ex2((y[k] - top) * c)) * inv : 0.f;
-    }
-    if (i >= mine) return;
-    const int64_t r = base + int64_t(i) * 8;
+  auto store = [&](int r, const float (&v)[8]) {
+    if (r - int(base) >= mine * 8) return;
     if (aligned && r >= 0 && r + 8 <= p.V) {
       float4 *to = reinterpret_cast<float4 *>(out + r);
       __stcs(to, make_float4(v[0], v[1], v[2], v[3]));
@@ -537,6 +325,530 @@ __global__ void __launch_bounds__(kDrawThreads, 1) sample_kernel(const __grid_co
       for (int k = 0; k < 8; ++k)
         if (r + k >= 0 && r + k < p.V) out[r + k] = v[k];
     }
+  };
+
+  // ---------------------------------------------------- the first largest alone
+  if (cold || top_k == 1 || top_p <= 0.f || min_p > 1.f) {
+    int first = INT32_MAX;
+    if (m == top)                                        // (this warp's largest)
+      each([&](int r, const float (&y)[8]) {
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+          if (y[k] == top) first = min(first, r + k);
+      });
+    first = __reduce_min_sync(~0u, first);
+    if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, uint32_t(first), 0);
+    sync_all();
+    first = INT32_MAX;
+    for (int i = lane; i < entries; i += 32) first = min(first, int(sums[i].x));
+    first = __reduce_min_sync(~0u, first);
+    if (rank == 0)
+      for (int i = tid; i < p.draws; i += kDrawThreads) p.tokens[row * p.draws + i] = first;
+    if (out)
+      each([&](int r, const float (&)[8]) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = r + k == first ? 1.f : 0.f;
+        store(r, v);
+      });
+    return;
+  }
+  Scale scale = told_scale;
+  scale.top = top;
+  const int up = p.bits - 30;
+  auto weigh = [&](float y) { return Weight<T>(scale, powers, y).value(up); };
+
+  // What is kept: y > x_f, and those equal to it up to index i_f.
+  float x_f = -INFINITY;
+  int i_f = -1;
+  auto kept = [&](float y, int index) { return y > x_f || (y == x_f && index <= i_f); };
+  // The block's 512 threads' sums of `mine`, up to each and in all.
+  auto scan_block = [&](uint64_t v, uint64_t &whole) {
+    uint64_t run = scan_up(v, lane);
+    __syncthreads();                                     // (scan has been read)
+    if (lane == 31) scan[warp] = run;
+    __syncthreads();
+    whole = 0;
+#pragma unroll
+    for (int w = 0; w < kDrawWarps; ++w) {
+      if (w < warp) run += scan[w];
+      whole += scan[w];
+    }
+    return run;
+  };
+  // Tells all blocks what the first one's thread 0 has put into `what`.
+  auto tell = [&](auto *what) {
+    static_assert(sizeof(*what) % 16 == 0, "goes by 16 bytes");
+    __syncthreads();
+    if (blocks > 1 && tid && tid < int(blocks)) {
+      const uint64_t *from = reinterpret_cast<const uint64_t *>(what);
+#pragma unroll
+      for (int k = 0; k < int(sizeof(*what) / 16); ++k)
+        cluster_store(reinterpret_cast<ulonglong2 *>(what) + k, uint32_t(tid), from[2 * k], from[2 * k + 1]);
+    }
+  };
+  // Four bins a thread, of all blocks.
+  auto gather_bins = [&](uint64_t (&v)[4], bool both) {
+    static_assert(kBins == 4 * kDrawThreads, "four bins a thread");
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = 0;
+    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(bin_lo + tid * 4));
+#pragma unroll 4
+    for (uint32_t r = 0; r < blocks; ++r) {
+      uint32_t a[4], b[4] = {};
+      asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %4, %5; ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [at]; }"
+                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                   : "r"(here), "r"(r)
+                   : "memory");
+      if (both)
+        asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %4, %5; ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [at]; }"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(here + kBins * 4), "r"(r)
+                     : "memory");
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += uint64_t(b[k]) << 32 | a[k];
+    }
+  };
+  // The first block's: which bin the running sum of v reaches the target in (0: of top_p of the whole).
+  auto find_bin = [&](const uint64_t (&v)[4], uint64_t target) {
+    const uint64_t sum = v[0] + v[1] + v[2] + v[3];
+    uint64_t whole;
+    const uint64_t run = scan_block(sum, whole);
+    uint64_t before = run - sum;
+    if (target == 0) {
+      bool exact;
+      target = part_of(top_p, whole, exact);
+      target = max(target + !exact, uint64_t(1));
+    }
+    if (target > whole) {
+      if (tid == 0) told = Found{kBins - 1, 0, -1, kAll, target - whole, whole};
+    } else if (before < target && target <= run) {
+      uint32_t b = 0;
+#pragma unroll
+      for (uint32_t k = 0; k < 3; ++k)
+        if (b == k && before + v[k] < target) {
+          before += v[k];
+          ++b;
+        }
+      told = Found{uint32_t(tid) * 4 + b, 0, -1, kGo, target - before, whole};
+    }
+  };
+  auto clear_bins = [&] {
+    for (int i = tid; i < 2 * kBins; i += kDrawThreads) bin_lo[i] = 0;
+    __syncthreads();
+  };
+  // Each block's tokens that `wanted` says to its list; the first block's `list` then has all
+  // of them in order, and how many there are.
+  auto collect = [&](auto &&wanted) {
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    each([&](int r, const float (&y)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (wanted(y[k], r + k)) {
+          const uint32_t at = atomicAdd(&listed, 1u);
+          if (at < kLocal) local[at] = uint64_t(~code_of<float>(y[k])) << 32 | uint32_t(r + k);
+        }
+    });
+    sync_all();
+  };
+  auto gather_list = [&] {
+    uint32_t n = 0, mine_at = 0, mine_n = 0;             // lane r: block r's
+    const uint32_t count_at = static_cast<uint32_t>(__cvta_generic_to_shared(&listed));
+    if (lane < int(blocks))
+      asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %1, %2; ld.shared::cluster.u32 %0, [at]; }"
+                   : "=r"(mine_n)
+                   : "r"(count_at), "r"(lane)
+                   : "memory");
+    mine_at = uint32_t(scan_up(mine_n, lane)) - mine_n;
+    n = __shfl_sync(~0u, mine_at + mine_n, 31);
+    if (n > kSorted || __any_sync(~0u, mine_n > kLocal)) return -1;
+    int size = 64;
+    while (size < int(n)) size *= 2;
+    const uint32_t list_at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+    // a warp takes every 16th piece of 32 entries
+    for (uint32_t r = 0; r < blocks; ++r) {
+      const uint32_t count = __shfl_sync(~0u, mine_n, r), to = __shfl_sync(~0u, mine_at, r);
+      for (uint32_t i = tid; i < count; i += kDrawThreads) {
+        uint64_t v;
+        asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %1, %2; ld.shared::cluster.u64 %0, [at]; }"
+                     : "=l"(v)
+                     : "r"(list_at + i * 8), "r"(r)
+                     : "memory");
+        list[to + i] = v;
+      }
+    }
+    for (int i = int(n) + tid; i < size; i += kDrawThreads) list[i] = ~uint64_t(0);
+    __syncthreads();
+    sort_up(list, size);
+    return int(n);
+  };
+  auto logit_at = [&](uint64_t e) { return logit_of<float>(~uint32_t(e >> 32)); };
+  // The smallest logit that weighs min_p.
+  const float f_min = min_p > 0.f ? fminf(__double2float_ru(double(top) + min_at), top) : -INFINITY;
+  // In the sorted list of n: how many are kept, with the target of what is before and in it
+  // (limit: of tokens; target 0: no limit of weight).  Every thread has up to four entries.
+  auto cut_list = [&](int n, int limit, uint64_t target, bool of_list) {
+    uint64_t v[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = tid * 4 + k;
+      v[k] = i < min(n, limit) ? weigh(logit_at(list[i])) : 0;
+      sum += v[k];
+    }
+    uint64_t whole;
+    uint64_t run = scan_block(sum, whole) - sum;
+    if (of_list && top_p < 1.f) {
+      bool exact;
+      target = part_of(top_p, whole, exact);
+      target = max(target + !exact, uint64_t(1));
+    }
+    if (tid == 0) n_keep = 0;
+    __syncthreads();
+    int last = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = tid * 4 + k;
+      if (i < min(n, limit) && (target == 0 || run < target) && logit_at(list[i]) >= f_min) last = i + 1;
+      run += v[k];
+    }
+    if (last) atomicMax(&n_keep, last);
+    __syncthreads();
+  };
+  bool too_many = false, done = false;
+  uint64_t whole = 0;
+
+  if (top_k > 0 && top_k <= kSmallK && top_k < p.V) {
+    // ----------------------------------------------------------- a small top-k
+    clear_bins();
+    if (p.V >= kByThread) {
+      if (my_top > -INFINITY) atomicAdd(bin_lo + bin_of(scale, my_top), 1u);
+    } else {
+      each([&](int, const float (&y)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (y[k] > -INFINITY) atomicAdd(bin_lo + bin_of(scale, y[k]), 1u);
+      });
+    }
+    sync_all();
+    if (rank == 0) {
+      uint64_t v[4];
+      gather_bins(v, false);
+      find_bin(v, uint64_t(top_k));
+      tell(&told);
+    }
+    sync_all();
+    const uint32_t last = told.bin;
+    collect([&](float y, int) { return y > -INFINITY && bin_of(scale, y) <= last; });
+    if (rank == 0) {
+      const int n = gather_list();
+      if (n < 0) {
+        if (tid == 0) told.state = kTooMany;
+      } else {
+        cut_list(n, top_k, 0, true);
+        const int keep = n_keep;
+        // in the order of the indices: each token's sum before it
+        uint64_t w = 0, before = 0, all = 0;
+        const uint32_t index = tid < keep ? uint32_t(list[tid]) : 0;
+        if (tid < keep) w = weigh(logit_at(list[tid]));
+        uint64_t *weights = local;                       // (has been read)
+        if (tid < kSmallK) weights[tid] = w;
+        __syncthreads();
+        if (warp < kSmallK / 32)
+          for (int i = 0; i < keep; ++i) {
+            const uint64_t v = weights[i];
+            all += v;
+            if (uint32_t(list[i]) < index) before += v;
+          }
+        for (int d = 0; d < p.draws; ++d) {
+          float u = p.u[row * p.draws + d];
+          u = u >= 1.f ? 0x1.fffffep-1f : u;
+          bool exact;
+          const uint64_t want = part_of(u, all, exact);  // the first running sum above it
+          if (tid < keep && want >= before && want < before + w) p.tokens[row * p.draws + d] = int32_t(index);
+        }
+        if (tid == 0) {
+          const uint64_t e = list[keep - 1];
+          told = Found{last, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all};
+        }
+      }
+      tell(&told);
+    }
+    sync_all();
+    too_many = told.state == kTooMany;
+    if (!too_many) {
+      done = true;
+      x_f = logit_of<float>(told.code);
+      i_f = told.index;
+      whole = told.whole;
+    }
+  } else {
+    // A round: the last token by counts (kMass: weights) among what is kept so far.
+    auto round = [&](auto mass, uint64_t target) {
+      constexpr bool kMass = decltype(mass)::value;
+      clear_bins();
+      each([&](int r, const float (&y)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!kept(y[k], r + k)) continue;
+          if constexpr (kMass) {
+            const Weight<T> w(scale, powers, y[k]);
+            const uint32_t b = w.bin(), low = w.in_bin();
+            if (atomicAdd(bin_lo + b, low) + low < low) atomicAdd(bin_hi + b, 1u);
+          } else {
+            atomicAdd(bin_lo + bin_of(scale, y[k]), 1u);
+          }
+        }
+      });
+      sync_all();
+      if (rank == 0) {
+        uint64_t v[4];
+        gather_bins(v, kMass);
+        if constexpr (kMass) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = v[k] << up >> ((tid * 4 + k) >> 6);
+        }
+        find_bin(v, target);
+        tell(&told);
+      }
+      sync_all();
+      const Found f = told;
+      if (f.state == kAll) return;
+      if (kMass && f_min > -INFINITY && bin_of(scale, f_min) < f.bin) return;   // min-p ends it before
+      collect([&](float y, int r) { return kept(y, r) && bin_of(scale, y) == f.bin; });
+      if (rank == 0) {
+        const int n = gather_list();
+        if (n >= 0) {
+          if constexpr (kMass) cut_list(n, n, f.target, false);
+          else if (tid == 0) n_keep = int(f.target);
+          __syncthreads();
+        }
+        if (tid == 0) {
+          if (n < 0) told.state = kTooMany;
+          else if (n_keep == 0) told.state = kAll;       // min-p leaves out the whole bin
+          else {
+            const uint64_t e = list[n_keep - 1];
+            told.code = ~uint32_t(e >> 32);
+            told.index = int32_t(uint32_t(e));
+          }
+        }
+        tell(&told);
+      }
+      sync_all();
+      if (told.state == kTooMany) too_many = true;
+      else if (told.state == kGo) {
+        x_f = logit_of<float>(told.code);
+        i_f = told.index;
+      }
+    };
+    if (top_k > 0 && top_k < p.V) round(std::false_type{}, uint64_t(top_k));
+    if (!too_many && top_p < 1.f) round(std::true_type{}, 0);
+  }
+  if (too_many) {
+    // ------------------------------------------------- any row, by codes alone
+    // Looks for the logit at which the running count (kMass: weight) of the order reaches the
+    // target, among those above `floor`; kMass: the target is top_p of their sum and
+    // `beyond`, the weight of what is kept of those equal to the floor.
+    auto search = [&](auto mass, float floor, uint64_t target, uint64_t beyond) {
+      constexpr bool kMass = decltype(mass)::value;
+      Search s;
+      s.hi = code_of<T>(top);
+      s.lo = code_of<T>(floor) + 1;
+      s.shift = shift_for(s.hi - s.lo);
+      s.target = target;
+      s.done = 0;
+      bool first = true;
+      while (true) {
+        clear_bins();
+        each([&](int, const float (&y)[8]) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t code = code_of<T>(y[k]);
+            if (code > s.hi || code < s.lo) continue;
+            const uint32_t b = min((s.hi - code) >> s.shift, uint32_t(kBins - 1));
+            if constexpr (kMass) {
+              const uint64_t w = weigh(y[k]);
+              const uint32_t low = uint32_t(w);
+              const uint32_t more = uint32_t(w >> 32) + (atomicAdd(bin_lo + b, low) + low < low);
+              if (more) atomicAdd(bin_hi + b, more);
+            } else {
+              atomicAdd(bin_lo + b, 1u);
+            }
+          }
+        });
+        sync_all();
+        if (rank == 0) {
+          uint64_t v[4], all;
+          gather_bins(v, kMass);
+          const uint64_t sum = v[0] + v[1] + v[2] + v[3], run = scan_block(sum, all);
+          uint64_t before = run - sum;
+          Search next = s;
+          if (kMass && first) {
+            bool exact;
+            next.target = part_of(top_p, all + beyond, exact);
+            next.target = max(next.target + !exact, uint64_t(1));
+          }
+          if (next.target > all) {
+            if (tid == 0) {
+              next.done = 2;
+              next.target -= all;
+              told_search = next;
+            }
+          } else if (before < next.target && next.target <= run) {
+            uint32_t b = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < 3; ++k)
+              if (b == k && before + v[k] < next.target) {
+                before += v[k];
+                ++b;
+              }
+            const uint32_t bin = uint32_t(tid) * 4 + b;
+            next.target -= before;
+            const uint32_t above = s.hi - (bin << s.shift);
+            if (bin < kBins - 1) {
+              next.done = s.shift == 0;
+              next.lo = max(s.lo, above - ((1u << s.shift) - 1));
+            }
+            next.hi = above;
+            next.shift = shift_for(next.hi - next.lo);
+            if (next.done) {
+              const uint64_t w = kMass ? weigh(logit_of<T>(above)) : 1;
+              next.ties = (next.target + w - 1) / w;
+            }
+            told_search = next;
+          }
+          tell(&told_search);
+        }
+        sync_all();
+        s = told_search;
+        first = false;
+        if (s.done) return s;
+        sync_all();                                      // (it is read before it is written again)
+      }
+    };
+    x_f = -INFINITY;
+    uint64_t ties = 0;                                   // how many equal to x_f are kept
+    if (top_k > 0 && top_k < p.V) {
+      const Search s = search(std::false_type{}, -INFINITY, uint64_t(top_k), 0);
+      if (s.done == 1) {
+        x_f = logit_of<T>(s.hi);
+        ties = s.ties;
+      }
+      sync_all();
+    }
+    if (top_p < 1.f) {
+      const uint64_t w = ties ? weigh(x_f) : 0;
+      const Search s = search(std::true_type{}, x_f, 0, ties * w);
+      if (s.done == 1) {
+        x_f = logit_of<T>(s.hi);
+        ties = s.ties;
+      } else if (w) {
+        ties = min(ties, (s.target + w - 1) / w);
+      }
+    }
+    // the index of the last of them
+    uint32_t n = 0;
+    each([&](int, const float (&y)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) n += y[k] == x_f && y[k] > -INFINITY;
+    });
+    n = __reduce_add_sync(~0u, n);
+    if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, n, 0);
+    sync_all();
+    uint64_t before = 0;
+    for (int i = lane; i < int(rank) * kDrawWarps + warp; i += 32) before += sums[i].x;
+#pragma unroll
+    for (int w = 16; w; w /= 2) before += __shfl_xor_sync(~0u, before, w);
+    if (ties > before && ties <= before + n) {
+      uint32_t left = uint32_t(ties - before);
+      each([&](int r, const float (&y)[8]) {
+        uint32_t here = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) here += y[k] == x_f;
+        uint32_t run = uint32_t(scan_up(here, lane));
+        const uint32_t all = __shfl_sync(~0u, run, 31);
+        run -= here;
+        if (left && run < left && left <= run + here)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (y[k] == x_f && ++run == left) {
+              for (uint32_t b = 0; b < blocks; ++b) cluster_store(&told.target, b, uint64_t(uint32_t(r + k)), 0);
+            }
+        left = left > all ? left - all : 0;
+      });
+    }
+    sync_all();
+    i_f = ties ? int(told.target) : -1;
+    sync_all();                                          // (sums are read before they are written again)
+  }
+  if (!done) {
+    if (f_min > x_f) {
+      x_f = f_min;
+      i_f = INT32_MAX;
+    }
+    // -------------------------------------------------------------- the draw
+    uint64_t mass = 0;
+    each([&](int r, const float (&y)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (kept(y[k], r + k)) mass += weigh(y[k]);
+    });
+#pragma unroll
+    for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
+    if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, mass, 0);
+    sync_all();
+    uint64_t my_mass = 0;                                // of the warps before this one
+    for (int i = lane; i < entries; i += 32) {
+      whole += sums[i].x;
+      my_mass += i < int(rank) * kDrawWarps + warp ? sums[i].x : 0;
+    }
+#pragma unroll
+    for (int w = 16; w; w /= 2) {
+      whole += __shfl_xor_sync(~0u, whole, w);
+      my_mass += __shfl_xor_sync(~0u, my_mass, w);
+    }
+    for (int d = 0; d < p.draws; ++d) {
+      float u = p.u[row * p.draws + d];
+      u = u >= 1.f ? 0x1.fffffep-1f : u;
+      bool exact;
+      const uint64_t want = part_of(u, whole, exact);    // the first running sum above it
+      if (want < my_mass || want >= my_mass + mass) continue;
+      uint64_t run = my_mass;
+      bool found = false;
+      each([&](int r, const float (&y)[8]) {
+        if (found) return;
+        uint64_t sum = 0, each_w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          each_w[k] = kept(y[k], r + k) ? weigh(y[k]) : 0;
+          sum += each_w[k];
+        }
+        const uint64_t to = scan_up(sum, lane);
+        uint64_t from = run + to - sum;
+        if (want >= from && want < run + to) {
+          int at8 = 0;
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            if (at8 == k && want >= from + each_w[k]) {
+              from += each_w[k];
+              ++at8;
+            }
+          p.tokens[row * p.draws + d] = r + at8;
+        }
+        run += __shfl_sync(~0u, to, 31);
+        found = run > want;
+      });
+    }
+  }
+  if (!out) return;
+  // ------------------------------------------------------- the distribution
+  const float c = scale.c * (1.f / 32), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
+  each([&](int r, const float (&y)[8]) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = kept(y[k], r + k) ? (y[k] == top ? 1.f : ex2((y[k] - top) * c)) * inv : 0.f;
+    store(r, v);
   });
 }
 
@@ -555,9 +867,8 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   static std::atomic<uint64_t> allowed[2];
   const bool held = share <= kDrawShareMax;
   void (*fn)(DrawParams) = held ? &sample_kernel<T, true> : &sample_kernel<T, false>;
-  constexpr int kBinBytes = 2 * kBins * 4;
-  if (const cudaError_t e = allow(fn, kBinBytes + (held ? kDrawShareMax : 0), allowed[held])) return e;
-  return launch_clusters(fn, unsigned(rows) * unsigned(c), kDrawThreads, c, kBinBytes + (held ? int(share) : 0), st, p);
+    if (const cudaError_t e = allow(fn, kListBytes + (held ? kDrawShareMax : 0), allowed[held])) return e;
+  return launch_clusters(fn, unsigned(rows) * unsigned(c), kDrawThreads, c, kListBytes + (held ? int(share) : 0), st, p);
 }
 
 }  // namespace
