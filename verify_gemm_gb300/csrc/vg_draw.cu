@@ -18,10 +18,9 @@
 // each warp a run of that, so that the warps' order is the index order.  The
 // last token is looked for in two steps: a histogram over z, 2048 bins of 1/64 of
 // an octave, says in which bin it lies (of counts for top-k, of weights for
-// top-p), and the tokens of that bin alone are sorted.  Up to 256 tokens of
-// top-k are found from each thread's largest logit alone: the k-th largest of
-// those is at most the k-th largest of all, so that all that is kept, and little
-// else, lies in the bins down to it.
+// top-p), and the tokens of that bin alone are sorted.  A top-k up to 200 goes without: all
+// blocks know the largest logits of 256 groups of a row's threads, the k-th largest of those is
+// at most the k-th largest of all, and the tokens down to it, few more than k, are sorted.
 #include <algorithm>
 #include <cmath>
 
@@ -35,10 +34,17 @@ constexpr int kBins = 2048;
 constexpr int kDrawShare = 76 * 1024;         // bytes of a row a block should hold at most ...
 constexpr int kDrawShareMax = 160 * 1024;     // ... and may
 constexpr int kLocal = 1024, kSorted = 2048;  // tokens of a block, of the row, that a list holds
-constexpr int kSmallK = 256;
-constexpr int kByThread = 16384;              // from this vocabulary on each thread's largest stands for its logits
+constexpr int kGroups = 256;                  // of which the largest logit is known to all blocks
+static_assert(kMaxCluster * kDrawWarps == kGroups, "at least one group a warp");
+constexpr int kSmallK = 200;
 constexpr int kListBytes = (kLocal + kSorted) * 8;   // (and the bins, which are read before a list is made)
 static_assert(kListBytes >= 2 * kBins * 4, "room for the bins");
+
+template <typename T>
+struct alignas(2 * sizeof(T)) Pair {
+  T x[2];
+};
+__device__ __forceinline__ float to_f(float x) { return x; }
 
 struct DrawParams {
   const void *x;
@@ -62,49 +68,64 @@ struct Scale {
   float top, c, c_low, cap;          // c as two floats; differences beyond cap weigh nothing
 };
 
-// The weight of logit x is w 2^(up - (bin >> 6)) (up = bits - 30, and w some 2^30).  With
+// a + b, a * b + c, two at a time (mul2 and add2 are those of vg_rows.cuh).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The weight of a finite logit x is w 2^(up - (bin >> 6)) (up = bits - 30, and w some 2^30).  With
 // z = (k + r) / 32, k whole, |r| <= 1/2, it is 2^-(k / 32) from a table times
 // 2^-(r / 32) by its series.  max - x is exact in FP32 for 16-bit logits but for
 // those that are 2^-16 of the largest or less; for FP32 ones what it loses is
 // carried along.  The bin is z in units of 1/64: the larger logit never has the
 // larger bin, as it goes by the rounded difference alone.
-template <typename T>
+constexpr float kMagic = 12582912.f;           // 1.5 2^23: what is added to it is rounded to a whole number
 struct Weight {
   int w, k, half;
-  __device__ __forceinline__ Weight(const Scale &s, const uint32_t *powers, float x) {
-    constexpr float kMagic = 12582912.f;       // 1.5 2^23: what is added to it is rounded to a whole number
-    const float d = fminf(s.top - x, s.cap);
-    float low = d * s.c_low;
-    if constexpr (std::is_same_v<T, float>) {
-      const float a = s.top - x, b = a - s.top;
-      const float e = (s.top - (a - b)) + (-x - b);
-      low = a < s.cap ? fmaf(e, s.c, low) : low;
-    }
-    const float t = fmaf(d, s.c, kMagic);
-    k = __float_as_int(t) - __float_as_int(kMagic);
-    float r = fmaf(d, s.c, -(t - kMagic));
-    half = r >= 0.f;
-    r += low;
-    // 2^28 (2^-(r / 32) - 1)
-    float q = fmaf(r, 2.46224105f, -454.689658f);
-    q = fmaf(r, q, 62973.9374f);
-    q = fmaf(r, q, -5814539.98f);
-    const int f = __float_as_int(fmaf(r, q, kMagic)) - __float_as_int(kMagic);
-    const int p = int(powers[k & 31]);
-    w = p + __mulhi(p, f << 4);
-    if (x == -INFINITY) k = 2048;
-  }
   __device__ __forceinline__ uint64_t value(int up) const { return uint64_t(uint32_t(w)) << up >> min(k >> 5, 63); }
   __device__ __forceinline__ uint32_t bin() const { return min(uint32_t(2 * k + half), uint32_t(kBins - 1)); }
   // w in the units of its bin: the last one has all weights below 2^-32
   __device__ __forceinline__ uint32_t in_bin() const { return uint32_t(w) >> min(max((k >> 5) - 31, 0), 31); }
 };
+// Of two logits at a time.
+template <typename T>
+__device__ __forceinline__ void weigh2(const Scale &s, const uint32_t *powers, float x0, float x1, Weight &w0, Weight &w1) {
+  const float2 x = make_float2(-x0, -x1), all = add2(both(s.top), x);
+  const float2 d = make_float2(fminf(all.x, s.cap), fminf(all.y, s.cap));
+  float2 low = mul2(d, both(s.c_low));
+  if constexpr (std::is_same_v<T, float>) {
+    const float2 b = add2(all, both(-s.top)), c = add2(all, make_float2(-b.x, -b.y));
+    const float2 e = add2(add2(both(s.top), make_float2(-c.x, -c.y)), add2(x, make_float2(-b.x, -b.y)));
+    const float2 more = fma2(e, both(s.c), low);
+    low = make_float2(all.x < s.cap ? more.x : low.x, all.y < s.cap ? more.y : low.y);
+  }
+  const float2 t = fma2(d, both(s.c), both(kMagic)), whole = add2(t, both(-kMagic));
+  const float2 r0 = fma2(d, both(s.c), make_float2(-whole.x, -whole.y)), r = add2(r0, low);
+  // 2^28 (2^-(r / 32) - 1)
+  float2 q = fma2(r, both(2.46224105f), both(-454.689658f));
+  q = fma2(r, q, both(62973.9374f));
+  q = fma2(r, q, both(-5814539.98f));
+  q = fma2(r, q, both(kMagic));
+  auto one = [&](Weight &w, float t, float r0, float q) {
+    w.k = __float_as_int(t) - __float_as_int(kMagic);
+    w.half = r0 >= 0.f;
+    const int f = __float_as_int(q) - __float_as_int(kMagic), p = int(powers[w.k & 31]);
+    w.w = p + __mulhi(p, f << 4);
+  };
+  one(w0, t.x, r0.x, q.x);
+  one(w1, t.y, r0.y, q.y);
+}
 // Its bin alone.
 __device__ __forceinline__ uint32_t bin_of(const Scale &s, float x) {
-  constexpr float kMagic = 12582912.f;
   const float d = fminf(s.top - x, s.cap), t = fmaf(d, s.c, kMagic);
   const int k = __float_as_int(t) - __float_as_int(kMagic);
-  return x == -INFINITY ? kBins - 1 : min(uint32_t(2 * k + (fmaf(d, s.c, -(t - kMagic)) >= 0.f)), uint32_t(kBins - 1));
+  return min(uint32_t(2 * k + (fmaf(d, s.c, -(t - kMagic)) >= 0.f)), uint32_t(kBins - 1));
 }
 
 // Logits' codes in their order; logits of 16 bits have as many codes.
@@ -112,7 +133,7 @@ template <typename T>
 constexpr int kCodeShift = std::is_same_v<T, float> ? 0 : std::is_same_v<T, __half> ? 13 : 16;
 template <typename T>
 __device__ __forceinline__ uint32_t code_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);           // (-0 is 0)
   return (b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) >> kCodeShift<T>;
 }
 template <typename T>
@@ -152,12 +173,15 @@ __device__ __forceinline__ uint64_t scan_up(uint64_t v, int lane) {
 }
 
 // Sorts n (a power of two, at least 64) entries, the smallest first; the whole block.
+// A thread holds entries 2 t and 2 t + 1 of every 1024: exchanges within a warp's 64
+// entries go by shuffles, the others by shared memory.
+__device__ __forceinline__ uint64_t other(uint64_t v, int lanes) { return __shfl_xor_sync(~0u, v, lanes); }
 __device__ __forceinline__ void sort_up(uint64_t *v, int n) {
-  for (int size = 2; size <= n; size *= 2)
-    for (int stride = size / 2; stride; stride /= 2) {
-      // (pairs at most 32 apart stay within a warp's 64 entries)
-      if (stride > 16) __syncthreads();
-      else __syncwarp();
+#pragma unroll 1
+  for (int size = 64; size <= n; size *= 2) {
+#pragma unroll 1
+    for (int stride = size / 2; stride >= 64; stride /= 2) {
+      __syncthreads();
       for (int q = threadIdx.x; q < n / 2; q += kDrawThreads) {
         const int a = 2 * q - (q & (stride - 1)), b = a + stride;
         const uint64_t x = v[a], y = v[b];
@@ -167,6 +191,28 @@ __device__ __forceinline__ void sort_up(uint64_t *v, int n) {
         }
       }
     }
+    __syncthreads();
+    for (int at = 2 * int(threadIdx.x); at < n; at += 2 * kDrawThreads) {   // (whole warps)
+      uint64_t a = v[at], b = v[at + 1];
+      // the first time all sizes up to 64, then this one's last strides
+#pragma unroll 1
+      for (int inner = size == 64 ? 2 : size; inner <= size; inner *= 2) {
+        const bool up = (at & inner) == 0;
+#pragma unroll 1
+        for (int lanes = min(inner, 64) / 4; lanes; lanes /= 2) {
+          const uint64_t x = other(a, lanes), y = other(b, lanes);
+          const bool small = ((threadIdx.x & lanes) == 0) == up;
+          a = (x < a) == small ? x : a;
+          b = (y < b) == small ? y : b;
+        }
+        const uint64_t x = a < b ? a : b, y = a < b ? b : a;
+        a = up ? x : y;
+        b = up ? y : x;
+      }
+      v[at] = a;
+      v[at + 1] = b;
+    }
+  }
   __syncthreads();
 }
 
@@ -175,6 +221,8 @@ struct Found {
   uint32_t bin, code;                // the last token's bin; its logit
   int32_t index, state;              // its index
   uint64_t target, whole;            // the count or weight wanted of the bin; the weight of what is kept
+  float from, to;                    // the bin's logits
+  uint64_t pad;
 };
 enum { kGo = 0, kAll = 1, kTooMany = 2 };      // state; kAll: nothing is left out
 // Where a search by codes is: codes [lo, hi], bins of 2^shift of them from hi down, the last
@@ -182,7 +230,7 @@ enum { kGo = 0, kAll = 1, kTooMany = 2 };      // state; kAll: nothing is left o
 struct Search {
   uint32_t hi, lo;
   int shift, done;                   // 1: hi is the code, 2: there are fewer
-  uint64_t target, ties;             // ties: of the code
+  uint64_t target, ties;             // ties: how many of the code
 };
 __device__ __forceinline__ int shift_for(uint32_t span) {
   // the smallest with span >> shift below the last bin
@@ -193,10 +241,10 @@ __device__ __forceinline__ int shift_for(uint32_t span) {
 template <typename T, bool kHeld>
 __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_constant__ DrawParams p) {
   extern __shared__ __align__(16) uint8_t draw_smem[];
-  __shared__ __align__(16) ulonglong2 tops[kMaxCluster * kDrawWarps];
+  __shared__ float tops[kGroups];
   __shared__ __align__(16) ulonglong2 sums[kMaxCluster * kDrawWarps];
   __shared__ __align__(16) Found told;
-  __shared__ __align__(16) Search told_search;
+  __shared__ __align__(16) ulonglong2 shares[kMaxCluster];
   __shared__ uint32_t powers[32];
   __shared__ Scale told_scale;
   __shared__ double min_at;          // T ln(min_p)
@@ -215,19 +263,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   const int64_t w0 = lo / 8 + int64_t(rank * kDrawWarps + warp) * p.chunk;
   const int mine = int(max(int64_t(0), min(int64_t(p.chunk), end - w0)));   // units of this warp
   if (blocks > 1) cluster_arrive();                      // a block must have begun before others write to it
-  constexpr int kPart = sizeof(T) / 2;
-  const int part = kDrawWarps * p.chunk;                 // 16-byte parts of a unit lie apart
-  uint4 *at = held + warp * p.chunk;
+  uint4 *run = held + int64_t(warp) * p.chunk * (sizeof(T) / 2);
   if constexpr (kHeld) {
-    for (int i = lane; i < mine; i += 32) {
-      const int64_t e = (w0 + i) * 8;
-      if (e >= lo && e + 8 <= hi) {
-#pragma unroll
-        for (int k = 0; k < kPart; ++k) copy16(at + k * part + i, reinterpret_cast<const uint4 *>(x + e) + k);
+    constexpr int kEach = 16 / sizeof(T);                // logits of a 16-byte piece
+    for (int i = lane; i < mine * int(sizeof(T) / 2); i += 32) {
+      const int64_t e = w0 * 8 + i * kEach;
+      if (e >= lo && e + kEach <= hi) {
+        copy16(run + i, x + e);
       } else {
-        const Unit<T> v = load_unit(x, w0 + i, lo, hi);
+        T t[kEach];
 #pragma unroll
-        for (int k = 0; k < kPart; ++k) at[k * part + i] = v.w[k];
+        for (int k = 0; k < kEach; ++k) t[k] = e + k >= lo && e + k < hi ? x[e + k] : T(-INFINITY);
+        memcpy(run + i, t, 16);
       }
     }
   }
@@ -246,36 +293,39 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
                                                               : double(temperature) * log(double(min_p));
     }
   }
-  if constexpr (kHeld) asm volatile("cp.async.wait_all;" ::: "memory");   // a thread reads only what it copied
-  auto unit = [&](int i) {
+  if constexpr (kHeld) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();                                        // a warp reads only what it copied
+  }
+  const int64_t base = w0 * 8 - lo;                      // index of the warp's first element in the row
+  // logits 2 j and 2 j + 1 of the warp's run as they came, -infinity beside the row
+  auto pair_at = [&](int j) {
     if constexpr (kHeld) {
-      Unit<T> v;
-#pragma unroll
-      for (int k = 0; k < kPart; ++k) v.w[k] = at[k * part + i];
-      return v;
+      return reinterpret_cast<const Pair<T> *>(run)[j];
     } else {
-      return load_unit(x, w0 + i, lo, hi);
+      Pair<T> v;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t e = w0 * 8 + 2 * j + k;
+        v.x[k] = e >= lo && e < hi ? x[e] : T(-INFINITY);
+      }
+      return v;
     }
   };
-  const int64_t base = w0 * 8 - lo;                      // index of the warp's first element in the row
-  // f(index of the first, 8 logits, 0 for -0), over the warp's run; all lanes come along
+  // f(index of the first, two logits), over the warp's run; all lanes come along.
+  // (Two at a time, and not the eight of a 16-byte piece: a row passes here but a
+  // few times, and what the code of eight takes to be fetched is more than it saves.)
   auto each = [&](auto &&f) {
-#pragma unroll 1
-    for (int i0 = 0; i0 < mine; i0 += 32) {
-      const int i = i0 + lane;
-      float y[8];
-      if (i < mine) {
-        const Unit<T> v = unit(i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[2 * k] = v.pair(k).x + 0.f;
-          y[2 * k + 1] = v.pair(k).y + 0.f;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = -INFINITY;
+#pragma unroll 2
+    for (int j0 = 0; j0 < mine * 4; j0 += 32) {
+      const int j = j0 + lane;
+      float a = -INFINITY, b = -INFINITY;
+      if (j < mine * 4) {
+        const Pair<T> v = pair_at(j);
+        a = to_f(v.x[0]);
+        b = to_f(v.x[1]);
       }
-      f(int(base) + i * 8, y);
+      f(int(base) + 2 * j, a, b);
     }
   };
   auto sync_all = [&] {
@@ -284,18 +334,33 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   };
 
   // ------------------------------------------------------------- the largest
-  Largest<T> largest;
-  for (int i = lane; i < mine; i += 32) largest.take(unit(i));
-  const float my_top = largest.value();
-  float m = my_top;
-#pragma unroll
-  for (int w = 16; w; w /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, w));
-  if (blocks > 1) cluster_wait();
-  if (lane < int(blocks)) cluster_store(&tops[rank * kDrawWarps + warp], lane, __float_as_uint(m), 0);
+  // Of each of 256 groups of threads: 16 / blocks in each warp.  All blocks get them all.
+  float m = -INFINITY;
+  for (int j = lane; j < mine * 4; j += 32) {
+    const Pair<T> v = pair_at(j);
+    m = max_nan(m, max_nan(to_f(v.x[0]), to_f(v.x[1])));
+  }
+  const int groups = kGroups / kDrawWarps / int(blocks), wide = 32 / groups;
+  for (int w = wide / 2; w; w /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, w));
+  {
+    const float v = __shfl_sync(~0u, m, lane % groups * wide);
+    if (blocks > 1) cluster_wait();
+    if (lane < kGroups / kDrawWarps) {
+      float *to = tops + (rank * kDrawWarps + warp) * groups + lane % groups;
+      asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %0, %1; st.shared::cluster.f32 [at], %2; }" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                   "r"(lane / groups), "f"(v)
+                   : "memory");
+    }
+  }
   sync_all();
   const int entries = int(blocks) * kDrawWarps;
-  float top = -INFINITY;
-  for (int i = lane; i < entries; i += 32) top = max_nan(top, __uint_as_float(uint32_t(tops[i].x)));
+  float top = -INFINITY, its[kGroups / 32];
+#pragma unroll
+  for (int i = 0; i < kGroups / 32; ++i) {
+    its[i] = tops[i * 32 + lane];
+    top = max_nan(top, its[i]);
+  }
 #pragma unroll
   for (int w = 16; w; w /= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, w));
   top += 0.f;
@@ -312,30 +377,24 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     return;
   }
-  // stores the 8 probabilities v of elements r .. r + 7
-  const bool aligned = ((row * p.V + base) & 3) == 0;
-  auto store = [&](int r, const float (&v)[8]) {
-    if (r - int(base) >= mine * 8) return;
-    if (aligned && r >= 0 && r + 8 <= p.V) {
-      float4 *to = reinterpret_cast<float4 *>(out + r);
-      __stcs(to, make_float4(v[0], v[1], v[2], v[3]));
-      __stcs(to + 1, make_float4(v[4], v[5], v[6], v[7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (r + k >= 0 && r + k < p.V) out[r + k] = v[k];
+  // stores the probabilities of elements r and r + 1
+  const bool aligned = ((row * p.V + base) & 1) == 0;
+  auto store = [&](int r, float a, float b) {
+    if (aligned && r >= 0 && r + 2 <= p.V && r - int(base) < mine * 8) {
+      __stcs(reinterpret_cast<float2 *>(out + r), make_float2(a, b));
+    } else if (r - int(base) < mine * 8) {
+      if (r >= 0 && r < p.V) out[r] = a;
+      if (r + 1 >= 0 && r + 1 < p.V) out[r + 1] = b;
     }
   };
 
   // ---------------------------------------------------- the first largest alone
   if (cold || top_k == 1 || top_p <= 0.f || min_p > 1.f) {
     int first = INT32_MAX;
-    if (m == top)                                        // (this warp's largest)
-      each([&](int r, const float (&y)[8]) {
-#pragma unroll
-        for (int k = 7; k >= 0; --k)
-          if (y[k] == top) first = min(first, r + k);
-      });
+    each([&](int r, float a, float b) {
+      if (b == top) first = min(first, r + 1);
+      if (a == top) first = min(first, r);
+    });
     first = __reduce_min_sync(~0u, first);
     if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, uint32_t(first), 0);
     sync_all();
@@ -345,18 +404,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     if (rank == 0)
       for (int i = tid; i < p.draws; i += kDrawThreads) p.tokens[row * p.draws + i] = first;
     if (out)
-      each([&](int r, const float (&)[8]) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = r + k == first ? 1.f : 0.f;
-        store(r, v);
-      });
+      each([&](int r, float, float) { store(r, r == first ? 1.f : 0.f, r + 1 == first ? 1.f : 0.f); });
     return;
   }
   Scale scale = told_scale;
   scale.top = top;
   const int up = p.bits - 30;
-  auto weigh = [&](float y) { return Weight<T>(scale, powers, y).value(up); };
+  auto weigh = [&](float y) {
+    Weight a, b;
+    weigh2<T>(scale, powers, y, y, a, b);
+    return a.value(up);
+  };
 
   // What is kept: y > x_f, and those equal to it up to index i_f.
   float x_f = -INFINITY;
@@ -376,62 +434,106 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     return run;
   };
-  // Tells all blocks what the first one's thread 0 has put into `what`.
+  // Tells the other blocks what this one has put into `what`.
   auto tell = [&](auto *what) {
     static_assert(sizeof(*what) % 16 == 0, "goes by 16 bytes");
     __syncthreads();
-    if (blocks > 1 && tid && tid < int(blocks)) {
+    if (tid < int(blocks) && tid != int(rank)) {
       const uint64_t *from = reinterpret_cast<const uint64_t *>(what);
 #pragma unroll
       for (int k = 0; k < int(sizeof(*what) / 16); ++k)
         cluster_store(reinterpret_cast<ulonglong2 *>(what) + k, uint32_t(tid), from[2 * k], from[2 * k + 1]);
     }
   };
-  // Four bins a thread, of all blocks.
-  auto gather_bins = [&](uint64_t (&v)[4], bool both) {
-    static_assert(kBins == 4 * kDrawThreads, "four bins a thread");
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = 0;
-    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(bin_lo + tid * 4));
-#pragma unroll 4
-    for (uint32_t r = 0; r < blocks; ++r) {
-      uint32_t a[4], b[4] = {};
+  // Which bin the running sum over all blocks' bins reaches the target in (0: of top_p of the
+  // whole and `beyond`); kWeights: the bins have two words, kScaled: and a unit each.  A block
+  // adds up a share of the bins, four a lane, one block's a lane, and the block whose share holds the
+  // target tells the others.  (One block that took all bins of 16 blocks was at it for 5 us.)
+  auto find = [&](auto weights, auto scaled, uint64_t target, uint64_t beyond) {
+    sync_all();
+    const int quad = warp * (32 / int(blocks)) + lane / int(blocks), share = kBins / int(blocks);
+    const uint32_t bin0 = rank * share + quad * 4;
+    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(bin_lo + bin0));
+    uint32_t a[4], b[4] = {};
+    auto fetch = [&](uint32_t (&w)[4], uint32_t at) {
       asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %4, %5; ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [at]; }"
-                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                   : "r"(here), "r"(r)
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(at), "r"(lane % blocks)
                    : "memory");
-      if (both)
-        asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %4, %5; ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [at]; }"
-                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                     : "r"(here + kBins * 4), "r"(r)
-                     : "memory");
+    };
+    fetch(a, here);
+    if constexpr (decltype(weights)::value) fetch(b, here + kBins * 4);
+    uint64_t v[4], sum = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += uint64_t(b[k]) << 32 | a[k];
+    for (int k = 0; k < 4; ++k) v[k] = uint64_t(b[k]) << 32 | a[k];
+    for (uint32_t w = 1; w < blocks; w *= 2)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += other(v[k], int(w));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (decltype(scaled)::value) v[k] = v[k] << up >> (bin0 >> 6);
+      sum += v[k];
     }
-  };
-  // The first block's: which bin the running sum of v reaches the target in (0: of top_p of the whole).
-  auto find_bin = [&](const uint64_t (&v)[4], uint64_t target) {
-    const uint64_t sum = v[0] + v[1] + v[2] + v[3];
-    uint64_t whole;
-    const uint64_t run = scan_block(sum, whole);
-    uint64_t before = run - sum;
+    const bool counts = lane % blocks == 0;              // (all lanes of a quad have its sums)
+    uint64_t mine_all, run = scan_block(counts ? sum : 0, mine_all), whole = 0;
+    if (blocks > 1) {
+      if (tid < int(blocks)) cluster_store(&shares[rank], uint32_t(tid), mine_all, 0);
+      sync_all();
+      for (uint32_t r = 0; r < blocks; ++r) {
+        if (r < rank) run += shares[r].x;
+        whole += shares[r].x;
+      }
+    } else {
+      whole = mine_all;
+    }
+    Found f{};
+    f.whole = whole;
     if (target == 0) {
       bool exact;
-      target = part_of(top_p, whole, exact);
+      target = part_of(top_p, whole + beyond, exact);
       target = max(target + !exact, uint64_t(1));
     }
     if (target > whole) {
-      if (tid == 0) told = Found{kBins - 1, 0, -1, kAll, target - whole, whole};
-    } else if (before < target && target <= run) {
-      uint32_t b = 0;
+      f.state = kAll;
+      f.target = target - whole;
+      sync_all();                                        // (the shares are read before they are written again)
+      return f;
+    }
+    uint64_t before = run - sum;
+    const bool it = counts && before < target && target <= run;
+    if (it) {
+      uint32_t k0 = 0;
 #pragma unroll
       for (uint32_t k = 0; k < 3; ++k)
-        if (b == k && before + v[k] < target) {
+        if (k0 == k && before + v[k] < target) {
           before += v[k];
-          ++b;
+          ++k0;
         }
-      told = Found{uint32_t(tid) * 4 + b, 0, -1, kGo, target - before, whole};
+      f.bin = bin0 + k0;
+      f.state = kGo;
+      f.target = target - before;
+      told = f;
     }
+    if (__syncthreads_or(it)) {
+      // the bin's logits, [from, to): the smallest code whose bin is at most this, and the one before
+      if (warp < 2) {
+        const uint32_t bin = told.bin - warp;
+        uint32_t lo = code_of<float>(-INFINITY), hi = code_of<float>(top) + 1;   // not so; so, or top's next
+#pragma unroll 1
+        while (hi - lo > 1) {                          // 32 codes between at a time
+          const uint32_t step = (hi - lo) / 33 + 1, code = min(hi, lo + uint32_t(lane + 1) * step);
+          const uint32_t so = __ballot_sync(~0u, code == hi || bin_of(scale, logit_of<float>(code)) <= bin);
+          const uint32_t n = so ? uint32_t(__ffs(int(so)) - 1) : 32;
+          hi = min(hi, lo + (n + 1) * step);
+          lo = lo + n * step;
+        }
+        const bool none = warp && told.bin == 0;
+        if (lane == 0) (warp ? told.to : told.from) = none ? INFINITY : logit_of<float>(hi);
+      }
+      tell(&told);
+    }
+    sync_all();
+    return told;
   };
   auto clear_bins = [&] {
     for (int i = tid; i < 2 * kBins; i += kDrawThreads) bin_lo[i] = 0;
@@ -439,16 +541,19 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   };
   // Each block's tokens that `wanted` says to its list; the first block's `list` then has all
   // of them in order, and how many there are.
+  uint64_t *const to_list = blocks == 1 ? list : local;
+  const uint32_t room = blocks == 1 ? kSorted : kLocal;
   auto collect = [&](auto &&wanted) {
     if (tid == 0) listed = 0;
     __syncthreads();
-    each([&](int r, const float (&y)[8]) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (wanted(y[k], r + k)) {
-          const uint32_t at = atomicAdd(&listed, 1u);
-          if (at < kLocal) local[at] = uint64_t(~code_of<float>(y[k])) << 32 | uint32_t(r + k);
-        }
+    each([&](int r, float a, float b) {
+      const bool wa = wanted(a, r), wb = wanted(b, r + 1);
+      if (wa || wb) {
+        uint32_t at = atomicAdd(&listed, uint32_t(wa) + uint32_t(wb));
+        if (wa && at < room) to_list[at] = uint64_t(~code_of<float>(a)) << 32 | uint32_t(r);
+        at += wa;
+        if (wb && at < room) to_list[at] = uint64_t(~code_of<float>(b)) << 32 | uint32_t(r + 1);
+      }
     });
     sync_all();
   };
@@ -462,14 +567,14 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
                    : "memory");
     mine_at = uint32_t(scan_up(mine_n, lane)) - mine_n;
     n = __shfl_sync(~0u, mine_at + mine_n, 31);
-    if (n > kSorted || __any_sync(~0u, mine_n > kLocal)) return -1;
+    if (n > kSorted || __any_sync(~0u, mine_n > room)) return -1;
     int size = 64;
     while (size < int(n)) size *= 2;
     const uint32_t list_at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-    // a warp takes every 16th piece of 32 entries
-    for (uint32_t r = 0; r < blocks; ++r) {
+    if (blocks > 1) {                                    // a warp, or several, for each block
+      const uint32_t share = kDrawWarps / blocks, r = warp / share;
       const uint32_t count = __shfl_sync(~0u, mine_n, r), to = __shfl_sync(~0u, mine_at, r);
-      for (uint32_t i = tid; i < count; i += kDrawThreads) {
+      for (uint32_t i = warp % share * 32 + lane; i < count; i += share * 32) {
         uint64_t v;
         asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %1, %2; ld.shared::cluster.u64 %0, [at]; }"
                      : "=l"(v)
@@ -520,26 +625,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
 
   if (top_k > 0 && top_k <= kSmallK && top_k < p.V) {
     // ----------------------------------------------------------- a small top-k
-    clear_bins();
-    if (p.V >= kByThread) {
-      if (my_top > -INFINITY) atomicAdd(bin_lo + bin_of(scale, my_top), 1u);
-    } else {
-      each([&](int, const float (&y)[8]) {
+    // the upper 16 bits of the code of the top_k-th largest of the groups' largest
+    uint32_t least = 0;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit /= 2) {
+      uint32_t n = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (y[k] > -INFINITY) atomicAdd(bin_lo + bin_of(scale, y[k]), 1u);
-      });
+      for (int i = 0; i < kGroups / 32; ++i) n += code_of<float>(its[i]) >= (least | bit);
+      if (int(__reduce_add_sync(~0u, n)) >= top_k) least |= bit;
     }
-    sync_all();
-    if (rank == 0) {
-      uint64_t v[4];
-      gather_bins(v, false);
-      find_bin(v, uint64_t(top_k));
-      tell(&told);
-    }
-    sync_all();
-    const uint32_t last = told.bin;
-    collect([&](float y, int) { return y > -INFINITY && bin_of(scale, y) <= last; });
+    const float floor = least > code_of<float>(-INFINITY) ? logit_of<float>(least) : -3.4028234e38f;
+    collect([&](float y, int) { return y >= floor; });
     if (rank == 0) {
       const int n = gather_list();
       if (n < 0) {
@@ -552,9 +648,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         const uint32_t index = tid < keep ? uint32_t(list[tid]) : 0;
         if (tid < keep) w = weigh(logit_at(list[tid]));
         uint64_t *weights = local;                       // (has been read)
-        if (tid < kSmallK) weights[tid] = w;
+        if (tid < keep) weights[tid] = w;
         __syncthreads();
-        if (warp < kSmallK / 32)
+        if (warp * 32 < keep)
           for (int i = 0; i < keep; ++i) {
             const uint64_t v = weights[i];
             all += v;
@@ -569,7 +665,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         }
         if (tid == 0) {
           const uint64_t e = list[keep - 1];
-          told = Found{last, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all};
+          told = Found{0, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all, 0.f, 0.f, 0};
         }
       }
       tell(&told);
@@ -587,35 +683,27 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     auto round = [&](auto mass, uint64_t target) {
       constexpr bool kMass = decltype(mass)::value;
       clear_bins();
-      each([&](int r, const float (&y)[8]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (!kept(y[k], r + k)) continue;
-          if constexpr (kMass) {
-            const Weight<T> w(scale, powers, y[k]);
+      each([&](int r, float y0, float y1) {
+        const bool k0 = kept(y0, r), k1 = kept(y1, r + 1);
+        if constexpr (kMass) {
+          if (!k0 && !k1) return;
+          Weight w[2];
+          weigh2<T>(scale, powers, y0, y1, w[0], w[1]);
+          auto add = [&](const Weight &w) {
             const uint32_t b = w.bin(), low = w.in_bin();
             if (atomicAdd(bin_lo + b, low) + low < low) atomicAdd(bin_hi + b, 1u);
-          } else {
-            atomicAdd(bin_lo + bin_of(scale, y[k]), 1u);
-          }
+          };
+          if (k0) add(w[0]);
+          if (k1) add(w[1]);
+        } else {
+          if (k0) atomicAdd(bin_lo + bin_of(scale, y0), 1u);
+          if (k1) atomicAdd(bin_lo + bin_of(scale, y1), 1u);
         }
       });
-      sync_all();
-      if (rank == 0) {
-        uint64_t v[4];
-        gather_bins(v, kMass);
-        if constexpr (kMass) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = v[k] << up >> ((tid * 4 + k) >> 6);
-        }
-        find_bin(v, target);
-        tell(&told);
-      }
-      sync_all();
-      const Found f = told;
+      const Found f = find(mass, mass, target, 0);
       if (f.state == kAll) return;
-      if (kMass && f_min > -INFINITY && bin_of(scale, f_min) < f.bin) return;   // min-p ends it before
-      collect([&](float y, int r) { return kept(y, r) && bin_of(scale, y) == f.bin; });
+      if (kMass && f_min >= f.to) return;                // min-p ends it before
+      collect([&](float y, int r) { return y >= f.from && y < f.to && kept(y, r); });
       if (rank == 0) {
         const int n = gather_list();
         if (n >= 0) {
@@ -660,14 +748,15 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       bool first = true;
       while (true) {
         clear_bins();
-        each([&](int, const float (&y)[8]) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t code = code_of<T>(y[k]);
+        each([&](int, float y0, float y1) {
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            const float y = k ? y1 : y0;
+            const uint32_t code = code_of<T>(y);
             if (code > s.hi || code < s.lo) continue;
             const uint32_t b = min((s.hi - code) >> s.shift, uint32_t(kBins - 1));
             if constexpr (kMass) {
-              const uint64_t w = weigh(y[k]);
+              const uint64_t w = weigh(y);
               const uint32_t low = uint32_t(w);
               const uint32_t more = uint32_t(w >> 32) + (atomicAdd(bin_lo + b, low) + low < low);
               if (more) atomicAdd(bin_hi + b, more);
@@ -676,54 +765,24 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
             }
           }
         });
-        sync_all();
-        if (rank == 0) {
-          uint64_t v[4], all;
-          gather_bins(v, kMass);
-          const uint64_t sum = v[0] + v[1] + v[2] + v[3], run = scan_block(sum, all);
-          uint64_t before = run - sum;
-          Search next = s;
-          if (kMass && first) {
-            bool exact;
-            next.target = part_of(top_p, all + beyond, exact);
-            next.target = max(next.target + !exact, uint64_t(1));
-          }
-          if (next.target > all) {
-            if (tid == 0) {
-              next.done = 2;
-              next.target -= all;
-              told_search = next;
-            }
-          } else if (before < next.target && next.target <= run) {
-            uint32_t b = 0;
-#pragma unroll
-            for (uint32_t k = 0; k < 3; ++k)
-              if (b == k && before + v[k] < next.target) {
-                before += v[k];
-                ++b;
-              }
-            const uint32_t bin = uint32_t(tid) * 4 + b;
-            next.target -= before;
-            const uint32_t above = s.hi - (bin << s.shift);
-            if (bin < kBins - 1) {
-              next.done = s.shift == 0;
-              next.lo = max(s.lo, above - ((1u << s.shift) - 1));
-            }
-            next.hi = above;
-            next.shift = shift_for(next.hi - next.lo);
-            if (next.done) {
-              const uint64_t w = kMass ? weigh(logit_of<T>(above)) : 1;
-              next.ties = (next.target + w - 1) / w;
-            }
-            told_search = next;
-          }
-          tell(&told_search);
-        }
-        sync_all();
-        s = told_search;
+        const Found f = find(mass, std::false_type{}, first && kMass ? 0 : s.target, beyond);
         first = false;
-        if (s.done) return s;
-        sync_all();                                      // (it is read before it is written again)
+        s.target = f.target;
+        if (f.state == kAll) {
+          s.done = 2;
+          return s;
+        }
+        s.hi -= f.bin << s.shift;
+        if (f.bin < kBins - 1) {
+          s.done = s.shift == 0;
+          s.lo = max(s.lo, s.hi - ((1u << s.shift) - 1));
+        }
+        s.shift = shift_for(s.hi - s.lo);
+        if (s.done) {
+          const uint64_t w = kMass ? weigh(logit_of<T>(s.hi)) : 1;
+          s.ties = (s.target + w - 1) / w;
+          return s;
+        }
       }
     };
     x_f = -INFINITY;
@@ -734,7 +793,6 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         x_f = logit_of<T>(s.hi);
         ties = s.ties;
       }
-      sync_all();
     }
     if (top_p < 1.f) {
       const uint64_t w = ties ? weigh(x_f) : 0;
@@ -748,9 +806,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     // the index of the last of them
     uint32_t n = 0;
-    each([&](int, const float (&y)[8]) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) n += y[k] == x_f && y[k] > -INFINITY;
+    each([&](int, float a, float b) {
+      if (x_f > -INFINITY) n += uint32_t(a == x_f) + uint32_t(b == x_f);
     });
     n = __reduce_add_sync(~0u, n);
     if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, n, 0);
@@ -761,19 +818,15 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     for (int w = 16; w; w /= 2) before += __shfl_xor_sync(~0u, before, w);
     if (ties > before && ties <= before + n) {
       uint32_t left = uint32_t(ties - before);
-      each([&](int r, const float (&y)[8]) {
-        uint32_t here = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) here += y[k] == x_f;
+      each([&](int r, float a, float b) {
+        const uint32_t here = uint32_t(a == x_f) + uint32_t(b == x_f);
         uint32_t run = uint32_t(scan_up(here, lane));
         const uint32_t all = __shfl_sync(~0u, run, 31);
         run -= here;
-        if (left && run < left && left <= run + here)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (y[k] == x_f && ++run == left) {
-              for (uint32_t b = 0; b < blocks; ++b) cluster_store(&told.target, b, uint64_t(uint32_t(r + k)), 0);
-            }
+        if (left > run && left <= run + here) {
+          const int its_index = a == x_f && left == run + 1 ? r : r + 1;
+          for (uint32_t to = 0; to < blocks; ++to) cluster_store(&told.target, to, uint64_t(uint32_t(its_index)), 0);
+        }
         left = left > all ? left - all : 0;
       });
     }
@@ -788,10 +841,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     // -------------------------------------------------------------- the draw
     uint64_t mass = 0;
-    each([&](int r, const float (&y)[8]) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (kept(y[k], r + k)) mass += weigh(y[k]);
+    each([&](int r, float a, float b) {
+      const bool ka = kept(a, r), kb = kept(b, r + 1);
+      if (!ka && !kb) return;
+      Weight wa, wb;
+      weigh2<T>(scale, powers, a, b, wa, wb);
+      mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
     });
 #pragma unroll
     for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
@@ -815,26 +870,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (want < my_mass || want >= my_mass + mass) continue;
       uint64_t run = my_mass;
       bool found = false;
-      each([&](int r, const float (&y)[8]) {
+      each([&](int r, float a, float b) {
         if (found) return;
-        uint64_t sum = 0, each_w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          each_w[k] = kept(y[k], r + k) ? weigh(y[k]) : 0;
-          sum += each_w[k];
-        }
-        const uint64_t to = scan_up(sum, lane);
-        uint64_t from = run + to - sum;
-        if (want >= from && want < run + to) {
-          int at8 = 0;
-#pragma unroll
-          for (int k = 0; k < 7; ++k)
-            if (at8 == k && want >= from + each_w[k]) {
-              from += each_w[k];
-              ++at8;
-            }
-          p.tokens[row * p.draws + d] = r + at8;
-        }
+        Weight w0, w1;
+        weigh2<T>(scale, powers, a, b, w0, w1);
+        const uint64_t wa = kept(a, r) ? w0.value(up) : 0, sum = wa + (kept(b, r + 1) ? w1.value(up) : 0);
+        const uint64_t to = scan_up(sum, lane), from = run + to - sum;
+        if (want >= from && want < run + to) p.tokens[row * p.draws + d] = want < from + wa ? r : r + 1;
         run += __shfl_sync(~0u, to, 31);
         found = run > want;
       });
@@ -843,13 +885,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   if (!out) return;
   // ------------------------------------------------------- the distribution
   const float c = scale.c * (1.f / 32), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
-  each([&](int r, const float (&y)[8]) {
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = kept(y[k], r + k) ? (y[k] == top ? 1.f : ex2((y[k] - top) * c)) * inv : 0.f;
-    store(r, v);
-  });
+  auto share = [&](float y, int r) { return kept(y, r) ? (y == top ? 1.f : ex2((y - top) * c)) * inv : 0.f; };
+  each([&](int r, float a, float b) { store(r, share(a, r), share(b, r + 1)); });
 }
 
 template <typename T>
@@ -859,7 +896,7 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   while (c < 8 &&
          (units * size > int64_t(kDrawShare) * c || (rows * c < 2 * sms && units > kDrawThreads * c)))
     c *= 2;
-  if (c == 8 && (units * size > int64_t(kDrawShare) * c || (units > 8 * kDrawThreads && rows * 32 <= sms)))
+  if (c == 8 && (units * size > int64_t(kDrawShare) * c || (units > 8 * kDrawThreads && rows * 16 <= sms)))
     c = kMaxCluster;
   const int64_t warps = int64_t(c) * kDrawWarps;
   p.chunk = int((units + warps - 1) / warps);
