@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   if (warp == 0) {
     powers[lane] = kPowers[lane];
     if (lane == 0) {
+      listed = 0;
       const double c = 32 * 1.4426950408889634074 / double(temperature);
       told_scale.c = c > 3.4e38 ? 3.4028234e38f : float(c);
       told_scale.c_low = c > 3.4e38 ? 0.f : float(c - double(told_scale.c));
@@ -312,6 +313,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       return v;
     }
   };
+  auto unit_at = [&](int i) {
+    Unit<T> v;
+#pragma unroll
+    for (int k = 0; k < int(sizeof(T) / 2); ++k) v.w[k] = run[i * int(sizeof(T) / 2) + k];
+    return v;
+  };
   // f(index of the first, two logits), over the warp's run; all lanes come along.
   // (Two at a time, and not the eight of a 16-byte piece: a row passes here but a
   // few times, and what the code of eight takes to be fetched is more than it saves.)
@@ -336,9 +343,15 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   // ------------------------------------------------------------- the largest
   // Of each of 256 groups of threads: 16 / blocks in each warp.  All blocks get them all.
   float m = -INFINITY;
-  for (int j = lane; j < mine * 4; j += 32) {
-    const Pair<T> v = pair_at(j);
-    m = max_nan(m, max_nan(to_f(v.x[0]), to_f(v.x[1])));
+  if (kHeld && mine >= 32) {                             // (every thread has a unit)
+    Largest<T> largest;
+    for (int i = lane; i < mine; i += 32) largest.take(unit_at(i));
+    m = largest.value();
+  } else {
+    for (int j = lane; j < mine * 4; j += 32) {
+      const Pair<T> v = pair_at(j);
+      m = max_nan(m, max_nan(to_f(v.x[0]), to_f(v.x[1])));
+    }
   }
   const int groups = kGroups / kDrawWarps / int(blocks), wide = 32 / groups;
   for (int w = wide / 2; w; w /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, w));
@@ -537,25 +550,21 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   };
   auto clear_bins = [&] {
     for (int i = tid; i < 2 * kBins; i += kDrawThreads) bin_lo[i] = 0;
-    __syncthreads();
-  };
-  // Each block's tokens that `wanted` says to its list; the first block's `list` then has all
-  // of them in order, and how many there are.
-  uint64_t *const to_list = blocks == 1 ? list : local;
-  const uint32_t room = blocks == 1 ? kSorted : kLocal;
-  auto collect = [&](auto &&wanted) {
     if (tid == 0) listed = 0;
     __syncthreads();
-    each([&](int r, float a, float b) {
-      const bool wa = wanted(a, r), wb = wanted(b, r + 1);
-      if (wa || wb) {
-        uint32_t at = atomicAdd(&listed, uint32_t(wa) + uint32_t(wb));
-        if (wa && at < room) to_list[at] = uint64_t(~code_of<float>(a)) << 32 | uint32_t(r);
-        at += wa;
-        if (wb && at < room) to_list[at] = uint64_t(~code_of<float>(b)) << 32 | uint32_t(r + 1);
-      }
-    });
-    sync_all();
+  };
+  // Those of two tokens that `wanted` says go to the block's list; the first block's `list` then has
+  // all of the row's in order, and how many there are.
+  uint64_t *const to_list = blocks == 1 ? list : local;
+  const uint32_t room = blocks == 1 ? kSorted : kLocal;
+  auto push = [&](float a, float b, int r, auto &&wanted) {
+    const bool wa = wanted(a, r), wb = wanted(b, r + 1);
+    if (wa || wb) {
+      uint32_t at = atomicAdd(&listed, uint32_t(wa) + uint32_t(wb));
+      if (wa && at < room) to_list[at] = uint64_t(~code_of<float>(a)) << 32 | uint32_t(r);
+      at += wa;
+      if (wb && at < room) to_list[at] = uint64_t(~code_of<float>(b)) << 32 | uint32_t(r + 1);
+    }
   };
   auto gather_list = [&] {
     uint32_t n = 0, mine_at = 0, mine_n = 0;             // lane r: block r's
@@ -635,7 +644,22 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (int(__reduce_add_sync(~0u, n)) >= top_k) least |= bit;
     }
     const float floor = least > code_of<float>(-INFINITY) ? logit_of<float>(least) : -3.4028234e38f;
-    collect([&](float y, int) { return y >= floor; });
+    if (kHeld && mine >= 32) {
+      // (few units of eight have a logit that is wanted)
+      for (int i = lane; i < mine; i += 32) {
+        Largest<T> largest;
+        largest.take(unit_at(i));
+        if (!(largest.value() >= floor)) continue;
+#pragma unroll 1
+        for (int j = 4 * i; j < 4 * i + 4; ++j) {
+          const Pair<T> v = pair_at(j);
+          push(to_f(v.x[0]), to_f(v.x[1]), int(base) + 2 * j, [&](float y, int) { return y >= floor; });
+        }
+      }
+    } else {
+      each([&](int r, float a, float b) { push(a, b, r, [&](float y, int) { return y >= floor; }); });
+    }
+    sync_all();
     if (rank == 0) {
       const int n = gather_list();
       if (n < 0) {
@@ -703,7 +727,10 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       const Found f = find(mass, mass, target, 0);
       if (f.state == kAll) return;
       if (kMass && f_min >= f.to) return;                // min-p ends it before
-      collect([&](float y, int r) { return y >= f.from && y < f.to && kept(y, r); });
+      each([&](int r, float a, float b) {
+        push(a, b, r, [&](float y, int i) { return y >= f.from && y < f.to && kept(y, i); });
+      });
+      sync_all();
       if (rank == 0) {
         const int n = gather_list();
         if (n >= 0) {
@@ -892,12 +919,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
 template <typename T>
 cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) {
   const int64_t units = p.V / 8 + 2, size = 8 * sizeof(T);
+  // as few blocks a row as hold it, and more while all rows' fit the device at once (two a SM);
+  // 16, more than a portable cluster, for a few rows alone.
   int c = 1;
-  while (c < 8 &&
-         (units * size > int64_t(kDrawShare) * c || (rows * c < 2 * sms && units > kDrawThreads * c)))
-    c *= 2;
-  if (c == 8 && (units * size > int64_t(kDrawShare) * c || (units > 8 * kDrawThreads && rows * 16 <= sms)))
-    c = kMaxCluster;
+  auto more = [&] { return units * size > int64_t(kDrawShare) * c; };
+  while (c < 8 && (more() || (rows * c <= sms && units > kDrawThreads * c))) c *= 2;
+  if (c == 8 && (more() || (units > 8 * kDrawThreads && rows * 16 <= sms))) c = kMaxCluster;
   const int64_t warps = int64_t(c) * kDrawWarps;
   p.chunk = int((units + warps - 1) / warps);
   const int64_t share = int64_t(p.chunk) * kDrawWarps * size;
