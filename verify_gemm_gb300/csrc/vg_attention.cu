@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "vg_attention.cuh"
+#include "vg_prefix.h"
 
 namespace vg {
 namespace {
@@ -91,8 +92,9 @@ AttnParams params_of(const vg_attention_desc *d, const vg_kv_cache *cache, void 
   return p;
 }
 
-// One launch over p.batch sequences of p.n nodes.
-vg_status launch(AttnParams p, const Variant &v, int type, const vg_kv_cache *cache, int sms, vg_stream_t stream) {
+// One launch over p.batch sequences of p.n nodes; what it is cut into goes to p.
+vg_status launch(AttnParams &p, const Variant &v, int type, const vg_kv_cache *cache, int sms, vg_stream_t stream,
+                 int *blocks = nullptr) {
   p.rows = p.n * p.group;
   p.blocks = (p.rows + v.rows - 1) / v.rows;
   // What a unit costs beside its tiles, in tiles, and half of it as the cut that
@@ -117,15 +119,26 @@ vg_status launch(AttnParams p, const Variant &v, int type, const vg_kv_cache *ca
   std::memcpy(&kmap, cache->opaque, sizeof kmap);
   std::memcpy(&vmap, cache->opaque + kCacheMapWords, sizeof vmap);
   if (vg_status s = allow_smem(v)) return s;
-  v.fn<<<grid, v.threads, size_t(v.smem), as_cuda(stream)>>>(p, kmap, vmap);
-  VG_LAUNCH_CHECK();
+  if (blocks) *blocks = int(grid);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(v.threads));
+  cfg.dynamicSmemBytes = size_t(v.smem);
+  cfg.stream = as_cuda(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.pass == kOwn;
+  VG_CUDA(cudaLaunchKernelEx(&cfg, v.fn, p, kmap, vmap));
   return VG_OK;
 }
 
-// What prefix attention adds: the kernels of its two launches and their workspace.
+// Prefix attention: the kernels of its first two launches and the parts of its workspace.
+// (The two overlap: each has partial results of its own.)
 struct Behind {
   const Variant *prefix, *own;
-  size_t seed_at, bytes;             // the prefix's outputs in the workspace, and its whole
+  size_t partial, prefix_part, own_part, bytes;    // where: the prefix's partial results, both launches' results
 };
 vg_status behind_prefix(int n, int q_heads, const vg_kv_cache *cache, int sms, Behind &b) {
   const int group = q_heads / cache->heads, type = cache_type(*cache);
@@ -135,10 +148,13 @@ vg_status behind_prefix(int n, int q_heads, const vg_kv_cache *cache, int sms, B
     return VG_ERR_UNSUPPORTED;
   b.prefix = &pick(type, cache->head_dim, int(rows));
   b.own = &pick(type, cache->head_dim, n * group);
-  const size_t fixed = workspace_bytes_of(std::max(b.prefix->partial, b.own->partial), sms);
-  const size_t lse = (size_t(nodes) * size_t(q_heads) * sizeof(float) + 15) / 16 * 16;
-  b.seed_at = (fixed + 15) / 16 * 16;
-  b.bytes = b.seed_at + lse + size_t(nodes) * size_t(q_heads) * size_t(cache->head_dim) * sizeof(float);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t all = size_t(nodes) * size_t(q_heads);
+  const size_t part = up(all * size_t(cache->head_dim) * sizeof(float)) + up(all * sizeof(float));
+  b.partial = up(workspace_bytes_of(b.own->partial, sms));
+  b.prefix_part = up(b.partial + size_t(sms) * 2 * size_t(b.prefix->partial) * sizeof(float));
+  b.own_part = b.prefix_part + part;
+  b.bytes = b.own_part + part;
   return VG_OK;
 }
 
@@ -168,7 +184,8 @@ extern "C" vg_status vg_tree_attention(const vg_attention_desc *d, const vg_kv_c
   const Variant &v = pick(type, cache->head_dim, d->n * (d->q_heads / cache->heads));
   if (!workspace || workspace_bytes < workspace_bytes_of(v.partial, sms)) return VG_ERR_WORKSPACE;
   if (!aligned16(workspace)) return VG_ERR_ALIGNMENT;
-  return launch(params_of(d, cache, workspace), v, type, cache, sms, stream);
+  AttnParams p = params_of(d, cache, workspace);
+  return launch(p, v, type, cache, sms, stream);
 }
 
 extern "C" vg_status vg_prefix_attention_workspace_size(int n, int q_heads, const vg_kv_cache *cache,
@@ -201,12 +218,18 @@ extern "C" vg_status vg_prefix_attention(const vg_attention_desc *d, const vg_kv
   const int type = cache_type(*cache);
   AttnParams own = params_of(d, cache, workspace);
   if (max_prefix_pages == 0) return launch(own, *b.own, type, cache, sms, stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const int64_t all = int64_t(own.batch) * own.n * own.hq;
+  auto part_at = [&](AttnParams &p, size_t at) {
+    p.part = reinterpret_cast<float *>(ws + at);
+    p.part_lse = p.part + (all * p.d + 63) / 64 * 64;
+  };
   own.pass = kOwn;
   own.prefix = prefix;
   own.prefix_pages = max_prefix_pages;
-  own.seed_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.seed_at);
-  own.seed = own.seed_lse + (int64_t(own.batch) * own.n * own.hq + 3) / 4 * 4;
   AttnParams first = own;
+  part_at(own, b.own_part);
+  part_at(first, b.prefix_part);
   first.pass = kPrefix;
   first.inner = own.n;
   first.inner_magic = own.n == 1 ? 0 : uint32_t((uint64_t(1) << 32) / uint64_t(own.n)) + 1;
@@ -214,6 +237,17 @@ extern "C" vg_status vg_prefix_attention(const vg_attention_desc *d, const vg_kv
   first.n = own.batch * own.n;
   first.cache.table = prefix_pages;
   first.cache.table_stride = first.cache.max_pages = max_prefix_pages;
-  if (vg_status s = launch(first, *b.prefix, type, cache, sms, stream)) return s;
-  return launch(own, *b.own, type, cache, sms, stream);
+  first.partial = reinterpret_cast<float *>(ws + b.partial);
+  PrefixJoin j{};
+  if (vg_status s = launch(first, *b.prefix, type, cache, sms, stream, &j.grid)) return s;
+  if (vg_status s = launch(own, *b.own, type, cache, sms, stream)) return s;
+  j.wide = is_wide(own.d, first.rows);
+  j.e4m3 = type == kE4M3;
+  j.rows = b.prefix->rows;
+  j.partial = b.prefix->partial;
+  j.columns = (b.prefix->partial - 2 * j.rows) / j.rows;
+  j.state = j.rows * j.columns;
+  j.lift = type == kBf16 ? 0.f : j.wide ? 7.f : 15.f;
+  VG_CUDA(launch_prefix_join(own, first, j, as_cuda(stream)));
+  return VG_OK;
 }

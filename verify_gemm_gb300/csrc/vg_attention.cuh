@@ -92,16 +92,17 @@ struct AttnParams {
   int tile_log2;                    // keys of a tile
   int box, least, extra, snap;      // tokens of a TMA box; tiles: of a run at least, a unit costs, a cut moves
   float c, v_scale;                 // scale * k_scale * log2 e
-  // Attention behind a shared prefix (vg_prefix_attention) is two launches.  The
-  // first takes the prefix's whole pages as a sequence by themselves, whose nodes
-  // are those of the whole batch, and leaves each row's output and the log2 of
-  // its sum of exponentials in `seed`.  The second takes what each sequence has behind
-  // them and joins the two.  Without a prefix `pass` is kAlone.
+  // Attention behind a shared prefix (vg_prefix_attention) is three launches.  One
+  // takes the prefix's whole pages as a sequence by themselves, whose nodes are
+  // those of the whole batch; one takes what each sequence has behind them.  Both leave
+  // outputs in FP32 and the log2 of the sums of exponentials in `part` and
+  // `part_lse`, the first also the partial results of units that are cut; a third
+  // joins them (vg_prefix.cu).  Without a prefix `pass` is kAlone.
   int pass, inner;                  // kPrefix: nodes of a sequence of the batch
   uint32_t inner_magic;             // 2^32 / inner + 1
   const int32_t *prefix;            // tokens of the prefix
   int prefix_pages;                 // pages there are of it at most
-  float *seed, *seed_lse;           // [batch][n][hq][d], [batch][n][hq]
+  float *part, *part_lse;           // [batch][n][hq][d], [batch][n][hq]
 };
 enum { kAlone = 0, kPrefix = 1, kOwn = 2 };
 
@@ -128,25 +129,15 @@ __device__ __forceinline__ uint64_t nodes_seen(const AttnParams &p, int b, int n
   return (count >= 64 ? ~0ull : (1ull << count) - 1) &
          (p.tree ? p.tree[int64_t(b) * p.n + node] : ~0ull >> (63 - node));
 }
-// A row's result without the prefix, o / l = `scale` o, and log2 l as `lse`, joined to
-// the prefix's: out = w_seed seed + w_own scale o.
-struct Seed {
-  const float *at;                  // NULL: nothing to join
-  float w_seed, w_own;
-  __device__ __forceinline__ Seed(const AttnParams &p, int64_t row, bool shares, bool unused, float &lse)
-      : at(nullptr), w_seed(0.f), w_own(1.f) {
-    if (p.pass != kOwn || !shares || unused) return;
-    const float theirs = __ldg(p.seed_lse + row);
-    if (theirs == -INFINITY) return;
-    const float top = fmaxf(theirs, lse);
-    float a = ex2(theirs - top), b = lse == -INFINITY ? 0.f : ex2(lse - top);
-    const float sum = a + b;
-    lse = top + log2f(sum);
-    at = p.seed + row * p.d;
-    w_seed = a / sum;
-    w_own = b / sum;
-  }
-};
+// The launches of a prefix attention overlap: the second begins where blocks of the
+// first have ended, and does not end before it (it writes nothing that the first reads
+// or writes).
+__device__ __forceinline__ void next_launch_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void launch_before_has_ended() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Slots in the whole pages of the prefix.
+__device__ __forceinline__ int shared_slots(const AttnParams &p) {
+  return min(max(*p.prefix, 0) / p.cache.page_size, p.prefix_pages) * p.cache.page_size;
+}
 // Cache head and row block of unit u of a sequence.
 __device__ __forceinline__ int head_of(const AttnParams &p, int u) { return p.blocks == 1 ? u : u / p.blocks; }
 __device__ __forceinline__ int block_of_rows(const AttnParams &p, int u) { return p.blocks == 1 ? 0 : u % p.blocks; }
@@ -383,13 +374,19 @@ struct Line {
     const int count = used(p, b, len, skip);
     return tiles_for(p, len + count);
   }
+  // A unit is cut into runs of at least 128 KB: shorter ones cost more in the
+  // joining than they save.
+  __device__ __forceinline__ int64_t runs_of(const AttnParams &p, int grid, int64_t all_units) const {
+    const int64_t wanted = total < int64_t(1) << 32 ? uint32_t(total) / uint32_t(p.least) : total / p.least;
+    return min(int64_t(grid), max(wanted, all_units));
+  }
   // The whole warp computes it.
   __device__ void init(const AttnParams &p, int units_) {
     const int lane = threadIdx.x % 32;
     units = units_;
     extra = p.extra;
     snap = p.snap;
-    shared = p.pass == kAlone ? 0 : min(max(*p.prefix, 0) / p.cache.page_size, p.prefix_pages) * p.cache.page_size;
+    shared = p.pass == kAlone ? 0 : shared_slots(p);
     auto long_of = [&](int i) { return i < p.batch ? tiles_of(p, i) + extra : 0; };
     const int own = long_of(lane);              // of the first 32 sequences
     int64_t sum = own;
@@ -397,10 +394,7 @@ struct Line {
 #pragma unroll
     for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(~0u, sum, w);
     total = sum * units;
-    // a unit is cut into runs of at least 128 KB: shorter ones cost more in the
-    // joining than they save
-    const int64_t wanted = total < int64_t(1) << 32 ? uint32_t(total) / uint32_t(p.least) : total / p.least;
-    runs = min(int64_t(gridDim.x), max(wanted, int64_t(p.batch) * units));
+    runs = runs_of(p, int(gridDim.x), int64_t(p.batch) * units);
     const int64_t mine = min(int64_t(blockIdx.x), runs);
     int64_t at;
     if (total * runs < int64_t(1) << 32) {      // 64-bit divisions are slow
@@ -623,6 +617,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
+  if (p.pass != kAlone) next_launch_may_begin();
   Line at;
   at.init(p, p.hkv * p.blocks);
 
@@ -1040,19 +1035,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // NaN is not nothing
         const bool unused = p.pass != kPrefix && node >= at.count;
         const bool empty = unused || (mm[r] == -INFINITY && ll[r] == 0.f);
-        float inv = empty ? 0.f : p.v_scale / ll[r];
-        float lse = empty ? -INFINITY : mm[r] - kLift<kType> + log2f(ll[r]);
+        const float inv = empty ? 0.f : p.v_scale / ll[r];
+        const float lse = empty ? -INFINITY : mm[r] - kLift<kType> + log2f(ll[r]);
         const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
-        const Seed seed(p, at_row, at.skip > 0, unused, lse);
-        if (seed.at) inv *= seed.w_own;
-        float *sums = p.pass == kPrefix ? p.seed + at_row * p.d : nullptr;
+        float *sums = p.pass != kAlone ? p.part + at_row * p.d : nullptr;
         uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
         const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
-        // element e of tile i, and what the prefix gives to it
-        auto value = [&](int i, int e, int col) {
-          const float v = empty ? 0.f : res[i][2 * r + e] * inv;
-          return seed.at ? fmaf(seed.at[col], seed.w_seed, v) : v;
-        };
+        auto value = [&](int i, int e) { return empty ? 0.f : res[i][2 * r + e] * inv; };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int nt = tile_of(i);
@@ -1062,8 +1051,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if constexpr (N >= 2) {
               if (i % 2 == 0 && 8 * nt < p.d) {
                 const int col = 8 * nt + 4 * t;
-                const float v0 = value(i, 0, col), u0 = value(i + 1, 0, col + 1);
-                const float v1 = value(i, 1, col + 2), u1 = value(i + 1, 1, col + 3);
+                const float v0 = value(i, 0), u0 = value(i + 1, 0);
+                const float v1 = value(i, 1), u1 = value(i + 1, 1);
                 if (sums)
                   *reinterpret_cast<float4 *>(sums + col) = make_float4(v0, u0, v1, u1);
                 else
@@ -1071,7 +1060,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             } else if (8 * (nt & ~1) < p.d) {
               const int col0 = out_col<kType>(nt, t, 0), col1 = out_col<kType>(nt, t, 1);
-              const float v0 = value(i, 0, col0), v1 = value(i, 1, col1);
+              const float v0 = value(i, 0), v1 = value(i, 1);
               if (sums) {
                 sums[col0] = v0;
                 sums[col1] = v1;
@@ -1083,7 +1072,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           } else if (8 * nt < p.d) {
             const int col = 8 * nt + 2 * t;
-            const float v0 = value(i, 0, col), v1 = value(i, 1, col + 1);
+            const float v0 = value(i, 0), v1 = value(i, 1);
             if (sums)
               *reinterpret_cast<float2 *>(sums + col) = make_float2(v0, v1);
             else
@@ -1092,7 +1081,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (t == 0 && first_warp) {
           if (sums)
-            p.seed_lse[at_row] = lse;
+            p.part_lse[at_row] = lse;
           else if (p.lse)
             p.lse[at_row] = lse * kLn2;
         }
@@ -1230,6 +1219,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           st[g] = make_float2(mj[0], lj[0]);
           st[g + 8] = make_float2(mj[1], lj[1]);
         }
+        if (p.pass == kPrefix) break;                    // (joined by the third launch)
         __threadfence();
         named_bar(1, kConsumers * 32);
         if (tid == 0) {
@@ -1279,6 +1269,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
     at = after;
   }
+  if (p.pass == kOwn && tid == 0) launch_before_has_ended();
 }
 
 // -------------------------------------------------------------------- host

@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_at;
+  if (p.pass != kAlone) next_launch_may_begin();
   Line at;
   at.init(p, p.hkv * p.blocks);
 
@@ -673,9 +674,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       const int first = whole ? 0 : at.first(), final = whole ? 0 : at.final();
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
       uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
-      float *sums = p.pass == kPrefix ? p.seed + at_row * p.d : nullptr;
+      float *sums = p.pass != kAlone ? p.part + at_row * p.d : nullptr;
       const bool unused = p.pass != kPrefix && node >= at.count;
-      auto store = [&](int c, const float (&y)[32], float inv, bool empty, const Seed &seed) {
+      auto store = [&](int c, const float (&y)[32], float inv, bool empty) {
         if (!real) return;
 #pragma unroll
         for (int k = 0; k < 32; k += 8)
@@ -683,13 +684,6 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
             float z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = empty ? 0.f : y[k + e] * inv;
-            if (seed.at) {
-              const float4 a = __ldg(reinterpret_cast<const float4 *>(seed.at + c + k));
-              const float4 b = __ldg(reinterpret_cast<const float4 *>(seed.at + c + k + 4));
-              const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = fmaf(s[e], seed.w_seed, z[e]);
-            }
             if (sums) {
               reinterpret_cast<float4 *>(sums + c + k)[0] = make_float4(z[0], z[1], z[2], z[3]);
               reinterpret_cast<float4 *>(sums + c + k)[1] = make_float4(z[4], z[5], z[6], z[7]);
@@ -701,22 +695,20 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
                            pack_out(z[4], z[5], f16), pack_out(z[6], z[7], f16));
           }
       };
-      // the log2 of a row's sum; a row that is none has no seed
+      // the log2 of a row's sum
       auto lse_of = [&](float mm, float ll, bool empty) {
         return empty ? -INFINITY : mm - kWideLift<kType> + log2f(ll);
       };
       auto store_lse = [&](float lse) {
         if (!real || (NQ == 1 && q == 1)) return;
         if (sums)
-          p.seed_lse[at_row] = lse;
+          p.part_lse[at_row] = lse;
         else if (p.lse)
           p.lse[at_row] = lse * kLn2;
       };
       if (whole) {
         const bool empty = unused || (m == -INFINITY && l == 0.f);   // NaN is not nothing
-        float inv = empty ? 0.f : p.v_scale / l, lse = lse_of(m, l, empty);
-        const Seed seed(p, at_row, at.skip > 0, unused || !real, lse);
-        if (seed.at) inv *= seed.w_own;
+        const float inv = empty ? 0.f : p.v_scale / l;
 #pragma unroll 1
         for (int k = col0; k < col1; k += 32) {
           uint32_t y[32];
@@ -724,9 +716,9 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
           float f[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(y[e]);
-          store(k, f, inv, empty, seed);
+          store(k, f, inv, empty);
         }
-        store_lse(lse);
+        store_lse(lse_of(m, l, empty));
       } else {
         // partial results: [4 columns][row], then (m, l) of each row
         const int mine_row = (NQ == 2 ? q * 128 : 0) + row_in;
@@ -751,6 +743,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         while (true) {
           if (NQ == 2 || q == 0)
             reinterpret_cast<float2 *>(to + L::kRows * L::D)[mine_row] = make_float2(m, l);
+          if (p.pass == kPrefix) break;                  // (joined by the third launch)
           __threadfence();
           sync_rows();
           if (tid == 0) {
@@ -773,9 +766,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
           const bool all = join.last();
           to = place(join.lo);
           const bool empty = unused || (m == -INFINITY && l == 0.f);
-          float inv = empty ? 0.f : p.v_scale / l, lse = lse_of(m, l, empty);
-          const Seed seed(p, at_row, all && at.skip > 0, unused || !real, lse);
-          if (seed.at) inv *= seed.w_own;
+          const float inv = empty ? 0.f : p.v_scale / l;
 #pragma unroll 1
           for (int k = col0; k < col1; k += 32) {
             float f[32];
@@ -796,7 +787,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
               }
             }
             if (all) {
-              store(k, f, inv, empty, seed);
+              store(k, f, inv, empty);
             } else {
               // (these columns of this row are read by no other thread)
 #pragma unroll
@@ -806,7 +797,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
             }
           }
           if (all) {
-            store_lse(lse);
+            store_lse(lse_of(m, l, empty));
             break;
           }
           sync_rows();                                   // everybody has read the group's states
@@ -825,6 +816,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
+  if (p.pass == kOwn && tid == 0) launch_before_has_ended();
 }
 
 template <int kCache, int DC, int NQ>
