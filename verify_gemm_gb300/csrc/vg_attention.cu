@@ -25,6 +25,15 @@ const Variant &pick(int type, int d, int rows) {
   return of[d <= 64 ? 0 : d <= 128 ? 1 : d <= 192 && r >= 2 ? 2 : 3][r];
 }
 
+// The same for the rows of a whole batch over a prefix.  Under 1024 of them the tcgen05 kernel takes
+// blocks of 128: 320 rows are 3 tiles of 128 and not 4 (65500 keys in E4M3: 156 us against 176), and
+// 240 rows leave half the partial results (8003 keys of 8 heads, a decode of 48: 74 us against 76).  From
+// there on blocks of 256, for which K and V are read half as often (4096 rows, 16384 keys: 290 us
+// against 293).
+const Variant &pick_prefix(int type, int d, int64_t rows) {
+  return pick(type, d, is_wide(d, int(rows)) && rows < 1024 ? 128 : int(rows));
+}
+
 int cache_type(const vg_kv_cache &c) {
   return c.type == VG_TYPE_E4M3 ? kE4M3 : c.type == VG_TYPE_FP16 ? kF16 : kBf16;
 }
@@ -146,7 +155,7 @@ vg_status behind_prefix(int n, int q_heads, const vg_kv_cache *cache, int sms, B
   // (node_of and q_of divide by multiplying)
   if (rows * group >= int64_t(1) << 32 || nodes * n >= int64_t(1) << 32 || rows >= int64_t(1) << 31)
     return VG_ERR_UNSUPPORTED;
-  b.prefix = &pick(type, cache->head_dim, int(rows));
+  b.prefix = &pick_prefix(type, cache->head_dim, rows);
   b.own = &pick(type, cache->head_dim, n * group);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t all = size_t(nodes) * size_t(q_heads);
@@ -243,6 +252,7 @@ extern "C" vg_status vg_prefix_attention(const vg_attention_desc *d, const vg_kv
   if (vg_status s = launch(own, *b.own, type, cache, sms, stream)) return s;
   j.wide = is_wide(own.d, first.rows);
   j.e4m3 = type == kE4M3;
+  j.sms = sms;
   j.rows = b.prefix->rows;
   j.partial = b.prefix->partial;
   j.columns = (b.prefix->partial - 2 * j.rows) / j.rows;

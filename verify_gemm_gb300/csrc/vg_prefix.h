@@ -9,7 +9,7 @@ namespace attn {
 // The partial results of the prefix's launch: `partial` floats each, [column / 4][row][4] (wide) or in
 // fragment order, then (m, l) of each row at `state`.
 struct PrefixJoin {
-  int wide, e4m3, rows, columns, partial, state, grid;
+  int wide, e4m3, rows, columns, partial, state, grid, sms;
   float lift;                       // of the weights, log2
 };
 
