@@ -24,7 +24,7 @@ struct NormParams {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormBlocks = 4;       // of an SM at once
-constexpr int kNormTokens = 16;
+constexpr int kNormTokens = 32;
 // A BF16 head's squares can pass FP32's range: such a head is taken times this,
 // which leaves the largest sum of 256 squares below 2^124 (and eps nothing).
 constexpr float kNormDown = 0x1p-70f;
@@ -106,24 +106,108 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParam
   }
 }
 
-// 16 elements a thread, 2^kLog threads a head (those past d / 16 idle).
-// blockIdx.x: tokens, blockIdx.y: heads.
+// Two at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (std::is_same_v<T, __half>) {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+  } else {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  uint32_t w;
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 h = __floats2half2_rn(a, b);
+    memcpy(&w, &h, 4);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    memcpy(&w, &h, 4);
+  }
+  return w;
+}
+
+// 16 elements a thread, 2^kLog threads a head (those past d / 16 idle), as two rows of 8: the first and
+// the second of the pairs that turn.  blockIdx.x: tokens, blockIdx.y: heads.
 template <typename T, typename C, bool kInterleaved, int kLog>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
     norm_rope_vector_kernel(const RopeParams p, const NormParams n, int tokens_per_block, int heads_per_block) {
-  extern __shared__ __align__(16) uint8_t norm_smem[];        // angles [tokens][rot / 2], the steps, the weights
+  extern __shared__ __align__(16) uint8_t norm_smem[];        // cosines, sines [tokens][rot / 2], the steps, the weights
   __shared__ Token tok[kNormTokens];
   __shared__ int64_t position[kNormTokens];
   const int half = p.rot / 2, tid = threadIdx.x;
-  float2 *angles = reinterpret_cast<float2 *>(norm_smem);
-  uint64_t *steps = reinterpret_cast<uint64_t *>(angles + tokens_per_block * half);
-  float *weights = reinterpret_cast<float *>(steps + half);   // [q, k][d]
+  float *cosines = reinterpret_cast<float *>(norm_smem), *sines = cosines + tokens_per_block * half;
+  uint64_t *steps = reinterpret_cast<uint64_t *>(sines + tokens_per_block * half);
+  float *weights = reinterpret_cast<float *>(steps + half);   // [q, k][4][thread of the head][4]
   const int64_t first = int64_t(blockIdx.x) * tokens_per_block;
   const int tokens = int(min(int64_t(tokens_per_block), p.tokens - first));
   const int h0 = blockIdx.y * heads_per_block;
   const int heads = min(heads_per_block, p.hq + 2 * p.hkv - h0);
+  const int c = tid & ((1 << kLog) - 1), items = (tokens * heads) << kLog;
+  const int turned = p.rot / 16;
+  const bool here = c < p.d / 16, turns = c < turned;
+  // "half" pairs lie rot / 2 apart; everything else is 16 elements in a row
+  const bool apart = turns && !kInterleaved;
+  const int e1 = apart ? 8 * c : 16 * c, e2 = apart ? 8 * c + half : 16 * c + 8;
+  const float inv_d = 1.f / float(p.d);
+  // An item's loads go ahead of the item before, and the first one's of the angles.
+  struct Item {
+    int ti, h;
+    uint4 r1, r2;
+  };
+  auto fetch = [&](Item &x, int w, auto &&begins) {
+    const int th = w >> kLog;
+    x.ti = th / heads;
+    x.h = h0 + th - x.ti * heads;
+    if (!here || x.ti >= tokens) return;
+    int64_t q, k, v;
+    begins(x.ti, q, k, v);
+    const T *src = x.h < p.hq           ? static_cast<const T *>(p.q) + q + x.h * p.qs[2]
+                   : x.h < p.hq + p.hkv ? static_cast<const T *>(p.k) + k + (x.h - p.hq) * p.ks[2]
+                                        : static_cast<const T *>(p.v) + v + (x.h - p.hq - p.hkv) * p.vs[2];
+    x.r1 = *reinterpret_cast<const uint4 *>(src + e1);
+    x.r2 = *reinterpret_cast<const uint4 *>(src + e2);
+  };
+  constexpr int kAhead = 2;
+  Item next[kAhead];
+  auto first_at = [&](int ti, int64_t &q, int64_t &k, int64_t &v) {
+    const int64_t at = first + ti;
+    const int b = int(uint32_t(at) / uint32_t(p.n)), i = int(at - int64_t(b) * p.n);
+    q = b * p.qs[0] + i * p.qs[1];
+    k = b * p.ks[0] + i * p.ks[1];
+    v = b * p.vs[0] + i * p.vs[1];
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if ((tid & ~31) + k * kNormThreads < items) fetch(next[k], tid + k * kNormThreads, first_at);
   for (int j = tid; j < half; j += kNormThreads) steps[j] = turn_step(p, j);
-  for (int j = tid; j < 2 * p.d; j += kNormThreads) weights[j] = weight_at<T>(n, j >= p.d, j >= p.d ? j - p.d : j);
+  for (int j = tid; j < 2 * p.d; j += kNormThreads) {
+    const int at = j >= p.d ? j - p.d : j, chunk = at / 16, k = at % 16;
+    const int e = kInterleaved     ? 16 * chunk + 2 * (k % 8) + k / 8
+                  : chunk < turned ? 8 * chunk + k % 8 + k / 8 * half
+                                   : at;
+    // fours of a head's threads lie side by side: a quarter of a warp reads 128 bytes in a row
+    weights[(((j >= p.d) * 4 + k / 4 << kLog) + chunk) * 4 + k % 4] = weight_at<T>(n, j >= p.d, e);
+  }
   if (tid < tokens) {
     int64_t at;
     const Token t = rope_token(p, first + tid, at);
@@ -131,40 +215,48 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
     tok[tid] = t;
   }
   __syncthreads();
-  for (int w = tid; w < tokens * half; w += kNormThreads)
-    angles[w] = turn(p, position[w / half], steps[w % half]);
+  for (int w = tid; w < tokens * half; w += kNormThreads) {
+    const int ti = w / half, j = w - ti * half, to = ti * half + (j / 4 % 2 * turned + j / 8) * 4 + j % 4;
+    const float2 a = turn(p, position[ti], steps[j]);
+    cosines[to] = a.x;
+    sines[to] = a.y;
+  }
   __syncthreads();
-  const int c = tid & ((1 << kLog) - 1), items = (tokens * heads) << kLog;
-  const bool here = c < p.d / 16, turns = c < p.rot / 16;
-  // "half" pairs lie rot / 2 apart; everything else is 16 elements in a row
-  const bool apart = turns && !kInterleaved;
-  const int e1 = apart ? 8 * c : 16 * c, e2 = apart ? 8 * c + half : 16 * c + 8;
-  const float inv_d = 1.f / float(p.d);
-#pragma unroll 2
   for (int w0 = tid & ~31; w0 < items; w0 += kNormThreads) {
-    const int th = (w0 + (tid & 31)) >> kLog, ti = th / heads, h = h0 + th - ti * heads;
+    const Item now = next[0];
+#pragma unroll
+    for (int k = 1; k < kAhead; ++k) next[k - 1] = next[k];
+    if (w0 + kAhead * kNormThreads < items)
+      fetch(next[kAhead - 1], w0 + kAhead * kNormThreads + (tid & 31), [&](int ti, int64_t &q, int64_t &k, int64_t &v) {
+        q = tok[ti].q;
+        k = tok[ti].k;
+        v = tok[ti].v;
+      });
+    const int ti = now.ti, h = now.h;
     const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
     const bool any = here && ti < tokens;
     const Token &t = tok[any ? ti : 0];
-    const T *src = is_q ? static_cast<const T *>(p.q) + t.q + h * p.qs[2]
-                 : is_v ? static_cast<const T *>(p.v) + t.v + (h - p.hq - p.hkv) * p.vs[2]
-                        : static_cast<const T *>(p.k) + t.k + (h - p.hq) * p.ks[2];
-    uint4 r1 = make_uint4(0, 0, 0, 0), r2 = r1;
-    if (any) {
-      r1 = *reinterpret_cast<const uint4 *>(src + e1);
-      r2 = *reinterpret_cast<const uint4 *>(src + e2);
-    }
-    float x1[8], x2[8];
-    unpack8<T>(x1, r1);
-    unpack8<T>(x2, r2);
-    auto squares = [&] {
-      float s1 = 0.f, s2 = 0.f;
+    const uint32_t r[8] = {now.r1.x, now.r1.y, now.r1.z, now.r1.w, now.r2.x, now.r2.y, now.r2.z, now.r2.w};
+    float2 x1[4], x2[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s1 = fmaf(x1[k], x1[k], s1);
-        s2 = fmaf(x2[k], x2[k], s2);
+    for (int j = 0; j < 4; ++j) {
+      if (kInterleaved) {
+        const float2 a = unpack2<T>(r[2 * j]), b = unpack2<T>(r[2 * j + 1]);
+        x1[j] = make_float2(a.x, b.x);
+        x2[j] = make_float2(a.y, b.y);
+      } else {
+        x1[j] = unpack2<T>(r[j]);
+        x2[j] = unpack2<T>(r[4 + j]);
       }
-      float s = s1 + s2;
+    }
+    auto squares = [&] {
+      float2 a = mul2(x1[0], x1[0]), b = mul2(x2[0], x2[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) {
+        a = fma2(x1[j], x1[j], a);
+        b = fma2(x2[j], x2[j], b);
+      }
+      float s = any ? (a.x + a.y) + (b.x + b.y) : 0.f;
 #pragma unroll
       for (int m = 1; m < 1 << kLog; m *= 2) s += __shfl_xor_sync(~0u, s, m);
       return s;
@@ -176,9 +268,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
         if (over) {
           eps = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x1[k] *= kNormDown;
-            x2[k] *= kNormDown;
+          for (int j = 0; j < 4; ++j) {
+            x1[j] = mul2(x1[j], both(kNormDown));
+            x2[j] = mul2(x2[j], both(kNormDown));
           }
         }
         s = squares();
@@ -186,23 +278,60 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
     }
     if (!any || (!is_q && t.ck < 0)) continue;
     if (!is_v) {
-      const float r = rsqrtf(s * inv_d + eps);
-      const float *wt = weights + (is_q ? 0 : p.d);
+      const float inv = rsqrtf(s * inv_d + eps);
+      const float4 *wt = reinterpret_cast<const float4 *>(weights) + (is_q ? 0 : 4 << kLog) + c;
 #pragma unroll
-      for (int k = 0; k < 8; k += 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(wt + e1 + k), b = *reinterpret_cast<const float4 *>(wt + e2 + k);
-        x1[k] = x1[k] * r * a.x;
-        x1[k + 1] = x1[k + 1] * r * a.y;
-        x1[k + 2] = x1[k + 2] * r * a.z;
-        x1[k + 3] = x1[k + 3] * r * a.w;
-        x2[k] = x2[k] * r * b.x;
-        x2[k + 1] = x2[k + 1] * r * b.y;
-        x2[k + 2] = x2[k + 2] * r * b.z;
-        x2[k + 3] = x2[k + 3] * r * b.w;
+      for (int j = 0; j < 4; j += 2) {
+        const float4 a = wt[j / 2 << kLog], b = wt[2 + j / 2 << kLog];
+        x1[j] = mul2(mul2(x1[j], both(inv)), make_float2(a.x, a.y));
+        x1[j + 1] = mul2(mul2(x1[j + 1], both(inv)), make_float2(a.z, a.w));
+        x2[j] = mul2(mul2(x2[j], both(inv)), make_float2(b.x, b.y));
+        x2[j + 1] = mul2(mul2(x2[j + 1], both(inv)), make_float2(b.z, b.w));
       }
-      if (turns) rotate16<kInterleaved>(x1, x2, angles + ti * half + 8 * c);
+      if (turns) {
+        const float4 *cs = reinterpret_cast<const float4 *>(cosines + ti * half) + c;
+        const float4 *sn = reinterpret_cast<const float4 *>(sines + ti * half) + c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 c4 = cs[j / 2 * turned], s4 = sn[j / 2 * turned];
+          const float2 co = j % 2 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+          const float2 si = j % 2 ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+          const float2 u = x1[j], v = x2[j], y = mul2(v, si);
+          x1[j] = fma2(u, co, make_float2(-y.x, -y.y));
+          x2[j] = fma2(u, si, mul2(v, co));
+        }
+      }
     }
-    store16<T, C>(p, t, h, e1, e2, x1, x2);
+    // the 8 words of e1 .. e1 + 7 and e2 .. e2 + 7
+    float2 y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[kInterleaved ? 2 * j : j] = kInterleaved ? make_float2(x1[j].x, x2[j].x) : x1[j];
+      y[kInterleaved ? 2 * j + 1 : 4 + j] = kInterleaved ? make_float2(x1[j].y, x2[j].y) : x2[j];
+    }
+    if (is_q || sizeof(C) == 2) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = is_q && !t.used ? 0 : round2<T>(y[j].x, y[j].y);
+      T *dst = is_q   ? static_cast<T *>(p.q_out) + t.out + h * p.d
+               : is_v ? static_cast<T *>(p.cv) + t.cv + (h - p.hq - p.hkv) * p.cvs[2]
+                      : static_cast<T *>(p.ck) + t.ck + (h - p.hq) * p.cks[2];
+      *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(dst + e2) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      const float2 inv = both(is_v ? p.v_inv : p.k_inv);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = mul2(y[2 * j], inv), b = mul2(y[2 * j + 1], inv);
+        w[j] = uint32_t(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
+               uint32_t(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
+      }
+      uint8_t *dst = is_v ? static_cast<uint8_t *>(p.cv) + t.cv + (h - p.hq - p.hkv) * p.cvs[2]
+                          : static_cast<uint8_t *>(p.ck) + t.ck + (h - p.hq) * p.cks[2];
+      *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(dst + e2) = make_uint2(w[2], w[3]);
+    }
   }
 }
 
@@ -218,11 +347,10 @@ void launch_norm_rope(const RopeParams &p, const NormParams &n, bool vector, int
   while (p.d / 16 > 1 << log) ++log;
   const int heads = p.hq + 2 * p.hkv;
   const int64_t resident = int64_t(kNormBlocks) * sms;
-  const int tb = int(std::max<int64_t>(
-      1, std::min({int64_t(kNormTokens), int64_t(2048 / (heads << log)), (p.tokens + resident - 1) / resident})));
+  const int tb = int(std::min(int64_t(kNormTokens), (p.tokens + resident - 1) / resident));
   const int hb = p.tokens < 2 * sms ? std::max(1, kNormThreads >> log) : heads;
   const dim3 grid(unsigned((p.tokens + tb - 1) / tb), unsigned((heads + hb - 1) / hb));
-  const size_t smem = size_t(tb) * half * sizeof(float2) + size_t(half) * sizeof(uint64_t) + size_t(2 * p.d) * sizeof(float);
+  const size_t smem = size_t(tb) * half * 2 * sizeof(float) + size_t(half) * sizeof(uint64_t) + (size_t(32) << log) * sizeof(float);
   auto go = [&](auto kernel) { kernel<<<grid, kNormThreads, smem, st>>>(p, n, tb, hb); };
   switch (log) {
     case 0: go(norm_rope_vector_kernel<T, C, kInterleaved, 0>); break;
