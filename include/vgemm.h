@@ -662,7 +662,7 @@ vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
  *   out    FP32 [rows][vocab] or NULL: that distribution, 0 for what is not kept: the p
  *     and the q of vg_verify_tree.  (Rows without a token: NaN, or 0 for one of
  *     nothing but -infinity and for one with T <= 0.)
- * x and out 16-byte aligned; vocab < 2^28, rows < 2^26, draws <= 65536. */
+ * vocab < 2^28, rows < 2^26, draws <= 65536. */
 typedef struct vg_sample_desc {
     const void *x;
     const float *u, *temperature, *top_p, *min_p;

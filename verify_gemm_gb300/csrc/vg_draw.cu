@@ -54,6 +54,7 @@ struct DrawParams {
   int32_t *tokens;
   float *out;
   int draws, chunk, bits;            // units of a warp; a weight of 1 is 2^bits
+  int lead;                          // elements between the 16-byte border that x is and the first row
 };
 
 // 2^(30 - j / 32)
@@ -258,8 +259,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   const int64_t row = blockIdx.x / blocks;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const T *x = static_cast<const T *>(p.x);
-  const int64_t lo = row * p.stride, hi = lo + p.V;
-  const int64_t end = (hi + 7) / 8;                      // units, on the grid of the whole array
+  const int64_t lo = p.lead + row * p.stride, hi = lo + p.V;
+  const int64_t end = (hi + 7) / 8;                      // units, on the grid of 16-byte borders
   const int64_t w0 = lo / 8 + int64_t(rank * kDrawWarps + warp) * p.chunk;
   const int mine = int(max(int64_t(0), min(int64_t(p.chunk), end - w0)));   // units of this warp
   if (blocks > 1) cluster_arrive();                      // a block must have begun before others write to it
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     return;
   }
   // stores the probabilities of elements r and r + 1
-  const bool aligned = ((row * p.V + base) & 1) == 0;
+  const bool aligned = (reinterpret_cast<uintptr_t>(out + base) & 7) == 0;
   auto store = [&](int r, float a, float b) {
     if (aligned && r >= 0 && r + 2 <= p.V && r - int(base) < mine * 8) {
       __stcs(reinterpret_cast<float2 *>(out + r), make_float2(a, b));
@@ -430,8 +431,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   };
 
   // What is kept: y > x_f, and those equal to it up to index i_f.
+  // (Elements beside the row, -infinity, have indices below 0.)
   float x_f = -INFINITY;
-  int i_f = -1;
+  int i_f = INT32_MIN;
   auto kept = [&](float y, int index) { return y > x_f || (y == x_f && index <= i_f); };
   // The block's 512 threads' sums of `mine`, up to each and in all.
   auto scan_block = [&](uint64_t v, uint64_t &whole) {
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       });
     }
     sync_all();
-    i_f = ties ? int(told.target) : -1;
+    i_f = ties ? int(told.target) : INT32_MIN;
     sync_all();                                          // (sums are read before they are written again)
   }
   if (!done) {
@@ -944,7 +946,9 @@ extern "C" vg_status vg_sample(const vg_sample_desc *d, vg_stream_t stream) {
   if (!d || !d->x || !d->u || !d->tokens || d->rows < 1 || d->vocab < 1 || d->draws < 1 || d->row_stride < d->vocab)
     return VG_ERR_INVALID_ARG;
   if (d->type != VG_TYPE_BF16 && d->type != VG_TYPE_FP16 && d->type != VG_TYPE_FP32) return VG_ERR_INVALID_ARG;
-  if (!aligned16(d->x) || !aligned16(d->out)) return VG_ERR_ALIGNMENT;
+  const int size = d->type == VG_TYPE_FP32 ? 4 : 2;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(d->x);
+  if (at % uintptr_t(size) || reinterpret_cast<uintptr_t>(d->out) & 3) return VG_ERR_ALIGNMENT;
   for (const void *p : {static_cast<const void *>(d->u), static_cast<const void *>(d->temperature),
                         static_cast<const void *>(d->top_k), static_cast<const void *>(d->top_p),
                         static_cast<const void *>(d->min_p), static_cast<const void *>(d->tokens)})
@@ -955,7 +959,8 @@ extern "C" vg_status vg_sample(const vg_sample_desc *d, vg_stream_t stream) {
   int sms = 0;
   if (vg_status s = device_sms(&sms)) return s;
   DrawParams p{};
-  p.x = d->x;
+  p.x = reinterpret_cast<const void *>(at & ~uintptr_t(15));
+  p.lead = int(at & 15) / size;
   p.V = d->vocab;
   p.stride = d->row_stride;
   p.u = d->u;
