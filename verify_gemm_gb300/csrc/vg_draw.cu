@@ -57,14 +57,18 @@ struct DrawParams {
   int lead;                          // elements between the 16-byte border that x is and the first row
 };
 
-// 2^(30 - j / 32)
-__constant__ uint32_t kPowers[32] = {
-    1073741824, 1050733751, 1028218693, 1006186087, 984625594, 963527098, 942880699, 922676710,
-    902905651,  883558244,  864625413,  846098274,  827968132, 810226483, 792865000, 775875538,
-    759250125,  742980960,  727060411,  711481005,  696235434, 681316545, 666717336, 652430958,
-    638450708,  624770026,  611382493,  598281827,  585461881, 572916640, 560640218, 548626854};
+// 2^(30 - j / 64)
+__constant__ uint32_t kPowers[64] = {
+    1073741824, 1062175491, 1050733751, 1039415261, 1028218693, 1017142735, 1006186087, 995347464,
+    984625594, 974019220, 963527098, 953147997, 942880699, 932724001, 922676710, 912737649,
+    902905651, 893179563, 883558244, 874040567, 864625413, 855311680, 846098274, 836984114,
+    827968132, 819049271, 810226483, 801498734, 792865000, 784324269, 775875538, 767517817,
+    759250125, 751071493, 742980960, 734977579, 727060411, 719228525, 711481005, 703816941,
+    696235434, 688735596, 681316545, 673977412, 666717336, 659535466, 652430958, 645402981,
+    638450708, 631573326, 624770026, 618040012, 611382493, 604796689, 598281827, 591837143,
+    585461881, 579155293, 572916640, 566745190, 560640218, 554601009, 548626854, 542717053};
 
-// What a row's weights need: z in units of 1/32 is (max - x) c.
+// What a row's weights need: z in units of 1/64 is (max - x) c.
 struct Scale {
   float top, c, c_low, cap;          // c as two floats; differences beyond cap weigh nothing
 };
@@ -81,18 +85,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // The weight of a finite logit x is w 2^(up - (bin >> 6)) (up = bits - 30, and w some 2^30).  With
-// z = (k + r) / 32, k whole, |r| <= 1/2, it is 2^-(k / 32) from a table times
-// 2^-(r / 32) by its series.  max - x is exact in FP32 for 16-bit logits but for
+// z = (k + r) / 64, k whole, |r| <= 1/2, it is 2^-(k / 64) from a table times
+// 2^-(r / 64) by its series to the third power (the fourth is 2^-34).  max - x is exact in FP32 for 16-bit logits but for
 // those that are 2^-16 of the largest or less; for FP32 ones what it loses is
-// carried along.  The bin is z in units of 1/64: the larger logit never has the
-// larger bin, as it goes by the rounded difference alone.
+// carried along.  The bin is k: the larger logit never has the larger one, as it goes by the
+// rounded difference alone.
 constexpr float kMagic = 12582912.f;           // 1.5 2^23: what is added to it is rounded to a whole number
+constexpr int kMagicBits = 0x4B400000;
 struct Weight {
-  int w, k, half;
-  __device__ __forceinline__ uint64_t value(int up) const { return uint64_t(uint32_t(w)) << up >> min(k >> 5, 63); }
-  __device__ __forceinline__ uint32_t bin() const { return min(uint32_t(2 * k + half), uint32_t(kBins - 1)); }
+  int w, k;
+  __device__ __forceinline__ uint64_t value(int up) const { return uint64_t(uint32_t(w)) << up >> min(k >> 6, 63); }
+  __device__ __forceinline__ uint32_t bin() const { return min(uint32_t(k), uint32_t(kBins - 1)); }
   // w in the units of its bin: the last one has all weights below 2^-32
-  __device__ __forceinline__ uint32_t in_bin() const { return uint32_t(w) >> min(max((k >> 5) - 31, 0), 31); }
+  __device__ __forceinline__ uint32_t in_bin() const { return uint32_t(w) >> min(max(k >> 6, 31) - 31, 31); }
 };
 // Of two logits at a time.
 template <typename T>
@@ -106,27 +111,24 @@ __device__ __forceinline__ void weigh2(const Scale &s, const uint32_t *powers, f
     const float2 more = fma2(e, both(s.c), low);
     low = make_float2(all.x < s.cap ? more.x : low.x, all.y < s.cap ? more.y : low.y);
   }
-  const float2 t = fma2(d, both(s.c), both(kMagic)), whole = add2(t, both(-kMagic));
-  const float2 r0 = fma2(d, both(s.c), make_float2(-whole.x, -whole.y)), r = add2(r0, low);
-  // 2^28 (2^-(r / 32) - 1)
-  float2 q = fma2(r, both(2.46224105f), both(-454.689658f));
-  q = fma2(r, q, both(62973.9374f));
-  q = fma2(r, q, both(-5814539.98f));
+  const float2 t = fma2(d, both(s.c), both(kMagic)), whole = add2(both(kMagic), make_float2(-t.x, -t.y));
+  const float2 r = add2(fma2(d, both(s.c), whole), low);
+  // 2^28 (2^-(r / 64) - 1)
+  float2 q = fma2(r, both(-56.8362f), both(15743.4844f));
+  q = fma2(r, q, both(-2907269.99f));
   q = fma2(r, q, both(kMagic));
-  auto one = [&](Weight &w, float t, float r0, float q) {
-    w.k = __float_as_int(t) - __float_as_int(kMagic);
-    w.half = r0 >= 0.f;
-    const int f = __float_as_int(q) - __float_as_int(kMagic), p = int(powers[w.k & 31]);
-    w.w = p + __mulhi(p, f << 4);
+  auto one = [&](Weight &w, float t, float q) {
+    w.k = __float_as_int(t) - kMagicBits;
+    const int p = int(powers[__float_as_int(t) & 63]);
+    w.w = p + __mulhi(p, __float_as_int(q) * 16 - int(unsigned(kMagicBits) * 16u));
   };
-  one(w0, t.x, r0.x, q.x);
-  one(w1, t.y, r0.y, q.y);
+  one(w0, t.x, q.x);
+  one(w1, t.y, q.y);
 }
 // Its bin alone.
 __device__ __forceinline__ uint32_t bin_of(const Scale &s, float x) {
-  const float d = fminf(s.top - x, s.cap), t = fmaf(d, s.c, kMagic);
-  const int k = __float_as_int(t) - __float_as_int(kMagic);
-  return min(uint32_t(2 * k + (fmaf(d, s.c, -(t - kMagic)) >= 0.f)), uint32_t(kBins - 1));
+  const float d = fminf(s.top - x, s.cap);
+  return min(uint32_t(__float_as_int(fmaf(d, s.c, kMagic)) - kMagicBits), uint32_t(kBins - 1));
 }
 
 // Logits' codes in their order; logits of 16 bits have as many codes.
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   __shared__ __align__(16) ulonglong2 sums[kMaxCluster * kDrawWarps];
   __shared__ __align__(16) Found told;
   __shared__ __align__(16) ulonglong2 shares[kMaxCluster];
-  __shared__ uint32_t powers[32];
+  __shared__ uint32_t powers[64];
   __shared__ Scale told_scale;
   __shared__ double min_at;          // T ln(min_p)
   __shared__ uint64_t scan[kDrawWarps];
@@ -284,12 +286,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   const int top_k = p.top_k ? p.top_k[row] : 0;
   if (warp == 0) {
     powers[lane] = kPowers[lane];
+    powers[lane + 32] = kPowers[lane + 32];
     if (lane == 0) {
       listed = 0;
-      const double c = 32 * 1.4426950408889634074 / double(temperature);
+      const double c = 64 * 1.4426950408889634074 / double(temperature);
       told_scale.c = c > 3.4e38 ? 3.4028234e38f : float(c);
       told_scale.c_low = c > 3.4e38 ? 0.f : float(c - double(told_scale.c));
-      told_scale.cap = fminf(2048.f / told_scale.c, 3.4028234e38f);
+      told_scale.cap = fminf(4096.f / told_scale.c, 3.4028234e38f);
       // (over an infinite temperature every finite logit weighs 1)
       min_at = !(min_p > 0.f) ? 0.0 : temperature == INFINITY ? (min_p > 1.f ? 1e300 : -1e300)
                                                               : double(temperature) * log(double(min_p));
@@ -324,11 +327,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   // (Two at a time, and not the eight of a 16-byte piece: a row passes here but a
   // few times, and what the code of eight takes to be fetched is more than it saves.)
   auto each = [&](auto &&f) {
+    const int count = mine * 4;
+    int j0 = 0;
 #pragma unroll 2
-    for (int j0 = 0; j0 < mine * 4; j0 += 32) {
+    for (; j0 + 32 <= count; j0 += 32) {
+      const Pair<T> v = pair_at(j0 + lane);
+      f(int(base) + 2 * (j0 + lane), to_f(v.x[0]), to_f(v.x[1]));
+    }
+    if (j0 < count) {
       const int j = j0 + lane;
       float a = -INFINITY, b = -INFINITY;
-      if (j < mine * 4) {
+      if (j < count) {
         const Pair<T> v = pair_at(j);
         a = to_f(v.x[0]);
         b = to_f(v.x[1]);
@@ -434,7 +443,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   // (Elements beside the row, -infinity, have indices below 0.)
   float x_f = -INFINITY;
   int i_f = INT32_MIN;
-  auto kept = [&](float y, int index) { return y > x_f || (y == x_f && index <= i_f); };
+  auto kept = [&](float y, int index) {
+    bool k = y > x_f;
+    if (i_f >= 0) k |= y == x_f && index <= i_f;
+    return k;
+  };
   // The block's 512 threads' sums of `mine`, up to each and in all.
   auto scan_block = [&](uint64_t v, uint64_t &whole) {
     uint64_t run = scan_up(v, lane);
@@ -913,7 +926,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   }
   if (!out) return;
   // ------------------------------------------------------- the distribution
-  const float c = scale.c * (1.f / 32), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
+  const float c = scale.c * (1.f / 64), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
   auto share = [&](float y, int r) { return kept(y, r) ? (y == top ? 1.f : ex2((y - top) * c)) * inv : 0.f; };
   each([&](int r, float a, float b) { store(r, share(a, r), share(b, r + 1)); });
 }
