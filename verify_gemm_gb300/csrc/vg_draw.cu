@@ -644,8 +644,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     if (last) atomicMax(&n_keep, last);
     __syncthreads();
   };
-  bool too_many = false, done = false;
+  bool too_many = false, done = false, summed = false;
   uint64_t whole = 0;
+  const int me = int(rank) * kDrawWarps + warp;
 
   if (top_k > 0 && top_k <= kSmallK && top_k < p.V) {
     // ----------------------------------------------------------- a small top-k
@@ -719,8 +720,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
   } else {
     // A round: the last token by counts (kMass: weights) among what is kept so far.
-    auto round = [&](auto mass, uint64_t target) {
-      constexpr bool kMass = decltype(mass)::value;
+    auto round = [&](auto by_weight, uint64_t target) {
+      constexpr bool kMass = decltype(by_weight)::value;
       clear_bins();
       each([&](int r, float y0, float y1) {
         const bool k0 = kept(y0, r), k1 = kept(y1, r + 1);
@@ -739,12 +740,27 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           if (k1) atomicAdd(bin_lo + bin_of(scale, y1), 1u);
         }
       });
-      const Found f = find(mass, mass, target, 0);
+      const Found f = find(by_weight, by_weight, target, 0);
       if (f.state == kAll) return;
       if (kMass && f_min >= f.to) return;                // min-p ends it before
+      // kMass: what lies in the bins before is kept, and is weighed on the way
+      uint64_t mass = 0;
       each([&](int r, float a, float b) {
+        if constexpr (kMass) {
+          const bool ka = a >= f.to, kb = b >= f.to;
+          if (ka || kb) {
+            Weight wa, wb;
+            weigh2<T>(scale, powers, a, b, wa, wb);
+            mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
+          }
+        }
         push(a, b, r, [&](float y, int i) { return y >= f.from && y < f.to && kept(y, i); });
       });
+      if constexpr (kMass) {
+#pragma unroll
+        for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
+        if (lane < int(blocks)) cluster_store(&sums[me], lane, mass, 0);
+      }
       sync_all();
       if (rank == 0) {
         const int n = gather_list();
@@ -752,6 +768,16 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           if constexpr (kMass) cut_list(n, n, f.target, false);
           else if (tid == 0) n_keep = int(f.target);
           __syncthreads();
+          if constexpr (kMass) {
+            // each kept token's weight to the sum of the warp that has it, and the sums to the other blocks
+            for (int i = tid; i < n_keep; i += kDrawThreads) {
+              const uint32_t warp_of = (uint32_t(list[i]) + uint32_t(lo & 7)) / uint32_t(8 * p.chunk);
+              atomicAdd(reinterpret_cast<unsigned long long *>(&sums[warp_of].x), weigh(logit_at(list[i])));
+            }
+            __syncthreads();
+            for (int i = entries + tid; i < entries * int(blocks); i += kDrawThreads)
+              cluster_store(&sums[i % entries], uint32_t(i / entries), sums[i % entries].x, 0);
+          }
         }
         if (tid == 0) {
           if (n < 0) told.state = kTooMany;
@@ -770,6 +796,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         x_f = logit_of<float>(told.code);
         i_f = told.index;
       }
+      summed = kMass && !too_many;
     };
     if (top_k > 0 && top_k < p.V) round(std::false_type{}, uint64_t(top_k));
     if (!too_many && top_p < 1.f) round(std::true_type{}, 0);
@@ -852,10 +879,10 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (x_f > -INFINITY) n += uint32_t(a == x_f) + uint32_t(b == x_f);
     });
     n = __reduce_add_sync(~0u, n);
-    if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, n, 0);
+    if (lane < int(blocks)) cluster_store(&sums[me], lane, n, 0);
     sync_all();
     uint64_t before = 0;
-    for (int i = lane; i < int(rank) * kDrawWarps + warp; i += 32) before += sums[i].x;
+    for (int i = lane; i < me; i += 32) before += sums[i].x;
 #pragma unroll
     for (int w = 16; w; w /= 2) before += __shfl_xor_sync(~0u, before, w);
     if (ties > before && ties <= before + n) {
@@ -882,22 +909,25 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       i_f = INT32_MAX;
     }
     // -------------------------------------------------------------- the draw
-    uint64_t mass = 0;
-    each([&](int r, float a, float b) {
-      const bool ka = kept(a, r), kb = kept(b, r + 1);
-      if (!ka && !kb) return;
-      Weight wa, wb;
-      weigh2<T>(scale, powers, a, b, wa, wb);
-      mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
-    });
+    if (!summed) {
+      uint64_t mass = 0;
+      each([&](int r, float a, float b) {
+        const bool ka = kept(a, r), kb = kept(b, r + 1);
+        if (!ka && !kb) return;
+        Weight wa, wb;
+        weigh2<T>(scale, powers, a, b, wa, wb);
+        mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
+      });
 #pragma unroll
-    for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
-    if (lane < int(blocks)) cluster_store(&sums[rank * kDrawWarps + warp], lane, mass, 0);
-    sync_all();
+      for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
+      if (lane < int(blocks)) cluster_store(&sums[me], lane, mass, 0);
+      sync_all();
+    }
+    const uint64_t mass = sums[me].x;
     uint64_t my_mass = 0;                                // of the warps before this one
     for (int i = lane; i < entries; i += 32) {
       whole += sums[i].x;
-      my_mass += i < int(rank) * kDrawWarps + warp ? sums[i].x : 0;
+      my_mass += i < me ? sums[i].x : 0;
     }
 #pragma unroll
     for (int w = 16; w; w /= 2) {
