@@ -964,11 +964,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
 template <typename T>
 cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) {
   const int64_t units = p.V / 8 + 2, size = 8 * sizeof(T);
-  // as few blocks a row as hold it, and more while all rows' fit the device at once (two a SM);
-  // 16, more than a portable cluster, for a few rows alone.
+  // As few blocks a row as hold it in 76 KB each (two blocks an SM; 256 rows of 151936 BF16 logits
+  // with settings of their own 125 us on 4 blocks of 76 KB, 159 on 8 of 38), and more while all rows'
+  // fit the device about at once (41 such rows 60 us on 4, 42 on 8); 16, more than a portable cluster, for a
+  // few rows alone (8 rows of top-p 40 us, 42 on 8).
   int c = 1;
   auto more = [&] { return units * size > int64_t(kDrawShare) * c; };
-  while (c < 8 && (more() || (rows * c <= sms && units > kDrawThreads * c))) c *= 2;
+  while (c < 8 && (more() || (8 * rows * c <= 9 * sms && units > kDrawThreads * c))) c *= 2;
   if (c == 8 && (more() || (units > 8 * kDrawThreads && rows * 16 <= sms))) c = kMaxCluster;
   const int64_t warps = int64_t(c) * kDrawWarps;
   p.chunk = int((units + warps - 1) / warps);
