@@ -178,6 +178,20 @@ def test_equal_logits(vg, dtype):
         check(vg, x, u, T=[1.0, 0.5, 2.0, 1.0, 1.0, 3.0], k=[k] * 6, p=[p] * 6, mp=[mp] * 6)
 
 
+@pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 151936), (torch.float16, 700001), (torch.float32, 600007),
+                                         (torch.float32, 1000003), (torch.bfloat16, 2500001)])
+def test_long_rows(vg, dtype, vocab):
+    """Rows that fill the shared memory of 16 blocks, and more; likely tokens beside each other."""
+    g = torch.Generator().manual_seed(13)
+    x = randn(g, 3, vocab, dtype=dtype, scale=2.0)
+    x[1] = torch.sort(x[1].float(), descending=True).values.to(dtype)
+    x[2, 1000:3000] += 6.0
+    u = torch.rand((3, 2), generator=g).to(DEV)
+    for T, k, p, mp in ((1.0, 0, 1.0, 0.0), (0.8, 60, 0.9, 0.0), (0.9, 200, 1.0, 0.001), (1.0, 0, 0.7, 0.0),
+                        (1.1, 3000, 0.8, 0.0), (0.7, 0, 1.0, 0.2), (0.0, 0, 1.0, 0.0)):
+        check(vg, x, u, T=[T] * 3, k=[k] * 3, p=[p] * 3, mp=[mp] * 3)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_masked_rows(vg, dtype):
     """-infinity, the type's lowest value, infinities and NaN."""
