@@ -18,9 +18,10 @@ bool is_wide(int d, int rows) { return d <= 128 && rows > 32; }
 // as can share out the keys; above 128 rows, blocks of 128.
 int row_index(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
-const Variant &pick(int type, int d, int rows) {
-  if (is_wide(d, rows)) return kWide[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
-  const Variants &of = type == kBf16 ? kVariantsBf16 : type == kF16 ? kVariantsF16 : kVariantsE4M3;
+const Variant &pick(int type, int d, int rows, bool parts = false) {
+  if (is_wide(d, rows)) return (parts ? kWideParts : kWide)[type][d <= 64 ? 0 : 1][rows <= 128 ? 0 : 1];
+  const Variants &of = parts ? (type == kBf16 ? kPartsBf16 : type == kF16 ? kPartsF16 : kPartsE4M3)
+                             : (type == kBf16 ? kVariantsBf16 : type == kF16 ? kVariantsF16 : kVariantsE4M3);
   const int r = row_index(rows);
   return of[d <= 64 ? 0 : d <= 128 ? 1 : d <= 192 && r >= 2 ? 2 : 3][r];
 }
@@ -31,7 +32,7 @@ const Variant &pick(int type, int d, int rows) {
 // there on blocks of 256, for which K and V are read half as often (4096 rows, 16384 keys: 290 us
 // against 293).
 const Variant &pick_prefix(int type, int d, int64_t rows) {
-  return pick(type, d, is_wide(d, int(rows)) && rows < 1024 ? 128 : int(rows));
+  return pick(type, d, is_wide(d, int(rows)) && rows < 1024 ? 128 : int(rows), true);
 }
 
 int cache_type(const vg_kv_cache &c) {
@@ -156,7 +157,7 @@ vg_status behind_prefix(int n, int q_heads, const vg_kv_cache *cache, int sms, B
   if (rows * group >= int64_t(1) << 32 || nodes * n >= int64_t(1) << 32 || rows >= int64_t(1) << 31)
     return VG_ERR_UNSUPPORTED;
   b.prefix = &pick_prefix(type, cache->head_dim, rows);
-  b.own = &pick(type, cache->head_dim, n * group);
+  b.own = &pick(type, cache->head_dim, n * group, true);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t all = size_t(nodes) * size_t(q_heads);
   const size_t part = up(all * size_t(cache->head_dim) * sizeof(float)) + up(all * sizeof(float));
@@ -226,7 +227,8 @@ extern "C" vg_status vg_prefix_attention(const vg_attention_desc *d, const vg_kv
   if (!aligned16(workspace)) return VG_ERR_ALIGNMENT;
   const int type = cache_type(*cache);
   AttnParams own = params_of(d, cache, workspace);
-  if (max_prefix_pages == 0) return launch(own, *b.own, type, cache, sms, stream);
+  if (max_prefix_pages == 0)
+    return launch(own, pick(type, cache->head_dim, own.n * own.group), type, cache, sms, stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const int64_t all = int64_t(own.batch) * own.n * own.hq;
   auto part_at = [&](AttnParams &p, size_t at) {

@@ -105,6 +105,12 @@ struct AttnParams {
   float *part, *part_lse;           // [batch][n][hq][d], [batch][n][hq]
 };
 enum { kAlone = 0, kPrefix = 1, kOwn = 2 };
+// The kernels are compiled with parts (kPrefix, kOwn) and without (kAlone): asked at run time, what
+// the parts need took registers that the others lack (262001 E4M3 keys 156 -> 159 us).
+template <bool kParts>
+__device__ __forceinline__ int pass_of(const AttnParams &p) {
+  return kParts ? p.pass : int(kAlone);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -118,14 +124,16 @@ __device__ __forceinline__ int node_of(const AttnParams &p, int row) {
   return p.group == 1 ? row : int(__umulhi(uint32_t(row), p.group_magic));
 }
 // Where q of node `node` of sequence b begins; the prefix's nodes are those of all sequences.
+template <bool kParts>
 __device__ __forceinline__ int64_t q_of(const AttnParams &p, int b, int node) {
-  if (p.pass != kPrefix) return b * p.qs[0] + node * p.qs[1];
+  if (pass_of<kParts>(p) != kPrefix) return b * p.qs[0] + node * p.qs[1];
   const int seq = p.inner == 1 ? node : int(__umulhi(uint32_t(node), p.inner_magic));
   return seq * p.qs[0] + (node - seq * p.inner) * p.qs[1];
 }
 // The drafted nodes that a node attends to, of `count` there are.
+template <bool kParts>
 __device__ __forceinline__ uint64_t nodes_seen(const AttnParams &p, int b, int node, int count) {
-  if (p.pass == kPrefix) return 0;
+  if (pass_of<kParts>(p) == kPrefix) return 0;
   return (count >= 64 ? ~0ull : (1ull << count) - 1) &
          (p.tree ? p.tree[int64_t(b) * p.n + node] : ~0ull >> (63 - node));
 }
@@ -341,6 +349,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 // unit costs about as much as `extra` tiles: without that, blocks with a
 // second unit ended 7 us after the others (39 us in all).  A cut less than
 // `snap` places from a unit's end moves there: it would cost a joining.
+template <bool kParts>
 struct Line {
   int64_t total, end, unit0;        // the line's length, the run's end, where the unit begins
   int64_t runs;                     // blocks that have a run
@@ -353,14 +362,14 @@ struct Line {
   // prefix begins behind it.
   __device__ __forceinline__ int used(const AttnParams &p, int b, int &len, int &skip) const {
     skip = 0;
-    if (p.pass == kPrefix) {
+    if (pass_of<kParts>(p) == kPrefix) {
       len = shared;
       return 0;
     }
     // no slot past the table exists: such lengths end with it
     const int64_t room = int64_t(p.cache.max_pages) * p.cache.page_size;
     len = int(min(int64_t(max(p.lens[b], 0)), room));
-    if (p.pass == kOwn && len >= shared) {
+    if (pass_of<kParts>(p) == kOwn && len >= shared) {
       skip = shared;
       len -= shared;
     }
@@ -386,7 +395,7 @@ struct Line {
     units = units_;
     extra = p.extra;
     snap = p.snap;
-    shared = p.pass == kAlone ? 0 : shared_slots(p);
+    shared = pass_of<kParts>(p) == kAlone ? 0 : shared_slots(p);
     auto long_of = [&](int i) { return i < p.batch ? tiles_of(p, i) + extra : 0; };
     const int own = long_of(lane);              // of the first 32 sequences
     int64_t sum = own;
@@ -480,8 +489,8 @@ struct Line {
 // The page numbers of 32 boxes are fetched at a time, one a lane, and the
 // next 32 while those are copied: a fetch for each tile cost 1200 clocks a
 // tile, more than an E4M3 tile takes to arrive (2.8 TB/s).
-template <typename L, int NS>
-__device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map, int kv,
+template <typename L, int NS, bool kParts>
+__device__ void copy_tiles(const AttnParams &p, Line<kParts> at, const CUtensorMap *map, int kv,
                            uint32_t ring0, uint32_t full0, uint32_t empty0, uint32_t *page_ok,
                            volatile int *failed, volatile int *stale) {
   const int lane = threadIdx.x % 32;
@@ -495,7 +504,7 @@ __device__ void copy_tiles(const AttnParams &p, Line at, const CUtensorMap *map,
   for (; going && at.valid(); at.next(p)) {
     const int head = head_of(p, at.u);
     const int total = at.len + at.count;
-    const int skipped = at.skip / p.cache.page_size;
+    const int skipped = kParts ? at.skip / p.cache.page_size : 0;
     const int32_t *table = p.cache.table + at.b * p.cache.table_stride + skipped;
     auto fetch = [&](int window) {
       const int box = window * 32 + lane, i = box / page_boxes;
@@ -586,11 +595,12 @@ __device__ __forceinline__ int out_col(int nt, int t, int e) {
   return kType == kE4M3 ? 16 * (nt / 2) + 4 * t + 2 * e + (nt & 1) : 8 * nt + 2 * t + e;
 }
 
-template <int kType, int DC, int RW>
+template <int kType, int DC, int RW, bool kParts>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using L = Cfg<kType, DC, RW>;
+  using Line = attn::Line<kParts>;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t *ring = smem;
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (p.pass != kAlone) next_launch_may_begin();
+  if (pass_of<kParts>(p) != kAlone) next_launch_may_begin();
   Line at;
   at.init(p, p.hkv * p.blocks);
 
@@ -660,7 +670,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   auto q_row = [&](const Line &u, int r) {
     const int row = block_of_rows(p, u.u) * L::kRows + r, node = node_of(p, row);
     if (row >= p.rows || lane * 8 >= p.d) return make_uint4(0, 0, 0, 0);
-    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of(p, u.b, node) +
+    return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of<kParts>(p, u.b, node) +
                                             (head_of(p, u.u) * p.group + row - node * p.group) * p.qs[2] + lane * 8);
   };
   auto fetch_q = [&](const Line &u) {
@@ -756,7 +766,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int node = node_of(p, row0 + rw * 16 + g + 8 * r);
-      word[r] = node < p.n ? nodes_seen(p, at.b, node, at.count) : 0;
+      word[r] = node < p.n ? nodes_seen<kParts>(p, at.b, node, at.count) : 0;
     }
     float o[L::NT][4];
 #pragma unroll
@@ -1033,12 +1043,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (row >= p.rows) continue;
         const int h = head * p.group + row - node * p.group;
         // NaN is not nothing
-        const bool unused = p.pass != kPrefix && node >= at.count;
+        const bool unused = pass_of<kParts>(p) != kPrefix && node >= at.count;
         const bool empty = unused || (mm[r] == -INFINITY && ll[r] == 0.f);
         const float inv = empty ? 0.f : p.v_scale / ll[r];
         const float lse = empty ? -INFINITY : mm[r] - kLift<kType> + log2f(ll[r]);
         const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
-        float *sums = p.pass != kAlone ? p.part + at_row * p.d : nullptr;
+        float *sums = pass_of<kParts>(p) != kAlone ? p.part + at_row * p.d : nullptr;
         uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
         const bool f16 = kType == kF16 || (kType == kE4M3 && p.q_f16);
         auto value = [&](int i, int e) { return empty ? 0.f : res[i][2 * r + e] * inv; };
@@ -1219,7 +1229,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           st[g] = make_float2(mj[0], lj[0]);
           st[g + 8] = make_float2(mj[1], lj[1]);
         }
-        if (p.pass == kPrefix) break;                    // (joined by the third launch)
+        if (pass_of<kParts>(p) == kPrefix) break;                    // (joined by the third launch)
         __threadfence();
         named_bar(1, kConsumers * 32);
         if (tid == 0) {
@@ -1269,7 +1279,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     named_bar(1, kConsumers * 32);                       // scratch, q and *last are free again
     at = after;
   }
-  if (p.pass == kOwn && tid == 0) launch_before_has_ended();
+  if (pass_of<kParts>(p) == kOwn && tid == 0) launch_before_has_ended();
 }
 
 // -------------------------------------------------------------------- host
@@ -1281,31 +1291,32 @@ struct Variant {
   std::atomic<uint64_t> *allowed;   // bit d: device d lets fn have its shared memory
 };
 
-template <int kType, int DC, int RW>
+template <int kType, int DC, int RW, bool kParts>
 Variant variant() {
   using L = Cfg<kType, DC, RW>;
   static std::atomic<uint64_t> allowed{0};
-  return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW>), L::kSmem, L::kRows, L::kPartial,
+  return {reinterpret_cast<Kernel>(&attention_kernel<kType, DC, RW, kParts>), L::kSmem, L::kRows, L::kPartial,
           kAttnThreads, &allowed};
 }
 
 // The variants of one cache type, by head_dim up to 64, 128, 192, 256 and by
-// row groups 1, 2, 4, 8: a translation unit each.
+// row groups 1, 2, 4, 8, and the same with parts: a translation unit each.
 using Variants = Variant[4][4];
 extern const Variants kVariantsBf16, kVariantsF16, kVariantsE4M3;
+extern const Variants kPartsBf16, kPartsF16, kPartsE4M3;
 
 // The tcgen05 kernel (vg_attention_wide.cuh): by cache type, head_dim up to 64
 // and 128, one and two row tiles of 128.
 using WideVariants = Variant[3][2][2];
-extern const WideVariants kWide;
+extern const WideVariants kWide, kWideParts;
 
 // (Heads up to 128 go to the tcgen05 kernel above 32 rows.  Up to 32 the bytes
 // and not the products bound heads of 192, and those of 256 serve.)
-#define VG_ATTENTION_VARIANTS(T)                      \
-  {{variant<T, 1, 1>(), variant<T, 1, 2>()},           \
-   {variant<T, 2, 1>(), variant<T, 2, 2>()},           \
-   {{}, {}, variant<T, 3, 4>(), variant<T, 3, 8>()},  \
-   {variant<T, 4, 1>(), variant<T, 4, 2>(), variant<T, 4, 4>(), variant<T, 4, 8>()}}
+#define VG_ATTENTION_VARIANTS(T, P)                                                              \
+  {{variant<T, 1, 1, P>(), variant<T, 1, 2, P>()},                                               \
+   {variant<T, 2, 1, P>(), variant<T, 2, 2, P>()},                                               \
+   {{}, {}, variant<T, 3, 4, P>(), variant<T, 3, 8, P>()},                                       \
+   {variant<T, 4, 1, P>(), variant<T, 4, 2, P>(), variant<T, 4, 4, P>(), variant<T, 4, 8, P>()}}
 
 }  // namespace attn
 }  // namespace vg

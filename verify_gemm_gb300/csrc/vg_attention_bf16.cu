@@ -3,6 +3,6 @@
 
 namespace vg {
 namespace attn {
-const Variants kVariantsBf16 = VG_ATTENTION_VARIANTS(kBf16);
+const Variants kVariantsBf16 = VG_ATTENTION_VARIANTS(kBf16, false);
 }  // namespace attn
 }  // namespace vg

@@ -3,6 +3,6 @@
 
 namespace vg {
 namespace attn {
-const Variants kVariantsE4M3 = VG_ATTENTION_VARIANTS(kE4M3);
+const Variants kVariantsE4M3 = VG_ATTENTION_VARIANTS(kE4M3, false);
 }  // namespace attn
 }  // namespace vg

@@ -3,6 +3,6 @@
 
 namespace vg {
 namespace attn {
-const Variants kVariantsF16 = VG_ATTENTION_VARIANTS(kF16);
+const Variants kVariantsF16 = VG_ATTENTION_VARIANTS(kF16, false);
 }  // namespace attn
 }  // namespace vg

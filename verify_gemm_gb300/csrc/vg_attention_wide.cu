@@ -3,9 +3,6 @@
 
 namespace vg {
 namespace attn {
-#define VG_WIDE(T)                                      \
-  {{wide_variant<T, 1, 1>(), wide_variant<T, 1, 2>()},  \
-   {wide_variant<T, 2, 1>(), wide_variant<T, 2, 2>()}}
-const WideVariants kWide = {VG_WIDE(kBf16), VG_WIDE(kF16), VG_WIDE(kE4M3)};
+const WideVariants kWide = {VG_WIDE(kBf16, false), VG_WIDE(kF16, false), VG_WIDE(kE4M3, false)};
 }  // namespace attn
 }  // namespace vg

@@ -183,12 +183,13 @@ __device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
-template <int kCache, int DC, int NQ>
+template <int kCache, int DC, int NQ, bool kParts>
 __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
     wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
   using L = WideCfg<kCache, DC, NQ>;
   using W = WideThreads<L::kF8>;
+  using Line = attn::Line<kParts>;
   constexpr int kType = L::kType;
   extern __shared__ __align__(1024) uint8_t wide_smem[];
   if (smem_addr(wide_smem) & 1023) {                     // the swizzles need it
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_at;
-  if (p.pass != kAlone) next_launch_may_begin();
+  if (pass_of<kParts>(p) != kAlone) next_launch_may_begin();
   Line at;
   at.init(p, p.hkv * p.blocks);
 
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         const int rw = row0 + row_of(k), node = node_of(p, rw);
         qv[k] = make_uint4(0, 0, 0, 0);
         if (rw < p.rows && piece * 8 < p.d)
-          qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of(p, u.b, node) +
+          qv[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + q_of<kParts>(p, u.b, node) +
                                                    (head * p.group + rw - node * p.group) * p.qs[2] + piece * 8);
       }
     };
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       const int row0 = rb * L::kRows, row = row0 + (NQ == 2 ? q * 128 : 0) + row_in;
       const int node = node_of(p, row), h = head * p.group + row - node * p.group;
       const bool real = row < p.rows;
-      const uint64_t word = real ? nodes_seen(p, at.b, node, at.count) : 0;
+      const uint64_t word = real ? nodes_seen<kParts>(p, at.b, node, at.count) : 0;
       float m = -INFINITY, l = 0.f;                      // the maximum in use
       const int tiles = at.t1 - at.t0;
 
@@ -674,8 +675,8 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
       const int first = whole ? 0 : at.first(), final = whole ? 0 : at.final();
       const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
       uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
-      float *sums = p.pass != kAlone ? p.part + at_row * p.d : nullptr;
-      const bool unused = p.pass != kPrefix && node >= at.count;
+      float *sums = pass_of<kParts>(p) != kAlone ? p.part + at_row * p.d : nullptr;
+      const bool unused = pass_of<kParts>(p) != kPrefix && node >= at.count;
       auto store = [&](int c, const float (&y)[32], float inv, bool empty) {
         if (!real) return;
 #pragma unroll
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
         while (true) {
           if (NQ == 2 || q == 0)
             reinterpret_cast<float2 *>(to + L::kRows * L::D)[mine_row] = make_float2(m, l);
-          if (p.pass == kPrefix) break;                  // (joined by the third launch)
+          if (pass_of<kParts>(p) == kPrefix) break;                  // (joined by the third launch)
           __threadfence();
           sync_rows();
           if (tid == 0) {
@@ -816,16 +817,20 @@ __global__ void __launch_bounds__(WideThreads<kCache == kE4M3>::kThreads, 1)
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  if (p.pass == kOwn && tid == 0) launch_before_has_ended();
+  if (pass_of<kParts>(p) == kOwn && tid == 0) launch_before_has_ended();
 }
 
-template <int kCache, int DC, int NQ>
+template <int kCache, int DC, int NQ, bool kParts>
 Variant wide_variant() {
   using L = WideCfg<kCache, DC, NQ>;
   static std::atomic<uint64_t> allowed{0};
-  return {reinterpret_cast<Kernel>(&wide_kernel<kCache, DC, NQ>), L::kSmem, L::kRows, L::kPartial,
+  return {reinterpret_cast<Kernel>(&wide_kernel<kCache, DC, NQ, kParts>), L::kSmem, L::kRows, L::kPartial,
           WideThreads<L::kF8>::kThreads, &allowed};
 }
+
+#define VG_WIDE(T, P)                                         \
+  {{wide_variant<T, 1, 1, P>(), wide_variant<T, 1, 2, P>()},  \
+   {wide_variant<T, 2, 1, P>(), wide_variant<T, 2, 2, P>()}}
 
 }  // namespace attn
 }  // namespace vg

@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kJoinRows *kJoinWarps)
       const int64_t room = int64_t(own.cache.max_pages) * own.cache.page_size;
       if (shared > 0 && min(int64_t(max(own.lens[b], 0)), room) >= shared &&
           node - b * own.n < (own.counts ? own.counts[b] : own.n)) {
-        Line line;                                             // the prefix's unit on its line
-        line.tiles = Line::tiles_for(first, shared);
+        Line<true> line;                                         // the prefix's unit on its line
+        line.tiles = Line<true>::tiles_for(first, shared);
         line.extra = first.extra;
         line.snap = first.snap;
         const int units = first.hkv * first.blocks;
