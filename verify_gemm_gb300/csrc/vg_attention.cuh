@@ -1046,7 +1046,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool unused = pass_of<kParts>(p) != kPrefix && node >= at.count;
         const bool empty = unused || (mm[r] == -INFINITY && ll[r] == 0.f);
         const float inv = empty ? 0.f : p.v_scale / ll[r];
-        const float lse = empty ? -INFINITY : mm[r] - kLift<kType> + log2f(ll[r]);
         const int64_t at_row = (int64_t(at.b) * p.n + node) * p.hq + h;
         float *sums = pass_of<kParts>(p) != kAlone ? p.part + at_row * p.d : nullptr;
         uint16_t *out = static_cast<uint16_t *>(p.out) + at_row * p.d;
@@ -1089,12 +1088,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               *reinterpret_cast<uint32_t *>(out + col) = pack_out(v0, v1, f16);
           }
         }
-        if (t == 0 && first_warp) {
-          if (sums)
-            p.part_lse[at_row] = lse;
-          else if (p.lse)
-            p.lse[at_row] = lse * kLn2;
-        }
+        float *to = sums ? p.part_lse : p.lse;
+        if (to && t == 0 && first_warp)
+          to[at_row] = empty ? -INFINITY : (mm[r] - kLift<kType> + log2f(ll[r])) * (sums ? 1.f : kLn2);
       }
     };
     if constexpr (kSolo) {
