@@ -21,6 +21,15 @@
 // top-p), and the tokens of that bin alone are sorted.  A top-k up to 200 goes without: all
 // blocks know the largest logits of 256 groups of a row's threads, the k-th largest of those is
 // at most the k-th largest of all, and the tokens down to it, few more than k, are sorted.
+//
+// What bounds it: for a few rows the exchanges between a cluster's blocks, some 1.7 us each (one row of
+// 151936 BF16 logits, top-k 50 and top-p 0.95: 14 us, of which 2 to the largest, 2 to the list, 3 for its
+// gathering and order, 2 for the draw; top-p alone 28), and instructions that are fetched for the
+// first time; for many rows, of 35 instructions an element for a weight and its place in the bins, the
+// barriers between steps of which the first block of a row does some alone.  256 rows with settings of
+// their own 125 us (78 MB: 0.6 TB/s), 128 FP32 rows with their distributions 114 us (156 MB).
+// (Two searches by codes alone, one level of bins after another, took 550 us and 1.7 ms: the
+// bins of codes near zero are nearly empty and those of the body full.)
 #include <algorithm>
 #include <cmath>
 
@@ -71,6 +80,13 @@ __constant__ uint32_t kPowers[64] = {
 // What a row's weights need: z in units of 1/64 is (max - x) c.
 struct Scale {
   float top, c, c_low, cap;          // c as two floats; differences beyond cap weigh nothing
+};
+// A row's settings: read by its first block alone, as all blocks have to take the same way.
+struct Settings {
+  float temperature, top_p, min_p;
+  int top_k;
+  Scale scale;
+  double min_at, pad;                // T ln(min_p)
 };
 
 // a + b, a * b + c, two at a time (mul2 and add2 are those of vg_rows.cuh).
@@ -249,11 +265,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   __shared__ __align__(16) Found told;
   __shared__ __align__(16) ulonglong2 shares[kMaxCluster];
   __shared__ uint32_t powers[64];
-  __shared__ Scale told_scale;
-  __shared__ double min_at;          // T ln(min_p)
+  __shared__ __align__(16) Settings settings;
   __shared__ uint64_t scan[kDrawWarps];
   __shared__ uint32_t listed;
   __shared__ int n_keep;
+  __shared__ uint64_t weights[kSmallK];
   uint32_t *bin_lo = reinterpret_cast<uint32_t *>(draw_smem), *bin_hi = bin_lo + kBins;
   uint64_t *local = reinterpret_cast<uint64_t *>(draw_smem), *list = local + kLocal;
   uint4 *held = reinterpret_cast<uint4 *>(draw_smem + kListBytes);
@@ -281,21 +297,27 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       }
     }
   }
-  const float temperature = p.temperature ? p.temperature[row] : 1.f;
-  const float min_p = p.min_p ? p.min_p[row] : 0.f, top_p = p.top_p ? p.top_p[row] : 1.f;
-  const int top_k = p.top_k ? p.top_k[row] : 0;
   if (warp == 0) {
     powers[lane] = kPowers[lane];
     powers[lane + 32] = kPowers[lane + 32];
     if (lane == 0) {
       listed = 0;
-      const double c = 64 * 1.4426950408889634074 / double(temperature);
-      told_scale.c = c > 3.4e38 ? 3.4028234e38f : float(c);
-      told_scale.c_low = c > 3.4e38 ? 0.f : float(c - double(told_scale.c));
-      told_scale.cap = fminf(4096.f / told_scale.c, 3.4028234e38f);
-      // (over an infinite temperature every finite logit weighs 1)
-      min_at = !(min_p > 0.f) ? 0.0 : temperature == INFINITY ? (min_p > 1.f ? 1e300 : -1e300)
-                                                              : double(temperature) * log(double(min_p));
+      if (rank == 0) {
+        Settings now{};
+        now.temperature = p.temperature ? p.temperature[row] : 1.f;
+        now.top_p = p.top_p ? p.top_p[row] : 1.f;
+        now.min_p = p.min_p ? p.min_p[row] : 0.f;
+        now.top_k = p.top_k ? p.top_k[row] : 0;
+        const double c = 64 * 1.4426950408889634074 / double(now.temperature);
+        now.scale.c = c > 3.4e38 ? 3.4028234e38f : float(c);
+        now.scale.c_low = c > 3.4e38 ? 0.f : float(c - double(now.scale.c));
+        now.scale.cap = fminf(4096.f / now.scale.c, 3.4028234e38f);
+        // (over an infinite temperature every finite logit weighs 1)
+        now.min_at = !(now.min_p > 0.f)              ? 0.0
+                     : now.temperature == INFINITY ? (now.min_p > 1.f ? 1e300 : -1e300)
+                                                   : double(now.temperature) * log(double(now.min_p));
+        settings = now;
+      }
     }
   }
   if constexpr (kHeld) {
@@ -375,8 +397,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
                    "r"(lane / groups), "f"(v)
                    : "memory");
     }
+    if (rank == 0 && warp == 0) {
+      __syncwarp();
+      const uint64_t *from = reinterpret_cast<const uint64_t *>(&settings);
+      if (lane && lane < int(blocks))
+#pragma unroll
+        for (int k = 0; k < int(sizeof(Settings) / 16); ++k)
+          cluster_store(reinterpret_cast<ulonglong2 *>(&settings) + k, lane, from[2 * k], from[2 * k + 1]);
+    }
   }
   sync_all();
+  const float temperature = settings.temperature, top_p = settings.top_p, min_p = settings.min_p;
+  const int top_k = settings.top_k;
   const int entries = int(blocks) * kDrawWarps;
   float top = -INFINITY, its[kGroups / 32];
 #pragma unroll
@@ -430,7 +462,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       each([&](int r, float, float) { store(r, r == first ? 1.f : 0.f, r + 1 == first ? 1.f : 0.f); });
     return;
   }
-  Scale scale = told_scale;
+  Scale scale = settings.scale;
   scale.top = top;
   const int up = p.bits - 30;
   auto weigh = [&](float y) {
@@ -581,19 +613,24 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (wb && at < room) to_list[at] = uint64_t(~code_of<float>(b)) << 32 | uint32_t(r + 1);
     }
   };
-  auto gather_list = [&] {
-    uint32_t n = 0, mine_at = 0, mine_n = 0;             // lane r: block r's
+  auto count_list = [&](uint32_t &mine_n, uint32_t &mine_at) {   // lane r: block r's; -1: too many
     const uint32_t count_at = static_cast<uint32_t>(__cvta_generic_to_shared(&listed));
+    mine_n = 0;
     if (lane < int(blocks))
       asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %1, %2; ld.shared::cluster.u32 %0, [at]; }"
                    : "=r"(mine_n)
                    : "r"(count_at), "r"(lane)
                    : "memory");
     mine_at = uint32_t(scan_up(mine_n, lane)) - mine_n;
-    n = __shfl_sync(~0u, mine_at + mine_n, 31);
-    if (n > kSorted || __any_sync(~0u, mine_n > room)) return -1;
+    const uint32_t n = __shfl_sync(~0u, mine_at + mine_n, 31);
+    return n > kSorted || __any_sync(~0u, mine_n > room) ? -1 : int(n);
+  };
+  auto gather_list = [&] {
+    uint32_t mine_at, mine_n;
+    const int n = count_list(mine_n, mine_at);
+    if (n < 0) return -1;
     int size = 64;
-    while (size < int(n)) size *= 2;
+    while (size < n) size *= 2;
     const uint32_t list_at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
     if (blocks > 1) {                                    // a warp, or several, for each block
       const uint32_t share = kDrawWarps / blocks, r = warp / share;
@@ -607,14 +644,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         list[to + i] = v;
       }
     }
-    for (int i = int(n) + tid; i < size; i += kDrawThreads) list[i] = ~uint64_t(0);
+    for (int i = n + tid; i < size; i += kDrawThreads) list[i] = ~uint64_t(0);
     __syncthreads();
+    return n;
+  };
+  auto sort_list = [&](int n) {
+    int size = 64;
+    while (size < n) size *= 2;
     sort_up(list, size);
-    return int(n);
   };
   auto logit_at = [&](uint64_t e) { return logit_of<float>(~uint32_t(e >> 32)); };
   // The smallest logit that weighs min_p.
-  const float f_min = min_p > 0.f ? fminf(__double2float_ru(double(top) + min_at), top) : -INFINITY;
+  const float f_min = min_p > 0.f ? fminf(__double2float_ru(double(top) + settings.min_at), top) : -INFINITY;
   // In the sorted list of n: how many are kept, with the target of what is before and in it
   // (limit: of tokens; target 0: no limit of weight).  Every thread has up to four entries.
   auto cut_list = [&](int n, int limit, uint64_t target, bool of_list) {
@@ -676,19 +717,28 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       each([&](int r, float a, float b) { push(a, b, r, [&](float y, int) { return y >= floor; }); });
     }
     sync_all();
-    if (rank == 0) {
-      const int n = gather_list();
-      if (n < 0) {
-        if (tid == 0) told.state = kTooMany;
-      } else {
+    uint32_t unused[2];
+    // (every block comes to the same answer: the counts stay until all have them)
+    too_many = count_list(unused[0], unused[1]) < 0;
+    if (too_many) {
+      sync_all();
+    } else {
+      // without a distribution the other blocks end when the first has their lists
+      if (!out && rank) {
+        cluster_arrive();
+        cluster_wait();
+        return;
+      }
+      if (rank == 0) {
+        const int n = gather_list();
+        if (!out && blocks > 1) cluster_arrive();
+        sort_list(n);
         cut_list(n, top_k, 0, true);
         const int keep = n_keep;
         // in the order of the indices: each token's sum before it
         uint64_t w = 0, before = 0, all = 0;
         const uint32_t index = tid < keep ? uint32_t(list[tid]) : 0;
-        if (tid < keep) w = weigh(logit_at(list[tid]));
-        uint64_t *weights = local;                       // (has been read)
-        if (tid < keep) weights[tid] = w;
+        if (tid < keep) weights[tid] = w = weigh(logit_at(list[tid]));
         __syncthreads();
         if (warp * 32 < keep)
           for (int i = 0; i < keep; ++i) {
@@ -703,16 +753,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           const uint64_t want = part_of(u, all, exact);  // the first running sum above it
           if (tid < keep && want >= before && want < before + w) p.tokens[row * p.draws + d] = int32_t(index);
         }
+        if (!out) {
+          if (blocks > 1) cluster_wait();
+          return;
+        }
         if (tid == 0) {
           const uint64_t e = list[keep - 1];
           told = Found{0, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all, 0.f, 0.f, 0};
         }
+        tell(&told);
       }
-      tell(&told);
-    }
-    sync_all();
-    too_many = told.state == kTooMany;
-    if (!too_many) {
+      sync_all();
       done = true;
       x_f = logit_of<float>(told.code);
       i_f = told.index;
@@ -765,6 +816,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (rank == 0) {
         const int n = gather_list();
         if (n >= 0) {
+          sort_list(n);
           if constexpr (kMass) cut_list(n, n, f.target, false);
           else if (tid == 0) n_keep = int(f.target);
           __syncthreads();
