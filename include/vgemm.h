@@ -476,9 +476,11 @@ vg_status vg_verify_plan_destroy(vg_verify_plan *plan);
 
 /* ------------------------------------- the rest of a verify round
  * What runs between the products of a verify round and behind its head:
- * rotary positions with the append to a paged key/value cache, attention of
- * a tree of drafted tokens over that cache, the probabilities of logits and
- * the verification of the drafted tokens.
+ * rotary positions with the append to a paged key/value cache (and norms of
+ * the heads of q and k before it), attention of a tree of drafted tokens
+ * over that cache (and of a batch that shares a prefix), the probabilities
+ * of logits, draws from truncated distributions of them and the
+ * verification of the drafted tokens.
  *
  * A sequence's tree has n nodes: node 0 is the last committed token, nodes
  * 1..n-1 are drafted, every parent comes before its children, and a plain

@@ -7,7 +7,8 @@ mtp7-device-confidence engine card's Design table); MXFP8 and groupwise
 INT4 weights as well, and a fused verify pass over a layer stack with RMS
 norms and the gated activation.  ``verify_round`` has what a verify round
 runs around these products: rotary positions with the append to a paged
-cache, tree attention over it, probabilities and the drafts' verification.
+cache, with norms of the heads where a model has them, tree attention over it,
+behind a shared prefix, too, probabilities, draws and the drafts' verification.
 
 Every step runs in the CUDA kernels of ``libvgemm.so`` (C ABI declared in
 ``include/vgemm.h``); this module only marshals torch tensors (device

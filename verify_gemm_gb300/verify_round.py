@@ -1,7 +1,8 @@
 """The operators of a verify round between and behind its products: rotary
-positions with the append to a paged cache, attention of a tree of drafted
-tokens over that cache, the probabilities of logits and the verification of
-the drafted tokens.
+positions with the append to a paged cache (and norms of the heads before it),
+attention of a tree of drafted tokens over that cache (and behind a prefix that a
+batch shares), the probabilities of logits, draws from truncated distributions
+of them and the verification of the drafted tokens.
 
 Every step runs in the CUDA kernels of ``libvgemm.so``.  The calls go through
 ``_vgtorch.so``, which checks the tensors, allocates the outputs and calls the
