@@ -130,6 +130,38 @@ def test_rows_and_vocabularies(vg, dtype, rows, vocab):
     check(vg, x, u)
 
 
+@pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 20000), (torch.float32, 9001)])
+@pytest.mark.parametrize("rows", [305, 511, 512, 513])
+@pytest.mark.parametrize("which", ["all", "slow rows last", "none slow", "all slow", "top-k alone", "top-p alone"])
+def test_rows_begin_in_any_order(vg, dtype, vocab, rows, which):
+    """Many rows, of which those that take longest may begin first: each is what it is among few."""
+    g = torch.Generator().manual_seed(rows)
+    x = randn(g, rows, vocab, dtype=dtype, scale=2.5)
+    u = torch.rand((rows, 2), generator=g).to(DEV)
+    T, k, p, mp = settings(g, rows, vocab)
+    if which != "all":
+        k, p = [40] * rows, [1.0] * rows
+    if which in ("slow rows last", "all slow"):
+        n = 3 if which == "slow rows last" else rows
+        k[rows - n:], p[rows - n:], T[rows - n:] = [0] * n, [0.8] * n, [0.9] * n
+    t = lambda v, d: torch.tensor(v, dtype=d, device=DEV)                # noqa: E731
+    args = dict(temperature=t(T, torch.float32), top_k=t(k, torch.int32), top_p=t(p, torch.float32),
+                min_p=t(mp, torch.float32))
+    if which.endswith("alone"):
+        name = which.replace("-", "_").split()[0]
+        args = {name: t([(250 if r % 3 else 30) if name == "top_k" else 0.2 + r % 5 / 5 for r in range(rows)],
+                        torch.int32 if name == "top_k" else torch.float32)}
+    out = torch.full((rows, vocab), 7.0, device=DEV)
+    tokens = vg.sample(x, u, out=out, **args)
+    assert torch.equal(tokens, vg.sample(x, u, **args))
+    for at in range(0, rows, 61):
+        few = torch.empty_like(out[at:at + 61])
+        part = vg.sample(x[at:at + 61], u[at:at + 61], out=few, **{n: a[at:at + 61] for n, a in args.items()})
+        assert torch.equal(part, tokens[at:at + 61]) and torch.equal(few, out[at:at + 61]), at
+    check(vg, x[-4:], u[-4:], *[None if n not in args else args[n][-4:].tolist()
+                                for n in ("temperature", "top_k", "top_p", "min_p")])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("k", [0, -3, 1, 2, 50, 199, 200, 201, 1000, 4999, 5000, 5001, 2 ** 31 - 1])
 def test_top_k(vg, dtype, k):

@@ -27,7 +27,7 @@
 // gathering and order, 2 for the draw; top-p alone 28), and instructions that are fetched for the
 // first time; for many rows, of 35 instructions an element for a weight and its place in the bins, the
 // barriers between steps of which the first block of a row does some alone.  256 rows with settings of
-// their own 125 us (78 MB: 0.6 TB/s), 128 FP32 rows with their distributions 114 us (156 MB).
+// their own 107 us (78 MB: 0.7 TB/s), 128 FP32 rows with their distributions 107 us (156 MB).
 // (Two searches by codes alone, one level of bins after another, took 550 us and 1.7 ms: the
 // bins of codes near zero are nearly empty and those of the body full.)
 #include <algorithm>
@@ -63,6 +63,7 @@ struct DrawParams {
   int32_t *tokens;
   float *out;
   int draws, chunk, bits;            // units of a warp; a weight of 1 is 2^bits
+  int rows;                          // at most one a thread, where those that take longest begin first
   int lead;                          // elements between the 16-byte border that x is and the first row
 };
 
@@ -257,7 +258,7 @@ __device__ __forceinline__ int shift_for(uint32_t span) {
   return (span >> s) < kBins - 1 ? s : s + 1;
 }
 
-template <typename T, bool kHeld>
+template <typename T, bool kHeld, bool kOrdered>
 __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_constant__ DrawParams p) {
   extern __shared__ __align__(16) uint8_t draw_smem[];
   __shared__ float tops[kGroups];
@@ -275,8 +276,27 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   uint64_t *local = reinterpret_cast<uint64_t *>(draw_smem), *list = local + kLocal;
   uint4 *held = reinterpret_cast<uint4 *>(draw_smem + kListBytes);
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
-  const int64_t row = blockIdx.x / blocks;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int64_t row = blockIdx.x / blocks;
+  if constexpr (kOrdered) {
+    // The rows with a search over the bins before those without.  (The blocks of a row whose settings
+    // change meanwhile may see other orders: each still has a row, and the first's settings.)
+    bool slow = false;
+    if (tid < p.rows) {
+      const int k = p.top_k ? p.top_k[tid] : 0;
+      const float q = p.top_p ? p.top_p[tid] : 1.f, t = p.temperature ? p.temperature[tid] : 1.f;
+      slow = t > 0.f && (k > kSmallK || (k <= 0 && q > 0.f && q < 1.f));
+    }
+    const uint32_t those = __ballot_sync(~0u, slow);
+    if (lane == 0) scan[warp] = __popc(those);
+    __syncthreads();
+    const int count = lane < kDrawWarps ? int(scan[lane]) : 0;
+    const int before = __reduce_add_sync(~0u, lane < warp ? count : 0) + __popc(those & ((1u << lane) - 1));
+    const int all = __reduce_add_sync(~0u, count), place = slow ? before : all + tid - before;
+    if (place == int(row)) n_keep = tid;
+    __syncthreads();
+    row = n_keep;
+  }
   const T *x = static_cast<const T *>(p.x);
   const int64_t lo = p.lead + row * p.stride, hi = lo + p.V;
   const int64_t end = (hi + 7) / 8;                      // units, on the grid of 16-byte borders
@@ -1022,7 +1042,7 @@ template <typename T>
 cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) {
   const int64_t units = p.V / 8 + 2, size = 8 * sizeof(T);
   // As few blocks a row as hold it in 76 KB each (two blocks an SM; 256 rows of 151936 BF16 logits
-  // with settings of their own 125 us on 4 blocks of 76 KB, 159 on 8 of 38), and more while all rows'
+  // with settings of their own 107 us on 4 blocks of 76 KB, 148 on 8 of 38), and more while all rows'
   // fit the device about at once (41 such rows 60 us on 4, 42 on 8); 16, more than a portable cluster, for a
   // few rows alone (8 rows of top-p 40 us, 42 on 8).
   int c = 1;
@@ -1032,10 +1052,18 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   const int64_t warps = int64_t(c) * kDrawWarps;
   p.chunk = int((units + warps - 1) / warps);
   const int64_t share = int64_t(p.chunk) * kDrawWarps * size;
-  static std::atomic<uint64_t> allowed[2];
   const bool held = share <= kDrawShareMax;
-  void (*fn)(DrawParams) = held ? &sample_kernel<T, true> : &sample_kernel<T, false>;
-    if (const cudaError_t e = allow(fn, kListBytes + (held ? kDrawShareMax : 0), allowed[held])) return e;
+  // In what order they begin: with more blocks than run at once the rows that take longest should not be
+  // the last (256 rows of mixed settings 107 us, in their own order 122; 138 rows of equal ones, for
+  // which it is a search for nothing, 57.5 and 55.1).  Rows of short blocks keep theirs: the settings
+  // take a microsecond to read.
+  const bool ordered = held && rows <= kDrawThreads && rows * c > 2 * sms && share >= 32 * 1024 && (p.top_k || p.top_p);
+  p.rows = int(std::min<int64_t>(rows, kDrawThreads));
+  static std::atomic<uint64_t> allowed[3];
+  void (*fn)(DrawParams) = ordered ? &sample_kernel<T, true, true>
+                           : held ? &sample_kernel<T, true, false>
+                                  : &sample_kernel<T, false, false>;
+  if (const cudaError_t e = allow(fn, kListBytes + (held ? kDrawShareMax : 0), allowed[held + ordered])) return e;
   return launch_clusters(fn, unsigned(rows) * unsigned(c), kDrawThreads, c, kListBytes + (held ? int(share) : 0), st, p);
 }
 
