@@ -666,10 +666,23 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     __syncthreads();
     return n;
   };
-  auto sort_list = [&](int n) {
+  auto sort_list = [&](int n, auto short_too) {
     int size = 64;
     while (size < n) size *= 2;
-    sort_up(list, size);
+    if (!decltype(short_too)::value || size > 256) {
+      sort_up(list, size);
+      return;
+    }
+    // a short one, all different: each goes to where as many are before it, counted by 512 / size threads
+    const int parts = kDrawThreads / size, i = tid / parts;
+    const uint64_t v = i < n ? list[i] : 0;
+    int before = 0;
+#pragma unroll 4
+    for (int j = tid % parts; j < n; j += parts) before += list[j] < v;
+    for (int w = 1; w < parts; w *= 2) before += __shfl_xor_sync(~0u, before, w);
+    __syncthreads();
+    if (i < n && tid % parts == 0) list[before] = v;
+    __syncthreads();
   };
   auto logit_at = [&](uint64_t e) { return logit_of<float>(~uint32_t(e >> 32)); };
   // The smallest logit that weighs min_p.
@@ -757,7 +770,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (rank == 0) {
         const int n = gather_list();
         if (!out && blocks > 1) cluster_arrive();
-        sort_list(n);
+        sort_list(n, std::true_type{});
         cut_list(n, top_k, 0, true);
         const int keep = n_keep;
         // in the order of the indices: each token's sum before it
@@ -841,7 +854,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       if (rank == 0) {
         const int n = gather_list();
         if (n >= 0) {
-          sort_list(n);
+          sort_list(n, std::false_type{});
           if constexpr (kMass) cut_list(n, n, f.target, false);
           else if (tid == 0) n_keep = int(f.target);
           __syncthreads();
