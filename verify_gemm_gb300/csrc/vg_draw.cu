@@ -643,12 +643,16 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     const uint32_t n = __shfl_sync(~0u, mine_at + mine_n, 31);
     return n > kSorted || __any_sync(~0u, mine_n > room) ? -1 : int(n);
   };
+  auto pad_list = [&](int n) {
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kDrawThreads) list[i] = ~uint64_t(0);
+    __syncthreads();
+  };
   auto gather_list = [&] {
     uint32_t mine_at, mine_n;
     const int n = count_list(mine_n, mine_at);
     if (n < 0) return -1;
-    int size = 64;
-    while (size < n) size *= 2;
     const uint32_t list_at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
     if (blocks > 1) {                                    // a warp, or several, for each block
       const uint32_t share = kDrawWarps / blocks, r = warp / share;
@@ -662,8 +666,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         list[to + i] = v;
       }
     }
-    for (int i = n + tid; i < size; i += kDrawThreads) list[i] = ~uint64_t(0);
-    __syncthreads();
+    pad_list(n);
     return n;
   };
   auto sort_list = [&](int n, auto short_too) {
@@ -754,22 +757,54 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     } else {
       each([&](int r, float a, float b) { push(a, b, r, [&](float y, int) { return y >= floor; }); });
     }
+    // All blocks tell their counts, and those with few give the first their tokens, a place of its own
+    // each, before they meet (fetched by it afterwards: a microsecond more).
+    __syncthreads();
+    const uint32_t few = kSorted / blocks, my_count = listed;
+    if (tid < int(blocks)) cluster_store(&shares[rank], uint32_t(tid), my_count, 0);
+    if (blocks > 1 && my_count <= few)
+      for (uint32_t i = tid; i < my_count; i += kDrawThreads) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(list + rank * few + i));
+        asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %0, 0; st.shared::cluster.u64 [at], %1; }" ::"r"(at),
+                     "l"(local[i])
+                     : "memory");
+      }
     sync_all();
-    uint32_t unused[2];
-    // (every block comes to the same answer: the counts stay until all have them)
-    too_many = count_list(unused[0], unused[1]) < 0;
+    const uint32_t count = lane < int(blocks) ? uint32_t(shares[lane].x) : 0;
+    const int in_all = __reduce_add_sync(~0u, int(min(count, uint32_t(kSorted + 1))));
+    const bool given = !__any_sync(~0u, count > few);
+    too_many = in_all > kSorted || __any_sync(~0u, count > room);
     if (too_many) {
-      sync_all();
+      sync_all();                                        // (the counts stay until all have read them)
     } else {
       // without a distribution the other blocks end when the first has their lists
       if (!out && rank) {
-        cluster_arrive();
-        cluster_wait();
+        if (!given) {
+          cluster_arrive();
+          cluster_wait();
+        }
         return;
       }
       if (rank == 0) {
-        const int n = gather_list();
-        if (!out && blocks > 1) cluster_arrive();
+        int n = in_all;
+        if (given && blocks > 1) {
+          constexpr int kEach = kSorted / kDrawThreads;  // of a block's place, by the threads that are its own
+          const uint32_t threads = kDrawThreads / blocks, r = uint32_t(tid) / threads, i0 = uint32_t(tid) % threads;
+          const uint32_t there = __shfl_sync(~0u, count, int(r));
+          const uint32_t to = __shfl_sync(~0u, uint32_t(scan_up(count, lane)) - count, int(r));
+          uint64_t v[kEach];
+#pragma unroll
+          for (int k = 0; k < kEach; ++k)
+            if (i0 + k * threads < there) v[k] = list[r * few + i0 + k * threads];
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < kEach; ++k)
+            if (i0 + k * threads < there) list[to + i0 + k * threads] = v[k];
+          pad_list(n);
+        } else {
+          n = gather_list();
+          if (!out && blocks > 1) cluster_arrive();
+        }
         sort_list(n, std::true_type{});
         cut_list(n, top_k, 0, true);
         const int keep = n_keep;
@@ -792,7 +827,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           if (tid < keep && want >= before && want < before + w) p.tokens[row * p.draws + d] = int32_t(index);
         }
         if (!out) {
-          if (blocks > 1) cluster_wait();
+          if (!given) cluster_wait();
           return;
         }
         if (tid == 0) {
