@@ -197,6 +197,30 @@ def test_min_p(vg, dtype, mp):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 30])
+@pytest.mark.parametrize("loud", [100, 129, 190, 300, 700, 1100, 2500])
+def test_large_logits_in_one_place(vg, dtype, rows, loud):
+    """A small top-k whose tokens all lie with one of a row's blocks, the first, one between or the last."""
+    g = torch.Generator().manual_seed(loud)
+    V = 151936
+    x = randn(g, rows, V, dtype=dtype, scale=1.0)
+    for r in range(rows):
+        at = [0, 70001, V - loud][(r + loud) % 3]
+        x[r, at:at + loud] += 20
+    u = torch.rand((rows, 3), generator=g).to(DEV)
+    n = min(rows, 3)
+    check(vg, x[:n], u[:n], k=[200, 199, 50][:n], p=[0.9, 1.0, 0.99][:n])
+    args = [torch.tensor(v, device=DEV) for v in ([1.0] * rows, [200, 199, 50] * 10, [0.9, 1.0, 0.99] * 10)]
+    args = [args[0], args[1][:rows].to(torch.int32), args[2][:rows]]
+    out = torch.empty((rows, V), device=DEV)
+    got = vg.sample(x, u, args[0], top_k=args[1], top_p=args[2], out=out)
+    for r in range(0, rows, 7):                          # (alone: on more blocks)
+        alone = torch.empty((1, V), device=DEV)
+        part = vg.sample(x[r:r + 1], u[r:r + 1], args[0][:1], top_k=args[1][r:r + 1], top_p=args[2][r:r + 1], out=alone)
+        assert torch.equal(part[0], got[r]) and torch.equal(alone[0], out[r])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_equal_logits(vg, dtype):
     """Rows of one value, of two, in order and against it: the lowest index goes first."""
     V = 20011

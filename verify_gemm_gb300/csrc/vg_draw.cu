@@ -23,11 +23,11 @@
 // at most the k-th largest of all, and the tokens down to it, few more than k, are sorted.
 //
 // What bounds it: for a few rows the exchanges between a cluster's blocks, some 1.7 us each (one row of
-// 151936 BF16 logits, top-k 50 and top-p 0.95: 14 us, of which 2 to the largest, 2 to the list, 3 for its
-// gathering and order, 2 for the draw; top-p alone 28), and instructions that are fetched for the
+// 151936 BF16 logits, top-k 50 and top-p 0.95: 12.5 us, of which 3 to the largest, 3.5 to the list at the first block, 2 for its
+// order and cut; top-p alone 28), and instructions that are fetched for the
 // first time; for many rows, of 35 instructions an element for a weight and its place in the bins, the
 // barriers between steps of which the first block of a row does some alone.  256 rows with settings of
-// their own 107 us (78 MB: 0.7 TB/s), 128 FP32 rows with their distributions 107 us (156 MB).
+// their own 106 us (78 MB: 0.7 TB/s), 128 FP32 rows with their distributions 106 us (156 MB).
 // (Two searches by codes alone, one level of bins after another, took 550 us and 1.7 ms: the
 // bins of codes near zero are nearly empty and those of the body full.)
 #include <algorithm>
@@ -1090,7 +1090,7 @@ template <typename T>
 cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) {
   const int64_t units = p.V / 8 + 2, size = 8 * sizeof(T);
   // As few blocks a row as hold it in 76 KB each (two blocks an SM; 256 rows of 151936 BF16 logits
-  // with settings of their own 107 us on 4 blocks of 76 KB, 148 on 8 of 38), and more while all rows'
+  // with settings of their own 106 us on 4 blocks of 76 KB, 148 on 8 of 38), and more while all rows'
   // fit the device about at once (41 such rows 60 us on 4, 42 on 8); 16, more than a portable cluster, for a
   // few rows alone (8 rows of top-p 40 us, 42 on 8).
   int c = 1;
@@ -1103,7 +1103,7 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   const bool held = share <= kDrawShareMax;
   // In what order they begin: with more blocks than run at once the rows that take longest should not be
   // the last (256 rows of mixed settings 107 us, in their own order 122; 138 rows of equal ones, for
-  // which it is a search for nothing, 57.5 and 55.1).  Rows of short blocks keep theirs: the settings
+  // which it is a search for nothing, 57 and 55).  Rows of short blocks keep theirs: the settings
   // take a microsecond to read.
   const bool ordered = held && rows <= kDrawThreads && rows * c > 2 * sms && share >= 32 * 1024 && (p.top_k || p.top_p);
   p.rows = int(std::min<int64_t>(rows, kDrawThreads));
