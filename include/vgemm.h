@@ -651,9 +651,10 @@ vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
  *     of these the ones at least min_p times as probable as the first (<= 0 or
  *       NaN: all; at least one).
  * A token is the first index whose running sum of probabilities over what is
- * kept, in the order of the indices, exceeds u times their sum.  Weights are good
- * to some 2^-29 of themselves and sums are exact in integers, so the same call
- * gives the same tokens.
+ * kept, in the order of the indices, exceeds u times their sum.  Sums are exact in
+ * integers, so the same call gives the same tokens.  They are of weights good to
+ * 2^-27.6 of themselves and rounded down to 2^-46 of the largest (2^-56 from 2^18
+ * tokens on), so that a row loses 2^-28 of the largest at most.
  * With T <= 0 the first largest logit alone is kept.  A logit of -infinity is never
  * kept.  A row with a NaN, with a T of NaN, or with +infinity and T > 0, and a row of
  * nothing but -infinity have the token -1.

@@ -8,11 +8,10 @@
 // logit x_f, index i_f.  The token drawn is the first index whose running sum
 // over what is kept exceeds u times the whole.
 //
-// Sums are integers (a weight of 1 is 2^bits with sums below 2^62), so that no order
-// of addition changes what is kept or drawn, and weights are exact to some
-// 2^-29 of themselves: a draw is a comparison of u with the boundaries of 150000
-// tokens, and with sums good to 2^-22 one row in some hundred would end on the
-// neighbour.
+// Sums are integers, so that no order of addition changes what is kept or drawn, and weights are
+// good to 2^-27.6 of themselves, rounded down to units of which V are 2^-28 of the largest or less: a draw
+// is a comparison of u with the boundaries of 150000 tokens, and with sums good to 2^-22 one row in some
+// hundred would end on the neighbour.
 //
 // A cluster of blocks a row; a block holds a run of it in shared memory, and
 // each warp a run of that, so that the warps' order is the index order.  The
@@ -47,7 +46,20 @@ constexpr int kGroups = 256;                  // of which the largest logit is k
 static_assert(kMaxCluster * kDrawWarps == kGroups, "at least one group a warp");
 constexpr int kSmallK = 200;
 constexpr int kListBytes = (kLocal + kSorted) * 8;   // (and the bins, which are read before a list is made)
-static_assert(kListBytes >= 2 * kBins * 4, "room for the bins");
+static_assert(kListBytes >= 3 * kBins * 4, "room for the bins");
+
+// A weight of 1 is 2^kOne and every weight is rounded down, so that the V of a row lose V 2^-kOne of the largest
+// at most, 2^-28.  Rows of fewer than 2^18 tokens have sums of 64 bits, longer ones (kLong) of 96: there a pair of each thread of a
+// warp, what a thread has of a row that is held, and a small top-k still sum to less than 2^64.  (151936
+// tokens in 96 bits: 8 rows of top-p 44.6 us and not 40.8, 256 rows of mixed settings 110 and not 106.  2^27 tokens in 64
+// bits left weights 35 of them: all that lay 35 octaves down, some 2^-9 of a row, was never drawn.)
+using Wide = unsigned __int128;
+constexpr int64_t kLongVocab = 1 << 18;
+template <bool kLong>
+using SumOf = std::conditional_t<kLong, Wide, uint64_t>;
+template <bool kLong>
+constexpr int kOne = kLong ? 56 : 46;
+static_assert(kSmallK < 1 << 8 && kDrawShareMax / 2 / kDrawThreads < 1 << 8, "sums of 64 bits of weights of 2^56");
 
 template <typename T>
 struct alignas(2 * sizeof(T)) Pair {
@@ -62,7 +74,7 @@ struct DrawParams {
   const int32_t *top_k;
   int32_t *tokens;
   float *out;
-  int draws, chunk, bits;            // units of a warp; a weight of 1 is 2^bits
+  int draws, chunk;                  // units of a warp
   int rows;                          // at most one a thread, where those that take longest begin first
   int lead;                          // elements between the 16-byte border that x is and the first row
 };
@@ -101,7 +113,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// The weight of a finite logit x is w 2^(up - (bin >> 6)) (up = bits - 30, and w some 2^30).  With
+// The weight of a finite logit x is w 2^(kOne - 30 - (bin >> 6)) (w some 2^30), rounded down.  With
 // z = (k + r) / 64, k whole, |r| <= 1/2, it is 2^-(k / 64) from a table times
 // 2^-(r / 64) by its series to the third power (the fourth is 2^-34).  max - x is exact in FP32 for 16-bit logits but for
 // those that are 2^-16 of the largest or less; for FP32 ones what it loses is
@@ -111,7 +123,7 @@ constexpr float kMagic = 12582912.f;           // 1.5 2^23: what is added to it 
 constexpr int kMagicBits = 0x4B400000;
 struct Weight {
   int w, k;
-  __device__ __forceinline__ uint64_t value(int up) const { return uint64_t(uint32_t(w)) << up >> min(k >> 6, 63); }
+  __device__ __forceinline__ uint64_t value(int one) const { return uint64_t(uint32_t(w)) << (one - 30) >> min(k >> 6, 63); }
   __device__ __forceinline__ uint32_t bin() const { return min(uint32_t(k), uint32_t(kBins - 1)); }
   // w in the units of its bin: the last one has all weights below 2^-32
   __device__ __forceinline__ uint32_t in_bin() const { return uint32_t(w) >> min(max(k >> 6, 31) - 31, 31); }
@@ -163,8 +175,9 @@ __device__ __forceinline__ float logit_of(uint32_t code) {
   return __uint_as_float(b);
 }
 
-// floor(a s) for 0 <= a < 1
-__device__ __forceinline__ uint64_t part_of(float a, uint64_t s, bool &exact) {
+// floor(a s) for 0 <= a < 1, and whether that is a s; s below 2^96
+template <typename S>
+__device__ __forceinline__ S part_of(float a, S s, bool &exact) {
   if (!(a > 0.f)) {
     exact = true;
     return 0;
@@ -173,29 +186,72 @@ __device__ __forceinline__ uint64_t part_of(float a, uint64_t s, bool &exact) {
   const uint32_t e = b >> 23;
   const uint64_t m = e ? (b & 0x7FFFFF) | 0x800000 : b & 0x7FFFFF;
   const int right = 150 - int(e ? e : 1);      // a = m 2^-right, right >= 24
-  const uint64_t lo = m * s, hi = __umul64hi(m, s);
-  if (right >= 64) {
-    const uint64_t v = right < 128 ? hi >> (right - 64) : 0;
-    exact = false;                             // (some bits are lost, or the product is 0)
-    return v;
+  if constexpr (sizeof(S) == 8) {
+    const uint64_t lo = m * s, hi = __umul64hi(m, s);
+    if (right >= 64) {
+      exact = false;                           // (some bits are lost, or the product is 0)
+      return right < 128 ? hi >> (right - 64) : 0;
+    }
+    exact = (lo & ((uint64_t(1) << right) - 1)) == 0;
+    return hi << (64 - right) | lo >> right;
+  } else {
+    const Wide v = s * m, whole = right < 128 ? v >> right : Wide(0);
+    exact = right < 128 && whole << right == v;
+    return whole;
   }
-  exact = (lo & ((uint64_t(1) << right) - 1)) == 0;
-  return hi << (64 - right) | lo >> right;
+}
+// How many of weight w it takes to weigh `target`, if not more than 2^29.
+template <typename S>
+__device__ __forceinline__ uint64_t count_for(S target, uint64_t w) {
+  uint32_t fewer = 0;                            // these weigh less
+#pragma unroll 1
+  for (uint32_t bit = 1u << 28; bit; bit /= 2)
+    if (Wide(fewer | bit) * w < target) fewer |= bit;
+  return target == 0 ? 0 : fewer + 1;
 }
 
-__device__ __forceinline__ uint64_t scan_up(uint64_t v, int lane) {
+__device__ __forceinline__ uint64_t shuffle_up(uint64_t v, int lanes) { return __shfl_up_sync(~0u, v, lanes); }
+__device__ __forceinline__ Wide shuffle_up(Wide v, int lanes) {
+  return Wide(__shfl_up_sync(~0u, uint32_t(v >> 64), lanes)) << 64 | __shfl_up_sync(~0u, uint64_t(v), lanes);
+}
+template <typename S>
+__device__ __forceinline__ S scan_up(S v, int lane) {
 #pragma unroll
   for (int w = 1; w < 32; w *= 2) {
-    const uint64_t y = __shfl_up_sync(~0u, v, w);
+    const S y = shuffle_up(v, w);
     if (lane >= w) v += y;
   }
   return v;
+}
+// The sum of a warp, by 27 bits at a time.
+template <typename S, typename V>
+__device__ __forceinline__ S warp_sum(V v) {
+  constexpr uint32_t k27 = (1u << 27) - 1;
+  S sum = __reduce_add_sync(~0u, uint32_t(v) & k27) + (S(__reduce_add_sync(~0u, uint32_t(v >> 27) & k27)) << 27);
+  if constexpr (sizeof(V) == 8) {
+    sum += S(__reduce_add_sync(~0u, uint32_t(v >> 54))) << 54;
+  } else {
+    sum += S(__reduce_add_sync(~0u, uint32_t(v >> 54) & k27)) << 54;
+    sum += S(__reduce_add_sync(~0u, uint32_t(v >> 81))) << 81;
+  }
+  return sum;
+}
+// A sum as two words.
+__device__ __forceinline__ uint64_t upper(uint64_t) { return 0; }
+__device__ __forceinline__ uint64_t upper(Wide v) { return uint64_t(v >> 64); }
+template <typename S>
+__device__ __forceinline__ S sum_of(const ulonglong2 &v) {
+  if constexpr (sizeof(S) == 8) return v.x;
+  else return Wide(v.y) << 64 | v.x;
 }
 
 // Sorts n (a power of two, at least 64) entries, the smallest first; the whole block.
 // A thread holds entries 2 t and 2 t + 1 of every 1024: exchanges within a warp's 64
 // entries go by shuffles, the others by shared memory.
 __device__ __forceinline__ uint64_t other(uint64_t v, int lanes) { return __shfl_xor_sync(~0u, v, lanes); }
+__device__ __forceinline__ Wide other(Wide v, int lanes) {
+  return Wide(__shfl_xor_sync(~0u, uint32_t(v >> 64), lanes)) << 64 | __shfl_xor_sync(~0u, uint64_t(v), lanes);
+}
 __device__ __forceinline__ void sort_up(uint64_t *v, int n) {
 #pragma unroll 1
   for (int size = 64; size <= n; size *= 2) {
@@ -237,20 +293,22 @@ __device__ __forceinline__ void sort_up(uint64_t *v, int n) {
 }
 
 // What the first block of a row tells the others.
-struct Found {
+template <typename S>
+struct alignas(16) Found {
   uint32_t bin, code;                // the last token's bin; its logit
   int32_t index, state;              // its index
-  uint64_t target, whole;            // the count or weight wanted of the bin; the weight of what is kept
+  S target, whole;                   // the count or weight wanted of the bin; the weight of what is kept
   float from, to;                    // the bin's logits
-  uint64_t pad;
 };
 enum { kGo = 0, kAll = 1, kTooMany = 2 };      // state; kAll: nothing is left out
 // Where a search by codes is: codes [lo, hi], bins of 2^shift of them from hi down, the last
 // bin with all that is below; what is wanted of them.
+template <typename S>
 struct Search {
   uint32_t hi, lo;
   int shift, done;                   // 1: hi is the code, 2: there are fewer
-  uint64_t target, ties;             // ties: how many of the code
+  S target;
+  uint64_t ties;                     // how many of the code
 };
 __device__ __forceinline__ int shift_for(uint32_t span) {
   // the smallest with span >> shift below the last bin
@@ -258,8 +316,12 @@ __device__ __forceinline__ int shift_for(uint32_t span) {
   return (span >> s) < kBins - 1 ? s : s + 1;
 }
 
-template <typename T, bool kHeld, bool kOrdered>
+template <typename T, bool kHeld, bool kOrdered, bool kLong>
 __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_constant__ DrawParams p) {
+  using Sum = SumOf<kLong>;
+  using Found = vg::Found<Sum>;
+  using Search = vg::Search<Sum>;
+  constexpr int kOne = vg::kOne<kLong>;
   extern __shared__ __align__(16) uint8_t draw_smem[];
   __shared__ float tops[kGroups];
   __shared__ __align__(16) ulonglong2 sums[kMaxCluster * kDrawWarps];
@@ -267,12 +329,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   __shared__ __align__(16) ulonglong2 shares[kMaxCluster];
   __shared__ uint32_t powers[64];
   __shared__ __align__(16) Settings settings;
-  __shared__ uint64_t scan[kDrawWarps];
+  __shared__ Sum scan[kDrawWarps];
   __shared__ uint32_t listed;
   __shared__ int n_keep;
   __shared__ float list_floor;
   __shared__ uint64_t weights[kSmallK];
-  uint32_t *bin_lo = reinterpret_cast<uint32_t *>(draw_smem), *bin_hi = bin_lo + kBins;
+  uint32_t *bin_lo = reinterpret_cast<uint32_t *>(draw_smem), *bin_hi = bin_lo + kBins, *bin_top = bin_hi + kBins;
   uint64_t *local = reinterpret_cast<uint64_t *>(draw_smem), *list = local + kLocal;
   uint4 *held = reinterpret_cast<uint4 *>(draw_smem + kListBytes);
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
@@ -430,7 +492,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   sync_all();
   const float temperature = settings.temperature, top_p = settings.top_p, min_p = settings.min_p;
   const int top_k = settings.top_k;
-  const int entries = int(blocks) * kDrawWarps;
+  const int entries = int(blocks) * kDrawWarps, me = int(rank) * kDrawWarps + warp;
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kGroups / 32; ++i) top = max_nan(top, tops[i * 32 + lane]);
@@ -482,11 +544,10 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   }
   Scale scale = settings.scale;
   scale.top = top;
-  const int up = p.bits - 30;
   auto weigh = [&](float y) {
     Weight a, b;
     weigh2<T>(scale, powers, y, y, a, b);
-    return a.value(up);
+    return a.value(kOne);
   };
 
   // What is kept: y > x_f, and those equal to it up to index i_f.
@@ -498,12 +559,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     if (i_f >= 0) k |= y == x_f && index <= i_f;
     return k;
   };
-  // The block's 512 threads' sums of `mine`, up to each and in all.
-  auto scan_block = [&](uint64_t v, uint64_t &whole) {
-    uint64_t run = scan_up(v, lane);
+  // The block's 512 threads' sums of `v`, up to each and in all.
+  auto scan_block = [&](auto v, Sum &whole) {
+    const Sum in_warp = scan_up(v, lane);
     __syncthreads();                                     // (scan has been read)
-    if (lane == 31) scan[warp] = run;
+    if (lane == 31) scan[warp] = in_warp;
     __syncthreads();
+    Sum run = in_warp;
     whole = 0;
 #pragma unroll
     for (int w = 0; w < kDrawWarps; ++w) {
@@ -511,6 +573,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       whole += scan[w];
     }
     return run;
+  };
+  // The warps' weights of what is kept, for all blocks.
+  using Mass = SumOf<kLong && !kHeld>;
+  auto tell_mass = [&](Mass mass) {
+    const Sum sum = warp_sum<Sum>(mass);
+    if (lane < int(blocks)) cluster_store(&sums[me], lane, uint64_t(sum), upper(sum));
   };
   // Tells the other blocks what this one has put into `what`.
   auto tell = [&](auto *what) {
@@ -524,42 +592,48 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
   };
   // Which bin the running sum over all blocks' bins reaches the target in (0: of top_p of the
-  // whole and `beyond`); kWeights: the bins have two words, kScaled: and a unit each.  A block
+  // whole and `beyond`).  kOf: of counts, of weights in the bins' units, of weights.  A block
   // adds up a share of the bins, four a lane, one block's a lane, and the block whose share holds the
   // target tells the others.  (One block that took all bins of 16 blocks was at it for 5 us.)
-  auto find = [&](auto weights, auto scaled, uint64_t target, uint64_t beyond) {
+  enum { kCounts, kScaled, kWeights };
+  auto find = [&](auto of, Sum target, Sum beyond) {
+    constexpr int kOf = decltype(of)::value, kWords = kOf == kCounts ? 1 : kOf == kWeights && kLong ? 3 : 2;
+    using Bin = SumOf<kWords == 3>;
+    using Part = SumOf<kLong && kOf != kCounts>;
     sync_all();
     const int quad = warp * (32 / int(blocks)) + lane / int(blocks), share = kBins / int(blocks);
     const uint32_t bin0 = rank * share + quad * 4;
     const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(bin_lo + bin0));
-    uint32_t a[4], b[4] = {};
-    auto fetch = [&](uint32_t (&w)[4], uint32_t at) {
+    Bin bin[4] = {};
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      uint32_t w[4];
       asm volatile("{ .reg .b32 at; mapa.shared::cluster.u32 at, %4, %5; ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [at]; }"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(at), "r"(lane % blocks)
+                   : "r"(here + k * kBins * 4), "r"(lane % blocks)
                    : "memory");
-    };
-    fetch(a, here);
-    if constexpr (decltype(weights)::value) fetch(b, here + kBins * 4);
-    uint64_t v[4], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = uint64_t(b[k]) << 32 | a[k];
+      for (int i = 0; i < 4; ++i) bin[i] |= Bin(w[i]) << (32 * k);
+    }
     for (uint32_t w = 1; w < blocks; w *= 2)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += other(v[k], int(w));
+      for (int k = 0; k < 4; ++k) bin[k] += other(bin[k], int(w));
+    Part v[4], sum = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if constexpr (decltype(scaled)::value) v[k] = v[k] << up >> (bin0 >> 6);
+      v[k] = bin[k];
+      if constexpr (kOf == kScaled) v[k] = v[k] << (kOne - 30) >> (bin0 >> 6);
       sum += v[k];
     }
     const bool counts = lane % blocks == 0;              // (all lanes of a quad have its sums)
-    uint64_t mine_all, run = scan_block(counts ? sum : 0, mine_all), whole = 0;
+    Sum mine_all, run = scan_block(counts ? sum : Part(0), mine_all), whole = 0;
     if (blocks > 1) {
-      if (tid < int(blocks)) cluster_store(&shares[rank], uint32_t(tid), mine_all, 0);
+      if (tid < int(blocks)) cluster_store(&shares[rank], uint32_t(tid), uint64_t(mine_all), upper(mine_all));
       sync_all();
       for (uint32_t r = 0; r < blocks; ++r) {
-        if (r < rank) run += shares[r].x;
-        whole += shares[r].x;
+        const Sum part = sum_of<Sum>(shares[r]);
+        if (r < rank) run += part;
+        whole += part;
       }
     } else {
       whole = mine_all;
@@ -569,7 +643,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     if (target == 0) {
       bool exact;
       target = part_of(top_p, whole + beyond, exact);
-      target = max(target + !exact, uint64_t(1));
+      if (!exact || target == 0) ++target;
     }
     if (target > whole) {
       f.state = kAll;
@@ -577,7 +651,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       sync_all();                                        // (the shares are read before they are written again)
       return f;
     }
-    uint64_t before = run - sum;
+    Sum before = run - sum;
     const bool it = counts && before < target && target <= run;
     if (it) {
       uint32_t k0 = 0;
@@ -613,8 +687,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     sync_all();
     return told;
   };
-  auto clear_bins = [&] {
-    for (int i = tid; i < 2 * kBins; i += kDrawThreads) bin_lo[i] = 0;
+  auto clear_bins = [&](int words) {
+    for (int i = tid; i < words * kBins; i += kDrawThreads) bin_lo[i] = 0;
     if (tid == 0) listed = 0;
     __syncthreads();
   };
@@ -639,7 +713,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
                    : "=r"(mine_n)
                    : "r"(count_at), "r"(lane)
                    : "memory");
-    mine_at = uint32_t(scan_up(mine_n, lane)) - mine_n;
+    mine_at = uint32_t(scan_up(uint64_t(mine_n), lane)) - mine_n;
     const uint32_t n = __shfl_sync(~0u, mine_at + mine_n, 31);
     return n > kSorted || __any_sync(~0u, mine_n > room) ? -1 : int(n);
   };
@@ -692,7 +766,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   const float f_min = min_p > 0.f ? fminf(__double2float_ru(double(top) + settings.min_at), top) : -INFINITY;
   // In the sorted list of n: how many are kept, with the target of what is before and in it
   // (limit: of tokens; target 0: no limit of weight).  Every thread has up to four entries.
-  auto cut_list = [&](int n, int limit, uint64_t target, bool of_list) {
+  auto cut_list = [&](int n, int limit, Sum target, bool of_list) {
     uint64_t v[4], sum = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -700,12 +774,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       v[k] = i < min(n, limit) ? weigh(logit_at(list[i])) : 0;
       sum += v[k];
     }
-    uint64_t whole;
-    uint64_t run = scan_block(sum, whole) - sum;
+    Sum whole, run = scan_block(sum, whole) - sum;
     if (of_list && top_p < 1.f) {
       bool exact;
       target = part_of(top_p, whole, exact);
-      target = max(target + !exact, uint64_t(1));
+      if (!exact || target == 0) ++target;
     }
     if (tid == 0) n_keep = 0;
     __syncthreads();
@@ -720,9 +793,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     __syncthreads();
   };
   bool too_many = false, done = false, summed = false;
-  uint64_t whole = 0;
-  const int me = int(rank) * kDrawWarps + warp;
-
+  Sum whole = 0;
   if (top_k > 0 && top_k <= kSmallK && top_k < p.V) {
     // ----------------------------------------------------------- a small top-k
     // the upper 16 bits of the code of the top_k-th largest of the groups' largest, by one warp: the
@@ -791,7 +862,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           constexpr int kEach = kSorted / kDrawThreads;  // of a block's place, by the threads that are its own
           const uint32_t threads = kDrawThreads / blocks, r = uint32_t(tid) / threads, i0 = uint32_t(tid) % threads;
           const uint32_t there = __shfl_sync(~0u, count, int(r));
-          const uint32_t to = __shfl_sync(~0u, uint32_t(scan_up(count, lane)) - count, int(r));
+          const uint32_t to = __shfl_sync(~0u, uint32_t(scan_up(uint64_t(count), lane)) - count, int(r));
           uint64_t v[kEach];
 #pragma unroll
           for (int k = 0; k < kEach; ++k)
@@ -832,7 +903,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         }
         if (tid == 0) {
           const uint64_t e = list[keep - 1];
-          told = Found{0, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all, 0.f, 0.f, 0};
+          told = Found{0, ~uint32_t(e >> 32), int32_t(uint32_t(e)), kGo, 0, all, 0.f, 0.f};
         }
         tell(&told);
       }
@@ -844,9 +915,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
   } else {
     // A round: the last token by counts (kMass: weights) among what is kept so far.
-    auto round = [&](auto by_weight, uint64_t target) {
+    auto round = [&](auto by_weight, Sum target) {
       constexpr bool kMass = decltype(by_weight)::value;
-      clear_bins();
+      clear_bins(2);
       each([&](int r, float y0, float y1) {
         const bool k0 = kept(y0, r), k1 = kept(y1, r + 1);
         if constexpr (kMass) {
@@ -864,27 +935,23 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
           if (k1) atomicAdd(bin_lo + bin_of(scale, y1), 1u);
         }
       });
-      const Found f = find(by_weight, by_weight, target, 0);
+      const Found f = find(std::integral_constant<int, kMass ? kScaled : kCounts>{}, target, 0);
       if (f.state == kAll) return;
       if (kMass && f_min >= f.to) return;                // min-p ends it before
       // kMass: what lies in the bins before is kept, and is weighed on the way
-      uint64_t mass = 0;
+      Mass mass = 0;
       each([&](int r, float a, float b) {
         if constexpr (kMass) {
           const bool ka = a >= f.to, kb = b >= f.to;
           if (ka || kb) {
             Weight wa, wb;
             weigh2<T>(scale, powers, a, b, wa, wb);
-            mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
+            mass += (ka ? wa.value(kOne) : 0) + (kb ? wb.value(kOne) : 0);
           }
         }
         push(a, b, r, [&](float y, int i) { return y >= f.from && y < f.to && kept(y, i); });
       });
-      if constexpr (kMass) {
-#pragma unroll
-        for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
-        if (lane < int(blocks)) cluster_store(&sums[me], lane, mass, 0);
-      }
+      if constexpr (kMass) tell_mass(mass);
       sync_all();
       if (rank == 0) {
         const int n = gather_list();
@@ -897,11 +964,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
             // each kept token's weight to the sum of the warp that has it, and the sums to the other blocks
             for (int i = tid; i < n_keep; i += kDrawThreads) {
               const uint32_t warp_of = (uint32_t(list[i]) + uint32_t(lo & 7)) / uint32_t(8 * p.chunk);
-              atomicAdd(reinterpret_cast<unsigned long long *>(&sums[warp_of].x), weigh(logit_at(list[i])));
+              const uint64_t w = weigh(logit_at(list[i]));
+              const uint64_t low = atomicAdd(reinterpret_cast<unsigned long long *>(&sums[warp_of].x), w) + w;
+              if (kLong && low < w) atomicAdd(reinterpret_cast<unsigned long long *>(&sums[warp_of].y), 1ull);
             }
             __syncthreads();
             for (int i = entries + tid; i < entries * int(blocks); i += kDrawThreads)
-              cluster_store(&sums[i % entries], uint32_t(i / entries), sums[i % entries].x, 0);
+              cluster_store(&sums[i % entries], uint32_t(i / entries), sums[i % entries].x, sums[i % entries].y);
           }
         }
         if (tid == 0) {
@@ -923,7 +992,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       }
       summed = kMass && !too_many;
     };
-    if (top_k > 0 && top_k < p.V) round(std::false_type{}, uint64_t(top_k));
+    if (top_k > 0 && top_k < p.V) round(std::false_type{}, Sum(top_k));
     if (!too_many && top_p < 1.f) round(std::true_type{}, 0);
   }
   if (too_many) {
@@ -931,7 +1000,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     // Looks for the logit at which the running count (kMass: weight) of the order reaches the
     // target, among those above `floor`; kMass: the target is top_p of their sum and
     // `beyond`, the weight of what is kept of those equal to the floor.
-    auto search = [&](auto mass, float floor, uint64_t target, uint64_t beyond) {
+    auto search = [&](auto mass, float floor, Sum target, Sum beyond) {
       constexpr bool kMass = decltype(mass)::value;
       Search s;
       s.hi = code_of<T>(top);
@@ -941,7 +1010,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       s.done = 0;
       bool first = true;
       while (true) {
-        clear_bins();
+        clear_bins(kLong ? 3 : 2);
         each([&](int, float y0, float y1) {
 #pragma unroll 1
           for (int k = 0; k < 2; ++k) {
@@ -953,13 +1022,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
               const uint64_t w = weigh(y);
               const uint32_t low = uint32_t(w);
               const uint32_t more = uint32_t(w >> 32) + (atomicAdd(bin_lo + b, low) + low < low);
-              if (more) atomicAdd(bin_hi + b, more);
+              if (more && atomicAdd(bin_hi + b, more) + more < more && kLong) atomicAdd(bin_top + b, 1u);
             } else {
               atomicAdd(bin_lo + b, 1u);
             }
           }
         });
-        const Found f = find(mass, std::false_type{}, first && kMass ? 0 : s.target, beyond);
+        const Found f = find(std::integral_constant<int, kMass ? kWeights : kCounts>{}, first && kMass ? Sum(0) : s.target, beyond);
         first = false;
         s.target = f.target;
         if (f.state == kAll) {
@@ -974,7 +1043,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         s.shift = shift_for(s.hi - s.lo);
         if (s.done) {
           const uint64_t w = kMass ? weigh(logit_of<T>(s.hi)) : 1;
-          s.ties = (s.target + w - 1) / w;
+          s.ties = count_for(s.target, w);
           return s;
         }
       }
@@ -982,7 +1051,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     x_f = -INFINITY;
     uint64_t ties = 0;                                   // how many equal to x_f are kept
     if (top_k > 0 && top_k < p.V) {
-      const Search s = search(std::false_type{}, -INFINITY, uint64_t(top_k), 0);
+      const Search s = search(std::false_type{}, -INFINITY, Sum(top_k), 0);
       if (s.done == 1) {
         x_f = logit_of<T>(s.hi);
         ties = s.ties;
@@ -990,12 +1059,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     if (top_p < 1.f) {
       const uint64_t w = ties ? weigh(x_f) : 0;
-      const Search s = search(std::true_type{}, x_f, 0, ties * w);
+      const Search s = search(std::true_type{}, x_f, 0, Sum(ties) * w);
       if (s.done == 1) {
         x_f = logit_of<T>(s.hi);
         ties = s.ties;
       } else if (w) {
-        ties = min(ties, (s.target + w - 1) / w);
+        ties = min(ties, count_for(s.target, w));
       }
     }
     // the index of the last of them
@@ -1014,7 +1083,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
       uint32_t left = uint32_t(ties - before);
       each([&](int r, float a, float b) {
         const uint32_t here = uint32_t(a == x_f) + uint32_t(b == x_f);
-        uint32_t run = uint32_t(scan_up(here, lane));
+        uint32_t run = uint32_t(scan_up(uint64_t(here), lane));
         const uint32_t all = __shfl_sync(~0u, run, 31);
         run -= here;
         if (left > run && left <= run + here) {
@@ -1035,44 +1104,41 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     }
     // -------------------------------------------------------------- the draw
     if (!summed) {
-      uint64_t mass = 0;
+      Mass mass = 0;
       each([&](int r, float a, float b) {
         const bool ka = kept(a, r), kb = kept(b, r + 1);
         if (!ka && !kb) return;
         Weight wa, wb;
         weigh2<T>(scale, powers, a, b, wa, wb);
-        mass += (ka ? wa.value(up) : 0) + (kb ? wb.value(up) : 0);
+        mass += (ka ? wa.value(kOne) : 0) + (kb ? wb.value(kOne) : 0);
       });
-#pragma unroll
-      for (int w = 16; w; w /= 2) mass += __shfl_xor_sync(~0u, mass, w);
-      if (lane < int(blocks)) cluster_store(&sums[me], lane, mass, 0);
+      tell_mass(mass);
       sync_all();
     }
-    const uint64_t mass = sums[me].x;
-    uint64_t my_mass = 0;                                // of the warps before this one
+    const Sum mass = sum_of<Sum>(sums[me]);
+    Sum my_mass = 0;                                     // of the warps before this one
     for (int i = lane; i < entries; i += 32) {
-      whole += sums[i].x;
-      my_mass += i < me ? sums[i].x : 0;
+      const Sum part = sum_of<Sum>(sums[i]);
+      whole += part;
+      if (i < me) my_mass += part;
     }
-#pragma unroll
-    for (int w = 16; w; w /= 2) {
-      whole += __shfl_xor_sync(~0u, whole, w);
-      my_mass += __shfl_xor_sync(~0u, my_mass, w);
-    }
+    whole = warp_sum<Sum>(whole);
+    my_mass = warp_sum<Sum>(my_mass);
     for (int d = 0; d < p.draws; ++d) {
       float u = p.u[row * p.draws + d];
       u = u >= 1.f ? 0x1.fffffep-1f : u;
       bool exact;
-      const uint64_t want = part_of(u, whole, exact);    // the first running sum above it
+      const Sum want = part_of(u, whole, exact);         // the first running sum above it
       if (want < my_mass || want >= my_mass + mass) continue;
-      uint64_t run = my_mass;
+      Sum run = my_mass;
       bool found = false;
       each([&](int r, float a, float b) {
         if (found) return;
         Weight w0, w1;
         weigh2<T>(scale, powers, a, b, w0, w1);
-        const uint64_t wa = kept(a, r) ? w0.value(up) : 0, sum = wa + (kept(b, r + 1) ? w1.value(up) : 0);
-        const uint64_t to = scan_up(sum, lane), from = run + to - sum;
+        const uint64_t wa = kept(a, r) ? w0.value(kOne) : 0, sum = wa + (kept(b, r + 1) ? w1.value(kOne) : 0);
+        const uint64_t to = scan_up(sum, lane);
+        const Sum from = run + (to - sum);
         if (want >= from && want < run + to) p.tokens[row * p.draws + d] = want < from + wa ? r : r + 1;
         run += __shfl_sync(~0u, to, 31);
         found = run > want;
@@ -1081,7 +1147,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   }
   if (!out) return;
   // ------------------------------------------------------- the distribution
-  const float c = scale.c * (1.f / 64), inv = 1.f / (float(whole) * exp2f(float(-p.bits)));
+  const float c = scale.c * (1.f / 64), inv = 1.f / (float(uint64_t(whole >> (kLong ? 20 : 0))) * exp2f(float((kLong ? 20 : 0) - kOne)));
   auto share = [&](float y, int r) { return kept(y, r) ? (y == top ? 1.f : ex2((y - top) * c)) * inv : 0.f; };
   each([&](int r, float a, float b) { store(r, share(a, r), share(b, r + 1)); });
 }
@@ -1107,11 +1173,16 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   // take a microsecond to read.
   const bool ordered = held && rows <= kDrawThreads && rows * c > 2 * sms && share >= 32 * 1024 && (p.top_k || p.top_p);
   p.rows = int(std::min<int64_t>(rows, kDrawThreads));
-  static std::atomic<uint64_t> allowed[3];
-  void (*fn)(DrawParams) = ordered ? &sample_kernel<T, true, true>
-                           : held ? &sample_kernel<T, true, false>
-                                  : &sample_kernel<T, false, false>;
-  if (const cudaError_t e = allow(fn, kListBytes + (held ? kDrawShareMax : 0), allowed[held + ordered])) return e;
+  static std::atomic<uint64_t> allowed[5];
+  const bool is_long = p.V >= kLongVocab;
+  static_assert(kMaxCluster * kDrawShareMax / 2 / 4 >= kLongVocab, "what is not held is long");
+  using Kernel = void (*)(DrawParams);
+  constexpr Kernel kernels[5] = {&sample_kernel<T, true, false, false>, &sample_kernel<T, true, true, false>,
+                                 &sample_kernel<T, true, false, true>, &sample_kernel<T, true, true, true>,
+                                 &sample_kernel<T, false, false, true>};
+  const int which = held ? 2 * is_long + ordered : 4;
+  const Kernel fn = kernels[which];
+  if (const cudaError_t e = allow(fn, kListBytes + (held ? kDrawShareMax : 0), allowed[which])) return e;
   return launch_clusters(fn, unsigned(rows) * unsigned(c), kDrawThreads, c, kListBytes + (held ? int(share) : 0), st, p);
 }
 
@@ -1149,9 +1220,6 @@ extern "C" vg_status vg_sample(const vg_sample_desc *d, vg_stream_t stream) {
   p.tokens = d->tokens;
   p.out = d->out;
   p.draws = d->draws;
-  p.bits = 62;
-  while ((int64_t(1) << (62 - p.bits)) < d->vocab) --p.bits;
-  if (p.bits > 60) p.bits = 60;
   cudaError_t e;
   if (d->type == VG_TYPE_BF16) e = launch_sample<__nv_bfloat16>(p, d->rows, sms, as_cuda(stream));
   else if (d->type == VG_TYPE_FP16) e = launch_sample<__half>(p, d->rows, sms, as_cuda(stream));
