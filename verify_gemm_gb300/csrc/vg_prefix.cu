@@ -9,6 +9,12 @@
 // tcgen05 kernel's partial results; for the rows' outputs, which lie by columns, they change over in
 // shared memory.
 //
+// The grid may begin while the launches before still write what it reads: every load of that lies behind the
+// wait for them, and none goes by the read-only path, which promises memory that is not written meanwhile.
+// Plain loads, and not ones that pass by L1: a row's states are read twice and by each of its groups of
+// columns (4 rows of 2 cache heads of 128 over 25643 keys 24.8 us, 29.1 past L1).  64 registers a thread, so
+// that four blocks an SM begin as soon as an SM is left (64 trees of 8 nodes 279 us, with 76 registers 285).
+//
 // Measured (the whole of vg_prefix_attention): 48 sequences of 1 node, 40 query and 8 cache heads of
 // 128 in BF16, 8003 + up to 1201 keys, 69 us (91 with the join at the end of the first launch); of that
 // the prefix takes 24, the own keys 38, this launch some 7, and what overlaps is not
@@ -28,22 +34,22 @@ __device__ __forceinline__ float4 scaled_sum(float4 a, float wa, float4 b, float
 
 // Columns 4 c .. 4 c + 3 of a row in a partial result.
 __device__ __forceinline__ float4 partial_at(const PrefixJoin &j, const float *part, int row, int c) {
-  if (j.wide) return __ldg(reinterpret_cast<const float4 *>(part) + c * j.rows + row);
+  if (j.wide) return reinterpret_cast<const float4 *>(part)[c * j.rows + row];
   // mma.sync fragments: [row group][tile of 8 columns][lane][4]
   const int tiles = j.columns / 8, half = row % 16 / 8;
   const int nt = j.e4m3 ? c / 4 * 2 : c / 2, t = j.e4m3 ? c % 4 : c % 2 * 2;
   const float2 *at = reinterpret_cast<const float2 *>(part) + (row / 16 * tiles + nt) * 64 + (row % 8 * 4 + t) * 2 + half;
   if (j.e4m3) {                                // even columns in one tile, odd ones in the next
-    const float2 even = __ldg(at), odd = __ldg(at + 64);
+    const float2 even = at[0], odd = at[64];
     return make_float4(even.x, odd.x, even.y, odd.y);
   }
-  const float2 a = __ldg(at), b = __ldg(at + 2);
+  const float2 a = at[0], b = at[2];
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // kSplit warps share out a row's partial results, and each takes kGroups groups of four columns.
 template <int kSplit, int kGroups>
-__global__ void __launch_bounds__(kJoinRows *kJoinWarps)
+__global__ void __launch_bounds__(kJoinRows *kJoinWarps, 4)
     prefix_join_kernel(const __grid_constant__ AttnParams own, const __grid_constant__ AttnParams first,
                        const __grid_constant__ PrefixJoin j) {
   constexpr int kCols = kJoinWarps / kSplit * kGroups;         // groups of four columns of the block
@@ -96,7 +102,7 @@ __global__ void __launch_bounds__(kJoinRows *kJoinWarps)
       if (here(g)) v[g] = __ldcg(reinterpret_cast<const float4 *>(first.part + at * own.d) + c0 + g);
   }
   auto place = [&](int blk) { return first.partial + (int64_t(blk) * 2 + (blk == from)) * j.partial; };
-  auto state = [&](int blk) { return __ldg(reinterpret_cast<const float2 *>(place(blk) + j.state) + in); };
+  auto state = [&](int blk) { return reinterpret_cast<const float2 *>(place(blk) + j.state)[in]; };
   const int end = cut ? to : -1;
   float m = -INFINITY;
 #pragma unroll 4
