@@ -90,17 +90,21 @@ __constant__ uint32_t kPowers[64] = {
     638450708, 631573326, 624770026, 618040012, 611382493, 604796689, 598281827, 591837143,
     585461881, 579155293, 572916640, 566745190, 560640218, 554601009, 548626854, 542717053};
 
-// What a row's weights need: z in units of 1/64 is (max - x) c.
+// What a row's weights need: z in units of 1/64 is (top - h x) c, with top = h max.  h is a power of two: 1/4 for
+// temperatures from 2^64 on, by which differences past FP32's range count, 2^64 for those below 2^-120, of which c = 64 log2 e
+// / T itself is past it, and 1 for all others.
 struct Scale {
-  float top, c, c_low, cap;          // c as two floats; differences beyond cap weigh nothing
+  float top, minus;                  // minus: -h
+  float c, c_low, cap;               // c as two floats; differences beyond cap weigh nothing
 };
 // A row's settings: read by its first block alone, as all blocks have to take the same way.
 struct Settings {
   float temperature, top_p, min_p;
   int top_k;
   Scale scale;
-  double min_at, pad;                // T ln(min_p)
+  double min_at;                     // T ln(min_p)
 };
+static_assert(sizeof(Settings) == 48, "goes by 16 bytes");
 
 // a + b, a * b + c, two at a time (mul2 and add2 are those of vg_rows.cuh).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -131,12 +135,12 @@ struct Weight {
 // Of two logits at a time.
 template <typename T>
 __device__ __forceinline__ void weigh2(const Scale &s, const uint32_t *powers, float x0, float x1, Weight &w0, Weight &w1) {
-  const float2 x = make_float2(-x0, -x1), all = add2(both(s.top), x);
+  const float2 x = make_float2(x0, x1), minus = both(s.minus), all = fma2(x, minus, both(s.top));
   const float2 d = make_float2(fminf(all.x, s.cap), fminf(all.y, s.cap));
   float2 low = mul2(d, both(s.c_low));
   if constexpr (std::is_same_v<T, float>) {
     const float2 b = add2(all, both(-s.top)), c = add2(all, make_float2(-b.x, -b.y));
-    const float2 e = add2(add2(both(s.top), make_float2(-c.x, -c.y)), add2(x, make_float2(-b.x, -b.y)));
+    const float2 e = add2(add2(both(s.top), make_float2(-c.x, -c.y)), fma2(x, minus, make_float2(-b.x, -b.y)));
     const float2 more = fma2(e, both(s.c), low);
     low = make_float2(all.x < s.cap ? more.x : low.x, all.y < s.cap ? more.y : low.y);
   }
@@ -156,7 +160,7 @@ __device__ __forceinline__ void weigh2(const Scale &s, const uint32_t *powers, f
 }
 // Its bin alone.
 __device__ __forceinline__ uint32_t bin_of(const Scale &s, float x) {
-  const float d = fminf(s.top - x, s.cap);
+  const float d = fminf(fmaf(x, s.minus, s.top), s.cap);
   return min(uint32_t(__float_as_int(fmaf(d, s.c, kMagic)) - kMagicBits), uint32_t(kBins - 1));
 }
 
@@ -391,9 +395,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
         now.top_p = p.top_p ? p.top_p[row] : 1.f;
         now.min_p = p.min_p ? p.min_p[row] : 0.f;
         now.top_k = p.top_k ? p.top_k[row] : 0;
-        const double c = 64 * 1.4426950408889634074 / double(now.temperature);
-        now.scale.c = c > 3.4e38 ? 3.4028234e38f : float(c);
-        now.scale.c_low = c > 3.4e38 ? 0.f : float(c - double(now.scale.c));
+        const float h = now.temperature >= 0x1p64f ? 0.25f : now.temperature < 0x1p-120f ? 0x1p64f : 1.f;
+        const double c = 64 * 1.4426950408889634074 / double(now.temperature) / double(h);
+        now.scale.minus = -h;
+        now.scale.c = float(c);
+        now.scale.c_low = float(c - double(now.scale.c));
         now.scale.cap = fminf(4096.f / now.scale.c, 3.4028234e38f);
         // (over an infinite temperature every finite logit weighs 1)
         now.min_at = !(now.min_p > 0.f)              ? 0.0
@@ -543,7 +549,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     return;
   }
   Scale scale = settings.scale;
-  scale.top = top;
+  if (scale.minus < -1.f && fabsf(top) >= 0x1p60f) {       // 2^64 top would be past the range; what lies below it weighs nothing
+    scale.minus = -1.f;
+    scale.c = 0x1.fffffep127f;
+    scale.c_low = 0.f;
+    scale.cap = 4096.f / scale.c;
+  }
+  scale.top = -scale.minus * top;
   auto weigh = [&](float y) {
     Weight a, b;
     weigh2<T>(scale, powers, y, y, a, b);
@@ -1148,7 +1160,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
   if (!out) return;
   // ------------------------------------------------------- the distribution
   const float c = scale.c * (1.f / 64), inv = 1.f / (float(uint64_t(whole >> (kLong ? 20 : 0))) * exp2f(float((kLong ? 20 : 0) - kOne)));
-  auto share = [&](float y, int r) { return kept(y, r) ? (y == top ? 1.f : ex2((y - top) * c)) * inv : 0.f; };
+  auto share = [&](float y, int r) { return kept(y, r) ? (y == top ? 1.f : ex2(fmaf(y, -scale.minus, -scale.top) * c)) * inv : 0.f; };
   each([&](int r, float a, float b) { store(r, share(a, r), share(b, r + 1)); });
 }
 
