@@ -33,8 +33,8 @@ struct NormParams {
 constexpr int kNormThreads = 256;
 constexpr int kNormBlocks = 4;       // of an SM at once: 64 registers a thread (5 blocks spill: 139 us for 88)
 constexpr int kNormTokens = 32;
-// A BF16 head's squares can pass FP32's range: such a head is taken times this,
-// which leaves the largest sum of 256 squares below 2^124 (and eps nothing).
+// A BF16 head's squares, or their mean and eps, can pass FP32's range: such a head is taken times this (and eps
+// times its square), which leaves the largest sum of 256 squares below 2^124.
 constexpr float kNormDown = 0x1p-70f;
 
 template <typename T>
@@ -73,12 +73,12 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParam
         for (int m = 16; m; m /= 2) s += __shfl_xor_sync(~0u, s, m);
         return s;
       };
-      float s = squares();
-      if (s == INFINITY) {
+      float mean = squares() / float(p.d) + n.eps;
+      if (mean == INFINITY) {
         down = kNormDown;
-        s = squares();
+        mean = squares() / float(p.d) + n.eps * down * down;
       }
-      r = rsqrtf(s / float(p.d) + n.eps * (down * down));
+      r = rsqrtf(mean);
     }
     for (int w = lane; w < pairs; w += 32) {
       const bool single = w >= half;
@@ -269,24 +269,24 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
       for (int m = 1; m < 1 << kLog; m *= 2) s += __shfl_xor_sync(~0u, s, m);
       return s;
     };
-    float s = squares(), eps = n.eps;
+    float mean = fmaf(squares(), inv_d, n.eps);
     if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-      const bool over = !is_v && s == INFINITY;
+      const bool over = !is_v && mean == INFINITY;
       if (__any_sync(~0u, over)) {
         if (over) {
-          eps = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             x1[j] = mul2(x1[j], both(kNormDown));
             x2[j] = mul2(x2[j], both(kNormDown));
           }
         }
-        s = squares();
+        const float s = squares();
+        if (over) mean = fmaf(s, inv_d, n.eps * kNormDown * kNormDown);
       }
     }
     if (!any || (!is_q && t.ck < 0)) continue;
     if (!is_v) {
-      const float inv = rsqrtf(s * inv_d + eps);
+      const float inv = rsqrtf(mean);
       const float4 *wt = reinterpret_cast<const float4 *>(weights) + (is_q ? 0 : 4 << kLog) + c;
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
