@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kJoinRows *kJoinWarps, 4)
         line.snap = first.snap;
         const int units = first.hkv * first.blocks;
         line.total = int64_t(line.tiles + line.extra) * units;
-        line.runs = line.runs_of(first, j.grid, units);
+        line.runs = min(int64_t(j.grid), max(line.wanted(first), int64_t(units)));
         line.unit0 = int64_t(line.tiles + line.extra) * (head * first.blocks + row / j.rows);
         span = make_int2(line.first(), line.final());
       }
