@@ -659,7 +659,8 @@ vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
  * kept.  A row with a NaN, with a T of NaN, or with +infinity and T > 0, and a row of
  * nothing but -infinity have the token -1.
  *   x      rows of logits (BF16, FP16 or FP32), row_stride elements apart.
- *   u      FP32 [rows][draws] in [0, 1) (below: 0, above: the last token).
+ *   u      FP32 [rows][draws] in [0, 1) (below: 0, above: the last token that weighs
+ *     anything).
  *   temperature, top_p, min_p  FP32 [rows], top_k int32 [rows], or NULL: 1, and none.
  *   tokens int32 [rows][draws]: independent draws from one distribution.
  *   out    FP32 [rows][vocab] or NULL: that distribution, 0 for what is not kept: the p

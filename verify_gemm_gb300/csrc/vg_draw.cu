@@ -556,6 +556,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     scale.cap = 4096.f / scale.c;
   }
   scale.top = -scale.minus * top;
+  // What a draw's running sum has to exceed, of `all`.
+  auto drawn = [&](int d, auto all) {
+    const float u = p.u[row * p.draws + d];
+    bool exact;
+    return u >= 1.f ? all - 1 : part_of(u, all, exact);
+  };
   auto weigh = [&](float y) {
     Weight a, b;
     weigh2<T>(scale, powers, y, y, a, b);
@@ -903,10 +909,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
             if (uint32_t(list[i]) < index) before += v;
           }
         for (int d = 0; d < p.draws; ++d) {
-          float u = p.u[row * p.draws + d];
-          u = u >= 1.f ? 0x1.fffffep-1f : u;
-          bool exact;
-          const uint64_t want = part_of(u, all, exact);  // the first running sum above it
+          const uint64_t want = drawn(d, all);
           if (tid < keep && want >= before && want < before + w) p.tokens[row * p.draws + d] = int32_t(index);
         }
         if (!out) {
@@ -1137,10 +1140,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) sample_kernel(const __grid_co
     whole = warp_sum<Sum>(whole);
     my_mass = warp_sum<Sum>(my_mass);
     for (int d = 0; d < p.draws; ++d) {
-      float u = p.u[row * p.draws + d];
-      u = u >= 1.f ? 0x1.fffffep-1f : u;
-      bool exact;
-      const Sum want = part_of(u, whole, exact);         // the first running sum above it
+      const Sum want = drawn(d, whole);
       if (want < my_mass || want >= my_mass + mass) continue;
       Sum run = my_mass;
       bool found = false;
