@@ -621,7 +621,7 @@ vg_status vg_qk_norm_rope_append(const vg_qk_norm_rope_desc *desc, const vg_kv_c
  *     Entries outside 0..pages-1 are no pages, as in the table.
  * A sequence with lens[b] < F * page_size has no part in the prefix: all its slots are
  * taken from its own row of the table.  Of the others' rows the first F entries
- * are not read.  Both are read by the kernels, so one captured graph serves every
+ * are not read, and a row may have fewer.  Both are read by the kernels, so one captured graph serves every
  * prefix up to max_prefix_pages.
  * desc and limits as in vg_tree_attention; batch * n * (q_heads / heads)^2 and
  * batch * n^2 below 2^32.  workspace: vg_prefix_attention_workspace_size

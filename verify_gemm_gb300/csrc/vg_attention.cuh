@@ -369,9 +369,9 @@ struct Line {
     // no slot past the table exists: such lengths end with it
     const int64_t room = int64_t(p.cache.max_pages) * p.cache.page_size;
     len = int(min(int64_t(max(p.lens[b], 0)), room));
-    if (pass_of<kParts>(p) == kOwn && len >= shared) {
+    if (pass_of<kParts>(p) == kOwn && p.lens[b] >= shared) {   // (whose own row may hold less than the prefix)
       skip = shared;
-      len -= shared;
+      len = max(0, len - shared);
     }
     return p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   }

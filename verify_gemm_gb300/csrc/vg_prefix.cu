@@ -68,9 +68,7 @@ __global__ void __launch_bounds__(kJoinRows *kJoinWarps, 4)
     const int shared = shared_slots(own);
     int2 span = make_int2(1, 0);
     if (real) {
-      const int64_t room = int64_t(own.cache.max_pages) * own.cache.page_size;
-      if (shared > 0 && min(int64_t(max(own.lens[b], 0)), room) >= shared &&
-          node - b * own.n < (own.counts ? own.counts[b] : own.n)) {
+      if (shared > 0 && own.lens[b] >= shared && node - b * own.n < (own.counts ? own.counts[b] : own.n)) {
         Line<true> line;                                         // the prefix's unit on its line
         line.tiles = Line<true>::tiles_for(first, shared);
         line.extra = first.extra;
