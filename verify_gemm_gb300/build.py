@@ -32,7 +32,7 @@ SOURCES = ["vg_api.cu", "vg_pack.cu", "vg_gemv.cu", "vg_noalloc.cu", "vg_probe.c
            "vg_attention_wide.cu", "vg_sample.cu", "vg_norm_rope.cu", "vg_draw.cu",
            "vg_prefix.cu", "vg_attention_bf16_parts.cu", "vg_attention_f16_parts.cu", "vg_attention_e4m3_parts.cu",
            "vg_attention_wide_parts.cu"]
-HEADERS = ["vg_device.cuh", "vg_internal.h", "vg_cache.h", "vg_rope.cuh", "vg_rows.cuh", "vg_attention.cuh",
+HEADERS = ["vg_device.cuh", "vg_internal.h", "vg_cache.h", "vg_pairs.cuh", "vg_rope.cuh", "vg_rows.cuh", "vg_attention.cuh",
            "vg_attention_wide.cuh", "vg_prefix.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-prec-div=true",

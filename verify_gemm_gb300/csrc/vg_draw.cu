@@ -106,17 +106,6 @@ struct Settings {
 };
 static_assert(sizeof(Settings) == 48, "goes by 16 bytes");
 
-// a + b, a * b + c, two at a time (mul2 and add2 are those of vg_rows.cuh).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 y;
-  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
-      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return y;
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-
 // The weight of a finite logit x is w 2^(kOne - 30 - (bin >> 6)) (w some 2^30), rounded down.  With
 // z = (k + r) / 64, k whole, |r| <= 1/2, it is 2^-(k / 64) from a table times
 // 2^-(r / 64) by its series to the third power (the fourth is 2^-34).  max - x is exact in FP32 for 16-bit logits but for

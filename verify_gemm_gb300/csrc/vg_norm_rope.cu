@@ -19,6 +19,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "vg_pairs.cuh"
 #include "vg_rope.cuh"
 
 namespace vg {
@@ -114,23 +115,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const RopeParam
   }
 }
 
-// Two at a time.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 y;
-  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return y;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 y;
-  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
-      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return y;
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (std::is_same_v<T, __half>) {

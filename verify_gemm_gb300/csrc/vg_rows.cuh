@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "vg_internal.h"
+#include "vg_pairs.cuh"
 
 namespace vg {
 namespace {
@@ -101,22 +102,6 @@ __device__ __forceinline__ void copy16(void *to, const void *from) {
                    static_cast<uint32_t>(__cvta_generic_to_shared(to))),
                "l"(from)
                : "memory");
-}
-
-// a + b and a * b, two at a time.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 y;
-  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return y;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 y;
-  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return y;
 }
 
 template <typename T>
