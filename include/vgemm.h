@@ -621,8 +621,8 @@ vg_status vg_qk_norm_rope_append(const vg_qk_norm_rope_desc *desc, const vg_kv_c
  *     Entries outside 0..pages-1 are no pages, as in the table.
  * A sequence with lens[b] < F * page_size has no part in the prefix: all its slots are
  * taken from its own row of the table.  Of the others' rows the first F entries
- * are not read, and a row may have fewer.  Both are read by the kernels, so one captured graph serves every
- * prefix up to max_prefix_pages.
+ * are not read, and a row may have fewer.  prefix and prefix_pages are read by the
+ * kernels, so one captured graph serves every prefix up to max_prefix_pages.
  * desc and limits as in vg_tree_attention; batch * n * (q_heads / heads)^2 and
  * batch * n^2 below 2^32.  workspace: vg_prefix_attention_workspace_size
  * bytes, under the same rules. */
@@ -654,7 +654,9 @@ vg_status vg_probabilities(const void *x, int type, int64_t rows, int64_t vocab,
  * kept, in the order of the indices, exceeds u times their sum.  Sums are exact in
  * integers, so the same call gives the same tokens.  They are of weights good to
  * 2^-27.6 of themselves and rounded down to 2^-46 of the largest (2^-56 from 2^18
- * tokens on), so that a row loses 2^-28 of the largest at most.
+ * tokens on), so that a row loses 2^-28 of the largest at most.  (16-bit logits below
+ * 2^-13 of the largest's magnitude, whose difference to it FP32 does not hold: good to
+ * 2^-24 of that difference over T, too.)
  * With T <= 0 the first largest logit alone is kept.  A logit of -infinity is never
  * kept.  A row with a NaN, with a T of NaN, or with +infinity and T > 0, and a row of
  * nothing but -infinity have the token -1.

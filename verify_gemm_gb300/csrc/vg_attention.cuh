@@ -119,7 +119,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // Divisions by numbers that only the launch knows take some 150 clocks, and a
 // unit's beginning and end are a chain of them.
-// row / group, exact for row < 2^32 / group (rows are below 2^20 / 4).
+// row / group, exact for row < 2^32 / group: a sequence's rows are 64 times 4096 at most, and those of a whole batch
+// over a prefix are checked before the launch.
 __device__ __forceinline__ int node_of(const AttnParams &p, int row) {
   return p.group == 1 ? row : int(__umulhi(uint32_t(row), p.group_magic));
 }

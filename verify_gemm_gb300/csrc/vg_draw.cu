@@ -24,9 +24,10 @@
 // What bounds it: for a few rows the exchanges between a cluster's blocks, some 1.7 us each (one row of
 // 151936 BF16 logits, top-k 50 and top-p 0.95: 12.5 us, of which 3 to the largest, 3.5 to the list at the first block, 2 for its
 // order and cut; top-p alone 28), and instructions that are fetched for the
-// first time; for many rows, of 35 instructions an element for a weight and its place in the bins, the
+// first time; for many rows, of some 45 instructions an element (issue 42 %), the
 // barriers between steps of which the first block of a row does some alone.  256 rows with settings of
-// their own 106 us (78 MB: 0.7 TB/s), 128 FP32 rows with their distributions 106 us (156 MB).
+// their own 106 us (78 MB: 0.7 TB/s), 128 FP32 rows with their distributions 107 us (156 MB), 256 rows that
+// all search for a top-p 218 us.
 // (Two searches by codes alone, one level of bins after another, took 550 us and 1.7 ms: the
 // bins of codes near zero are nearly empty and those of the body full.)
 #include <algorithm>
@@ -44,6 +45,9 @@ constexpr int kDrawShareMax = 160 * 1024;     // ... and may
 constexpr int kLocal = 1024, kSorted = 2048;  // tokens of a block, of the row, that a list holds
 constexpr int kGroups = 256;                  // of which the largest logit is known to all blocks
 static_assert(kMaxCluster * kDrawWarps == kGroups, "at least one group a warp");
+// The largest top-k without a search: near 256 the groups' largest bound it badly, and the tokens to sort pass 512 and 1024.
+// 138 rows of 151936 take 56 us at 200 and 78 at 201, 8 rows 22.7 at both; with a list up to 250, 138 rows of 250 would take
+// 65 for 77, but 8 rows of 224 28 for 24 and of 248 35 for 24.
 constexpr int kSmallK = 200;
 constexpr int kListBytes = (kLocal + kSorted) * 8;   // (and the bins, which are read before a list is made)
 static_assert(kListBytes >= 3 * kBins * 4, "room for the bins");
@@ -108,10 +112,11 @@ static_assert(sizeof(Settings) == 48, "goes by 16 bytes");
 
 // The weight of a finite logit x is w 2^(kOne - 30 - (bin >> 6)) (w some 2^30), rounded down.  With
 // z = (k + r) / 64, k whole, |r| <= 1/2, it is 2^-(k / 64) from a table times
-// 2^-(r / 64) by its series to the third power (the fourth is 2^-34).  max - x is exact in FP32 for 16-bit logits but for
-// those that are 2^-16 of the largest or less; for FP32 ones what it loses is
-// carried along.  The bin is k: the larger logit never has the larger one, as it goes by the
-// rounded difference alone.
+// 2^-(r / 64) by its series to the third power (the fourth is 2^-34).  What max - x loses in FP32 is carried along
+// for FP32 logits.  It is exact for 16-bit ones but for those of less than 2^-16 (BF16) or 2^-13 (FP16) of the largest's
+// magnitude, whose weights are off by up to 2^-24 (max - x) / T of themselves (carried along there, too: 256 mixed rows 111 us
+// for 105).  The bin is k: the larger logit never has the larger one, as it goes by the rounded
+// difference alone.
 constexpr float kMagic = 12582912.f;           // 1.5 2^23: what is added to it is rounded to a whole number
 constexpr int kMagicBits = 0x4B400000;
 struct Weight {
@@ -1169,9 +1174,10 @@ cudaError_t launch_sample(DrawParams p, int64_t rows, int sms, cudaStream_t st) 
   const int64_t share = int64_t(p.chunk) * kDrawWarps * size;
   const bool held = share <= kDrawShareMax;
   // In what order they begin: with more blocks than run at once the rows that take longest should not be
-  // the last (256 rows of mixed settings 107 us, in their own order 122; 138 rows of equal ones, for
-  // which it is a search for nothing, 57 and 55).  Rows of short blocks keep theirs: the settings
-  // take a microsecond to read.
+  // the last (256 rows of mixed settings 121 us, in their own order 141, 512 rows 224 and 240; rows of equal
+  // ones, for which it is a search for nothing, 1.5 % more: 256 of top-p 217.5 and 214.5).  A thread looks at
+  // one row, so more than 512 keep their order.  Rows of short blocks keep theirs: the settings take a
+  // microsecond to read.
   const bool ordered = held && rows <= kDrawThreads && rows * c > 2 * sms && share >= 32 * 1024 && (p.top_k || p.top_p);
   p.rows = int(std::min<int64_t>(rows, kDrawThreads));
   static std::atomic<uint64_t> allowed[5];
